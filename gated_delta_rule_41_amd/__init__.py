@@ -16,43 +16,15 @@ from __future__ import annotations
 from typing import Optional
 
 from . import _lib
+from ._tensors import check as _check, dt_code as _dt_code, ptr as _ptr, torch_module as _torch
 from ._lib import (KDA_BF16, KDA_F32, KDA_FLAG_SAVE_FOR_BWD, KDA_FLAG_SEQUENTIAL, KdaConfig, KdaError, kda_bwd_workspace_size,
                    kda_fwd_workspace_size, kda_saved_size, make_config)
+from .linear import kda_linear, kda_linear_bwd, kda_linear_decode, kda_linear_fwd, kda_tree, kda_tree_commit
 
-__all__ = ["kda", "kda_fwd", "kda_fwd_staged", "kda_bwd", "kda_decode", "kda_saved_size", "kda_fwd_workspace_size", "kda_bwd_workspace_size",
+__all__ = ["kda_linear", "kda_linear_fwd", "kda_linear_bwd", "kda_linear_decode", "kda_tree", "kda_tree_commit",
+           "kda", "kda_fwd", "kda_fwd_staged", "kda_bwd", "kda_decode", "kda_saved_size", "kda_fwd_workspace_size", "kda_bwd_workspace_size",
            "make_config", "KdaConfig", "KdaError", "KDA_F32", "KDA_BF16", "KDA_FLAG_SAVE_FOR_BWD",
            "KDA_FLAG_SEQUENTIAL"]
-
-
-def _torch():
-    import torch
-    return torch
-
-
-def _dt_code(dtype):
-    torch = _torch()
-    if dtype == torch.bfloat16:
-        return KDA_BF16
-    if dtype == torch.float32:
-        return KDA_F32
-    raise TypeError(f"unsupported dtype {dtype}")
-
-
-def _ptr(t):
-    return 0 if t is None else int(t.data_ptr())
-
-
-def _check(t, name, shape, dtype, device):
-    if t is None:
-        return
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
 
 
 def _common(q, k, v, g, beta, cu_seqlens, num_seqs):

@@ -37,6 +37,40 @@ class KdaConfig(ctypes.Structure):
     ]
 
 
+KDA_GATE_TOKEN, KDA_GATE_HEAD = 0, 1
+KDA_RULE_DELTA, KDA_RULE_LINEAR = 0, 1
+KDA_TREE_MAX_NODES = 64
+
+
+class KdaLinearConfig(ctypes.Structure):
+    _fields_ = [
+        ("H", ctypes.c_int32),
+        ("Hk", ctypes.c_int32),
+        ("dk", ctypes.c_int32),
+        ("dv", ctypes.c_int32),
+        ("in_dtype", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int32),
+        ("gate", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+    ]
+
+
+class KdaTreeConfig(ctypes.Structure):
+    _fields_ = [
+        ("rule", ctypes.c_int32),
+        ("H", ctypes.c_int32),
+        ("Hk", ctypes.c_int32),
+        ("dk", ctypes.c_int32),
+        ("dv", ctypes.c_int32),
+        ("nodes", ctypes.c_int32),
+        ("in_dtype", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int32),
+        ("gate", ctypes.c_int32),
+        ("l2_eps", ctypes.c_float),
+        ("scale", ctypes.c_float),
+    ]
+
+
 class KdaError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"libkda status {status}: {message}")
@@ -92,6 +126,22 @@ def load():
         fn.restype = ctypes.c_int
     lib.kda_decode.argtypes = [cfgp, ctypes.c_int32] + [_vp] * 9
     lib.kda_decode.restype = ctypes.c_int
+    lincfg, treecfg, i32, size = ctypes.POINTER(KdaLinearConfig), ctypes.POINTER(KdaTreeConfig), ctypes.c_int32, ctypes.c_size_t
+    lib.kda_linear_config_init.argtypes = [lincfg] + [i32] * 4
+    lib.kda_linear_config_init.restype = None
+    for name in ("kda_linear_fwd_workspace_size", "kda_linear_bwd_workspace_size"):
+        fn = getattr(lib, name)
+        fn.argtypes = [lincfg, ctypes.c_int64, i32]
+        fn.restype = size
+    lib.kda_linear_fwd.argtypes = [lincfg, ctypes.c_int64, i32] + [_vp] * 9 + [size, _vp]
+    lib.kda_linear_bwd.argtypes = [lincfg, ctypes.c_int64, i32] + [_vp] * 14 + [size, _vp]
+    lib.kda_linear_decode.argtypes = [lincfg, i32] + [_vp] * 8
+    lib.kda_tree_config_init.argtypes = [treecfg] + [i32] * 6
+    lib.kda_tree_config_init.restype = None
+    lib.kda_tree.argtypes = [treecfg, i32] + [_vp] * 9
+    lib.kda_tree_commit.argtypes = [treecfg, i32] + [_vp] * 9
+    for name in ("kda_linear_fwd", "kda_linear_bwd", "kda_linear_decode", "kda_tree", "kda_tree_commit"):
+        getattr(lib, name).restype = ctypes.c_int
     lib.kda_status_string.argtypes = [ctypes.c_int]
     lib.kda_status_string.restype = ctypes.c_char_p
     lib.kda_last_error.argtypes = []
@@ -166,3 +216,51 @@ def kda_bwd_raw(cfg, total_tokens, num_seqs, q, k, v, g, beta, cu_seqlens, initi
 def kda_decode_raw(cfg, num_seqs, q, k, v, g, beta, state_in, state_out, o, stream) -> int:
     """Direct call of kda_decode with integer device addresses (0 = NULL); returns the status."""
     return load().kda_decode(ctypes.byref(cfg), num_seqs, q, k, v, g, beta, state_in, state_out, o, stream)
+
+
+# ---- the linear rule and drafted trees: direct calls with integer device addresses (0 = NULL)
+def make_linear_config(H, Hk, dk, dv, in_dtype=KDA_BF16, out_dtype=KDA_F32, gate=KDA_GATE_TOKEN, scale=1.0):
+    cfg = KdaLinearConfig()
+    load().kda_linear_config_init(ctypes.byref(cfg), H, Hk, dk, dv)
+    cfg.in_dtype, cfg.out_dtype, cfg.gate, cfg.scale = in_dtype, out_dtype, gate, scale
+    return cfg
+
+
+def make_tree_config(rule, H, Hk, dk, dv, nodes, in_dtype=KDA_BF16, out_dtype=KDA_F32, gate=KDA_GATE_TOKEN, eps=1e-6,
+                     scale=1.0):
+    cfg = KdaTreeConfig()
+    load().kda_tree_config_init(ctypes.byref(cfg), rule, H, Hk, dk, dv, nodes)
+    cfg.in_dtype, cfg.out_dtype, cfg.gate, cfg.l2_eps, cfg.scale = in_dtype, out_dtype, gate, eps, scale
+    return cfg
+
+
+def kda_linear_fwd_workspace_size(cfg: KdaLinearConfig, total_tokens: int, num_seqs: int) -> int:
+    return int(load().kda_linear_fwd_workspace_size(ctypes.byref(cfg), total_tokens, num_seqs))
+
+
+def kda_linear_bwd_workspace_size(cfg: KdaLinearConfig, total_tokens: int, num_seqs: int) -> int:
+    return int(load().kda_linear_bwd_workspace_size(ctypes.byref(cfg), total_tokens, num_seqs))
+
+
+def kda_linear_fwd_raw(cfg, total_tokens, num_seqs, q, k, v, g, cu_seqlens, initial_state, o, final_state, workspace,
+                       workspace_bytes, stream) -> int:
+    return load().kda_linear_fwd(ctypes.byref(cfg), total_tokens, num_seqs, q, k, v, g, cu_seqlens, initial_state, o,
+                                 final_state, workspace, workspace_bytes, stream)
+
+
+def kda_linear_bwd_raw(cfg, total_tokens, num_seqs, q, k, v, g, cu_seqlens, initial_state, dO, dS_final, dq, dk, dv, dg,
+                       d_initial_state, workspace, workspace_bytes, stream) -> int:
+    return load().kda_linear_bwd(ctypes.byref(cfg), total_tokens, num_seqs, q, k, v, g, cu_seqlens, initial_state, dO,
+                                 dS_final, dq, dk, dv, dg, d_initial_state, workspace, workspace_bytes, stream)
+
+
+def kda_linear_decode_raw(cfg, num_seqs, q, k, v, g, state_in, state_out, o, stream) -> int:
+    return load().kda_linear_decode(ctypes.byref(cfg), num_seqs, q, k, v, g, state_in, state_out, o, stream)
+
+
+def kda_tree_raw(cfg, num_seqs, q, k, v, g, beta, parent, state, o, stream) -> int:
+    return load().kda_tree(ctypes.byref(cfg), num_seqs, q, k, v, g, beta, parent, state, o, stream)
+
+
+def kda_tree_commit_raw(cfg, num_seqs, k, v, g, beta, parent, accept, state_in, state_out, stream) -> int:
+    return load().kda_tree_commit(ctypes.byref(cfg), num_seqs, k, v, g, beta, parent, accept, state_in, state_out, stream)

@@ -22,7 +22,7 @@
 
 namespace {
 
-thread_local char g_err[256] = "";
+thread_local char g_err[kda::kErrorBytes] = "";
 
 kda_status fail(kda_status s, const char* fmt, const char* what = "") {
     snprintf(g_err, sizeof g_err, fmt, what);
@@ -330,6 +330,8 @@ kda_status static_workspace(void** out) {
 }
 
 }  // namespace
+
+char* kda::error_text() { return g_err; }
 
 #define KDA_TRY(x) KDA_TRY_(x)
 

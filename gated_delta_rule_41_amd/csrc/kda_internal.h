@@ -161,6 +161,10 @@ struct DecodeParams {
     int32_t nslices;     // dv / kSlice
 };
 
+// The thread-local text behind kda_last_error(), for the other files of the C ABI.
+constexpr int kErrorBytes = 256;
+char* error_text();
+
 // in_dtype / out_dtype: 0 = fp32, 1 = bf16 (kda_dtype values).
 hipError_t launch_fwd(const FwdParams& p, int in_dtype, int out_dtype, int dk, bool save,
                       hipStream_t stream);

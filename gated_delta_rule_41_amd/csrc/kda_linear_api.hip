@@ -1,0 +1,395 @@
+// kda_linear_api.hip -- the C ABI of the linear rule and of the drafted-tree operators
+// (include/kda.h).  As in kda_api.hip every argument is checked on the host before any HIP
+// call, and nothing is allocated.
+#include <math.h>
+#include <stdio.h>
+#include <string.h>
+
+#include "../../include/kda.h"
+#include "kda_internal.h"
+#include "kda_linear.h"
+#include "kda_tree.h"
+
+#define KDA_TRY(x)                       \
+    do {                                 \
+        kda_status _s = (x);             \
+        if (_s != KDA_OK) return _s;     \
+    } while (0)
+
+namespace {
+
+using namespace kda;
+
+kda_status fail(kda_status s, const char* fmt, const char* what = "") {
+    snprintf(error_text(), kErrorBytes, fmt, what);
+    return s;
+}
+kda_status launched(hipError_t e) {
+    return e == hipSuccess ? KDA_OK : fail(KDA_ERR_HIP, "kernel launch failed: %s", hipGetErrorString(e));
+}
+
+size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+kda_status ptr(const void* p, const char* name, bool needed) {
+    if (!p) return needed ? fail(KDA_ERR_INVALID_ARG, "%s is NULL", name) : KDA_OK;
+    if ((uintptr_t)p & 15) return fail(KDA_ERR_INVALID_ARG, "%s is not 16-byte aligned", name);
+    return KDA_OK;
+}
+
+bool is_dtype(int32_t t) { return t == KDA_F32 || t == KDA_BF16; }
+
+kda_status check_heads(int32_t H, int32_t Hk, int32_t dk, int32_t dv, int32_t in, int32_t out, int32_t gate, float scale) {
+    if (H < 1 || Hk < 1 || H % Hk) return fail(KDA_ERR_INVALID_ARG, "H and Hk must be >= 1 and Hk must divide H%s");
+    if ((dk != 64 && dk != 128) || (dv != 64 && dv != 128)) return fail(KDA_ERR_UNSUPPORTED, "dk and dv must be 64 or 128%s");
+    if (!is_dtype(in) || !is_dtype(out)) return fail(KDA_ERR_INVALID_ARG, "unknown dtype%s");
+    if (gate != KDA_GATE_TOKEN && gate != KDA_GATE_HEAD) return fail(KDA_ERR_INVALID_ARG, "unknown gate%s");
+    if (!isfinite(scale)) return fail(KDA_ERR_INVALID_ARG, "scale must be finite%s");
+    return KDA_OK;
+}
+kda_status check_config(const kda_linear_config* c) {
+    if (!c) return fail(KDA_ERR_INVALID_ARG, "config is NULL%s");
+    return check_heads(c->H, c->Hk, c->dk, c->dv, c->in_dtype, c->out_dtype, c->gate, c->scale);
+}
+
+// One launch covers at most 2^32 - 1 work-items along x.
+bool grid_fits(int64_t workgroups, int threads) {
+    return workgroups >= 0 && workgroups <= (int64_t)UINT32_MAX / threads;
+}
+
+// ---------------------------------------------------------------- plans
+// A walk goes over a whole document; few documents and heads leave compute units idle.  Then
+// documents are cut into segments: the segments' own sums, the states entering them, the
+// walks from those.  The plan depends on the config and the sizes alone, so that the
+// workspace size is a host function.
+constexpr int64_t kWalkTarget = 512;     // workgroups a walk aims for
+constexpr int64_t kMinSegment = 512;     // tokens: below, a segment's state outweighs its rows
+
+struct Plan {
+    int32_t seg_len;   // 0: whole documents
+    int64_t chains;    // (document or segment slot, head) pairs
+};
+Plan walk_plan(const kda_linear_config* c, int64_t T, int32_t N, int dirs) {
+    Plan p = {0, (int64_t)N * c->H};
+    const int64_t wgs = p.chains * (c->dv / kSlice) * dirs;
+    const int64_t per_doc = (kWalkTarget + wgs - 1) / wgs, avg = T / N;
+    if (per_doc < 2 || avg < 2 * kMinSegment) return p;
+    int64_t L = (avg + per_doc - 1) / per_doc;
+    L = (L + kLinBlock - 1) / kLinBlock * kLinBlock;
+    if (L < kMinSegment) L = kMinSegment;
+    p.seg_len = (int32_t)L;
+    p.chains = linear_slots(T, N, p.seg_len) * c->H;
+    return p;
+}
+
+size_t elem(const kda_linear_config* c) { return c->in_dtype == KDA_BF16 ? 2 : 4; }
+size_t state_elems(const kda_linear_config* c) { return (size_t)c->dk * c->dv; }
+
+struct FwdLayout {
+    Plan plan;
+    size_t state, decay, total;
+};
+FwdLayout fwd_layout(const kda_linear_config* c, int64_t T, int32_t N) {
+    FwdLayout f = {walk_plan(c, T, N, 1), 0, 0, 0};
+    if (f.plan.seg_len) {
+        f.decay = align256((size_t)f.plan.chains * state_elems(c) * sizeof(float));
+        f.total = f.decay + align256((size_t)f.plan.chains * sizeof(float));
+    }
+    return f;
+}
+
+struct BwdLayout {
+    Plan plan;
+    int64_t blocks;
+    size_t S, dS, e, a, f, cross, part, seg[2], decay[2], total;
+};
+BwdLayout bwd_layout(const kda_linear_config* c, int64_t T, int32_t N) {
+    BwdLayout b;
+    memset(&b, 0, sizeof b);
+    b.plan = walk_plan(c, T, N, 2);
+    b.blocks = linear_slots(T, N, kLinBlock);
+    size_t at = 0;
+    auto take = [&at](size_t bytes) {
+        const size_t x = at;
+        at += align256(bytes);
+        return x;
+    };
+    const size_t states = (size_t)b.blocks * c->H * state_elems(c) * elem(c), rows = (size_t)T * c->H * sizeof(float);
+    b.S = take(states);
+    b.dS = take(states);
+    b.e = take(rows);
+    b.a = take(rows);
+    b.f = take(rows);
+    b.cross = take((size_t)b.blocks * c->H * sizeof(float));
+    b.part = take(c->gate == KDA_GATE_HEAD ? (size_t)b.blocks * c->H * sizeof(float) : 0);
+    if (b.plan.seg_len)
+        for (int i = 0; i < 2; ++i) {
+            b.seg[i] = take((size_t)b.plan.chains * state_elems(c) * sizeof(float));
+            b.decay[i] = take((size_t)b.plan.chains * sizeof(float));
+        }
+    b.total = at;
+    return b;
+}
+
+kda_status check_sizes(const kda_linear_config* c, int64_t T, int32_t N, const int32_t* cu) {
+    if (T < 0 || T >= ((int64_t)1 << 31)) return fail(KDA_ERR_INVALID_ARG, "total_tokens must be in [0, 2^31)%s");
+    if (N < 1) return fail(KDA_ERR_INVALID_ARG, "num_seqs must be >= 1%s");
+    if (!cu && T % N) return fail(KDA_ERR_INVALID_ARG, "cu_seqlens is NULL but total_tokens is not a multiple of num_seqs%s");
+    // the largest launches: walks of 64-column slices, blocks of gradients, the carry
+    if (!grid_fits(((linear_slots(T, N, kLinBlock) + 8) * c->H) * (c->dv / kSlice), kGradThreads) ||
+        !grid_fits((int64_t)N * c->H * (c->dk * c->dv / (4 * kThreads)), kThreads))
+        return fail(KDA_ERR_UNSUPPORTED, "num_seqs, H or total_tokens too large for one launch%s");
+    return KDA_OK;
+}
+
+bool overlap(const void* a, const void* b, size_t bytes) {
+    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+    return a && a != b && x < y + bytes && y < x + bytes;
+}
+
+kda_status check_tree(const kda_tree_config* c, int32_t N, int threads, int64_t per_head) {
+    if (!c) return fail(KDA_ERR_INVALID_ARG, "config is NULL%s");
+    if (c->rule != KDA_RULE_DELTA && c->rule != KDA_RULE_LINEAR) return fail(KDA_ERR_INVALID_ARG, "unknown rule%s");
+    KDA_TRY(check_heads(c->H, c->Hk, c->dk, c->dv, c->in_dtype, c->out_dtype, c->gate, c->scale));
+    if (c->rule == KDA_RULE_DELTA && (c->Hk != c->H || c->gate != KDA_GATE_TOKEN))
+        return fail(KDA_ERR_UNSUPPORTED, "the delta rule has Hk = H and a gate per token%s");
+    if (!(c->l2_eps >= 0.f) || !isfinite(c->l2_eps)) return fail(KDA_ERR_INVALID_ARG, "l2_eps must be finite and >= 0%s");
+    if (c->nodes < 1 || c->nodes > KDA_TREE_MAX_NODES) return fail(KDA_ERR_UNSUPPORTED, "nodes must be in [1, 64]%s");
+    if (N < 0) return fail(KDA_ERR_INVALID_ARG, "num_seqs must be >= 0%s");
+    if (!grid_fits((int64_t)N * c->H * per_head, threads)) return fail(KDA_ERR_UNSUPPORTED, "num_seqs * H too large for one launch%s");
+    return KDA_OK;
+}
+TreeParams tree_params(const kda_tree_config* c, int32_t N) {
+    TreeParams p;
+    memset(&p, 0, sizeof p);
+    p.N = N; p.H = c->H; p.Hk = c->Hk; p.L = c->nodes; p.dv = c->dv;
+    p.gate_head = c->gate == KDA_GATE_HEAD;
+    p.out_bf16 = c->out_dtype == KDA_BF16;
+    p.eps = c->l2_eps; p.scale = c->scale;
+    return p;
+}
+
+}  // namespace
+
+static_assert(KDA_TREE_MAX_NODES == kda::kTreeMaxNodes, "tree size");
+
+extern "C" {
+
+void kda_linear_config_init(kda_linear_config* cfg, int32_t H, int32_t Hk, int32_t dk, int32_t dv) {
+    if (!cfg) return;
+    memset(cfg, 0, sizeof *cfg);
+    cfg->H = H; cfg->Hk = Hk; cfg->dk = dk; cfg->dv = dv;
+    cfg->in_dtype = KDA_F32; cfg->out_dtype = KDA_F32;
+    cfg->gate = KDA_GATE_TOKEN;
+    cfg->scale = 1.0f;
+}
+
+size_t kda_linear_fwd_workspace_size(const kda_linear_config* cfg, int64_t T, int32_t N) {
+    if (check_config(cfg) != KDA_OK || T < 0 || N < 1) return 0;
+    return fwd_layout(cfg, T, N).total;
+}
+
+size_t kda_linear_bwd_workspace_size(const kda_linear_config* cfg, int64_t T, int32_t N) {
+    if (check_config(cfg) != KDA_OK || T < 0 || N < 1) return 0;
+    return bwd_layout(cfg, T, N).total;
+}
+
+kda_status kda_linear_fwd(const kda_linear_config* cfg, int64_t T, int32_t N, const void* q, const void* k, const void* v,
+                          const float* g, const int32_t* cu, const float* s0, void* o, float* sfinal, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+    error_text()[0] = 0;
+    KDA_TRY(check_config(cfg));
+    KDA_TRY(check_sizes(cfg, T, N, cu));
+    KDA_TRY(ptr(q, "q", T > 0));
+    KDA_TRY(ptr(k, "k", T > 0));
+    KDA_TRY(ptr(v, "v", T > 0));
+    KDA_TRY(ptr(g, "g", T > 0));
+    KDA_TRY(ptr(o, "o", T > 0));
+    KDA_TRY(ptr(cu, "cu_seqlens", false));
+    KDA_TRY(ptr(s0, "initial_state", false));
+    KDA_TRY(ptr(sfinal, "final_state", false));
+    const FwdLayout f = fwd_layout(cfg, T, N);
+    if (workspace_bytes < f.total) return fail(KDA_ERR_WORKSPACE, "workspace too small%s");
+    KDA_TRY(ptr(workspace, "workspace", f.total > 0));
+
+    hipStream_t st = (hipStream_t)stream;
+    LinearParams p;
+    memset(&p, 0, sizeof p);
+    p.q = q; p.k = k; p.v = v; p.g = g; p.cu = cu; p.s0 = s0; p.o = o; p.sfinal = sfinal;
+    p.T = T; p.N = N; p.H = cfg->H; p.Hk = cfg->Hk; p.dv = cfg->dv;
+    p.seqlen = cu ? 0 : (int32_t)(T / N);
+    p.g_stride = cfg->gate == KDA_GATE_TOKEN ? cfg->H : 0;
+    p.out_bf16 = cfg->out_dtype == KDA_BF16;
+    p.scale = cfg->scale;
+    p.seg_len = f.plan.seg_len;
+    p.chains = (int32_t)f.plan.chains;
+    if (p.seg_len) {
+        float* state = (float*)workspace;
+        float* decay = (float*)((char*)workspace + f.decay);
+        LinearStateParams s;
+        memset(&s, 0, sizeof s);
+        s.dir[0].a = k; s.dir[0].b = v; s.dir[0].last = state; s.dir[0].decay = decay;
+        s.g = g; s.cu = cu; s.T = T; s.N = N; s.H = p.H; s.Hk = p.Hk; s.dv = p.dv; s.seqlen = p.seqlen;
+        s.g_stride = p.g_stride; s.seg_len = p.seg_len; s.chains = p.chains; s.scale = p.scale;
+        KDA_TRY(launched(launch_linear_states(s, 1, cfg->in_dtype, cfg->dk, st)));
+        LinearCarryParams c;
+        memset(&c, 0, sizeof c);
+        c.dir[0].s0 = s0; c.dir[0].state = state; c.dir[0].decay = decay; c.dir[0].last = sfinal;
+        c.cu = cu; c.T = T; c.N = N; c.H = p.H; c.seqlen = p.seqlen; c.seg_len = p.seg_len; c.elems = cfg->dk * cfg->dv;
+        KDA_TRY(launched(launch_linear_carry(c, 1, st)));
+        p.s0 = state;
+    }
+    return launched(launch_linear_out(p, cfg->in_dtype, cfg->dk, st));
+}
+
+kda_status kda_linear_bwd(const kda_linear_config* cfg, int64_t T, int32_t N, const void* q, const void* k, const void* v,
+                          const float* g, const int32_t* cu, const float* s0, const void* dO, const float* dSf, void* dq,
+                          void* dk, void* dv, void* dg, float* dS0, void* workspace, size_t workspace_bytes, void* stream) {
+    error_text()[0] = 0;
+    KDA_TRY(check_config(cfg));
+    KDA_TRY(check_sizes(cfg, T, N, cu));
+    const bool any = T > 0;
+    KDA_TRY(ptr(q, "q", any));
+    KDA_TRY(ptr(k, "k", any));
+    KDA_TRY(ptr(v, "v", any));
+    KDA_TRY(ptr(g, "g", any));
+    KDA_TRY(ptr(dO, "dO", any));
+    KDA_TRY(ptr(dq, "dq", any));
+    KDA_TRY(ptr(dk, "dk", any));
+    KDA_TRY(ptr(dv, "dv", any));
+    KDA_TRY(ptr(dg, "dg", any || cfg->gate == KDA_GATE_HEAD));
+    KDA_TRY(ptr(cu, "cu_seqlens", false));
+    KDA_TRY(ptr(s0, "initial_state", false));
+    KDA_TRY(ptr(dSf, "dS_final", false));
+    KDA_TRY(ptr(dS0, "d_initial_state", false));
+    const BwdLayout b = bwd_layout(cfg, T, N);
+    if (workspace_bytes < b.total) return fail(KDA_ERR_WORKSPACE, "workspace too small%s");
+    KDA_TRY(ptr(workspace, "workspace", b.total > 0));
+
+    hipStream_t st = (hipStream_t)stream;
+    char* ws = (char*)workspace;
+    const int32_t seqlen = cu ? 0 : (int32_t)(T / N), g_stride = cfg->gate == KDA_GATE_TOKEN ? cfg->H : 0;
+    LinearStateParams s;
+    memset(&s, 0, sizeof s);
+    s.dir[0].a = k; s.dir[0].b = v;
+    s.dir[1].a = q; s.dir[1].b = dO; s.dir[1].rev = 1;
+    s.g = g; s.cu = cu; s.T = T; s.N = N; s.H = cfg->H; s.Hk = cfg->Hk; s.dv = cfg->dv; s.seqlen = seqlen;
+    s.g_stride = g_stride; s.seg_len = b.plan.seg_len; s.chains = (int32_t)b.plan.chains; s.scale = cfg->scale;
+    const float* first[2] = {s0, dSf};
+    float* last[2] = {nullptr, dS0};
+    if (s.seg_len) {
+        LinearCarryParams c;
+        memset(&c, 0, sizeof c);
+        for (int i = 0; i < 2; ++i) {
+            s.dir[i].last = (float*)(ws + b.seg[i]);
+            s.dir[i].decay = (float*)(ws + b.decay[i]);
+            c.dir[i].s0 = first[i]; c.dir[i].state = s.dir[i].last; c.dir[i].decay = s.dir[i].decay;
+            c.dir[i].last = last[i]; c.dir[i].rev = i;
+        }
+        c.cu = cu; c.T = T; c.N = N; c.H = cfg->H; c.seqlen = seqlen; c.seg_len = s.seg_len; c.elems = cfg->dk * cfg->dv;
+        KDA_TRY(launched(launch_linear_states(s, 2, cfg->in_dtype, cfg->dk, st)));
+        KDA_TRY(launched(launch_linear_carry(c, 2, st)));
+        for (int i = 0; i < 2; ++i) {
+            s.dir[i].s0 = s.dir[i].last;
+            s.dir[i].last = nullptr;
+            s.dir[i].decay = nullptr;
+        }
+    } else {
+        for (int i = 0; i < 2; ++i) {
+            s.dir[i].s0 = first[i];
+            s.dir[i].last = last[i];
+        }
+    }
+    s.dir[0].border = ws + b.S;
+    s.dir[1].border = ws + b.dS;
+    KDA_TRY(launched(launch_linear_states(s, 2, cfg->in_dtype, cfg->dk, st)));
+
+    LinearBwdParams p;
+    memset(&p, 0, sizeof p);
+    p.q = q; p.k = k; p.v = v; p.g = g; p.cu = cu; p.dO = dO;
+    p.S = ws + b.S; p.dS = ws + b.dS;
+    p.e = (float*)(ws + b.e); p.a = (float*)(ws + b.a); p.f = (float*)(ws + b.f); p.cross = (float*)(ws + b.cross);
+    p.dg_part = cfg->gate == KDA_GATE_HEAD ? (float*)(ws + b.part) : nullptr;
+    p.dq = dq; p.dk_out = dk; p.dv_out = dv; p.dg = dg;
+    p.T = T; p.blocks = T > 0 ? b.blocks : 0; p.N = N; p.H = cfg->H; p.Hk = cfg->Hk; p.dv = cfg->dv; p.seqlen = seqlen;
+    p.g_stride = g_stride; p.out_bf16 = cfg->out_dtype == KDA_BF16;
+    p.scale = cfg->scale;
+    return launched(launch_linear_grads(p, cfg->in_dtype, cfg->dk, st));
+}
+
+kda_status kda_linear_decode(const kda_linear_config* cfg, int32_t N, const void* q, const void* k, const void* v,
+                             const float* g, const float* state_in, float* state_out, void* o, void* stream) {
+    error_text()[0] = 0;
+    KDA_TRY(check_config(cfg));
+    if (N < 0) return fail(KDA_ERR_INVALID_ARG, "num_seqs must be >= 0%s");
+    if (!grid_fits((int64_t)N * cfg->H * (cfg->dv / kSlice), kThreads))
+        return fail(KDA_ERR_UNSUPPORTED, "num_seqs * H too large for one launch%s");
+    KDA_TRY(ptr(q, "q", N > 0));
+    KDA_TRY(ptr(k, "k", N > 0));
+    KDA_TRY(ptr(v, "v", N > 0));
+    KDA_TRY(ptr(g, "g", N > 0));
+    KDA_TRY(ptr(state_in, "state_in", false));
+    KDA_TRY(ptr(state_out, "state_out", N > 0));
+    KDA_TRY(ptr(o, "o", N > 0));
+    if (overlap(state_in, state_out, (size_t)N * cfg->H * state_elems(cfg) * sizeof(float)))
+        return fail(KDA_ERR_INVALID_ARG, "state_in and state_out overlap without being equal%s");
+    LinearDecodeParams p;
+    memset(&p, 0, sizeof p);
+    p.q = q; p.k = k; p.v = v; p.g = g; p.s_in = state_in; p.s_out = state_out; p.o = o;
+    p.N = N; p.H = cfg->H; p.Hk = cfg->Hk; p.dv = cfg->dv;
+    p.g_stride = cfg->gate == KDA_GATE_TOKEN ? cfg->H : 0;
+    p.out_bf16 = cfg->out_dtype == KDA_BF16;
+    p.scale = cfg->scale;
+    return launched(launch_linear_decode(p, cfg->in_dtype, cfg->dk, (hipStream_t)stream));
+}
+
+void kda_tree_config_init(kda_tree_config* cfg, int32_t rule, int32_t H, int32_t Hk, int32_t dk, int32_t dv, int32_t nodes) {
+    if (!cfg) return;
+    memset(cfg, 0, sizeof *cfg);
+    cfg->rule = rule; cfg->H = H; cfg->Hk = Hk; cfg->dk = dk; cfg->dv = dv; cfg->nodes = nodes;
+    cfg->in_dtype = KDA_F32; cfg->out_dtype = KDA_F32;
+    cfg->gate = KDA_GATE_TOKEN;
+    cfg->l2_eps = 1e-6f;
+    cfg->scale = 1.0f;
+}
+
+kda_status kda_tree(const kda_tree_config* cfg, int32_t N, const void* q, const void* k, const void* v, const void* g,
+                    const void* beta, const int32_t* parent, const float* state, void* o, void* stream) {
+    error_text()[0] = 0;
+    KDA_TRY(check_tree(cfg, N, 1024, 1));
+    const bool delta = cfg->rule == KDA_RULE_DELTA;
+    KDA_TRY(ptr(q, "q", N > 0));
+    KDA_TRY(ptr(k, "k", N > 0));
+    KDA_TRY(ptr(v, "v", N > 0));
+    KDA_TRY(ptr(g, "g", N > 0));
+    KDA_TRY(ptr(beta, "beta", N > 0 && delta));
+    KDA_TRY(ptr(parent, "parent", N > 0));
+    KDA_TRY(ptr(state, "state", false));
+    KDA_TRY(ptr(o, "o", N > 0));
+    TreeParams p = tree_params(cfg, N);
+    p.q = q; p.k = k; p.v = v; p.g = g; p.beta = beta; p.parent = parent; p.s_in = state; p.o = o;
+    return launched(launch_tree(p, delta, cfg->in_dtype, cfg->dk, (hipStream_t)stream));
+}
+
+kda_status kda_tree_commit(const kda_tree_config* cfg, int32_t N, const void* k, const void* v, const void* g,
+                           const void* beta, const int32_t* parent, const int32_t* accept, const float* state_in,
+                           float* state_out, void* stream) {
+    error_text()[0] = 0;
+    KDA_TRY(check_tree(cfg, N, kThreads, cfg ? cfg->dv / kSlice : 1));
+    const bool delta = cfg->rule == KDA_RULE_DELTA;
+    KDA_TRY(ptr(k, "k", N > 0));
+    KDA_TRY(ptr(v, "v", N > 0));
+    KDA_TRY(ptr(g, "g", N > 0));
+    KDA_TRY(ptr(beta, "beta", N > 0 && delta));
+    KDA_TRY(ptr(parent, "parent", N > 0));
+    KDA_TRY(ptr(accept, "accept", N > 0));
+    KDA_TRY(ptr(state_in, "state_in", false));
+    KDA_TRY(ptr(state_out, "state_out", N > 0));
+    if (overlap(state_in, state_out, (size_t)N * cfg->H * cfg->dk * cfg->dv * sizeof(float)))
+        return fail(KDA_ERR_INVALID_ARG, "state_in and state_out overlap without being equal%s");
+    TreeParams p = tree_params(cfg, N);
+    p.k = k; p.v = v; p.g = g; p.beta = beta; p.parent = parent; p.accept = accept;
+    p.s_in = state_in; p.s_out = state_out;
+    return launched(launch_tree_commit(p, delta, cfg->in_dtype, cfg->dk, (hipStream_t)stream));
+}
+
+}  // extern "C"

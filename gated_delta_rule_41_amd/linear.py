@@ -1,0 +1,229 @@
+"""The linear rule (linear attention with a decay for each head) and trees of
+drafted tokens over the state, for both rules.  Marshalling only, as in the
+package's ``__init__``: see include/kda.h for the layouts.
+"""
+from __future__ import annotations
+
+from typing import Optional
+
+from . import _lib
+from ._lib import KDA_GATE_HEAD, KDA_GATE_TOKEN, KDA_RULE_DELTA, KDA_RULE_LINEAR, KDA_TREE_MAX_NODES
+from ._tensors import check as _check, dt_code as _dt_code, ptr as _ptr, torch_module as _torch
+
+
+def _heads(q, k, v, lead_dims, names=("q", "k", "v")):
+    """Shapes, device and dtype of q/k ``[..., Hk, dk]`` and v ``[..., H, dv]`` (q may be None)."""
+    for name, t in zip(names, (q, k, v)):
+        if t is not None and t.dim() != lead_dims + 2:
+            raise ValueError(f"{name} must have {lead_dims + 2} dimensions, got shape {tuple(t.shape)}")
+    lead, (Hk, dk), (H, dv) = tuple(k.shape[:-2]), k.shape[-2:], v.shape[-2:]
+    dev, dt = k.device, k.dtype
+    if dev.type != "cuda":
+        raise ValueError("libkda runs on the GPU only: tensors must be on a cuda (HIP) device")
+    for name, t, shp in (("q", q, lead + (Hk, dk)), ("k", k, lead + (Hk, dk)), ("v", v, lead + (H, dv))):
+        _check(t, name, shp, dt, dev)
+    return lead, H, Hk, dk, dv, dev, dt
+
+
+def _gate(g, lead, H, dev):
+    """fp32 gates ``[..., H]`` or ``[H]``."""
+    torch = _torch()
+    if g.dim() == 1:
+        _check(g, "g", (H,), torch.float32, dev)
+        return KDA_GATE_HEAD
+    _check(g, "g", lead + (H,), torch.float32, dev)
+    return KDA_GATE_TOKEN
+
+
+def _packed(q, k, v, g, cu_seqlens, num_seqs):
+    torch = _torch()
+    (T,), H, Hk, dk, dv, dev, dt = _heads(q, k, v, 1)
+    gate = _gate(g, (T,), H, dev)
+    if cu_seqlens is not None:
+        if (cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.device != dev
+                or not cu_seqlens.is_contiguous()):
+            raise ValueError("cu_seqlens must be a contiguous 1-D int32 tensor on the same device")
+        N = cu_seqlens.numel() - 1
+        if num_seqs is not None and int(num_seqs) != N:
+            raise ValueError(f"num_seqs is {num_seqs}, but cu_seqlens holds {N} sequences")
+    else:
+        N = 1 if num_seqs is None else int(num_seqs)
+    return T, N, H, Hk, dk, dv, dev, dt, gate
+
+
+def kda_linear_fwd(q, k, v, g, cu_seqlens=None, initial_state=None, *, num_seqs: Optional[int] = None, out_dtype=None,
+                   scale: float = 1.0, output_final_state: bool = True):
+    """Linear attention with a decay for each head, over packed documents:
+    ``S_t = exp(g_t) S_{t-1} + k_t v_t^T``, ``o_t = scale S_t^T q_t``.
+
+    q, k ``[T, Hk, dk]``; v ``[T, H, dv]`` with Hk dividing H (head h reads
+    query/key head ``h // (H // Hk)``); g fp32, the log-decay (<= 0), ``[T, H]``
+    or ``[H]`` for a fixed decay; ``initial_state`` fp32 ``[N, H, dk, dv]`` or
+    None.  Returns ``(o, final_state)``; o is fp32 unless ``out_dtype`` says
+    otherwise.  ``num_seqs`` as in kda_fwd."""
+    torch = _torch()
+    T, N, H, Hk, dk, dv, dev, dt, gate = _packed(q, k, v, g, cu_seqlens, num_seqs)
+    out_dtype = out_dtype or torch.float32
+    _check(initial_state, "initial_state", (N, H, dk, dv), torch.float32, dev)
+    cfg = _lib.make_linear_config(H, Hk, dk, dv, _dt_code(dt), _dt_code(out_dtype), gate, scale)
+    o = torch.empty((T, H, dv), dtype=out_dtype, device=dev)
+    sf = torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev) if output_final_state else None
+    wsb = _lib.kda_linear_fwd_workspace_size(cfg, T, N)
+    ws = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
+    with torch.cuda.device(dev):
+        stream = torch.cuda.current_stream(dev).cuda_stream
+        _lib.check(_lib.kda_linear_fwd_raw(cfg, T, N, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(cu_seqlens),
+                                           _ptr(initial_state), _ptr(o), _ptr(sf), _ptr(ws), wsb, stream))
+    return o, sf
+
+
+def kda_linear_bwd(q, k, v, g, dO, cu_seqlens=None, initial_state=None, dS_final=None, *, num_seqs: Optional[int] = None,
+                   out_dtype=None, scale: float = 1.0, output_d_initial_state: bool = True):
+    """Backward of kda_linear_fwd for the loss <dO, o> + <dS_final, final_state>,
+    from the forward's inputs alone.  Returns a dict with dq, dk, dv, dg (the
+    shapes of q, k, v, g; fp32 unless ``out_dtype`` says otherwise) and dS0
+    (fp32, None unless requested)."""
+    torch = _torch()
+    T, N, H, Hk, dk, dv, dev, dt, gate = _packed(q, k, v, g, cu_seqlens, num_seqs)
+    out_dtype = out_dtype or torch.float32
+    _check(dO, "dO", (T, H, dv), dt, dev)
+    _check(initial_state, "initial_state", (N, H, dk, dv), torch.float32, dev)
+    _check(dS_final, "dS_final", (N, H, dk, dv), torch.float32, dev)
+    cfg = _lib.make_linear_config(H, Hk, dk, dv, _dt_code(dt), _dt_code(out_dtype), gate, scale)
+    out = {
+        "dq": torch.empty((T, Hk, dk), dtype=out_dtype, device=dev),
+        "dk": torch.empty((T, Hk, dk), dtype=out_dtype, device=dev),
+        "dv": torch.empty((T, H, dv), dtype=out_dtype, device=dev),
+        "dg": torch.empty(tuple(g.shape), dtype=out_dtype, device=dev),
+        "dS0": torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev) if output_d_initial_state else None,
+    }
+    wsb = _lib.kda_linear_bwd_workspace_size(cfg, T, N)
+    ws = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
+    with torch.cuda.device(dev):
+        stream = torch.cuda.current_stream(dev).cuda_stream
+        _lib.check(_lib.kda_linear_bwd_raw(cfg, T, N, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(cu_seqlens),
+                                           _ptr(initial_state), _ptr(dO), _ptr(dS_final), _ptr(out["dq"]),
+                                           _ptr(out["dk"]), _ptr(out["dv"]), _ptr(out["dg"]), _ptr(out["dS0"]), _ptr(ws),
+                                           wsb, stream))
+    return out
+
+
+def kda_linear_decode(q, k, v, g, state=None, *, out_state=None, out_dtype=None, scale: float = 1.0):
+    """One token per sequence of the linear rule on a resident fp32 state, as
+    kda_decode: q, k ``[N, Hk, dk]``, v ``[N, H, dv]``, g fp32 ``[N, H]`` or
+    ``[H]``, ``state`` ``[N, H, dk, dv]`` or None (zero).  ``out_state`` may be
+    ``state`` itself.  Returns ``(o, out_state)``."""
+    torch = _torch()
+    (N,), H, Hk, dk, dv, dev, dt = _heads(q, k, v, 1)
+    gate = _gate(g, (N,), H, dev)
+    _check(state, "state", (N, H, dk, dv), torch.float32, dev)
+    if out_state is None:
+        out_state = torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev)
+    _check(out_state, "out_state", (N, H, dk, dv), torch.float32, dev)
+    out_dtype = out_dtype or torch.float32
+    cfg = _lib.make_linear_config(H, Hk, dk, dv, _dt_code(dt), _dt_code(out_dtype), gate, scale)
+    o = torch.empty((N, H, dv), dtype=out_dtype, device=dev)
+    with torch.cuda.device(dev):
+        stream = torch.cuda.current_stream(dev).cuda_stream
+        _lib.check(_lib.kda_linear_decode_raw(cfg, N, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(state), _ptr(out_state),
+                                              _ptr(o), stream))
+    return o, out_state
+
+
+def _tree_common(q, k, v, g, beta, parent, state, out_dtype, eps, scale):
+    torch = _torch()
+    lead, H, Hk, dk, dv, dev, dt = _heads(q, k, v, 2)
+    N, L = lead
+    if not 1 <= L <= KDA_TREE_MAX_NODES:
+        raise ValueError(f"a tree has 1 to {KDA_TREE_MAX_NODES} nodes, got {L}")
+    if beta is None:
+        rule, gate = KDA_RULE_LINEAR, _gate(g, lead, H, dev)
+    else:
+        rule, gate = KDA_RULE_DELTA, KDA_GATE_TOKEN
+        if Hk != H:
+            raise ValueError(f"the delta rule has as many key heads as value heads, got {Hk} and {H}")
+        _check(g, "g", lead + (H, dk), dt, dev)
+        _check(beta, "beta", lead + (H,), dt, dev)
+    _check(parent, "parent", (N, L), torch.int32, dev)
+    _check(state, "state", (N, H, dk, dv), torch.float32, dev)
+    cfg = _lib.make_tree_config(rule, H, Hk, dk, dv, L, _dt_code(dt), _dt_code(out_dtype), gate, eps, scale)
+    return cfg, N, L, H, dk, dv, dev
+
+
+def kda_tree(q, k, v, g, beta, parent, state=None, *, out_dtype=None, eps: float = 1e-6, scale: float = 1.0):
+    """The outputs of a tree of drafted tokens over a recurrent state.
+
+    Per sequence up to 64 nodes: q, k ``[N, L, Hk, dk]``, v ``[N, L, H, dv]``,
+    ``parent`` int32 ``[N, L]`` (a node's parent, which comes before it; -1: the
+    node follows the state; below -1: no node, its output is 0).  With ``beta``
+    ``[N, L, H]`` and g ``[N, L, H, dk]`` the rule is kda_fwd's; with ``beta``
+    None and g fp32 ``[N, L, H]`` or ``[H]`` it is kda_linear_fwd's.  ``state``
+    fp32 ``[N, H, dk, dv]`` (None: zero) is read once and not changed.  Returns
+    o ``[N, L, H, dv]``, fp32 unless ``out_dtype`` says otherwise."""
+    torch = _torch()
+    out_dtype = out_dtype or torch.float32
+    cfg, N, L, H, dk, dv, dev = _tree_common(q, k, v, g, beta, parent, state, out_dtype, eps, scale)
+    o = torch.empty((N, L, H, dv), dtype=out_dtype, device=dev)
+    with torch.cuda.device(dev):
+        stream = torch.cuda.current_stream(dev).cuda_stream
+        _lib.check(_lib.kda_tree_raw(cfg, N, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(parent), _ptr(state),
+                                     _ptr(o), stream))
+    return o
+
+
+def kda_tree_commit(k, v, g, beta, parent, accept, state=None, *, out_state=None, eps: float = 1e-6):
+    """The state after the accepted path of a drafted tree: the recurrence over
+    the nodes root .. ``accept[n]`` (int32 ``[N]``; -1 accepts nothing and copies
+    the state).  The other arguments are kda_tree's.  ``out_state`` is a new
+    tensor if None, or a given one, which may be ``state`` itself.  Returns it."""
+    torch = _torch()
+    cfg, N, L, H, dk, dv, dev = _tree_common(None, k, v, g, beta, parent, state, torch.float32, eps, 1.0)
+    _check(accept, "accept", (N,), torch.int32, dev)
+    if out_state is None:
+        out_state = torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev)
+    _check(out_state, "out_state", (N, H, dk, dv), torch.float32, dev)
+    with torch.cuda.device(dev):
+        stream = torch.cuda.current_stream(dev).cuda_stream
+        _lib.check(_lib.kda_tree_commit_raw(cfg, N, _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(parent), _ptr(accept),
+                                            _ptr(state), _ptr(out_state), stream))
+    return out_state
+
+
+def _autograd_function():
+    torch = _torch()
+
+    class LinearFunction(torch.autograd.Function):
+        """Autograd glue: the backward runs from the inputs, so nothing else is saved.
+        Gradients flow to q, k, v, g and initial_state."""
+
+        @staticmethod
+        def forward(ctx, q, k, v, g, cu_seqlens, initial_state, num_seqs, scale):
+            o, sf = kda_linear_fwd(q, k, v, g, cu_seqlens, initial_state, num_seqs=num_seqs, scale=scale)
+            ctx.save_for_backward(q, k, v, g, cu_seqlens, initial_state)
+            ctx.num_seqs, ctx.scale = num_seqs, scale
+            return o, sf
+
+        @staticmethod
+        def backward(ctx, d_o, d_sf):
+            q, k, v, g, cu_seqlens, s0 = ctx.saved_tensors
+            d_o = (d_o if d_o is not None else torch.zeros_like(v)).to(q.dtype).contiguous()
+            d_sf = d_sf.contiguous() if d_sf is not None else None
+            gr = kda_linear_bwd(q, k, v, g, d_o, cu_seqlens, s0, d_sf, num_seqs=ctx.num_seqs, out_dtype=q.dtype,
+                                scale=ctx.scale, output_d_initial_state=s0 is not None)
+            return gr["dq"], gr["dk"], gr["dv"], gr["dg"].to(g.dtype), None, gr["dS0"], None, None
+
+    return LinearFunction
+
+
+_FN = None
+
+
+def kda_linear(q, k, v, g, cu_seqlens=None, initial_state=None, *, num_seqs: Optional[int] = None, scale: float = 1.0):
+    """kda_linear_fwd as a differentiable torch op: returns ``(o, final_state)``
+    (fp32) and, under autograd, back-propagates through kda_linear_bwd.  The
+    upstream gradient of o is cast to the input dtype, and the gradients of q,
+    k, v and g are rounded to it."""
+    global _FN
+    if _FN is None:
+        _FN = _autograd_function()
+    return _FN.apply(q, k, v, g, cu_seqlens, initial_state, num_seqs, scale)

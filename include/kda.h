@@ -271,6 +271,132 @@ kda_status kda_decode(const kda_config* cfg, int32_t num_seqs, const void* q, co
                       const void* g, const void* beta, const float* state_in, float* state_out, void* o,
                       void* stream);
 
+/* ------------------------------------------------------------------------
+ * The linear rule: linear attention with a decay for each head, the gated
+ * recurrence without the delta write.  Per document and head, with S a dk x dv
+ * fp32 state laid out as above:
+ *
+ *     S_t = exp(g_t) S_{t-1} + k_t v_t^T,      o_t = scale * S_t^T q_t
+ *
+ * q and k enter as given (no normalisation).  The conventions at the top of
+ * this file hold (packed documents, cu_seqlens, pointers, streams, errors,
+ * re-entrancy), with these layouts:
+ *   q, k : [total_tokens, Hk, dk]   v, o, dO : [total_tokens, H, dv]
+ *   g    : fp32, the log-decay, [total_tokens, H] (KDA_GATE_TOKEN) or [H], the
+ *          same for every token (KDA_GATE_HEAD); any g <= 0, -inf included
+ *          (the state restarts at that token).  Positive g works as long as
+ *          the decays between two tokens of a 128-token block stay in range.
+ *   states : fp32 [num_seqs, H, dk, dv]
+ * Head h of v, g and the states reads head h / (H / Hk) of q and k.
+ * bf16 inputs: products on bf16 operands with fp32 accumulation; P, dP and the
+ * state as it is read are rounded to bf16 once; the states themselves, their
+ * gradients and their updates keep fp32 accuracy.  fp32 inputs: fp32
+ * throughout.  Sums of g are kept in 64 bits.  Results are deterministic. */
+typedef enum kda_gate { KDA_GATE_TOKEN = 0, KDA_GATE_HEAD = 1 } kda_gate;
+
+typedef struct kda_linear_config {
+    int32_t H;         /* value heads                                  */
+    int32_t Hk;        /* query / key heads; divides H                 */
+    int32_t dk;        /* key / query head dim (64 or 128)             */
+    int32_t dv;        /* value head dim (64 or 128)                   */
+    int32_t in_dtype;  /* kda_dtype of q, k, v, dO                     */
+    int32_t out_dtype; /* kda_dtype of o, dq, dk, dv, dg               */
+    int32_t gate;      /* kda_gate                                     */
+    float scale;       /* multiplies the query (1.0)                   */
+} kda_linear_config;
+
+/* Fill *cfg with defaults: fp32/fp32, a gate per token, scale 1. */
+void kda_linear_config_init(kda_linear_config* cfg, int32_t H, int32_t Hk, int32_t dk, int32_t dv);
+
+/* Scratch for one call, in bytes (pure host functions; 0 for an invalid
+ * config).  The forward's is non-zero when it cuts long documents into
+ * segments (few documents and heads for the GPU; a rule on cfg and the sizes
+ * only): each segment's own sum of k v^T, then the states entering the
+ * segments.  The backward's holds S and dL/dS at every 128-token block (input
+ * type), per-token sums for dg, and the segments' states likewise. */
+size_t kda_linear_fwd_workspace_size(const kda_linear_config* cfg, int64_t total_tokens, int32_t num_seqs);
+size_t kda_linear_bwd_workspace_size(const kda_linear_config* cfg, int64_t total_tokens, int32_t num_seqs);
+
+/* Forward.  initial_state and final_state as for kda_fwd (either may be NULL).
+ * workspace may be NULL when kda_linear_fwd_workspace_size() is 0. */
+kda_status kda_linear_fwd(const kda_linear_config* cfg, int64_t total_tokens, int32_t num_seqs, const void* q,
+                          const void* k, const void* v, const float* g, const int32_t* cu_seqlens,
+                          const float* initial_state, void* o, float* final_state, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/* Backward of kda_linear_fwd for the loss <dO, o> + <dS_final, final_state>.
+ * Takes the forward's inputs (nothing is saved in between), dO
+ * ([total_tokens, H, dv], in_dtype) and dS_final (fp32 or NULL = 0).  Outputs:
+ * dq, dk [total_tokens, Hk, dk] (summed over the value heads that share them),
+ * dv [total_tokens, H, dv], dg (the shape of g; [H] sums over all tokens), all
+ * in out_dtype, and d_initial_state, fp32 or NULL. */
+kda_status kda_linear_bwd(const kda_linear_config* cfg, int64_t total_tokens, int32_t num_seqs, const void* q,
+                          const void* k, const void* v, const float* g, const int32_t* cu_seqlens,
+                          const float* initial_state, const void* dO, const float* dS_final, void* dq, void* dk,
+                          void* dv, void* dg, float* d_initial_state, void* workspace, size_t workspace_bytes,
+                          void* stream);
+
+/* One token per sequence on a resident state, as kda_decode: q, k
+ * [num_seqs, Hk, dk], v [num_seqs, H, dv], g [num_seqs, H] or [H]; state_in
+ * (NULL: zero), state_out (may be state_in itself, must not otherwise overlap
+ * it); o [num_seqs, H, dv] in out_dtype.  num_seqs = 0 enqueues nothing. */
+kda_status kda_linear_decode(const kda_linear_config* cfg, int32_t num_seqs, const void* q, const void* k,
+                             const void* v, const float* g, const float* state_in, float* state_out, void* o,
+                             void* stream);
+
+/* ------------------------------------------------------------------------
+ * A tree of drafted tokens over the state, for speculative decoding, under the
+ * gated delta rule (KDA_RULE_DELTA: kda_fwd's recurrence) or the linear rule
+ * (KDA_RULE_LINEAR: kda_linear_fwd's).  Every sequence has up to `nodes`
+ * drafted tokens; parent[n][i] is the index of node i's parent, -1 for a node
+ * that follows the state itself, below -1 for no node.  A parent's index is
+ * below its child's; an entry that is not, or that names an absent node, makes
+ * its node absent too.  Absent nodes get o = 0 and change nothing else.
+ *   q, k : [num_seqs, nodes, Hk, dk]   v, o : [num_seqs, nodes, H, dv]
+ *   g    : delta rule: [num_seqs, nodes, H, dk] in in_dtype; linear rule: fp32
+ *          [num_seqs, nodes, H] or [H]     (any g <= 0)
+ *   beta : delta rule: [num_seqs, nodes, H] in in_dtype (the logit); linear
+ *          rule: ignored
+ *   parent : int32 [num_seqs, nodes]       states : fp32 [num_seqs, H, dk, dv]
+ *
+ * kda_tree: o of node i is the output of the recurrence run from `state` (NULL:
+ * zero) over the tokens root .. i of its path.  The state is read once and not
+ * changed.
+ * kda_tree_commit: state_out is the state after the path root .. accept[n]
+ * (int32 [num_seqs]); an accept[n] below 0, not below `nodes`, or of an absent
+ * node accepts nothing and copies the state.  state_out may be state_in
+ * itself and must not otherwise overlap it.
+ * A chain (parent[n][i] = i - 1) equals a run of kda_decode /
+ * kda_linear_decode calls up to rounding.  num_seqs = 0 enqueues nothing. */
+#define KDA_TREE_MAX_NODES 64
+
+typedef enum kda_rule { KDA_RULE_DELTA = 0, KDA_RULE_LINEAR = 1 } kda_rule;
+
+typedef struct kda_tree_config {
+    int32_t rule;      /* kda_rule                                     */
+    int32_t H;         /* value heads                                  */
+    int32_t Hk;        /* query / key heads; divides H (delta: = H)    */
+    int32_t dk;        /* key / query head dim (64 or 128)             */
+    int32_t dv;        /* value head dim (64 or 128)                   */
+    int32_t nodes;     /* nodes per sequence, 1 .. KDA_TREE_MAX_NODES  */
+    int32_t in_dtype;  /* kda_dtype of q, k, v (delta: and g, beta)    */
+    int32_t out_dtype; /* kda_dtype of o                               */
+    int32_t gate;      /* kda_gate (delta: KDA_GATE_TOKEN)             */
+    float l2_eps;      /* eps inside the L2 norm (delta rule)          */
+    float scale;       /* multiplies the (delta: normalised) query     */
+} kda_tree_config;
+
+/* Fill *cfg with defaults: fp32/fp32, a gate per token, eps 1e-6, scale 1. */
+void kda_tree_config_init(kda_tree_config* cfg, int32_t rule, int32_t H, int32_t Hk, int32_t dk, int32_t dv,
+                          int32_t nodes);
+
+kda_status kda_tree(const kda_tree_config* cfg, int32_t num_seqs, const void* q, const void* k, const void* v,
+                    const void* g, const void* beta, const int32_t* parent, const float* state, void* o,
+                    void* stream);
+kda_status kda_tree_commit(const kda_tree_config* cfg, int32_t num_seqs, const void* k, const void* v,
+                           const void* g, const void* beta, const int32_t* parent, const int32_t* accept,
+                           const float* state_in, float* state_out, void* stream);
+
 /* Static description of a status code. */
 const char* kda_status_string(kda_status s);
 /* Thread-local description of the last failure on this thread ("" if none). */

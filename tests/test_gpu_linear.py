@@ -1,0 +1,404 @@
+"""The linear rule (kda_linear_fwd / _bwd / _decode) against the 64-bit token
+recurrence of tests/linear_ref.py.
+
+Tolerances, with M as defined there:
+  * o, dq, dk, dv from fp32 inputs: a sum over the dk (or dv) channels and the
+    tokens of a block (at most 128 + 128 + 128 terms), the decays' exponents
+    (|G| <= 100 in the factors that matter, each rounded by 2^-24 of itself):
+    512 half steps.
+  * the same from bf16 inputs: two roundings to bf16 more (P or dP, and the
+    state as it is read), each to its own terms: one 2^-8 of M.
+  * states: fp32 terms in any order, 512 half steps, bf16 inputs or not.
+  * dg: the crossing terms take two bf16 roundings in <S, dS>, 2^-7 of M; the row
+    and column sums cancel in fp32, 512 half steps of everything summed.
+  * an output stored in bf16: 2^-8 of the value more.
+Over a whole output, with V as defined there, the norm of the error is at most
+the same roundings times the norm of sqrt(V), with sqrt(512) < 32 half steps for
+the sums.
+"""
+import numpy as np
+import pytest
+
+import linear_ref as ref
+from linear_ref import BF16, F32
+
+from gpu_util import need_gpu, torch
+
+import gated_delta_rule_41_amd as kda
+
+pytestmark = pytest.mark.gpu
+
+STEPS, ROOT = 512 * F32, 32 * F32
+
+
+def _say(msg):
+    print(f"[gpu-linear] {msg}", flush=True)
+
+
+def make(seed, lens, H, Hk, dk, dv, dtype, gate="token", strength=-2.0, s0=True):
+    rng = np.random.default_rng([77, seed])
+    T, N = int(sum(lens)), len(lens)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+
+    def rounded(*shape):
+        return torch.from_numpy(rng.standard_normal(shape).astype(np.float32)).to(dt)
+
+    x = {"q": rounded(T, Hk, dk), "k": rounded(T, Hk, dk), "v": rounded(T, H, dv), "dO": rounded(T, H, dv)}
+    shape = (H,) if gate == "head" else (T, H)
+    x["g"] = torch.from_numpy(-np.log1p(np.exp(rng.standard_normal(shape) + strength)).astype(np.float32))
+    x["s0"] = torch.from_numpy((0.1 * rng.standard_normal((N, H, dk, dv))).astype(np.float32)) if s0 else None
+    x["dS"] = torch.from_numpy((0.1 * rng.standard_normal((N, H, dk, dv))).astype(np.float32)) if s0 else None
+    d = {n: None if t is None else t.cuda() for n, t in x.items()}
+    h = {n: None if t is None else t.float().numpy().astype(np.float64) for n, t in x.items()}
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+    return d, h, cu
+
+
+def host(t):
+    return t.detach().double().cpu().numpy()
+
+
+def check(name, x, r, M, rel, stored=0.0, extra=0.0, V=None, whole=0.0):
+    x = host(x)
+    assert np.isfinite(x).all(), name
+    if V is not None and x.size:
+        off, most = np.linalg.norm(x - r), whole * np.sqrt(V.sum()) + stored * np.linalg.norm(r)
+        _say(f"  {name}: the error's norm is {off / max(most, 1e-300):.3f} of its bound")
+        assert off <= most, name
+    bound = rel * M + stored * np.abs(r) + extra + 1e-30
+    worst = float((np.abs(x - r) / bound).max()) if x.size else 0.0
+    _say(f"  {name}: largest error is {worst:.3f} of its bound")
+    assert worst <= 1.0, name
+
+
+def check_fwd(d, h, cu, lens, dtype, out, scale, **kw):
+    o, sf = kda.kda_linear_fwd(d["q"], d["k"], d["v"], d["g"], cu, d["s0"], out_dtype=out, scale=scale, **kw)
+    torch.cuda.synchronize()
+    r, rf, _ = ref.linear_fwd(h["q"], h["k"], h["v"], h["g"], lens, h["s0"], scale)
+    M, Mf, _ = ref.linear_fwd(*ref.absolute(h["q"], h["k"], h["v"]), h["g"], lens, *ref.absolute(h["s0"]), abs(scale))
+    V, Vf, _ = ref.linear_fwd(*ref.squared(h["q"], h["k"], h["v"]), 2 * h["g"], lens, *ref.squared(h["s0"]), scale ** 2)
+    rounded = BF16 if dtype == "bf16" else 0
+    check("o", o, r, M, STEPS + rounded, BF16 if out == torch.bfloat16 else 0, V=V, whole=ROOT + rounded)
+    check("final", sf, rf, Mf, STEPS, V=Vf, whole=ROOT)
+    return o, sf
+
+
+def check_bwd(d, h, cu, lens, dtype, out, scale, **kw):
+    gr = kda.kda_linear_bwd(d["q"], d["k"], d["v"], d["g"], d["dO"], cu, d["s0"], d["dS"], out_dtype=out, scale=scale, **kw)
+    torch.cuda.synchronize()
+    r = ref.linear_bwd(h["q"], h["k"], h["v"], h["g"], lens, h["dO"], h["s0"], h["dS"], scale)
+    a = dict(zip(("q", "k", "v", "dO", "s0", "dS"), ref.absolute(*(h[n] for n in ("q", "k", "v", "dO", "s0", "dS")))))
+    M = ref.linear_bwd(a["q"], a["k"], a["v"], h["g"], lens, a["dO"], a["s0"], a["dS"], abs(scale))
+    a2 = dict(zip(("q", "k", "v", "dO", "s0", "dS"), ref.squared(*(h[n] for n in ("q", "k", "v", "dO", "s0", "dS")))))
+    V = ref.linear_bwd(a2["q"], a2["k"], a2["v"], 2 * h["g"], lens, a2["dO"], a2["s0"], a2["dS"], scale ** 2)
+    rounded = BF16 if dtype == "bf16" else 0
+    stored = BF16 if out == torch.bfloat16 else 0
+    for n in ("dq", "dk", "dv"):
+        check(n, gr[n], r[n], M[n], STEPS + rounded, stored, V=V[n], whole=ROOT + rounded)
+    check("dS0", gr["dS0"], r["dS0"], M["dS0"], STEPS, V=V["dS0"], whole=ROOT)
+    # everything the row and column sums hold: a head's q . dq over the document (an upper bound for a block)
+    R = d["v"].shape[1] // d["q"].shape[1]
+    all_ = np.repeat((a["q"] * M["dq"]).sum((0, 2)), R) * 2
+    check("dg", gr["dg"], r["dg"], M["dg"], STEPS + (2 * BF16 if dtype == "bf16" else 0), stored,
+          STEPS * all_ * (len(lens) if d["g"].dim() == 1 else 1))
+    return gr
+
+
+CASES = [
+    # lens, H, Hk, dk, dv, dtype, gate
+    ([1], 1, 1, 64, 64, "f32", "token"),
+    ([1], 2, 1, 128, 128, "bf16", "head"),
+    ([5, 64, 65], 3, 3, 64, 128, "f32", "head"),
+    ([0, 63, 0, 128, 1, 0], 2, 2, 128, 64, "f32", "token"),
+    ([127, 128, 129, 1, 30], 4, 2, 128, 128, "bf16", "token"),
+    ([257, 3], 6, 2, 64, 64, "bf16", "token"),
+    ([200], 4, 1, 128, 64, "bf16", "head"),
+    ([130, 40], 2, 2, 128, 128, "f32", "token"),
+    ([33, 95, 2], 3, 1, 64, 128, "bf16", "token"),
+]
+
+
+@pytest.mark.parametrize("lens,H,Hk,dk,dv,dtype,gate", CASES)
+def test_forward(lens, H, Hk, dk, dv, dtype, gate):
+    need_gpu()
+    _say(f"forward {lens} H={H} Hk={Hk} {dk}x{dv} {dtype} {gate}")
+    d, h, cu = make(1, lens, H, Hk, dk, dv, dtype, gate)
+    for out in (torch.float32, torch.bfloat16):
+        check_fwd(d, h, cu, lens, dtype, out, dk ** -0.5)
+
+
+@pytest.mark.parametrize("lens,H,Hk,dk,dv,dtype,gate", CASES)
+def test_backward(lens, H, Hk, dk, dv, dtype, gate):
+    need_gpu()
+    _say(f"backward {lens} H={H} Hk={Hk} {dk}x{dv} {dtype} {gate}")
+    d, h, cu = make(2, lens, H, Hk, dk, dv, dtype, gate)
+    for out in (torch.float32, torch.bfloat16):
+        check_bwd(d, h, cu, lens, dtype, out, dk ** -0.5)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_segments(dtype):
+    """Documents long enough to be cut into segments, ragged against the segments' and blocks' borders."""
+    need_gpu()
+    lens, H, Hk, dk, dv = [1500, 1, 1729, 0], 2, 1, 64, 64
+    _say(f"segments {lens} {dtype}")
+    d, h, cu = make(3, lens, H, Hk, dk, dv, dtype, "token", -3.0)
+    cfg = kda.linear._lib.make_linear_config(H, Hk, dk, dv)
+    assert kda.linear._lib.kda_linear_fwd_workspace_size(cfg, sum(lens), 2) > 0
+    lens2 = [1500, 1730]
+    cu2 = torch.tensor([0, 1500, 3230], dtype=torch.int32, device="cuda")
+    for n in ("s0", "dS"):
+        d[n], h[n] = d[n][:2].contiguous(), h[n][:2]
+    check_fwd(d, h, cu2, lens2, dtype, torch.float32, 0.125)
+    check_bwd(d, h, cu2, lens2, dtype, torch.float32, 0.125)
+
+
+def test_segments_with_uneven_documents():
+    """One long document among short and empty ones, the average long enough for segments."""
+    need_gpu()
+    lens = [0, 3, 2600, 130, 0, 2500]
+    _say(f"uneven {lens}")
+    d, h, cu = make(4, lens, 1, 1, 64, 64, "f32", "head")
+    # the plan goes by the average length: 6 documents need more tokens than this, 4 do not
+    cfg = kda.linear._lib.make_linear_config(1, 1, 64, 64)
+    lens4, keep = [3, 2600, 130, 2500], [1, 2, 3, 5]
+    assert kda.linear._lib.kda_linear_fwd_workspace_size(cfg, sum(lens4), 4) > 0
+    cu4 = torch.tensor(np.concatenate([[0], np.cumsum(lens4)]), dtype=torch.int32, device="cuda")
+    for n in ("s0", "dS"):
+        d[n], h[n] = d[n][keep].contiguous(), h[n][keep]
+    check_fwd(d, h, cu4, lens4, "f32", torch.float32, 0.125)
+    check_bwd(d, h, cu4, lens4, "f32", torch.float32, 0.125)
+
+
+def test_strong_and_infinite_gates():
+    """Gates of -8 a token, and -inf, which restarts the state at its token."""
+    need_gpu()
+    lens, H, Hk, dk, dv = [150, 70], 2, 2, 64, 64
+    for dtype in ("f32", "bf16"):
+        _say(f"strong gates {dtype}")
+        d, h, cu = make(5, lens, H, Hk, dk, dv, dtype)
+        g = np.full(h["g"].shape, -8.0, np.float32)
+        g[::3] = -0.01
+        g[40] = g[100, 1] = g[149] = g[150] = -np.inf
+        g[41:60] = -200.0
+        d["g"] = torch.from_numpy(g).cuda()
+        h["g"] = np.maximum(g.astype(np.float64), -1e3)   # e^-1000 is zero in 64 bits too
+        check_fwd(d, h, cu, lens, dtype, torch.float32, 1.0)
+        check_bwd(d, h, cu, lens, dtype, torch.float32, 1.0)
+
+
+def test_no_state_no_final():
+    need_gpu()
+    lens = [70, 129]
+    d, h, cu = make(6, lens, 2, 1, 64, 64, "f32", s0=False)
+    o, _ = check_fwd(d, h, cu, lens, "f32", torch.float32, 1.0)
+    o2, none = kda.kda_linear_fwd(d["q"], d["k"], d["v"], d["g"], cu, output_final_state=False)
+    assert none is None and torch.equal(o, o2)
+    check_bwd(d, h, cu, lens, "f32", torch.float32, 1.0)
+    gr = kda.kda_linear_bwd(d["q"], d["k"], d["v"], d["g"], d["dO"], cu, output_d_initial_state=False)
+    assert gr["dS0"] is None
+
+
+def test_equal_sequences_and_empty_stream():
+    need_gpu()
+    lens = [75, 75, 75]
+    d, h, cu = make(7, lens, 2, 2, 64, 64, "f32")
+    o, sf = kda.kda_linear_fwd(d["q"], d["k"], d["v"], d["g"], cu, d["s0"])
+    o2, sf2 = kda.kda_linear_fwd(d["q"], d["k"], d["v"], d["g"], None, d["s0"], num_seqs=3)
+    assert torch.equal(o, o2) and torch.equal(sf, sf2)
+    # no tokens: states pass through, a gate per head has a zero gradient
+    z, e = torch.zeros(3, dtype=torch.int32, device="cuda"), torch.empty((0, 2, 64), device="cuda")
+    s0, gh = d["s0"][:2].contiguous(), torch.full((2,), -0.1, device="cuda")
+    o, sf = kda.kda_linear_fwd(e, e, e, gh, z, s0)
+    gr = kda.kda_linear_bwd(e, e, e, gh, e, z, s0, s0)
+    torch.cuda.synchronize()
+    assert o.shape == (0, 2, 64) and torch.equal(sf, s0) and torch.equal(gr["dS0"], s0)
+    assert torch.equal(gr["dg"], torch.zeros_like(gh))
+
+
+def test_documents_do_not_touch_each_other():
+    """NaN in one document (inputs, gate, state) leaves the others bitwise alone; so do rows behind the last one."""
+    need_gpu()
+    lens, H, Hk, dk, dv = [70, 65, 140], 2, 2, 64, 64
+    d, h, cu = make(8, lens, H, Hk, dk, dv, "bf16")
+    T, pad = sum(lens), 37
+    clean = kda.kda_linear_fwd(d["q"], d["k"], d["v"], d["g"], cu, d["s0"])
+    cleang = kda.kda_linear_bwd(d["q"], d["k"], d["v"], d["g"], d["dO"], cu, d["s0"], d["dS"])
+    bad = {n: t.clone() for n, t in d.items()}
+    for n in ("q", "k", "v", "g", "dO"):
+        bad[n][70:135] = float("nan")
+    bad["s0"][1], bad["dS"][1] = float("nan"), float("inf")
+    o, sf = kda.kda_linear_fwd(bad["q"], bad["k"], bad["v"], bad["g"], cu, bad["s0"])
+    gr = kda.kda_linear_bwd(bad["q"], bad["k"], bad["v"], bad["g"], bad["dO"], cu, bad["s0"], bad["dS"])
+    torch.cuda.synchronize()
+    for a, b in [(o, clean[0])] + [(gr[n], cleang[n]) for n in ("dq", "dk", "dv", "dg")]:
+        assert torch.equal(a[:70], b[:70]) and torch.equal(a[135:], b[135:])
+    for a, b in ((sf, clean[1]), (gr["dS0"], cleang["dS0"])):
+        assert torch.equal(a[[0, 2]], b[[0, 2]])
+    # a stream with room behind the last document: its rows are neither read nor written
+    wide = {n: torch.cat([d[n], torch.full((pad,) + tuple(d[n].shape[1:]), float("nan"), device="cuda").to(d[n].dtype)])
+            for n in ("q", "k", "v", "g", "dO")}
+    lib = kda.linear._lib
+    cfg = lib.make_linear_config(H, Hk, dk, dv)
+    ow, sw = torch.full((T + pad, H, dv), 7.0, device="cuda"), torch.empty_like(sf)
+    st = torch.cuda.current_stream().cuda_stream
+    assert lib.kda_linear_fwd_raw(cfg, T + pad, 3, *(wide[n].data_ptr() for n in ("q", "k", "v", "g")), cu.data_ptr(),
+                                  d["s0"].data_ptr(), ow.data_ptr(), sw.data_ptr(), 0, 0, st) == 0
+    outs = {n: torch.full(s, 7.0, device="cuda") for n, s in
+            (("dq", (T + pad, Hk, dk)), ("dk", (T + pad, Hk, dk)), ("dv", (T + pad, H, dv)), ("dg", (T + pad, H)))}
+    wsb = lib.kda_linear_bwd_workspace_size(cfg, T + pad, 3)
+    ws, dS0 = torch.empty(wsb, dtype=torch.uint8, device="cuda"), torch.empty_like(sf)
+    assert lib.kda_linear_bwd_raw(cfg, T + pad, 3, *(wide[n].data_ptr() for n in ("q", "k", "v", "g")), cu.data_ptr(),
+                                  d["s0"].data_ptr(), wide["dO"].data_ptr(), d["dS"].data_ptr(),
+                                  *(outs[n].data_ptr() for n in ("dq", "dk", "dv", "dg")), dS0.data_ptr(), ws.data_ptr(),
+                                  wsb, st) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(ow[:T], clean[0]) and torch.equal(sw, clean[1]) and bool((ow[T:] == 7.0).all())
+    for n in outs:
+        assert torch.equal(outs[n][:T], cleang[n]) and bool((outs[n][T:] == 7.0).all()), n
+    assert torch.equal(dS0, cleang["dS0"])
+
+
+def test_gradients_against_differences():
+    """<dO, o> + <dS, final> is linear in each of q, k, v and the initial state: its difference along a direction is
+    exact up to rounding.  Along g the step is small.  fp32 inputs; the losses are summed in 64 bits."""
+    need_gpu()
+    lens = [130, 61]
+    for gate in ("token", "head"):
+        d, h, cu = make(9, lens, 4, 2, 64, 64, "f32", gate)
+
+        def loss(**kw):
+            x = dict(d, **kw)
+            o, sf = kda.kda_linear_fwd(x["q"], x["k"], x["v"], x["g"], cu, x["s0"], scale=0.125)
+            return float((o.double() * d["dO"].double()).sum() + (sf.double() * d["dS"].double()).sum())
+
+        gr = kda.kda_linear_bwd(d["q"], d["k"], d["v"], d["g"], d["dO"], cu, d["s0"], d["dS"], scale=0.125)
+        # rounding of each loss: every output is off by up to ROOT sqrt(V), independently of the others; six deviations.
+        # A step of at most 3 in one input makes no V more than 16 times larger.
+        a = ref.squared(h["q"], h["k"], h["v"], h["s0"], h["dO"], h["dS"])
+        V, Vf, _ = ref.linear_fwd(a[0], a[1], a[2], 2 * h["g"], lens, a[3], 0.125 ** 2)
+        noise = 6 * ROOT * 4 * float(np.sqrt((V * a[4]).sum() + (Vf * a[5]).sum()))
+        rng = torch.Generator(device="cuda").manual_seed(3)
+        for n, gn in (("q", "dq"), ("k", "dk"), ("v", "dv"), ("s0", "dS0"), ("g", "dg")):
+            u = torch.randn(d[n].shape, generator=rng, device="cuda")
+            eps = 0.5 if n != "g" else 2.0 ** -8 if gate == "token" else 2.0 ** -11
+            plus, minus = d[n] + eps * u, d[n] - eps * u
+            du = (plus.double() - minus.double())     # the step that fp32 made of it
+            diff = loss(**{n: plus}) - loss(**{n: minus})
+            want = float((gr[gn].double() * du).sum())
+            size = float((gr[gn].double() * du).abs().sum())
+            tol = 2 * noise + STEPS * size
+            if n == "g":
+                # third order: a path over t tokens moves by e^x with x at most t steps (a fixed gate: all of them the
+                # same way; gates per token: about sqrt(t)), x^3 / 6 of each term; terms beyond 32 tokens are small
+                x = eps * float(u.abs().max()) * (32 if gate == "head" else 6)
+                tol += x * x / 6 * size
+            _say(f"{gate} d{n}: difference {diff:.6f}, gradient {want:.6f}, tolerance {tol:.6f}")
+            assert abs(diff - want) <= tol, n
+
+
+@pytest.mark.parametrize("dtype,dk,dv", [("f32", 64, 64), ("f32", 128, 128), ("bf16", 128, 128), ("bf16", 64, 128),
+                                         ("bf16", 128, 64)])
+@pytest.mark.parametrize("gate", ["token", "head"])
+def test_decode(dtype, dk, dv, gate):
+    need_gpu()
+    N, H, Hk = 5, 4, 2
+    d, h, _ = make(10, [1] * N, H, Hk, dk, dv, dtype, gate)
+    r, rf, _ = ref.linear_fwd(h["q"], h["k"], h["v"], h["g"], [1] * N, h["s0"], 0.3)
+    M, Mf, _ = ref.linear_fwd(*ref.absolute(h["q"], h["k"], h["v"]), h["g"], [1] * N, *ref.absolute(h["s0"]), 0.3)
+    for out in (torch.float32, torch.bfloat16):
+        o, s = kda.kda_linear_decode(d["q"], d["k"], d["v"], d["g"], d["s0"], out_dtype=out, scale=0.3)
+        check("o", o, r, M, STEPS, BF16 if out == torch.bfloat16 else 0)
+        check("state", s, rf, Mf, 8 * F32)
+    keep = d["s0"].clone()
+    o2, s2 = kda.kda_linear_decode(d["q"], d["k"], d["v"], d["g"], keep, out_state=keep, scale=0.3)
+    assert s2 is keep and torch.equal(s2, s) and torch.equal(o2.to(torch.bfloat16), o)
+    # zero state, and an empty batch
+    o3, s3 = kda.kda_linear_decode(d["q"], d["k"], d["v"], d["g"], scale=0.3)
+    o4, s4 = kda.kda_linear_decode(d["q"], d["k"], d["v"], d["g"], torch.zeros_like(d["s0"]), scale=0.3)
+    assert torch.equal(o3, o4) and torch.equal(s3, s4)
+    g0 = d["g"] if gate == "head" else d["g"][:0]
+    o5, s5 = kda.kda_linear_decode(d["q"][:0], d["k"][:0], d["v"][:0], g0)
+    torch.cuda.synchronize()
+    assert o5.shape == (0, H, dv) and s5.shape == (0, H, dk, dv)
+
+
+def test_prefill_then_decode():
+    """The forward over a prefix and one decode step per further token equal the recurrence over the whole."""
+    need_gpu()
+    lens, steps, H, Hk, dk, dv = [90, 1, 130], 20, 4, 2, 128, 128
+    total = [n + steps for n in lens]
+    d, h, _ = make(11, total, H, Hk, dk, dv, "bf16")
+    r, rf, _ = ref.linear_fwd(h["q"], h["k"], h["v"], h["g"], total, h["s0"], 0.1)
+    M, Mf, _ = ref.linear_fwd(*ref.absolute(h["q"], h["k"], h["v"]), h["g"], total, *ref.absolute(h["s0"]), 0.1)
+    start = np.concatenate([[0], np.cumsum(total)])[:-1]
+    pre = np.concatenate([np.arange(s, s + n) for s, n in zip(start, lens)])
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+    _, s = kda.kda_linear_fwd(*(d[n][pre].contiguous() for n in ("q", "k", "v", "g")), cu, d["s0"], scale=0.1)
+    for t in range(steps):
+        rows = start + np.array(lens) + t
+        o, s = kda.kda_linear_decode(*(d[n][rows].contiguous() for n in ("q", "k", "v", "g")), s, out_state=s, scale=0.1)
+        check(f"o of step {t}", o, r[rows], M[rows], STEPS)
+    check("state", s, rf, Mf, STEPS)
+
+
+def test_autograd_matches_direct_calls():
+    need_gpu()
+    lens = [100, 33]
+    for gate in ("token", "head"):
+        d, h, cu = make(12, lens, 4, 2, 64, 64, "bf16", gate)
+        leaves = {n: d[n].clone().requires_grad_(True) for n in ("q", "k", "v", "g", "s0")}
+        o, sf = kda.kda_linear(leaves["q"], leaves["k"], leaves["v"], leaves["g"], cu, leaves["s0"], scale=0.125)
+        ((o * d["dO"].float()).sum() + (sf * d["dS"]).sum()).backward()
+        o2, sf2 = kda.kda_linear_fwd(d["q"], d["k"], d["v"], d["g"], cu, d["s0"], scale=0.125)
+        gr = kda.kda_linear_bwd(d["q"], d["k"], d["v"], d["g"], d["dO"], cu, d["s0"], d["dS"], scale=0.125,
+                                out_dtype=torch.bfloat16)
+        torch.cuda.synchronize()
+        assert torch.equal(o, o2) and torch.equal(sf, sf2)
+        for n, gn in (("q", "dq"), ("k", "dk"), ("v", "dv"), ("g", "dg"), ("s0", "dS0")):
+            assert leaves[n].grad.dtype == leaves[n].dtype
+            assert torch.equal(leaves[n].grad, gr[gn].to(leaves[n].dtype)), n
+        # only one output in the loss
+        leaves["q"].grad = None
+        o, sf = kda.kda_linear(leaves["q"], d["k"], d["v"], d["g"], cu, scale=0.125)
+        sf.sum().backward()
+        assert torch.equal(leaves["q"].grad, torch.zeros_like(d["q"]))
+
+
+def test_repeatable_graph_streams():
+    """Two calls agree bitwise; a captured forward, backward and decode replays bitwise, with eager work in between;
+    calls on two streams at once equal the same calls in turn."""
+    need_gpu()
+    lens, H, Hk, dk, dv = [700, 64, 1300], 4, 2, 128, 128
+    d, _, cu = make(13, lens, H, Hk, dk, dv, "bf16")
+    e, _, _ = make(14, lens, H, Hk, dk, dv, "bf16")
+
+    def call(x):
+        o, sf = kda.kda_linear_fwd(x["q"], x["k"], x["v"], x["g"], cu, x["s0"], scale=0.1)
+        gr = kda.kda_linear_bwd(x["q"], x["k"], x["v"], x["g"], x["dO"], cu, x["s0"], x["dS"], scale=0.1)
+        od, sd = kda.kda_linear_decode(x["q"][:3], x["k"][:3], x["v"][:3], x["g"][:3], sf, scale=0.1)
+        return [o, sf, od, sd] + [gr[n] for n in ("dq", "dk", "dv", "dg", "dS0")]
+
+    want, other = call(d), call(e)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, call(d)))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got2 = call(e)
+    got1 = call(d)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got1)) and all(torch.equal(a, b) for a, b in zip(other, got2))
+    x = {n: t.clone() for n, t in d.items()}
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = call(x)
+    for rep, (src, ref_) in enumerate(((d, want), (e, other), (d, want), (d, want))):
+        for n in x:
+            x[n].copy_(src[n])
+        junk = torch.randn(1 << 20, device="cuda").sum()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.isfinite(junk)
+        assert all(torch.equal(a, b) for a, b in zip(outs, ref_)), rep
