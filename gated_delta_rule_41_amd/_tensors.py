@@ -1,7 +1,7 @@
 """Tensor checks and conversions shared by the bindings."""
 from __future__ import annotations
 
-from ._lib import KDA_BF16, KDA_F32
+from ._lib import KDA_BF16, KDA_F32, check as lib_check
 
 
 def torch_module():
@@ -23,7 +23,7 @@ def ptr(t):
 
 
 def check(t, name, shape, dtype, device):
-    if t is None:
+    if t is None or (t.shape == shape and t.dtype == dtype and t.device == device and t.is_contiguous()):
         return
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
@@ -33,3 +33,23 @@ def check(t, name, shape, dtype, device):
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+
+
+def launch(dev, call, *args):
+    """call(*args, stream) with `dev` current, on its current stream; raises on a bad status.  The device is switched only
+    where it is another one, and the stream is asked for as its handle: both cost more than the checks of a small call."""
+    torch = torch_module()
+    index = dev.index
+    if index == torch.cuda.current_device():
+        lib_check(call(*args, _raw_stream(index)))
+    else:
+        with torch.cuda.device(dev):
+            lib_check(call(*args, _raw_stream(index)))
+
+
+def _raw_stream(index):
+    global _raw_stream
+    torch = torch_module()
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda i: torch.cuda.current_stream(i).cuda_stream)
+    return _raw_stream(index)

@@ -4,24 +4,36 @@ package's ``__init__``: see include/kda.h for the layouts.
 """
 from __future__ import annotations
 
+from functools import lru_cache
 from typing import Optional
 
 from . import _lib
 from ._lib import KDA_GATE_HEAD, KDA_GATE_TOKEN, KDA_RULE_DELTA, KDA_RULE_LINEAR, KDA_TREE_MAX_NODES
-from ._tensors import check as _check, dt_code as _dt_code, ptr as _ptr, torch_module as _torch
+from ._tensors import check as _check, dt_code as _dt_code, launch as _launch, ptr as _ptr, torch_module as _torch
+
+# Configs and workspace sizes depend on their arguments alone; made once for each set of them.
+_linear_config = lru_cache(maxsize=256)(_lib.make_linear_config)
+_tree_config = lru_cache(maxsize=256)(_lib.make_tree_config)
 
 
-def _heads(q, k, v, lead_dims, names=("q", "k", "v")):
+@lru_cache(maxsize=256)
+def _linear_workspace(size, T, N, *config):
+    return size(_linear_config(*config), T, N)
+
+
+def _heads(q, k, v, lead_dims):
     """Shapes, device and dtype of q/k ``[..., Hk, dk]`` and v ``[..., H, dv]`` (q may be None)."""
-    for name, t in zip(names, (q, k, v)):
+    for name, t in (("q", q), ("k", k), ("v", v)):
         if t is not None and t.dim() != lead_dims + 2:
             raise ValueError(f"{name} must have {lead_dims + 2} dimensions, got shape {tuple(t.shape)}")
-    lead, (Hk, dk), (H, dv) = tuple(k.shape[:-2]), k.shape[-2:], v.shape[-2:]
+    shape = tuple(k.shape)
+    lead, (Hk, dk), (H, dv) = shape[:-2], shape[-2:], tuple(v.shape[-2:])
     dev, dt = k.device, k.dtype
     if dev.type != "cuda":
         raise ValueError("libkda runs on the GPU only: tensors must be on a cuda (HIP) device")
-    for name, t, shp in (("q", q, lead + (Hk, dk)), ("k", k, lead + (Hk, dk)), ("v", v, lead + (H, dv))):
-        _check(t, name, shp, dt, dev)
+    _check(q, "q", shape, dt, dev)
+    _check(k, "k", shape, dt, dev)
+    _check(v, "v", lead + (H, dv), dt, dev)
     return lead, H, Hk, dk, dv, dev, dt
 
 
@@ -65,15 +77,13 @@ def kda_linear_fwd(q, k, v, g, cu_seqlens=None, initial_state=None, *, num_seqs:
     T, N, H, Hk, dk, dv, dev, dt, gate = _packed(q, k, v, g, cu_seqlens, num_seqs)
     out_dtype = out_dtype or torch.float32
     _check(initial_state, "initial_state", (N, H, dk, dv), torch.float32, dev)
-    cfg = _lib.make_linear_config(H, Hk, dk, dv, _dt_code(dt), _dt_code(out_dtype), gate, scale)
+    config = (H, Hk, dk, dv, _dt_code(dt), _dt_code(out_dtype), gate, scale)
     o = torch.empty((T, H, dv), dtype=out_dtype, device=dev)
     sf = torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev) if output_final_state else None
-    wsb = _lib.kda_linear_fwd_workspace_size(cfg, T, N)
+    wsb = _linear_workspace(_lib.kda_linear_fwd_workspace_size, T, N, *config)
     ws = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
-    with torch.cuda.device(dev):
-        stream = torch.cuda.current_stream(dev).cuda_stream
-        _lib.check(_lib.kda_linear_fwd_raw(cfg, T, N, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(cu_seqlens),
-                                           _ptr(initial_state), _ptr(o), _ptr(sf), _ptr(ws), wsb, stream))
+    _launch(dev, _lib.kda_linear_fwd_raw, _linear_config(*config), T, N, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(cu_seqlens),
+            _ptr(initial_state), _ptr(o), _ptr(sf), _ptr(ws), wsb)
     return o, sf
 
 
@@ -89,7 +99,7 @@ def kda_linear_bwd(q, k, v, g, dO, cu_seqlens=None, initial_state=None, dS_final
     _check(dO, "dO", (T, H, dv), dt, dev)
     _check(initial_state, "initial_state", (N, H, dk, dv), torch.float32, dev)
     _check(dS_final, "dS_final", (N, H, dk, dv), torch.float32, dev)
-    cfg = _lib.make_linear_config(H, Hk, dk, dv, _dt_code(dt), _dt_code(out_dtype), gate, scale)
+    config = (H, Hk, dk, dv, _dt_code(dt), _dt_code(out_dtype), gate, scale)
     out = {
         "dq": torch.empty((T, Hk, dk), dtype=out_dtype, device=dev),
         "dk": torch.empty((T, Hk, dk), dtype=out_dtype, device=dev),
@@ -97,14 +107,11 @@ def kda_linear_bwd(q, k, v, g, dO, cu_seqlens=None, initial_state=None, dS_final
         "dg": torch.empty(tuple(g.shape), dtype=out_dtype, device=dev),
         "dS0": torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev) if output_d_initial_state else None,
     }
-    wsb = _lib.kda_linear_bwd_workspace_size(cfg, T, N)
+    wsb = _linear_workspace(_lib.kda_linear_bwd_workspace_size, T, N, *config)
     ws = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
-    with torch.cuda.device(dev):
-        stream = torch.cuda.current_stream(dev).cuda_stream
-        _lib.check(_lib.kda_linear_bwd_raw(cfg, T, N, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(cu_seqlens),
-                                           _ptr(initial_state), _ptr(dO), _ptr(dS_final), _ptr(out["dq"]),
-                                           _ptr(out["dk"]), _ptr(out["dv"]), _ptr(out["dg"]), _ptr(out["dS0"]), _ptr(ws),
-                                           wsb, stream))
+    _launch(dev, _lib.kda_linear_bwd_raw, _linear_config(*config), T, N, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(cu_seqlens),
+            _ptr(initial_state), _ptr(dO), _ptr(dS_final), _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]), _ptr(out["dg"]),
+            _ptr(out["dS0"]), _ptr(ws), wsb)
     return out
 
 
@@ -119,14 +126,12 @@ def kda_linear_decode(q, k, v, g, state=None, *, out_state=None, out_dtype=None,
     _check(state, "state", (N, H, dk, dv), torch.float32, dev)
     if out_state is None:
         out_state = torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev)
-    _check(out_state, "out_state", (N, H, dk, dv), torch.float32, dev)
+    else:
+        _check(out_state, "out_state", (N, H, dk, dv), torch.float32, dev)
     out_dtype = out_dtype or torch.float32
-    cfg = _lib.make_linear_config(H, Hk, dk, dv, _dt_code(dt), _dt_code(out_dtype), gate, scale)
+    cfg = _linear_config(H, Hk, dk, dv, _dt_code(dt), _dt_code(out_dtype), gate, scale)
     o = torch.empty((N, H, dv), dtype=out_dtype, device=dev)
-    with torch.cuda.device(dev):
-        stream = torch.cuda.current_stream(dev).cuda_stream
-        _lib.check(_lib.kda_linear_decode_raw(cfg, N, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(state), _ptr(out_state),
-                                              _ptr(o), stream))
+    _launch(dev, _lib.kda_linear_decode_raw, cfg, N, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(state), _ptr(out_state), _ptr(o))
     return o, out_state
 
 
@@ -146,7 +151,7 @@ def _tree_common(q, k, v, g, beta, parent, state, out_dtype, eps, scale):
         _check(beta, "beta", lead + (H,), dt, dev)
     _check(parent, "parent", (N, L), torch.int32, dev)
     _check(state, "state", (N, H, dk, dv), torch.float32, dev)
-    cfg = _lib.make_tree_config(rule, H, Hk, dk, dv, L, _dt_code(dt), _dt_code(out_dtype), gate, eps, scale)
+    cfg = _tree_config(rule, H, Hk, dk, dv, L, _dt_code(dt), _dt_code(out_dtype), gate, eps, scale)
     return cfg, N, L, H, dk, dv, dev
 
 
@@ -164,10 +169,7 @@ def kda_tree(q, k, v, g, beta, parent, state=None, *, out_dtype=None, eps: float
     out_dtype = out_dtype or torch.float32
     cfg, N, L, H, dk, dv, dev = _tree_common(q, k, v, g, beta, parent, state, out_dtype, eps, scale)
     o = torch.empty((N, L, H, dv), dtype=out_dtype, device=dev)
-    with torch.cuda.device(dev):
-        stream = torch.cuda.current_stream(dev).cuda_stream
-        _lib.check(_lib.kda_tree_raw(cfg, N, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(parent), _ptr(state),
-                                     _ptr(o), stream))
+    _launch(dev, _lib.kda_tree_raw, cfg, N, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(parent), _ptr(state), _ptr(o))
     return o
 
 
@@ -181,11 +183,10 @@ def kda_tree_commit(k, v, g, beta, parent, accept, state=None, *, out_state=None
     _check(accept, "accept", (N,), torch.int32, dev)
     if out_state is None:
         out_state = torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev)
-    _check(out_state, "out_state", (N, H, dk, dv), torch.float32, dev)
-    with torch.cuda.device(dev):
-        stream = torch.cuda.current_stream(dev).cuda_stream
-        _lib.check(_lib.kda_tree_commit_raw(cfg, N, _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(parent), _ptr(accept),
-                                            _ptr(state), _ptr(out_state), stream))
+    else:
+        _check(out_state, "out_state", (N, H, dk, dv), torch.float32, dev)
+    _launch(dev, _lib.kda_tree_commit_raw, cfg, N, _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(parent), _ptr(accept),
+            _ptr(state), _ptr(out_state))
     return out_state
 
 
