@@ -10,6 +10,7 @@ namespace kda {
 
 constexpr int kLinChunk = 64;     // tokens per step of the walks over a document
 constexpr int kLinBlock = 128;    // tokens per gradient workgroup; saved states sit at its borders
+constexpr int kWalkTarget = 512;  // workgroups a walk aims for: two a compute unit
 constexpr int kGradThreads = 512; // 8 wave64: one 16-row block of a 128-token block each
 
 // g[token * g_stride + head]: g_stride = H for a gate per token, 0 for a gate per head.
@@ -73,8 +74,8 @@ struct LinearBwdParams {
     const void* dO;        // [T,H,dv]
     const void* S;         // state entering every block (input type) [blocks,H,dk,dv]
     const void* dS;        // dL/dS at the end of every block
-    float* e;              // [H,T] q . dq through the entering state
-    float* a;              // [H,T] row sums minus column sums of P o dP inside the block
+    float* e;              // [H,T] q . dq through the entering state, plus row sums of A (see kda_linear_bwd.hip)
+    float* a;              // [H,T] column sums of A
     float* f;              // [H,T] k . dk through dS
     float* cross;          // [blocks,H] e^{G} <S, dS>
     float* dg_part;        // [blocks,H] sum of dg over the block (gate per head), or nullptr

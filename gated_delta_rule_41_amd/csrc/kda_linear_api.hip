@@ -61,16 +61,16 @@ bool grid_fits(int64_t workgroups, int threads) {
 // documents are cut into segments: the segments' own sums, the states entering them, the
 // walks from those.  The plan depends on the config and the sizes alone, so that the
 // workspace size is a host function.
-constexpr int64_t kWalkTarget = 512;     // workgroups a walk aims for
 constexpr int64_t kMinSegment = 512;     // tokens: below, a segment's state outweighs its rows
 
 struct Plan {
     int32_t seg_len;   // 0: whole documents
     int64_t chains;    // (document or segment slot, head) pairs
 };
-Plan walk_plan(const kda_linear_config* c, int64_t T, int32_t N, int dirs) {
+// ways: workgroups that share a chain (directions, slices of the value columns)
+Plan walk_plan(const kda_linear_config* c, int64_t T, int32_t N, int ways) {
     Plan p = {0, (int64_t)N * c->H};
-    const int64_t wgs = p.chains * (c->dv / kSlice) * dirs;
+    const int64_t wgs = p.chains * ways;
     const int64_t per_doc = (kWalkTarget + wgs - 1) / wgs, avg = T / N;
     if (per_doc < 2 || avg < 2 * kMinSegment) return p;
     int64_t L = (avg + per_doc - 1) / per_doc;
@@ -105,7 +105,7 @@ struct BwdLayout {
 BwdLayout bwd_layout(const kda_linear_config* c, int64_t T, int32_t N) {
     BwdLayout b;
     memset(&b, 0, sizeof b);
-    b.plan = walk_plan(c, T, N, 2);
+    b.plan = walk_plan(c, T, N, 2 * (c->dv / 64));
     b.blocks = linear_slots(T, N, kLinBlock);
     size_t at = 0;
     auto take = [&at](size_t bytes) {
@@ -134,8 +134,10 @@ kda_status check_sizes(const kda_linear_config* c, int64_t T, int32_t N, const i
     if (T < 0 || T >= ((int64_t)1 << 31)) return fail(KDA_ERR_INVALID_ARG, "total_tokens must be in [0, 2^31)%s");
     if (N < 1) return fail(KDA_ERR_INVALID_ARG, "num_seqs must be >= 1%s");
     if (!cu && T % N) return fail(KDA_ERR_INVALID_ARG, "cu_seqlens is NULL but total_tokens is not a multiple of num_seqs%s");
-    // the largest launches: walks of 64-column slices, blocks of gradients, the carry
-    if (!grid_fits(((linear_slots(T, N, kLinBlock) + 8) * c->H) * (c->dv / kSlice), kGradThreads) ||
+    // the kernels address a block's rows with 32-bit byte offsets from a 64-bit base
+    if ((int64_t)kLinBlock * c->H * 128 * 4 >= ((int64_t)1 << 31)) return fail(KDA_ERR_UNSUPPORTED, "H too large%s");
+    // the largest launches: the walks' chains, the a block's gradients in at most three roles a head, the carry
+    if (!grid_fits((linear_slots(T, N, kLinBlock) + 8) * 3 * (int64_t)c->H, kGradThreads) ||
         !grid_fits((int64_t)N * c->H * (c->dk * c->dv / (4 * kThreads)), kThreads))
         return fail(KDA_ERR_UNSUPPORTED, "num_seqs, H or total_tokens too large for one launch%s");
     return KDA_OK;

@@ -12,11 +12,17 @@
 // column sums of A are fp32 products), unlike the sum of q . dq - k . dk to the end of the
 // document, whose rounding grows with its length.
 //
-// linear_dq_kernel and linear_dkv_kernel: one workgroup (8 waves) per block and key head,
-// wave w a 16-row block of queries (keys), looping over the key head's value heads, so the
-// gradients of shared heads add up in registers in a fixed order.  A wave forms its own rows
-// of P and dP in the transposed orientation, in which the accumulators are at once the
-// operand of the next product: no exchange between waves.  linear_dg_kernel finishes dg.
+// linear_grads_kernel: one workgroup (8 waves) per block, head and role: dq (with e and the
+// row sums of A), dk (with f and its column sums) or dv (with <S, dS>), wave w a 16-row block of queries or keys.  dq and dk belong to
+// a key head and loop over its value heads, so the gradients of shared heads add up in
+// registers in a fixed order.  A wave forms its own rows of P or dP in the transposed
+// orientation, in which the accumulators are at once the operand of the next product: no
+// exchange between waves, at the price of forming dP twice and P twice.  One role needs two
+// 128-row tiles in LDS and fits 128 registers, so two workgroups share a compute unit and one
+// computes while the other loads; the three roles of a block are issued eight workgroups
+// apart, on one XCD, whose L2 serves the rows that they share.  (One kernel for dk and dv at
+// 255 registers, one workgroup per compute unit, took 620 us at 4 x 8192 tokens x 32 heads,
+// and dq beside it 461 us.)  linear_dg_kernel finishes dg.
 #include "kda_linear_device.h"
 
 namespace kda {
@@ -29,7 +35,7 @@ constexpr int kB = kLinBlock;
 __device__ __forceinline__ void block_gates(double* sG, const float* gp, int64_t stride, int rows, int l) {
     const double x = l < rows ? gate_log2(gp[(int64_t)l * stride]) : 0.0;
     const double y = l + 64 < rows ? gate_log2(gp[(int64_t)(l + 64) * stride]) : 0.0;
-    const double a = wave_scan(x, l), b = wave_scan(y, l) + __shfl(a, 63, 64);
+    const double a = wave_scan(x), b = wave_scan(y) + last_lane(a);
     sG[l] = a;
     sG[l + 64] = b;
 }
@@ -39,9 +45,13 @@ __device__ __forceinline__ float qsum4(float v) {
     return v + __shfl_xor(v, 32);
 }
 
-// Four elements of a global row as fp32.
-template <typename T> __device__ __forceinline__ f32x4 load4f(const T* p) {
-    return unpack4(*reinterpret_cast<const typename V4<T>::t*>(p));
+// Elements 4 hi .. 4 hi + 3 of a fragment as fp32: of a row fragment in the k order of
+// stacked accumulator blocks, what block 2 s + hi holds of that row.
+__device__ __forceinline__ f32x4 half4(bf16x8 x, int hi) {
+    return hi ? unpack4(__builtin_shufflevector(x, x, 4, 5, 6, 7)) : unpack4(__builtin_shufflevector(x, x, 0, 1, 2, 3));
+}
+__device__ __forceinline__ f32x4 half4(f32x8 x, int hi) {
+    return hi ? __builtin_shufflevector(x, x, 4, 5, 6, 7) : __builtin_shufflevector(x, x, 0, 1, 2, 3);
 }
 __device__ __forceinline__ float dot4(f32x4 a, f32x4 b) { return a[0] * b[0] + a[1] * b[1] + a[2] * b[2] + a[3] * b[3]; }
 
@@ -55,232 +65,342 @@ template <typename T, int D> __device__ __forceinline__ void row_frags(typename 
     }
 }
 
-template <typename T, int DK, int DV>
-__global__ __launch_bounds__(kGradThreads) void linear_dq_kernel(LinearBwdParams p) {
-    constexpr int LK = DK + 8, LV = DV + 8;
-    typedef typename V8<T>::t frag;
-    __shared__ __align__(32) T sK[kB * LK];
-    __shared__ __align__(32) T sB[kB * LV];   // the state, then V
-    __shared__ __align__(16) double sG[kB];
+// The same row in the k order of two stacked accumulator blocks.
+template <typename T, int D> __device__ __forceinline__ void row_perms(typename V8<T>::t (&f)[D / 32], const T* base, int64_t ld, int row, int rows, int qg) {
+    const T* p = base + (int64_t)(row < rows ? row : rows - 1) * ld + 4 * qg;
+#pragma unroll
+    for (int s = 0; s < D / 32; ++s) {
+        f[s] = join(*reinterpret_cast<const typename V4<T>::t*>(p + 32 * s), *reinterpret_cast<const typename V4<T>::t*>(p + 32 * s + 16));
+        if (row >= rows) f[s] = typename V8<T>::t{};
+    }
+}
 
-    const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, cl = l & 15, qg = l >> 4;
-    const int64_t slot = blockIdx.x / p.Hk;
-    const int hk = (int)(blockIdx.x % p.Hk), R = p.H / p.Hk;
-    const Range rg = piece_range(p.cu, p.N, p.seqlen, p.T, slot, kB);
-    const int rows = (int)(rg.hi - rg.lo);
-    if (rows <= 0) return;
-    // row blocks are given out so that the waves of one SIMD (w, w + 4) share the causal work evenly
-    const int rb = w < 4 ? w : 11 - w, row = 16 * rb + cl;
+// What a role's workgroup knows of its block.
+struct Task {
+    int64_t slot, lo;
+    int rows, hk, R;
+};
+
+// LDS of a role: two tiles of 128 rows (the second one also holds the state), the gates, and
+// the waves' own decays.
+template <typename T, int DK, int DV> struct GradTiles {
+    static constexpr int A = kB * (DK > DV ? DK : DV), D = DK * DV, B = A > D ? A : D;
+    __align__(32) T a[A];
+    __align__(32) T b[B];
+    __align__(16) double G[kB];
+    __align__(16) float F[8][kB];
+    float sum[8];
+};
+
+// Wave w's 16 rows of a block: row blocks are given out so that the waves of one SIMD (w and
+// w + 4) share the causal work evenly.
+__device__ __forceinline__ int row_block(int w) { return w < 4 ? w : 11 - w; }
+
+template <typename T, int DK, int DV, bool GROUPED>
+__device__ __forceinline__ void dq_role(const LinearBwdParams& p, const Task& t, GradTiles<T, DK, DV>& s) {
+    typedef typename V8<T>::t frag;
+    constexpr int RK = 16 * DK * sizeof(T), RV = 16 * DV * sizeof(T);   // bytes of 16 rows
+    const int w = threadIdx.x >> 6, rb = row_block(w), rows = t.rows;
     const int64_t ldk = (int64_t)p.Hk * DK, ldv = (int64_t)p.H * DV;
-    const T* q = (const T*)p.q + (rg.lo * p.Hk + hk) * DK;
+    const T* q = (const T*)p.q + t.lo * ldk + t.hk * DK;
 
     f32x4 dq[DK / 16];
 #pragma unroll
     for (int m = 0; m < DK / 16; ++m) dq[m] = zero4();
-    {
-        Tile<T, kB, DK, kGradThreads> t;
-        t.load((const T*)p.k + (rg.lo * p.Hk + hk) * DK, ldk, rows, tid);
-        t.store(sK, LK, rows, tid);
-    }
-    for (int r = 0; r < R; ++r) {
-        const int h = hk * R + r;
-        {
-            Tile<T, DK, DV, kGradThreads> t;
-            t.load((const T*)p.S + (slot * p.H + h) * DK * DV, DV, DK, tid);
-            t.store(sB, LV, DK, tid);
-        }
-        if (w == 0) block_gates(sG, p.g + (p.g_stride ? rg.lo * p.g_stride : 0) + h, p.g_stride, rows, l);
-        frag dof[DV / 32];
-        row_frags<T, DV>(dof, (const T*)p.dO + (rg.lo * p.H + h) * DV, ldv, row, rows, qg);
+    for (int r = 0; r < (GROUPED ? t.R : 1); ++r) {
+        const int h = GROUPED ? t.hk * t.R + r : t.hk, tid = GROUPED ? opaque(threadIdx.x) : threadIdx.x, l = tid & 63, cl = l & 15, qg = l >> 4, row = 16 * rb + cl;
+        // every load of the step is issued before the first wait
+        Tile<T, DK, DV, kGradThreads> ts;
+        ts.load((const T*)p.S + (t.slot * p.H + h) * DK * DV, DV, DK, tid);
+        frag dof[DV / 32], qf[DK / 32];
+        row_frags<T, DV>(dof, (const T*)p.dO + t.lo * ldv + h * DV, ldv, row, rows, qg);
+        row_perms<T, DK>(qf, q, ldk, row, rows, qg);
         Tile<T, kB, DV, kGradThreads> tv;
-        tv.load((const T*)p.v + (rg.lo * p.H + h) * DV, ldv, rows, tid);
+        tv.load((const T*)p.v + t.lo * ldv + h * DV, ldv, rows, tid);
+        if (r == 0) {
+            Tile<T, kB, DK, kGradThreads> tk;
+            tk.load((const T*)p.k + t.lo * ldk + t.hk * DK, ldk, rows, tid);
+            if (w == 0) block_gates(s.G, p.g + (p.g_stride ? t.lo * p.g_stride : 0) + h, p.g_stride, rows, l);
+            ts.store(s.b, DK, tid);
+            tk.store(s.a, rows, tid);
+        } else {
+            if (w == 0) block_gates(s.G, p.g + (p.g_stride ? t.lo * p.g_stride : 0) + h, p.g_stride, rows, l);
+            ts.store(s.b, DK, tid);
+        }
         lds_barrier();
-        const double gq = sG[row];
         // through the entering state; row = key channel 16m + 4qg + i, column = query
+        const Lane<T, DK> lk(cl, qg);
+        const Lane<T, DV> lv(cl, qg);
+        const double gq = s.G[row];
         const float eq = fast_exp2((float)gq) * p.scale;
-        float e = 0.f;
+        float e = 0.f;   // q . dq through the state, then the row sums of A
 #pragma unroll
         for (int m = 0; m < DK / 16; ++m) {
             f32x4 x = zero4();
 #pragma unroll
-            for (int s = 0; s < DV / 32; ++s) x = mma_k32(x, lds8(sB + (16 * m + cl) * LV + 32 * s + 8 * qg), dof[s]);
+            for (int y = 0; y < DV / 32; ++y) x = mma_k32(x, lv.row(s.b, m * RV, y), dof[y]);
             x *= eq;
-            e += dot4(x, load4f(q + (int64_t)(row < rows ? row : 0) * ldk + 16 * m + 4 * qg));
+            e += dot4(x, half4(qf[m / 2], m & 1));
             dq[m] += x;
+            if (m & 1) __builtin_amdgcn_sched_barrier(0);   // keeps the reads ahead of it to two blocks' registers
         }
-        e = qsum4(e);
-        if (qg == 0 && row < rows) p.e[(int64_t)h * p.T + rg.lo + row] = e;
+        lds_barrier();   // the last readers of the state are done
+        tv.store(s.b, rows, tid);
+        // Below the diagonal block the decay is split at the last key before the wave's
+        // queries, both factors at most 1: two exponentials a lane instead of four a block.
+        const double gref = s.G[rb ? 16 * rb - 1 : 0];
+        const float fq = fast_exp2((float)(gq - gref)) * p.scale;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (l + 64 * i < 16 * rb) s.F[w][l + 64 * i] = fast_exp2((float)(gref - s.G[l + 64 * i]));
         lds_barrier();
-        tv.store(sB, LV, rows, tid);
-        lds_barrier();
-        for (int s = 0; s <= rb / 2; ++s) {
+        for (int x = 0; x <= rb / 2; ++x) {
             f32x4 a[2];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const int n = 2 * s + u;
+                const int n = 2 * x + u;
+                f32x4 b = zero4();
                 a[u] = zero4();
 #pragma unroll
-                for (int x = 0; x < DV / 32; ++x) a[u] = mma_k32(a[u], lds8(sB + (16 * n + cl) * LV + 32 * x + 8 * qg), dof[x]);
+                for (int y = 0; y < DV / 32; ++y) a[u] = mma_k32(a[u], lv.row(s.b, n * RV, y), dof[y]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int key = 16 * n + 4 * qg + i;
-                    const float d = fast_exp2((float)(gq - sG[key])) * p.scale;
-                    a[u][i] = key <= row ? a[u][i] * d : 0.f;
+                for (int y = 0; y < DK / 32; ++y) b = mma_k32(b, lk.perm(s.a, n * RK, y), qf[y]);
+                if (n < rb) {
+                    a[u] *= lds4(&s.F[w][16 * n + 4 * qg]) * fq;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int key = 16 * n + 4 * qg + i;
+                        const bool on = key <= row;
+                        a[u][i] = keep(a[u][i] * (fast_exp2((float)(gq - s.G[key])) * p.scale), on);
+                        b[i] = keep(b[i], on);
+                    }
                 }
+                e += dot4(a[u], b);   // A_ij = dP_ij q_i . k_j
             }
             const frag f = pack8<T>(a[0], a[1]);   // bf16 inputs: dP rounded to the products' type
 #pragma unroll
-            for (int m = 0; m < DK / 16; ++m)
-                dq[m] = mma_k32(dq[m], col_frag(sK, LK, 32 * s + 4 * qg, 32 * s + 16 + 4 * qg, 16 * m, cl), f);
+            for (int m = 0; m < DK / 16; ++m) dq[m] = mma_k32(dq[m], lk.col(s.a, 2 * x * RK, m), f);
         }
+        e = qsum4(e);
+        if (qg == 0 && row < rows) p.e[(int64_t)h * p.T + t.lo + row] = e;
         lds_barrier();
     }
+    const int l = threadIdx.x & 63, row = 16 * rb + (l & 15);
     if (row < rows)
 #pragma unroll
         for (int m = 0; m < DK / 16; ++m)
-            store4(p.dq, ((rg.lo + row) * p.Hk + hk) * DK + 16 * m + 4 * qg, dq[m], p.out_bf16);
+            store4(p.dq, ((t.lo + row) * p.Hk + t.hk) * DK + 16 * m + 4 * (l >> 4), dq[m], p.out_bf16);
 }
 
-template <typename T, int DK, int DV>
-__global__ __launch_bounds__(kGradThreads) void linear_dkv_kernel(LinearBwdParams p) {
-    constexpr int LK = DK + 8, LV = DV + 8;
-    constexpr int A = kB * LK > DK * LV ? kB * LK : DK * LV;
+template <typename T, int DK, int DV, bool GROUPED>
+__device__ __forceinline__ void dk_role(const LinearBwdParams& p, const Task& t, GradTiles<T, DK, DV>& s) {
     typedef typename V8<T>::t frag;
-    __shared__ __align__(32) T sA[A];         // Q, then dS
-    __shared__ __align__(32) T sB[kB * LV];   // dO
-    __shared__ __align__(16) double sG[kB];
-    __shared__ float sRow[8][kB];
-    __shared__ float sCol[kB];
-    __shared__ float sSum[8];
-
-    const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, cl = l & 15, qg = l >> 4;
-    const int64_t slot = blockIdx.x / p.Hk;
-    const int hk = (int)(blockIdx.x % p.Hk), R = p.H / p.Hk;
-    const Range rg = piece_range(p.cu, p.N, p.seqlen, p.T, slot, kB);
-    const int rows = (int)(rg.hi - rg.lo);
-    if (rows <= 0) return;
-    const int rb = w < 4 ? w : 11 - w, key = 16 * rb + cl;
+    constexpr int RK = 16 * DK * sizeof(T), RV = 16 * DV * sizeof(T);
+    const int w = threadIdx.x >> 6, rb = row_block(w), rows = t.rows;
     const int64_t ldk = (int64_t)p.Hk * DK, ldv = (int64_t)p.H * DV;
-    const T* k = (const T*)p.k + (rg.lo * p.Hk + hk) * DK;
+    const T* k = (const T*)p.k + t.lo * ldk + t.hk * DK;
 
-    frag kf[DK / 32];
-    row_frags<T, DK>(kf, k, ldk, key, rows, qg);
     f32x4 dk[DK / 16];
 #pragma unroll
     for (int m = 0; m < DK / 16; ++m) dk[m] = zero4();
-    for (int r = 0; r < R; ++r) {
-        const int h = hk * R + r;
-        {
-            Tile<T, kB, DK, kGradThreads> t;
-            t.load((const T*)p.q + (rg.lo * p.Hk + hk) * DK, ldk, rows, tid);
-            Tile<T, kB, DV, kGradThreads> u;
-            u.load((const T*)p.dO + (rg.lo * p.H + h) * DV, ldv, rows, tid);
-            t.store(sA, LK, rows, tid);
-            u.store(sB, LV, rows, tid);
-        }
-        if (w == 0) block_gates(sG, p.g + (p.g_stride ? rg.lo * p.g_stride : 0) + h, p.g_stride, rows, l);
-        for (int x = tid; x < 8 * kB; x += kGradThreads) sRow[0][x] = 0.f;
-        frag vf[DV / 32];
-        row_frags<T, DV>(vf, (const T*)p.v + (rg.lo * p.H + h) * DV, ldv, key, rows, qg);
-        f32x4 dv[DV / 16];
-#pragma unroll
-        for (int m = 0; m < DV / 16; ++m) dv[m] = zero4();
-        lds_barrier();
-        const double gk = sG[key];
-        float colsum = 0.f;
-        for (int s = rb / 2; s < (rows + 31) / 32; ++s) {
-            f32x4 a[2], b[2];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int n = 2 * s + u;
-                a[u] = b[u] = zero4();
-#pragma unroll
-                for (int x = 0; x < DK / 32; ++x) a[u] = mma_k32(a[u], lds8(sA + (16 * n + cl) * LK + 32 * x + 8 * qg), kf[x]);
-#pragma unroll
-                for (int x = 0; x < DV / 32; ++x) b[u] = mma_k32(b[u], lds8(sB + (16 * n + cl) * LV + 32 * x + 8 * qg), vf[x]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int query = 16 * n + 4 * qg + i;
-                    const float d = fast_exp2((float)(sG[query] - gk)) * p.scale;
-                    const bool on = key <= query;
-                    const float P = on ? a[u][i] * d : 0.f;
-                    const float x = on ? P * b[u][i] : 0.f;
-                    a[u][i] = P;
-                    b[u][i] = on ? b[u][i] * d : 0.f;
-                    colsum += x;
-                    const float rs = row16_sum(x);
-                    if (cl == 0) sRow[w][query] = rs;
-                }
-            }
-            const frag fp = pack8<T>(a[0], a[1]), fd = pack8<T>(b[0], b[1]);   // bf16 inputs: P and dP rounded
-#pragma unroll
-            for (int m = 0; m < DV / 16; ++m)
-                dv[m] = mma_k32(dv[m], col_frag(sB, LV, 32 * s + 4 * qg, 32 * s + 16 + 4 * qg, 16 * m, cl), fp);
-#pragma unroll
-            for (int m = 0; m < DK / 16; ++m)
-                dk[m] = mma_k32(dk[m], col_frag(sA, LK, 32 * s + 4 * qg, 32 * s + 16 + 4 * qg, 16 * m, cl), fd);
-        }
-        colsum = qsum4(colsum);
-        if (qg == 0) sCol[key] = colsum;
-        float cross = 0.f;
+    for (int r = 0; r < (GROUPED ? t.R : 1); ++r) {
+        const int h = GROUPED ? t.hk * t.R + r : t.hk, tid = GROUPED ? opaque(threadIdx.x) : threadIdx.x, l = tid & 63, cl = l & 15, qg = l >> 4, key = 16 * rb + cl;
         Tile<T, DK, DV, kGradThreads> td;
-        td.load((const T*)p.dS + (slot * p.H + h) * DK * DV, DV, DK, tid);
-        {
-            Tile<T, DK, DV, kGradThreads> ts;
-            ts.load((const T*)p.S + (slot * p.H + h) * DK * DV, DV, DK, tid);
-#pragma unroll
-            for (int i = 0; i < Tile<T, DK, DV, kGradThreads>::PIECES; ++i) {
-                typedef T piece __attribute__((ext_vector_type(16 / sizeof(T))));
-                const piece x = __builtin_bit_cast(piece, ts.r[i]), y = __builtin_bit_cast(piece, td.r[i]);
-#pragma unroll
-                for (int j = 0; j < (int)(16 / sizeof(T)); ++j) cross += to_f32(x[j]) * to_f32(y[j]);
-            }
-        }
-#pragma unroll
-        for (int m = 32; m >= 1; m >>= 1) cross += __shfl_xor(cross, m, 64);
-        if (l == 0) sSum[w] = cross;
-        lds_barrier();   // the last readers of Q are done; the sums are there
-        td.store(sA, LV, DK, tid);
-        if (tid < rows && tid < kB) {
-            float x = -sCol[tid];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x += sRow[i][tid];
-            p.a[(int64_t)h * p.T + rg.lo + tid] = x;
-        }
-        if (tid == 0) {
-            float x = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x += sSum[i];
-            p.cross[slot * p.H + h] = x * fast_exp2((float)sG[kB - 1]);
+        td.load((const T*)p.dS + (t.slot * p.H + h) * DK * DV, DV, DK, tid);
+        frag vf[DV / 32], kf[DK / 32];
+        row_frags<T, DV>(vf, (const T*)p.v + t.lo * ldv + h * DV, ldv, key, rows, qg);
+        row_perms<T, DK>(kf, k, ldk, key, rows, qg);
+        Tile<T, kB, DV, kGradThreads> to;
+        to.load((const T*)p.dO + t.lo * ldv + h * DV, ldv, rows, tid);
+        if (r == 0) {
+            Tile<T, kB, DK, kGradThreads> tq;
+            tq.load((const T*)p.q + t.lo * ldk + t.hk * DK, ldk, rows, tid);
+            if (w == 0) block_gates(s.G, p.g + (p.g_stride ? t.lo * p.g_stride : 0) + h, p.g_stride, rows, l);
+            td.store(s.b, DK, tid);
+            tq.store(s.a, rows, tid);
+        } else {
+            if (w == 0) block_gates(s.G, p.g + (p.g_stride ? t.lo * p.g_stride : 0) + h, p.g_stride, rows, l);
+            td.store(s.b, DK, tid);
         }
         lds_barrier();
-        const float wj = fast_exp2((float)(sG[kB - 1] - gk));
+        // through the state's gradient; row = key channel, column = key
+        const Lane<T, DK> lk(cl, qg);
+        const Lane<T, DV> lv(cl, qg);
+        const double gk = s.G[key];
+        const float wj = fast_exp2((float)(s.G[kB - 1] - gk));
         float f = 0.f;
 #pragma unroll
         for (int m = 0; m < DK / 16; ++m) {
             f32x4 x = zero4();
 #pragma unroll
-            for (int s = 0; s < DV / 32; ++s) x = mma_k32(x, lds8(sA + (16 * m + cl) * LV + 32 * s + 8 * qg), vf[s]);
+            for (int y = 0; y < DV / 32; ++y) x = mma_k32(x, lv.row(s.b, m * RV, y), vf[y]);
             x *= wj;
-            f += dot4(x, load4f(k + (int64_t)(key < rows ? key : 0) * ldk + 16 * m + 4 * qg));
+            f += dot4(x, half4(kf[m / 2], m & 1));
             dk[m] += x;
+            if (m & 1) __builtin_amdgcn_sched_barrier(0);
         }
         f = qsum4(f);
-        if (qg == 0 && key < rows) p.f[(int64_t)h * p.T + rg.lo + key] = f;
+        if (qg == 0 && key < rows) p.f[(int64_t)h * p.T + t.lo + key] = f;
+        lds_barrier();   // the last readers of dS are done
+        to.store(s.b, rows, tid);
+        // Above the diagonal block the decay is split at the wave's last key.
+        const double gref = s.G[16 * rb + 15];
+        const float fk = fast_exp2((float)(gref - gk)) * p.scale;
 #pragma unroll
-        for (int m = 0; m < DV / 16; ++m) {
-            f32x4 x = zero4();
+        for (int i = 0; i < 2; ++i)
+            if (l + 64 * i >= 16 * rb + 16) s.F[w][l + 64 * i] = fast_exp2((float)(s.G[l + 64 * i] - gref));
+        lds_barrier();
+        float colsum = 0.f;
+        for (int x = rb / 2; x < (rows + 31) / 32; ++x) {
+            f32x4 b[2];
 #pragma unroll
-            for (int s = 0; s < DK / 32; ++s) x = mma_k32(x, col_frag(sA, LV, 32 * s + 8 * qg, 32 * s + 8 * qg + 4, 16 * m, cl), kf[s]);
-            dv[m] += x * wj;
-            if (key < rows) store4(p.dv_out, ((rg.lo + key) * p.H + h) * DV + 16 * m + 4 * qg, dv[m], p.out_bf16);
+            for (int u = 0; u < 2; ++u) {
+                const int n = 2 * x + u;
+                f32x4 a = zero4();
+                b[u] = zero4();
+#pragma unroll
+                for (int y = 0; y < DK / 32; ++y) a = mma_k32(a, lk.perm(s.a, n * RK, y), kf[y]);
+#pragma unroll
+                for (int y = 0; y < DV / 32; ++y) b[u] = mma_k32(b[u], lv.row(s.b, n * RV, y), vf[y]);
+                if (n > rb) {
+                    b[u] *= lds4(&s.F[w][16 * n + 4 * qg]) * fk;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int query = 16 * n + 4 * qg + i;
+                        const bool on = key <= query;
+                        b[u][i] = keep(b[u][i] * (fast_exp2((float)(s.G[query] - gk)) * p.scale), on);
+                        a[i] = keep(a[i], on);
+                    }
+                }
+                colsum += dot4(a, b[u]);   // A_ij = q_i . k_j dP_ij
+            }
+            const frag f = pack8<T>(b[0], b[1]);   // bf16 inputs: dP rounded to the products' type
+#pragma unroll
+            for (int m = 0; m < DK / 16; ++m) dk[m] = mma_k32(dk[m], lk.col(s.a, 2 * x * RK, m), f);
         }
+        colsum = qsum4(colsum);
+        if (qg == 0 && key < rows) p.a[(int64_t)h * p.T + t.lo + key] = colsum;
         lds_barrier();
     }
+    const int l = threadIdx.x & 63, key = 16 * rb + (l & 15);
     if (key < rows)
 #pragma unroll
         for (int m = 0; m < DK / 16; ++m)
-            store4(p.dk_out, ((rg.lo + key) * p.Hk + hk) * DK + 16 * m + 4 * qg, dk[m], p.out_bf16);
+            store4(p.dk_out, ((t.lo + key) * p.Hk + t.hk) * DK + 16 * m + 4 * (l >> 4), dk[m], p.out_bf16);
+}
+
+template <typename T, int DK, int DV>
+__device__ __forceinline__ void dv_role(const LinearBwdParams& p, const Task& t, int h, GradTiles<T, DK, DV>& s) {
+    typedef typename V8<T>::t frag;
+    constexpr int RK = 16 * DK * sizeof(T), RV = 16 * DV * sizeof(T);
+    const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, cl = l & 15, qg = l >> 4;
+    const int rb = row_block(w), key = 16 * rb + cl, rows = t.rows;
+    const int64_t ldk = (int64_t)p.Hk * DK, ldv = (int64_t)p.H * DV;
+
+    // the keys in the k order of the state's columns as they are read here
+    frag kf[DK / 32];
+    row_perms<T, DK>(kf, (const T*)p.k + t.lo * ldk + t.hk * DK, ldk, key, rows, qg);
+    Tile<T, kB, DK, kGradThreads> tq;
+    tq.load((const T*)p.q + t.lo * ldk + t.hk * DK, ldk, rows, tid);
+    {
+        Tile<T, DK, DV, kGradThreads> td, ts;
+        td.load((const T*)p.dS + (t.slot * p.H + h) * DK * DV, DV, DK, tid);
+        ts.load((const T*)p.S + (t.slot * p.H + h) * DK * DV, DV, DK, tid);
+        Tile<T, kB, DV, kGradThreads> to;
+        to.load((const T*)p.dO + t.lo * ldv + h * DV, ldv, rows, tid);
+        if (w == 0) block_gates(s.G, p.g + (p.g_stride ? t.lo * p.g_stride : 0) + h, p.g_stride, rows, l);
+        td.store(s.b, DK, tid);
+        float cross = 0.f;
+#pragma unroll
+        for (int i = 0; i < Tile<T, DK, DV, kGradThreads>::PIECES; ++i) {
+            typedef T piece __attribute__((ext_vector_type(16 / sizeof(T))));
+            const piece x = __builtin_bit_cast(piece, ts.r[i]), y = __builtin_bit_cast(piece, td.r[i]);
+#pragma unroll
+            for (int j = 0; j < (int)(16 / sizeof(T)); ++j) cross += to_f32(x[j]) * to_f32(y[j]);
+        }
+#pragma unroll
+        for (int m = 32; m >= 1; m >>= 1) cross += __shfl_xor(cross, m, 64);
+        if (l == 0) s.sum[w] = cross;
+        to.store(s.a, rows, tid);
+    }
+    lds_barrier();
+    if (tid == 0) {
+        float x = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x += s.sum[i];
+        p.cross[t.slot * p.H + h] = x * fast_exp2((float)s.G[kB - 1]);
+    }
+    // through the state's gradient; row = value channel, column = key
+    const Lane<T, DK> lk(cl, qg);
+    const Lane<T, DV> lv(cl, qg);
+    const double gk = s.G[key];
+    const float wj = fast_exp2((float)(s.G[kB - 1] - gk));
+    f32x4 dv[DV / 16];
+#pragma unroll
+    for (int m = 0; m < DV / 16; ++m) {
+        f32x4 x = zero4();
+#pragma unroll
+        for (int y = 0; y < DK / 32; ++y) x = mma_k32(x, lv.col(s.b, 2 * y * RV, m), kf[y]);
+        dv[m] = x * wj;
+    }
+    lds_barrier();   // the last readers of dS are done
+    tq.store(s.b, rows, tid);
+    const double gref = s.G[16 * rb + 15];
+    const float fk = fast_exp2((float)(gref - gk)) * p.scale;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if (l + 64 * i >= 16 * rb + 16) s.F[w][l + 64 * i] = fast_exp2((float)(s.G[l + 64 * i] - gref));
+    lds_barrier();
+    for (int x = rb / 2; x < (rows + 31) / 32; ++x) {
+        f32x4 a[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int n = 2 * x + u;
+            a[u] = zero4();
+#pragma unroll
+            for (int y = 0; y < DK / 32; ++y) a[u] = mma_k32(a[u], lk.perm(s.b, n * RK, y), kf[y]);
+            if (n > rb) {
+                a[u] *= lds4(&s.F[w][16 * n + 4 * qg]) * fk;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int query = 16 * n + 4 * qg + i;
+                    a[u][i] = keep(a[u][i] * (fast_exp2((float)(s.G[query] - gk)) * p.scale), key <= query);
+                }
+            }
+        }
+        const frag f = pack8<T>(a[0], a[1]);   // bf16 inputs: P rounded to the products' type
+#pragma unroll
+        for (int m = 0; m < DV / 16; ++m) dv[m] = mma_k32(dv[m], lv.col(s.a, 2 * x * RV, m), f);
+    }
+    if (key < rows)
+#pragma unroll
+        for (int m = 0; m < DV / 16; ++m)
+            store4(p.dv_out, ((t.lo + key) * p.H + h) * DV + 16 * m + 4 * qg, dv[m], p.out_bf16);
+}
+
+// GROUPED: several value heads to a key head.
+template <typename T, int DK, int DV, bool GROUPED>
+__global__ __launch_bounds__(kGradThreads, sizeof(T) == 2 ? 4 : 2) void linear_grads_kernel(LinearBwdParams p) {
+    __shared__ GradTiles<T, DK, DV> s;
+    const int R = GROUPED ? p.H / p.Hk : 1, roles = 2 + R;
+    const int64_t group = blockIdx.x / (8 * roles);
+    const int x = (int)(blockIdx.x % (8 * roles)), role = x >> 3;
+    const int64_t task = group * 8 + (x & 7);
+    Task t;
+    t.slot = task / p.Hk;
+    if (t.slot >= p.blocks) return;
+    t.hk = (int)(task % p.Hk);
+    t.R = R;
+    const Range rg = piece_range(p.cu, p.N, p.seqlen, p.T, t.slot, kB);
+    t.lo = rg.lo;
+    t.rows = (int)(rg.hi - rg.lo);
+    if (t.rows <= 0) return;
+    if (role == 0) dq_role<T, DK, DV, GROUPED>(p, t, s);
+    else if (role == 1) dk_role<T, DK, DV, GROUPED>(p, t, s);
+    else dv_role<T, DK, DV>(p, t, t.hk * R + role - 2, s);
 }
 
 // dg of a block, one wave per (block, head): lane l holds tokens l and l + 64.  64-bit sums.
@@ -301,16 +421,16 @@ __global__ __launch_bounds__(kThreads) void linear_dg_kernel(LinearBwdParams p) 
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int t = l + 64 * i;
-        x[i] = t < rows ? (double)p.e[at + t] + (double)p.a[at + t] : 0.0;
+        x[i] = t < rows ? (double)p.e[at + t] - (double)p.a[at + t] : 0.0;
         f[i] = t < rows ? (double)p.f[at + t] : 0.0;
     }
     const double c = p.cross[id];
     double xs[2], fs[2];
-    xs[0] = wave_scan(x[0], l);
-    fs[0] = wave_scan(f[0], l);
-    xs[1] = wave_scan(x[1], l) + __shfl(xs[0], 63, 64);
-    fs[1] = wave_scan(f[1], l) + __shfl(fs[0], 63, 64);
-    const double all = __shfl(xs[1], 63, 64);
+    xs[0] = wave_scan(x[0]);
+    fs[0] = wave_scan(f[0]);
+    xs[1] = wave_scan(x[1]) + last_lane(xs[0]);
+    fs[1] = wave_scan(f[1]) + last_lane(fs[0]);
+    const double all = last_lane(xs[1]);
     double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -344,9 +464,10 @@ __global__ __launch_bounds__(kThreads) void linear_dg_head_kernel(LinearBwdParam
 }
 
 template <typename T, int DK, int DV> static void grads_t(const LinearBwdParams& p, hipStream_t stream) {
-    const dim3 grid((unsigned)(p.blocks * p.Hk));
-    hipLaunchKernelGGL((linear_dq_kernel<T, DK, DV>), grid, dim3(kGradThreads), 0, stream, p);
-    hipLaunchKernelGGL((linear_dkv_kernel<T, DK, DV>), grid, dim3(kGradThreads), 0, stream, p);
+    const int64_t tasks = (p.blocks * p.Hk + 7) / 8 * 8;
+    const dim3 grid((unsigned)(tasks * (2 + p.H / p.Hk)));
+    if (p.H == p.Hk) hipLaunchKernelGGL((linear_grads_kernel<T, DK, DV, false>), grid, dim3(kGradThreads), 0, stream, p);
+    else hipLaunchKernelGGL((linear_grads_kernel<T, DK, DV, true>), grid, dim3(kGradThreads), 0, stream, p);
 }
 template <typename T> static void grads_d(const LinearBwdParams& p, int dk, hipStream_t stream) {
     if (dk == 128) {

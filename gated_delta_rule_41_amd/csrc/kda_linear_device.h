@@ -9,6 +9,13 @@ namespace lin {
 
 typedef double f64x2 __attribute__((ext_vector_type(2)));
 
+// A lane value the compiler cannot see through: LDS offsets made from it stay inside the loop
+// (a few integer operations) instead of being kept in registers across it.
+__device__ __forceinline__ int opaque(int x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
 __device__ __forceinline__ f32x4 zero4() { return f32x4{0.f, 0.f, 0.f, 0.f}; }
 
 // Token range of piece j of document n; pieces of `piece` tokens, piece = 0 for the whole
@@ -24,15 +31,25 @@ __device__ __forceinline__ void doc_bounds(const int32_t* cu, int seqlen, int64_
     s = s < 0 ? 0 : (s > T ? T : s);
     e = e < s ? s : (e > T ? T : e);
 }
+// The document that owns `slot` when document n's pieces start at slot start / piece + n:
+// the last n whose first slot is not past it.  Every lane of the wave takes part: 64
+// documents are looked at per load, where a binary search would wait for one load per halving.
 __device__ __forceinline__ int piece_owner(const int32_t* cu, int N, int seqlen, int64_t slot, int piece) {
-    int lo = 0, hi = N - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        const int64_t start = cu ? (int64_t)cu[mid] : (int64_t)mid * seqlen;
-        if (start / piece + mid <= slot) lo = mid;
-        else hi = mid - 1;
+    const int l = threadIdx.x & 63;
+    int lo = 0, n = N;
+    while (true) {
+        const int step = (n + 63) / 64, i = lo + l * step;
+        bool past = true;
+        if (l * step < n) {
+            const int64_t start = cu ? (int64_t)cu[i] : (int64_t)i * seqlen;
+            past = start / piece + i > slot;
+        }
+        const unsigned long long m = __ballot(!past);
+        const int last = m ? 63 - __clzll((long long)m) : 0;
+        lo += last * step;
+        n = n - last * step < step ? n - last * step : step;
+        if (step == 1) return __builtin_amdgcn_readfirstlane(lo);
     }
-    return lo;
 }
 __device__ __forceinline__ Range piece_range(const int32_t* cu, int N, int seqlen, int64_t T, int64_t slot, int piece) {
     Range r;
@@ -60,67 +77,160 @@ __device__ __forceinline__ Range piece_range(const int32_t* cu, int N, int seqle
 // sums stays finite.  NaN stays NaN.
 __device__ __forceinline__ double gate_log2(float g) { return (double)(g < -128.f ? -128.f : g) * 1.4426950408889634; }
 
-// Inclusive sum over the 64 lanes.  64 bits: the decay between two tokens is the difference
-// of two sums, and sums of strong gates would leave fp32 differences only ~1e-4 exact.
-__device__ __forceinline__ double wave_scan(double x, int lane) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const double y = __shfl_up(x, d, 64);
-        if (lane >= d) x += y;
-    }
+// Inclusive sum over the 64 lanes, by data-parallel moves within and across rows of 16 (no
+// LDS round trips: the scan sits on a chunk's critical path).  64 bits: the decay between two
+// tokens is the difference of two sums, and sums of strong gates would leave fp32
+// differences only ~1e-4 exact.  Every lane must be active.
+template <int CTRL, int ROWS> __device__ __forceinline__ double dpp64(double x) {
+    typedef int i32x2 __attribute__((ext_vector_type(2)));
+    const i32x2 v = __builtin_bit_cast(i32x2, x);
+    i32x2 r;
+    r[0] = __builtin_amdgcn_update_dpp(0, v[0], CTRL, ROWS, 0xF, false);
+    r[1] = __builtin_amdgcn_update_dpp(0, v[1], CTRL, ROWS, 0xF, false);
+    return __builtin_bit_cast(double, r);
+}
+__device__ __forceinline__ double wave_scan(double x) {
+    x += dpp64<0x111, 0xF>(x);   // row_shr 1, 2, 4, 8: sums within each row of 16
+    x += dpp64<0x112, 0xF>(x);
+    x += dpp64<0x114, 0xF>(x);
+    x += dpp64<0x118, 0xF>(x);
+    x += dpp64<0x142, 0xA>(x);   // row_bcast 15 into rows 1 and 3
+    x += dpp64<0x143, 0xC>(x);   // row_bcast 31 into rows 2 and 3
     return x;
 }
+__device__ __forceinline__ double last_lane(double x) {
+    typedef int i32x2 __attribute__((ext_vector_type(2)));
+    i32x2 v = __builtin_bit_cast(i32x2, x);
+    v[0] = __builtin_amdgcn_readlane(v[0], 63);
+    v[1] = __builtin_amdgcn_readlane(v[1], 63);
+    return __builtin_bit_cast(double, v);
+}
 
-// Fragment of the transpose of a row-major tile: elements 0..3 are rows r0..r0+3 and 4..7
-// rows r1..r1+3 of column c0 + lane % 16.  16-bit elements go through the LDS transpose
-// read (each lane names four columns of one row; see lds_tr4 in kda_f16.h), 32-bit ones
-// are read one by one.
+// Row-major LDS tile without padding, its 16-byte pieces permuted inside each row by
+// piece ^ swz(row).  LDS reads see 64 banks, 16 lanes a cycle for 16-byte reads and 32 for
+// 8-byte and transpose reads.  With r3..r0 the low bits of the row, the permutations below
+// are one to one over 16 rows, so 16-byte reads of one piece of 16 rows touch every bank
+// once, and they move eight rows r..r+3, r+4..r+7 (or r+8..r+11) to eight different pairs of
+// pieces, so transpose reads of 16 columns do too.  (With rows padded by 16 bytes instead the
+// transpose reads were 2-way conflicts.)
+template <typename T, int COLS> struct Swz {
+    static constexpr int E = 16 / (int)sizeof(T), PR = COLS / E;   // elements per piece, pieces per row
+    static __device__ __forceinline__ int swz(int r) {
+        if constexpr (sizeof(T) == 4) return r & 15;
+        else if constexpr (PR == 16) return (r & 3) << 2 | (((r >> 2) ^ (r >> 3)) & 1) << 1 | ((r >> 3) & 1);
+        else return ((r >> 1) & 1) << 2 | (((r >> 2) ^ (r >> 3)) & 1) << 1 | ((r >> 3) & 1);
+    }
+    static __device__ __forceinline__ int at(int row, int piece) { return row * COLS + (piece ^ swz(row)) * E; }
+};
+
 __device__ __forceinline__ bf16x4 tr4(const bf16* p) {
     typedef short v4s __attribute__((__vector_size__(4 * sizeof(short))));
     const v4s r = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(const_cast<bf16*>(p)));
     return __builtin_bit_cast(bf16x4, r);
 }
-__device__ __forceinline__ bf16x8 col_frag(const bf16* t, int ld, int r0, int r1, int c0, int cl) {
-    const bf16* p = t + (cl >> 2) * ld + c0 + 4 * (cl & 3);
-    const bf16x4 a = tr4(p + r0 * ld), b = tr4(p + r1 * ld);
-    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+template <typename V> __device__ __forceinline__ auto join(V a, V b) { return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7); }
+
+// A lane's byte offsets into a Swz tile, and the product fragments read through them.  With
+// `off` the byte offset of the first row (a multiple of 16 rows):
+//   row(y):  columns 32 y + 8 qg + j of row cl
+//   perm(y): columns 32 y + 4 qg + j and 32 y + 16 + 4 qg + j of row cl, the k order of two
+//            stacked accumulator blocks
+//   col(m):  rows 4 qg + j and 16 + 4 qg + j of column 16 m + cl, the same order by rows
+// The permutation makes every further fragment of a row an exclusive-or of one lane constant
+// with a literal.  16-bit columns go through the LDS transpose read (each lane names four
+// columns of one row; see lds_tr4 in kda_f16.h), 32-bit ones are read one by one.
+template <typename V> __device__ __forceinline__ V at_byte(const void* t, int off) {
+    return *reinterpret_cast<const V*>((const char*)t + off);
 }
-__device__ __forceinline__ f32x8 col_frag(const float* t, int ld, int r0, int r1, int c0, int cl) {
-    f32x8 x;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        x[j] = t[(r0 + j) * ld + c0 + cl];
-        x[j + 4] = t[(r1 + j) * ld + c0 + cl];
+template <typename T, int COLS> struct Lane;
+template <int COLS> struct Lane<bf16, COLS> {
+    typedef Swz<bf16, COLS> Z;
+    static constexpr int RB = COLS * 2;   // bytes per row
+    int r, p, c;
+    __device__ __forceinline__ Lane(int cl, int qg) {
+        const int cr = 4 * qg + (cl >> 2);
+        r = cl * RB + (qg ^ Z::swz(cl)) * 16;
+        p = cl * RB + ((qg >> 1) ^ Z::swz(cl)) * 16 + 8 * (qg & 1);
+        c = cr * RB + (((cl >> 1) & 1) ^ Z::swz(cr)) * 16 + 8 * (cl & 1);
     }
-    return x;
+    __device__ __forceinline__ bf16x8 row(const bf16* t, int off, int y) const { return at_byte<bf16x8>(t, (r + off) ^ (64 * y)); }
+    __device__ __forceinline__ bf16x8 perm(const bf16* t, int off, int y) const {
+        return join(at_byte<bf16x4>(t, (p + off) ^ (64 * y)), at_byte<bf16x4>(t, (p + off) ^ (64 * y + 32)));
+    }
+    __device__ __forceinline__ bf16x8 col(const bf16* t, int off, int m) const {
+        const bf16* x = (const bf16*)((const char*)t + ((c + off) ^ (32 * m)));
+        return join(tr4(x), tr4(x + 16 * COLS));
+    }
+};
+template <int COLS> struct Lane<float, COLS> {
+    typedef Swz<float, COLS> Z;
+    static constexpr int RB = COLS * 4;
+    int r, p, c[4];
+    __device__ __forceinline__ Lane(int cl, int qg) {
+        r = cl * RB + ((2 * qg) ^ Z::swz(cl)) * 16;
+        p = cl * RB + (qg ^ Z::swz(cl)) * 16;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c[j] = (4 * qg + j) * RB + ((cl >> 2) ^ Z::swz(4 * qg + j)) * 16 + 4 * (cl & 3);
+    }
+    __device__ __forceinline__ f32x8 row(const float* t, int off, int y) const {
+        return join(at_byte<f32x4>(t, (r + off) ^ (128 * y)), at_byte<f32x4>(t, (r + off) ^ (128 * y + 16)));
+    }
+    __device__ __forceinline__ f32x8 perm(const float* t, int off, int y) const {
+        return join(at_byte<f32x4>(t, (p + off) ^ (128 * y)), at_byte<f32x4>(t, (p + off) ^ (128 * y + 64)));
+    }
+    __device__ __forceinline__ f32x8 col(const float* t, int off, int m) const {
+        f32x8 x;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int o = (c[j] + off) ^ (64 * m);
+            x[j] = at_byte<float>(t, o);
+            x[j + 4] = at_byte<float>(t, o + 16 * RB);
+        }
+        return x;
+    }
+};
+// Where four accumulator values (row cl, columns 16 n + 4 qg + i) go in a tile.
+template <typename T, int COLS> __device__ __forceinline__ void put4(T* t, int row, int n, int qg, f32x4 x) {
+    typedef Swz<T, COLS> Z;
+    if constexpr (sizeof(T) == 2) sts4(t + Z::at(row, 2 * n + (qg >> 1)) + 4 * (qg & 1), x);
+    else sts4(t + Z::at(row, 4 * n + qg), x);
 }
-// Two groups of four contiguous elements: the k order of two stacked accumulator blocks.
-template <typename T> __device__ __forceinline__ typename V8<T>::t two4(const T* a, const T* b) {
-    const typename V4<T>::t x = lds4<T>(a), y = lds4<T>(b);
-    return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+// x where `on`, else 0, without a branch (a branch around the few instructions that make x
+// costs more than they do).
+__device__ __forceinline__ float keep(float x, bool on) {
+    return __builtin_bit_cast(float, __builtin_bit_cast(int, x) & (on ? -1 : 0));
 }
 
 __device__ __forceinline__ f32x8 widen8(bf16x8 x) { return __builtin_convertvector(x, f32x8); }
 __device__ __forceinline__ f32x8 widen8(f32x8 x) { return x; }
 
-// c += a^T-operand x * b where x is an fp32 fragment.  bf16: x enters as three bf16 terms
-// (24 bits), so that fp32 states and state gradients keep fp32 accuracy; fp32: exact.
-template <bool X_IS_A> __device__ __forceinline__ f32x4 mma_f32x(f32x4 c, f32x8 x, bf16x8 b) {
-    bf16x8 h = __builtin_convertvector(x, bf16x8);
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-        c = X_IS_A ? mma_k32(c, h, b) : mma_k32(c, b, h);
-        if (i < 2) {
-            x -= __builtin_convertvector(h, f32x8);
-            h = __builtin_convertvector(x, bf16x8);
-        }
+// An fp32 fragment as a product operand.  bf16: three bf16 terms (24 bits), so that fp32
+// states and state gradients keep fp32 accuracy; fp32: itself.
+template <typename T> struct Split;
+template <> struct Split<bf16> {
+    bf16x8 h[3];
+    __device__ __forceinline__ Split() {}
+    __device__ __forceinline__ explicit Split(f32x8 x) {
+        h[0] = __builtin_convertvector(x, bf16x8);
+        x -= __builtin_convertvector(h[0], f32x8);
+        h[1] = __builtin_convertvector(x, bf16x8);
+        x -= __builtin_convertvector(h[1], f32x8);
+        h[2] = __builtin_convertvector(x, bf16x8);
     }
-    return c;
-}
-
-template <bool X_IS_A> __device__ __forceinline__ f32x4 mma_f32x(f32x4 c, f32x8 x, f32x8 b) {
-    return X_IS_A ? mma_k32(c, x, b) : mma_k32(c, b, x);
-}
+    template <bool IS_A> __device__ __forceinline__ f32x4 mma(f32x4 c, bf16x8 b) const {
+#pragma unroll
+        for (int i = 2; i >= 0; --i) c = IS_A ? mma_k32(c, h[i], b) : mma_k32(c, b, h[i]);
+        return c;
+    }
+};
+template <> struct Split<float> {
+    f32x8 x;
+    __device__ __forceinline__ Split() {}
+    __device__ __forceinline__ explicit Split(f32x8 y) : x(y) {}
+    template <bool IS_A> __device__ __forceinline__ f32x4 mma(f32x4 c, f32x8 b) const {
+        return IS_A ? mma_k32(c, x, b) : mma_k32(c, b, x);
+    }
+};
 
 __device__ __forceinline__ void store4(void* base, int64_t at, f32x4 x, int out_bf16) {
     if (out_bf16) *reinterpret_cast<bf16x4*>((bf16*)base + at) = pack4<bf16>(x);
@@ -132,29 +242,42 @@ __device__ __forceinline__ void store1(void* base, int64_t at, float x, int out_
 }
 
 // A tile of ROWS x COLS (row-major in global with row stride `ld` elements) held in
-// registers between its loads and its LDS stores, 16 bytes a piece.  Rows at or past
-// `rows` are read from the last valid row and stored as zeros.
+// registers between its loads and its stores to a Swz tile, 16 bytes a piece.  Rows at or
+// past `rows` are read from the last valid row and stored as zeros.  Addresses are a uniform
+// base and a 32-bit lane offset (ROWS rows of ld elements are below 2^31 bytes).
 template <typename T, int ROWS, int COLS, int THREADS> struct Tile {
-    static constexpr int E = 16 / (int)sizeof(T);            // elements per piece
-    static constexpr int PR = COLS / E;                       // pieces per row
-    static constexpr int PIECES = ROWS * PR / THREADS;
-    static_assert(ROWS * PR % THREADS == 0, "tile pieces");
+    typedef Swz<T, COLS> Z;
+    static constexpr int PIECES = ROWS * Z::PR / THREADS, STEP = THREADS / Z::PR;   // rows between a lane's pieces
+    static_assert(ROWS * Z::PR % THREADS == 0, "tile pieces");
     typedef unsigned u4 __attribute__((ext_vector_type(4)));
     u4 r[PIECES];
     __device__ __forceinline__ void load(const T* g, int64_t ld, int rows, int tid) {
+        const int row = tid / Z::PR;
+        const unsigned c = (tid % Z::PR) * 16u, step = (unsigned)ld * sizeof(T);
+        if (rows >= ROWS) {
+            const unsigned off = (unsigned)row * step + c;
 #pragma unroll
-        for (int i = 0; i < PIECES; ++i) {
-            const int x = tid + i * THREADS, row = x / PR, c = x % PR;
-            const int rr = row < rows ? row : rows - 1;
-            r[i] = *reinterpret_cast<const u4*>(g + (int64_t)rr * ld + c * E);
+            for (int i = 0; i < PIECES; ++i)
+                r[i] = *reinterpret_cast<const u4*>((const char*)(g + i * STEP * ld) + off);
+        } else {
+#pragma unroll
+            for (int i = 0; i < PIECES; ++i) {
+                const int x = row + i * STEP;
+                r[i] = *reinterpret_cast<const u4*>((const char*)g + ((unsigned)(x < rows ? x : rows - 1) * step + c));
+            }
         }
     }
-    __device__ __forceinline__ void store(T* s, int lds, int rows, int tid) const {
+    __device__ __forceinline__ void store(T* s, int rows, int tid) const {
+        const int row = tid / Z::PR, c = tid % Z::PR;
+        if (rows >= ROWS) {
 #pragma unroll
-        for (int i = 0; i < PIECES; ++i) {
-            const int x = tid + i * THREADS, row = x / PR, c = x % PR;
-            const u4 z = {0u, 0u, 0u, 0u};
-            *reinterpret_cast<u4*>(s + row * lds + c * E) = row < rows ? r[i] : z;
+            for (int i = 0; i < PIECES; ++i) *reinterpret_cast<u4*>(s + Z::at(row + i * STEP, c)) = r[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < PIECES; ++i) {
+                const u4 z = {0u, 0u, 0u, 0u};
+                *reinterpret_cast<u4*>(s + Z::at(row + i * STEP, c)) = row + i * STEP < rows ? r[i] : z;
+            }
         }
     }
 };

@@ -9,9 +9,11 @@
 // sums, at most 1 for g <= 0.
 //
 // linear_out_kernel: one workgroup (4 waves) walks one document (or one segment of it) for
-// one head and 64 value columns; wave c holds the state's columns 16c..16c+15.  Wave w forms
-// rows 16w..16w+15 of P and hands them over through LDS; everything else a wave needs of the
-// state is its own.  The next chunk's rows are loaded into registers while this one runs.
+// one head; wave w holds the state's columns [w dv/4, (w + 1) dv/4), so an operand fragment
+// of q or k read from LDS serves two products at dv = 128.  Wave w forms rows 16w..16w+15 of
+// P and hands them over through LDS; everything else a wave needs of the state is its own.
+// The next chunk's rows are loaded into registers while this one runs, and its gates are
+// summed by wave 0, which has the least of P.
 //
 // linear_state_kernel: the state alone, forward or in reverse (the same sum with q, dO and
 // weights e^{G_i}), for the segments of long documents and for the backward.
@@ -23,241 +25,305 @@
 namespace kda {
 using namespace lin;
 
-// Chains of one head's value slices sit eight workgroups apart, on one XCD, whose L2 then
-// serves the rows that they share.
-__device__ __forceinline__ bool chain_slice(int64_t b, int slices, int chains, int& chain, int& slice) {
-    const int64_t group = b / (8 * slices);
-    const int r = (int)(b % (8 * slices));
-    chain = (int)(group * 8 + (r & 7));
-    slice = r >> 3;
-    return chain < chains;
+// The gates of one chunk, by one wave (lane = token): G (log2 units, 64 bits), and the
+// weights of its tokens' writes and of the state.
+struct Gates {
+    double G[kLinChunk];
+    float W[kLinChunk];
+    float E;
+};
+__device__ __forceinline__ double put_gates(Gates& s, float g, int rows, int l, bool rev, float scale) {
+    const double G = wave_scan(l < rows ? gate_log2(g) : 0.0), Gt = last_lane(G);
+    s.G[l] = G;
+    s.W[l] = rev ? fast_exp2((float)G) * scale : fast_exp2((float)(Gt - G));
+    if (l == 0) s.E = fast_exp2((float)Gt);
+    return Gt;
+}
+__device__ __forceinline__ float load_gate(const float* g, int stride, int t, int rows, int l) {
+    return g[(int64_t)(t + (l < rows ? l : rows - 1)) * stride];
 }
 
-template <typename T, int DK>
-__global__ __launch_bounds__(kThreads) void linear_out_kernel(LinearParams p) {
-    constexpr int C = kLinChunk, LQ = DK + 8, LV = kSlice + 8, LP = C + 8;
+template <typename T, int DK, int DV>
+__global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void linear_out_kernel(LinearParams p) {
+    constexpr int C = kLinChunk, NC = DV / 64;   // column groups of 16 per wave
     typedef typename V8<T>::t frag;
-    __shared__ __align__(32) T sQ[C * LQ];
-    __shared__ __align__(32) T sK[C * LQ];
-    __shared__ __align__(32) T sV[C * LV];
-    __shared__ __align__(32) T sP[C * LP];
-    __shared__ __align__(16) double sG[C];
-    __shared__ __align__(32) float sW[C];
-    __shared__ float sE;
+    __shared__ __align__(32) T sQ[C * DK];
+    __shared__ __align__(32) T sK[C * DK];
+    __shared__ __align__(32) T sV[C * DV];
+    __shared__ __align__(32) T sP[C * C];
+    __shared__ __align__(16) float sF[4][C];   // a wave's own decays
+    __shared__ __align__(32) Gates gates[2];
 
     const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, cl = l & 15, qg = l >> 4;
-    int chain, slice;
-    if (!chain_slice(blockIdx.x, p.dv / kSlice, p.chains, chain, slice)) return;
-    const int64_t slot = chain / p.H;
-    const int h = chain % p.H, hk = h / (p.H / p.Hk);
+    const int64_t slot = blockIdx.x / p.H;
+    const int h = blockIdx.x % p.H, hk = h / (p.H / p.Hk);
     const Range rg = piece_range(p.cu, p.N, p.seqlen, p.T, slot, p.seg_len);
-    const int dv = p.dv, col = slice * kSlice + 16 * w;
+    const int col = 16 * NC * w;
     if (p.seg_len && rg.lo >= rg.hi) return;
 
-    // the state: block d holds rows 16d + 4qg + i, column col + cl
-    f32x4 S[DK / 16];
+    // the state: block d of group c holds rows 16d + 4qg + i, column col + 16c + cl
+    f32x4 S[NC][DK / 16];
     {
-        const float* s0 = p.s0 ? p.s0 + ((int64_t)(p.seg_len ? slot : rg.n) * p.H + h) * DK * dv + col + cl : nullptr;
+        const float* s0 = p.s0 ? p.s0 + ((int64_t)(p.seg_len ? slot : rg.n) * p.H + h) * DK * DV + col + cl : nullptr;
 #pragma unroll
-        for (int d = 0; d < DK / 16; ++d)
+        for (int c = 0; c < NC; ++c)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) S[d][i] = s0 ? s0[(int64_t)(16 * d + 4 * qg + i) * dv] : 0.f;
+            for (int d = 0; d < DK / 16; ++d)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) S[c][d][i] = s0 ? s0[(16 * d + 4 * qg + i) * DV + 16 * c] : 0.f;
     }
 
-    const T* qp = (const T*)p.q + (rg.lo * p.Hk + hk) * DK;
-    const T* kp = (const T*)p.k + (rg.lo * p.Hk + hk) * DK;
-    const T* vp = (const T*)p.v + (rg.lo * p.H + h) * dv + slice * kSlice;
+    const int64_t ldk = (int64_t)p.Hk * DK, ldv = (int64_t)p.H * DV;
+    const T* qp = (const T*)p.q + rg.lo * ldk + hk * DK;
+    const T* kp = (const T*)p.k + rg.lo * ldk + hk * DK;
+    const T* vp = (const T*)p.v + rg.lo * ldv + h * DV;
     const float* gp = p.g + (p.g_stride ? rg.lo * p.g_stride : 0) + h;
-    const int64_t ldk = (int64_t)p.Hk * DK, ldv = (int64_t)p.H * dv;
-    const int total = (int)(rg.hi - rg.lo);
+    const int total = (int)(rg.hi - rg.lo), es = p.out_bf16 ? 2 : 4;
+    char* op = (char*)p.o + (rg.lo * ldv + h * DV) * es;
+    const unsigned ooff = ((unsigned)cl * (unsigned)ldv + col + 4 * qg) * es;
 
     // key blocks above the diagonal that a 32-wide product step still covers stay zero
-    for (int x = tid; x < C * LP; x += kThreads) sP[x] = (T)0.f;
+    for (int x = tid; x < C * C; x += kThreads) sP[x] = (T)0.f;
 
     Tile<T, C, DK, kThreads> tq, tk;
-    Tile<T, C, kSlice, kThreads> tv;
+    Tile<T, C, DV, kThreads> tv;
     float g = 0.f;
     if (total > 0) {
         tq.load(qp, ldk, total, tid);
         tk.load(kp, ldk, total, tid);
         tv.load(vp, ldv, total, tid);
-        if (w == 0) g = gp[(int64_t)(l < total ? l : total - 1) * p.g_stride];
+        if (w == 0) {
+            put_gates(gates[0], load_gate(gp, p.g_stride, 0, total, l), total, l, false, 0.f);
+            if (total > C) g = load_gate(gp, p.g_stride, C, total - C, l);
+        }
     }
     for (int t0 = 0; t0 < total; t0 += C) {
-        const int rows = total - t0;
+        const int rows = total - t0, cl = opaque(l & 15), qg = opaque(l >> 4);
+        const Gates& G = gates[(t0 / C) & 1];
         lds_barrier();   // the last chunk's readers are done
-        tq.store(sQ, LQ, rows, tid);
-        tk.store(sK, LQ, rows, tid);
-        tv.store(sV, LV, rows, tid);
-        if (w == 0) {
-            const double G = wave_scan(l < rows ? gate_log2(g) : 0.0, l);
-            const double Gt = __shfl(G, 63, 64);
-            sG[l] = G;
-            sW[l] = fast_exp2((float)(Gt - G));
-            if (l == 0) sE = fast_exp2((float)Gt);
-        }
+        tq.store(sQ, rows, tid);
+        tk.store(sK, rows, tid);
+        tv.store(sV, rows, tid);
+        float gn = g;
         if (rows > C) {
             tq.load(qp + (t0 + C) * ldk, ldk, rows - C, tid);
             tk.load(kp + (t0 + C) * ldk, ldk, rows - C, tid);
             tv.load(vp + (t0 + C) * ldv, ldv, rows - C, tid);
-            if (w == 0) g = gp[(int64_t)(t0 + C + (l < rows - C ? l : rows - C - 1)) * p.g_stride];
+            if (w == 0 && rows > 2 * C) g = load_gate(gp, p.g_stride, t0 + 2 * C, rows - 2 * C, l);
         }
         lds_barrier();
 
-        // P, transposed in the accumulators: row = key 16n + 4qg + i, column = query 16w + cl
+        const Lane<T, DK> lk(cl, qg);
+        const Lane<T, DV> lv(cl, qg);
+        const Lane<T, C> lp(cl, qg);
+        constexpr int RK = 16 * DK * sizeof(T), RV = 16 * DV * sizeof(T), RP = 16 * C * sizeof(T);   // bytes of 16 rows
+        // P, transposed in the accumulators: row = key 16n + 4qg + i, column = query 16w + cl.
+        // Below the diagonal block the decay is split at the last key before the wave's
+        // queries, both factors at most 1: one exponential a lane instead of four a block.
         {
+            const double gq = G.G[16 * w + cl];
+            const double gref = G.G[w ? 16 * w - 1 : 0];
+            const float fq = fast_exp2((float)(gq - gref)) * p.scale;
+            if (l < 16 * w) sF[w][l] = fast_exp2((float)(gref - G.G[l]));
             frag qf[DK / 32];
 #pragma unroll
-            for (int s = 0; s < DK / 32; ++s) qf[s] = lds8(sQ + (16 * w + cl) * LQ + 32 * s + 8 * qg);
-            const double gq = sG[16 * w + cl];
+            for (int s = 0; s < DK / 32; ++s) qf[s] = lk.row(sQ, w * RK, s);
 #pragma unroll
             for (int n = 0; n < 4; ++n)
                 if (n <= w) {
                     f32x4 a = zero4();
 #pragma unroll
-                    for (int s = 0; s < DK / 32; ++s) a = mma_k32(a, lds8(sK + (16 * n + cl) * LQ + 32 * s + 8 * qg), qf[s]);
+                    for (int s = 0; s < DK / 32; ++s) a = mma_k32(a, lk.row(sK, n * RK, s), qf[s]);
+                    if (n < w) {
+                        a *= lds4(&sF[w][16 * n + 4 * qg]) * fq;
+                    } else {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int key = 16 * n + 4 * qg + i;
-                        const float d = fast_exp2((float)(gq - sG[key])) * p.scale;
-                        a[i] = key <= 16 * w + cl ? a[i] * d : 0.f;
+                        for (int i = 0; i < 4; ++i)
+                            a[i] = keep(a[i] * (fast_exp2((float)(gq - G.G[16 * w + 4 * qg + i])) * p.scale), 4 * qg + i <= cl);
                     }
-                    sts4(sP + (16 * w + cl) * LP + 16 * n + 4 * qg, a);
+                    put4<T, C>(sP, 16 * w + cl, n, qg, a);   // bf16 inputs: P rounded to the products' type
                 }
         }
+        if (w == 0 && rows > C) put_gates(gates[(t0 / C + 1) & 1], gn, rows - C, l, false, 0.f);
         // through the entering state; transposed: row = value column, column = token 16m + cl
-        f32x4 O[4];
+        f32x4 O[NC][4];
 #pragma unroll
-        for (int m = 0; m < 4; ++m) O[m] = zero4();
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int m = 0; m < 4; ++m) O[c][m] = zero4();
 #pragma unroll
         for (int s = 0; s < DK / 32; ++s) {
-            const frag sf = pack8<T>(S[2 * s], S[2 * s + 1]);   // bf16 inputs: the state rounded once, for this read only
+            frag sf[NC];
+#pragma unroll
+            for (int c = 0; c < NC; ++c) sf[c] = pack8<T>(S[c][2 * s], S[c][2 * s + 1]);   // bf16 inputs: the state rounded, for this read only
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-                const T* q = sQ + (16 * m + cl) * LQ + 32 * s + 4 * qg;
-                O[m] = mma_k32(O[m], sf, two4(q, q + 16));
+                const frag q = lk.perm(sQ, m * RK, s);
+#pragma unroll
+                for (int c = 0; c < NC; ++c) O[c][m] = mma_k32(O[c][m], sf[c], q);
             }
         }
 #pragma unroll
-        for (int m = 0; m < 4; ++m) O[m] *= fast_exp2((float)sG[16 * m + cl]) * p.scale;
-        frag vf[2];
+        for (int m = 0; m < 4; ++m) {
+            const float e = fast_exp2((float)G.G[16 * m + cl]) * p.scale;
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) vf[kk] = col_frag(sV, LV, 32 * kk + 8 * qg, 32 * kk + 8 * qg + 4, 16 * w, cl);
-        // the state
-        const float eC = sE;
-#pragma unroll
-        for (int d = 0; d < DK / 16; ++d) S[d] *= eC;
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-            const f32x8 u = widen8(vf[kk]) * lds8(sW + 32 * kk + 8 * qg);
-#pragma unroll
-            for (int d = 0; d < DK / 16; ++d)
-                S[d] = mma_f32x<false>(S[d], u, col_frag(sK, LQ, 32 * kk + 8 * qg, 32 * kk + 8 * qg + 4, 16 * d, cl));
+            for (int c = 0; c < NC; ++c) O[c][m] *= e;
         }
+        frag vf[NC][2];
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) vf[c][kk] = lv.col(sV, 2 * kk * RV, w * NC + c);
         lds_barrier();   // P is there
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
 #pragma unroll
-            for (int kk = 0; kk <= m / 2; ++kk)
-                O[m] = mma_k32(O[m], vf[kk], lds8(sP + (16 * m + cl) * LP + 32 * kk + 8 * qg));
-            const int t = t0 + 16 * m + cl;
-            if (t < total) store4(p.o, ((rg.lo + t) * p.H + h) * dv + col + 4 * qg, O[m], p.out_bf16);
+            for (int kk = 0; kk <= m / 2; ++kk) {
+                const frag f = lp.perm(sP, m * RP, kk);
+#pragma unroll
+                for (int c = 0; c < NC; ++c) O[c][m] = mma_k32(O[c][m], vf[c][kk], f);
+            }
+            if (16 * m + cl < rows) {
+                char* o = op + (int64_t)(t0 + 16 * m) * ldv * es;
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                    if (p.out_bf16) *reinterpret_cast<bf16x4*>(o + (ooff + 32u * c)) = pack4<bf16>(O[c][m]);
+                    else *reinterpret_cast<f32x4*>(o + (ooff + 64u * c)) = O[c][m];
+                }
+            }
+        }
+        // the state
+        const float eC = G.E;
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int d = 0; d < DK / 16; ++d) S[c][d] *= eC;
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+            const f32x8 wt = join(lds4(G.W + 32 * kk + 4 * qg), lds4(G.W + 32 * kk + 16 + 4 * qg));
+            Split<T> u[NC];
+#pragma unroll
+            for (int c = 0; c < NC; ++c) u[c] = Split<T>(widen8(vf[c][kk]) * wt);
+#pragma unroll
+            for (int d = 0; d < DK / 16; ++d) {
+                const frag k = lk.col(sK, 2 * kk * RK, d);
+#pragma unroll
+                for (int c = 0; c < NC; ++c) S[c][d] = u[c].template mma<false>(S[c][d], k);
+            }
         }
     }
     if (p.sfinal && !p.seg_len) {
-        float* sf = p.sfinal + ((int64_t)rg.n * p.H + h) * DK * dv + col + cl;
+        float* sf = p.sfinal + ((int64_t)rg.n * p.H + h) * DK * DV + col + cl;
 #pragma unroll
-        for (int d = 0; d < DK / 16; ++d)
+        for (int c = 0; c < NC; ++c)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) sf[(int64_t)(16 * d + 4 * qg + i) * dv] = S[d][i];
+            for (int d = 0; d < DK / 16; ++d)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sf[(16 * d + 4 * qg + i) * DV + 16 * c] = S[c][d][i];
     }
 }
 
-template <typename T, int DK>
-__global__ __launch_bounds__(kThreads) void linear_state_kernel(LinearStateParams p) {
-    constexpr int C = kLinChunk, LA = DK + 8, LB = kSlice + 8;
-    __shared__ __align__(32) T sA[C * LA];
-    __shared__ __align__(32) T sB[C * LB];
-    __shared__ __align__(32) float sW[C];
-    __shared__ float sE;
+// One workgroup per chain and 64 NC value columns (of a [DK][dv] state).
+template <typename T, int DK, int NC>
+__global__ __launch_bounds__(kThreads, 2) void linear_state_kernel(LinearStateParams p) {
+    constexpr int C = kLinChunk, DV = 64 * NC;
+    typedef typename V8<T>::t frag;
+    __shared__ __align__(32) T sA[C * DK];
+    __shared__ __align__(32) T sB[C * DV];
+    __shared__ __align__(32) Gates gates[2];
 
     const LinearStateDir D = p.dir[blockIdx.y];
     const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, cl = l & 15, qg = l >> 4;
-    int chain, slice;
-    if (!chain_slice(blockIdx.x, p.dv / kSlice, p.chains, chain, slice)) return;
-    const int64_t slot = chain / p.H;
-    const int h = chain % p.H, hk = h / (p.H / p.Hk);
+    const int64_t slot = blockIdx.x / p.H;
+    const int h = blockIdx.x % p.H, hk = h / (p.H / p.Hk);
     const Range rg = piece_range(p.cu, p.N, p.seqlen, p.T, slot, p.seg_len);
     if (p.seg_len && rg.lo >= rg.hi) return;
-    const int dv = p.dv, col = slice * kSlice + 16 * w + 4 * qg;
+    const int col = 16 * NC * w, dv = p.dv, slice = blockIdx.z * DV;
     const bool rev = D.rev != 0;
 
-    // transposed against linear_out_kernel, for 16-byte stores: block d holds state row
-    // 16d + cl, value columns col .. col + 3
-    f32x4 S[DK / 16];
+    // transposed against linear_out_kernel, for 16-byte stores: block d of group c holds state
+    // row 16d + cl, value columns col + 16c + 4qg + i
+    f32x4 S[NC][DK / 16];
+    const int lane = cl * dv + slice + col + 4 * qg;
     {
-        const float* s0 = D.s0 ? D.s0 + ((int64_t)(p.seg_len ? slot : rg.n) * p.H + h) * DK * dv + col : nullptr;
+        const float* s0 = D.s0 ? D.s0 + ((int64_t)(p.seg_len ? slot : rg.n) * p.H + h) * DK * dv + lane : nullptr;
 #pragma unroll
-        for (int d = 0; d < DK / 16; ++d)
-            S[d] = s0 ? *reinterpret_cast<const f32x4*>(s0 + (int64_t)(16 * d + cl) * dv) : zero4();
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int d = 0; d < DK / 16; ++d)
+                S[c][d] = s0 ? *reinterpret_cast<const f32x4*>(s0 + 16 * d * dv + 16 * c) : zero4();
     }
-    const T* ap = (const T*)D.a + (rg.lo * p.Hk + hk) * DK;
-    const T* bp = (const T*)D.b + (rg.lo * p.H + h) * dv + slice * kSlice;
-    const float* gp = p.g + (p.g_stride ? rg.lo * p.g_stride : 0) + h;
     const int64_t lda = (int64_t)p.Hk * DK, ldb = (int64_t)p.H * dv;
+    const T* ap = (const T*)D.a + rg.lo * lda + hk * DK;
+    const T* bp = (const T*)D.b + rg.lo * ldb + h * dv + slice;
+    const float* gp = p.g + (p.g_stride ? rg.lo * p.g_stride : 0) + h;
     const int total = (int)(rg.hi - rg.lo), chunks = (total + C - 1) / C;
     // a block of the document keeps its slot whatever the segments are
     const int64_t block0 = rg.start / kLinBlock + rg.n + (rg.lo - rg.start) / kLinBlock;
 
     Tile<T, C, DK, kThreads> ta;
-    Tile<T, C, kSlice, kThreads> tb;
+    Tile<T, C, DV, kThreads> tb;
     float g = 0.f;
     double gsum = 0.0;
+    const int dir = rev ? -C : C;
+    int t0 = rev ? (chunks - 1) * C : 0;
     if (chunks > 0) {
-        const int t0 = rev ? (chunks - 1) * C : 0, rows = total - t0;
-        ta.load(ap + t0 * lda, lda, rows, tid);
-        tb.load(bp + t0 * ldb, ldb, rows, tid);
-        if (w == 0) g = gp[(int64_t)(t0 + (l < rows ? l : rows - 1)) * p.g_stride];
-    }
-    for (int x = 0; x < chunks; ++x) {
-        const int c = rev ? chunks - 1 - x : x, t0 = c * C, rows = total - t0;
-        if (D.border && (rev ? ((c & 1) || x == 0) : !(c & 1))) {
-            T* b = (T*)D.border + ((block0 + c / 2) * p.H + h) * DK * dv + col;
-#pragma unroll
-            for (int d = 0; d < DK / 16; ++d) *reinterpret_cast<typename V4<T>::t*>(b + (int64_t)(16 * d + cl) * dv) = pack4<T>(S[d]);
-        }
-        lds_barrier();
-        ta.store(sA, LA, rows, tid);
-        tb.store(sB, LB, rows, tid);
+        ta.load(ap + t0 * lda, lda, total - t0, tid);
+        tb.load(bp + t0 * ldb, ldb, total - t0, tid);
         if (w == 0) {
-            const double G = wave_scan(l < rows ? gate_log2(g) : 0.0, l);
-            const double Gt = __shfl(G, 63, 64);
-            sW[l] = rev ? fast_exp2((float)G) * p.scale : fast_exp2((float)(Gt - G));
-            if (l == 0) sE = fast_exp2((float)Gt);
-            gsum += Gt;
+            gsum += put_gates(gates[0], load_gate(gp, p.g_stride, t0, total - t0, l), total - t0, l, rev, p.scale);
+            if (chunks > 1) g = load_gate(gp, p.g_stride, t0 + dir, total - t0 - dir, l);
         }
-        if (x + 1 < chunks) {
-            const int u0 = rev ? t0 - C : t0 + C, more = total - u0;
-            ta.load(ap + u0 * lda, lda, more, tid);
-            tb.load(bp + u0 * ldb, ldb, more, tid);
-            if (w == 0) g = gp[(int64_t)(u0 + (l < more ? l : more - 1)) * p.g_stride];
+    }
+    for (int x = 0; x < chunks; ++x, t0 += dir) {
+        const int rows = total - t0, c0 = t0 / C, cl = opaque(l & 15), qg = opaque(l >> 4);
+        const Gates& G = gates[x & 1];
+        if (D.border && (rev ? ((c0 & 1) || x == 0) : !(c0 & 1))) {
+            T* b = (T*)D.border + ((block0 + c0 / 2) * p.H + h) * DK * dv + lane;
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+#pragma unroll
+                for (int d = 0; d < DK / 16; ++d) *reinterpret_cast<typename V4<T>::t*>(b + 16 * d * dv + 16 * c) = pack4<T>(S[c][d]);
         }
         lds_barrier();
-        const float eC = sE;
+        ta.store(sA, rows, tid);
+        tb.store(sB, rows, tid);
+        const float gn = g;
+        const bool more = x + 1 < chunks;
+        if (more) {
+            ta.load(ap + (t0 + dir) * lda, lda, rows - dir, tid);
+            tb.load(bp + (t0 + dir) * ldb, ldb, rows - dir, tid);
+            if (w == 0 && x + 2 < chunks) g = load_gate(gp, p.g_stride, t0 + 2 * dir, rows - 2 * dir, l);
+        }
+        lds_barrier();
+        const Lane<T, DK> la(cl, qg);
+        const Lane<T, DV> lb(cl, qg);
+        if (w == 0 && more) gsum += put_gates(gates[(x + 1) & 1], gn, rows - dir, l, rev, p.scale);
+        const float eC = G.E;
 #pragma unroll
-        for (int d = 0; d < DK / 16; ++d) S[d] *= eC;
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int d = 0; d < DK / 16; ++d) S[c][d] *= eC;
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
-            const int r = 32 * kk + 8 * qg;
-            const f32x8 u = widen8(col_frag(sB, LB, r, r + 4, 16 * w, cl)) * lds8(sW + r);
+            const f32x8 wt = join(lds4(G.W + 32 * kk + 4 * qg), lds4(G.W + 32 * kk + 16 + 4 * qg));
+            Split<T> u[NC];
 #pragma unroll
-            for (int d = 0; d < DK / 16; ++d) S[d] = mma_f32x<true>(S[d], u, col_frag(sA, LA, r, r + 4, 16 * d, cl));
+            for (int c = 0; c < NC; ++c) u[c] = Split<T>(widen8(lb.col(sB, 2 * kk * 16 * DV * (int)sizeof(T), w * NC + c)) * wt);
+#pragma unroll
+            for (int d = 0; d < DK / 16; ++d) {
+                const frag a = la.col(sA, 2 * kk * 16 * DK * (int)sizeof(T), d);
+#pragma unroll
+                for (int c = 0; c < NC; ++c) S[c][d] = u[c].template mma<true>(S[c][d], a);
+            }
         }
     }
     if (D.last) {
-        float* s = D.last + ((int64_t)(p.seg_len ? slot : rg.n) * p.H + h) * DK * dv + col;
+        float* s = D.last + ((int64_t)(p.seg_len ? slot : rg.n) * p.H + h) * DK * dv + lane;
 #pragma unroll
-        for (int d = 0; d < DK / 16; ++d) *reinterpret_cast<f32x4*>(s + (int64_t)(16 * d + cl) * dv) = S[d];
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int d = 0; d < DK / 16; ++d) *reinterpret_cast<f32x4*>(s + 16 * d * dv + 16 * c) = S[c][d];
     }
     if (D.decay && slice == 0 && tid == 0) D.decay[slot * p.H + h] = fast_exp2((float)gsum);
 }
@@ -286,22 +352,32 @@ __global__ __launch_bounds__(kThreads) void linear_carry_kernel(LinearCarryParam
     if (D.last) *reinterpret_cast<f32x4*>(D.last + nh * p.elems + at) = cur;
 }
 
-static unsigned grid_of(int chains, int slices) { return (unsigned)((chains + 7) / 8 * 8 * slices); }
-
 template <typename T> static hipError_t out_t(const LinearParams& p, int dk, hipStream_t stream) {
-    const dim3 grid(grid_of(p.chains, p.dv / kSlice));
-    if (dk == 128) hipLaunchKernelGGL((linear_out_kernel<T, 128>), grid, dim3(kThreads), 0, stream, p);
-    else hipLaunchKernelGGL((linear_out_kernel<T, 64>), grid, dim3(kThreads), 0, stream, p);
+    const dim3 grid((unsigned)p.chains);
+    if (dk == 128) {
+        if (p.dv == 128) hipLaunchKernelGGL((linear_out_kernel<T, 128, 128>), grid, dim3(kThreads), 0, stream, p);
+        else hipLaunchKernelGGL((linear_out_kernel<T, 128, 64>), grid, dim3(kThreads), 0, stream, p);
+    } else {
+        if (p.dv == 128) hipLaunchKernelGGL((linear_out_kernel<T, 64, 128>), grid, dim3(kThreads), 0, stream, p);
+        else hipLaunchKernelGGL((linear_out_kernel<T, 64, 64>), grid, dim3(kThreads), 0, stream, p);
+    }
     return hipGetLastError();
 }
 hipError_t launch_linear_out(const LinearParams& p, int in_dtype, int dk, hipStream_t stream) {
     return in_dtype == 1 ? out_t<bf16>(p, dk, stream) : out_t<float>(p, dk, stream);
 }
 
+template <typename T, int DK> static void states_d(const LinearStateParams& p, int dirs, hipStream_t stream) {
+    // 128 columns a workgroup halve the reads of `a` from LDS; 64 are for launches that would
+    // leave compute units with less than two workgroups
+    const bool wide = p.dv == 128 && (int64_t)p.chains * dirs >= kWalkTarget;
+    const dim3 grid((unsigned)p.chains, dirs, p.dv / (wide ? 128 : 64));
+    if (wide) hipLaunchKernelGGL((linear_state_kernel<T, DK, 2>), grid, dim3(kThreads), 0, stream, p);
+    else hipLaunchKernelGGL((linear_state_kernel<T, DK, 1>), grid, dim3(kThreads), 0, stream, p);
+}
 template <typename T> static hipError_t states_t(const LinearStateParams& p, int dirs, int dk, hipStream_t stream) {
-    const dim3 grid(grid_of(p.chains, p.dv / kSlice), dirs);
-    if (dk == 128) hipLaunchKernelGGL((linear_state_kernel<T, 128>), grid, dim3(kThreads), 0, stream, p);
-    else hipLaunchKernelGGL((linear_state_kernel<T, 64>), grid, dim3(kThreads), 0, stream, p);
+    if (dk == 128) states_d<T, 128>(p, dirs, stream);
+    else states_d<T, 64>(p, dirs, stream);
     return hipGetLastError();
 }
 hipError_t launch_linear_states(const LinearStateParams& p, int dirs, int in_dtype, int dk, hipStream_t stream) {
