@@ -11,33 +11,37 @@ namespace kda {
 constexpr int kLinChunk = 64;     // tokens per step of the walks over a document
 constexpr int kLinBlock = 128;    // tokens per gradient workgroup; saved states sit at its borders
 constexpr int kWalkTarget = 512;  // workgroups a walk aims for: two a compute unit
+constexpr int kSegDocs = 512;     // more documents than this are not cut into segments
 constexpr int kGradThreads = 512; // 8 wave64: one 16-row block of a 128-token block each
 
 // g[token * g_stride + head]: g_stride = H for a gate per token, 0 for a gate per head.
+// seg_len: 0 for one walk per document, else tokens per segment (a multiple of kLinBlock).
+// chains: (document or segment slot, head) pairs.
 struct LinearParams {
     const void* q;         // [T,Hk,dk]
     const void* k;         // [T,Hk,dk]
     const void* v;         // [T,H,dv]
     const float* g;
     const int32_t* cu;     // device [N+1] or nullptr (equal documents of `seqlen`)
-    const float* s0;       // entering states: [N,H,dk,dv] per document, or per segment slot when seg_len > 0
+    const float* s0;       // [N,H,dk,dv] or nullptr (zero)
+    const float* seg_state; // [slots,H,dk,dv]: the states entering the segments after a document's first
     void* o;               // [T,H,dv] out dtype
     float* sfinal;         // [N,H,dk,dv] or nullptr
     int64_t T;
-    int32_t N, H, Hk, dv, seqlen, g_stride;
-    int32_t seg_len;       // 0: one walk per document; else tokens per segment (a multiple of kLinBlock)
-    int32_t out_bf16;
-    int32_t chains;        // (document or segment slot, head) pairs
+    int32_t N, H, Hk, dv, seqlen, g_stride, seg_len, out_bf16, chains;
     float scale;
 };
 
 // A walk that only carries the state, forward (a = k, b = v) or in reverse (a = q, b = dO).
+// With `decay` it starts from zero and leaves the segment's own sum in `seg`; without, it
+// starts from s0 or the carried `seg`.
 struct LinearStateDir {
     const void* a;         // [T,Hk,dk]
     const void* b;         // [T,H,dv]
-    const float* s0;       // entering states, as in LinearParams, or nullptr (zero)
-    float* last;           // state after the walk: [N,H,dk,dv], or per slot with `decay`; or nullptr
+    const float* s0;       // [N,H,dk,dv] or nullptr (zero)
+    float* seg;            // [slots,H,dk,dv]
     float* decay;          // [slots,H] e^{sum of g} of the segment, or nullptr
+    float* last;           // [N,H,dk,dv] or nullptr: the state after the document
     void* border;          // state before every 128-token block (input type) [blocks,H,dk,dv], or nullptr
     int32_t rev;
 };
@@ -46,23 +50,22 @@ struct LinearStateParams {
     const float* g;
     const int32_t* cu;
     int64_t T;
-    int32_t N, H, Hk, dv, seqlen, g_stride, seg_len, chains;
+    int32_t N, H, Hk, dv, seqlen, g_stride, seg_len, chains, dirs;
     float scale;
 };
 
-// The states entering every segment, from the segments' own sums: state (in place) [slots,H,dk,dv].
+// From the segments' own sums to the states entering them, in place.
 struct LinearCarryDir {
     const float* s0;       // [N,H,dk,dv] or nullptr
-    float* state;
+    float* seg;            // [slots,H,dk,dv]
     const float* decay;    // [slots,H]
-    float* last;           // [N,H,dk,dv] or nullptr
     int32_t rev;
 };
 struct LinearCarryParams {
     LinearCarryDir dir[2];
     const int32_t* cu;
     int64_t T;
-    int32_t N, H, seqlen, seg_len, elems;   // elems = dk * dv
+    int32_t N, H, seqlen, seg_len, elems, slots;   // elems = dk * dv; slots: room for segments
 };
 
 struct LinearBwdParams {
@@ -100,11 +103,11 @@ struct LinearDecodeParams {
     float scale;
 };
 
-// slots of a stream cut into pieces of `piece` tokens per document (see slot_owner)
+// At most so many pieces of `piece` tokens in the documents of a stream.
 inline int64_t linear_slots(int64_t T, int32_t N, int32_t piece) { return T / piece + N; }
 
 hipError_t launch_linear_out(const LinearParams& p, int in_dtype, int dk, hipStream_t stream);
-hipError_t launch_linear_states(const LinearStateParams& p, int dirs, int in_dtype, int dk, hipStream_t stream);
+hipError_t launch_linear_states(const LinearStateParams& p, int in_dtype, int dk, hipStream_t stream);
 hipError_t launch_linear_carry(const LinearCarryParams& p, int dirs, hipStream_t stream);
 hipError_t launch_linear_grads(const LinearBwdParams& p, int in_dtype, int dk, hipStream_t stream);
 hipError_t launch_linear_decode(const LinearDecodeParams& p, int in_dtype, int dk, hipStream_t stream);

@@ -57,10 +57,14 @@ bool grid_fits(int64_t workgroups, int threads) {
 }
 
 // ---------------------------------------------------------------- plans
-// A walk goes over a whole document; few documents and heads leave compute units idle.  Then
-// documents are cut into segments: the segments' own sums, the states entering them, the
-// walks from those.  The plan depends on the config and the sizes alone, so that the
-// workspace size is a host function.
+// A walk goes over a whole document; few documents and heads, or one document much longer than
+// the others, leave compute units idle.  Then documents are cut into segments of the tokens
+// that would give kWalkTarget workgroups equal shares: the segments' own sums, the states
+// entering them, the walks from those.  Documents that fit one segment take no part in the
+// first two.  The plan depends on the config and the sizes alone, so that the workspace size
+// is a host function; cu_seqlens is on the device, so any document may have all the tokens.
+// More than kSegDocs documents even out by their number (and finding a segment would take a
+// workgroup longer).
 constexpr int64_t kMinSegment = 512;     // tokens: below, a segment's state outweighs its rows
 
 struct Plan {
@@ -70,12 +74,10 @@ struct Plan {
 // ways: workgroups that share a chain (directions, slices of the value columns)
 Plan walk_plan(const kda_linear_config* c, int64_t T, int32_t N, int ways) {
     Plan p = {0, (int64_t)N * c->H};
-    const int64_t wgs = p.chains * ways;
-    const int64_t per_doc = (kWalkTarget + wgs - 1) / wgs, avg = T / N;
-    if (per_doc < 2 || avg < 2 * kMinSegment) return p;
-    int64_t L = (avg + per_doc - 1) / per_doc;
-    L = (L + kLinBlock - 1) / kLinBlock * kLinBlock;
+    const int64_t share = T * c->H / kWalkTarget * ways;
+    int64_t L = (share + kLinBlock - 1) / kLinBlock * kLinBlock;
     if (L < kMinSegment) L = kMinSegment;
+    if (T <= L || N > kSegDocs) return p;
     p.seg_len = (int32_t)L;
     p.chains = linear_slots(T, N, p.seg_len) * c->H;
     return p;
@@ -137,7 +139,7 @@ kda_status check_sizes(const kda_linear_config* c, int64_t T, int32_t N, const i
     // the kernels address a block's rows with 32-bit byte offsets from a 64-bit base
     if ((int64_t)kLinBlock * c->H * 128 * 4 >= ((int64_t)1 << 31)) return fail(KDA_ERR_UNSUPPORTED, "H too large%s");
     // the largest launches: the walks' chains, the a block's gradients in at most three roles a head, the carry
-    if (!grid_fits((linear_slots(T, N, kLinBlock) + 8) * 3 * (int64_t)c->H, kGradThreads) ||
+    if (!grid_fits((linear_slots(T, N, kLinBlock) + 8) * 4 * (int64_t)c->H, kGradThreads) ||
         !grid_fits((int64_t)N * c->H * (c->dk * c->dv / (4 * kThreads)), kThreads))
         return fail(KDA_ERR_UNSUPPORTED, "num_seqs, H or total_tokens too large for one launch%s");
     return KDA_OK;
@@ -229,16 +231,16 @@ kda_status kda_linear_fwd(const kda_linear_config* cfg, int64_t T, int32_t N, co
         float* decay = (float*)((char*)workspace + f.decay);
         LinearStateParams s;
         memset(&s, 0, sizeof s);
-        s.dir[0].a = k; s.dir[0].b = v; s.dir[0].last = state; s.dir[0].decay = decay;
+        s.dir[0].a = k; s.dir[0].b = v; s.dir[0].seg = state; s.dir[0].decay = decay;
         s.g = g; s.cu = cu; s.T = T; s.N = N; s.H = p.H; s.Hk = p.Hk; s.dv = p.dv; s.seqlen = p.seqlen;
-        s.g_stride = p.g_stride; s.seg_len = p.seg_len; s.chains = p.chains; s.scale = p.scale;
-        KDA_TRY(launched(launch_linear_states(s, 1, cfg->in_dtype, cfg->dk, st)));
+        s.g_stride = p.g_stride; s.seg_len = p.seg_len; s.chains = p.chains; s.dirs = 1; s.scale = p.scale;
+        KDA_TRY(launched(launch_linear_states(s, cfg->in_dtype, cfg->dk, st)));
         LinearCarryParams c;
         memset(&c, 0, sizeof c);
-        c.dir[0].s0 = s0; c.dir[0].state = state; c.dir[0].decay = decay; c.dir[0].last = sfinal;
-        c.cu = cu; c.T = T; c.N = N; c.H = p.H; c.seqlen = p.seqlen; c.seg_len = p.seg_len; c.elems = cfg->dk * cfg->dv;
+        c.dir[0].s0 = s0; c.dir[0].seg = state; c.dir[0].decay = decay;
+        c.cu = cu; c.T = T; c.N = N; c.H = p.H; c.seqlen = p.seqlen; c.seg_len = p.seg_len; c.elems = cfg->dk * cfg->dv; c.slots = (int32_t)linear_slots(T, N, p.seg_len);
         KDA_TRY(launched(launch_linear_carry(c, 1, st)));
-        p.s0 = state;
+        p.seg_state = state;
     }
     return launched(launch_linear_out(p, cfg->in_dtype, cfg->dk, st));
 }
@@ -275,35 +277,30 @@ kda_status kda_linear_bwd(const kda_linear_config* cfg, int64_t T, int32_t N, co
     s.dir[0].a = k; s.dir[0].b = v;
     s.dir[1].a = q; s.dir[1].b = dO; s.dir[1].rev = 1;
     s.g = g; s.cu = cu; s.T = T; s.N = N; s.H = cfg->H; s.Hk = cfg->Hk; s.dv = cfg->dv; s.seqlen = seqlen;
-    s.g_stride = g_stride; s.seg_len = b.plan.seg_len; s.chains = (int32_t)b.plan.chains; s.scale = cfg->scale;
+    s.g_stride = g_stride; s.seg_len = b.plan.seg_len; s.chains = (int32_t)b.plan.chains; s.dirs = 2; s.scale = cfg->scale;
     const float* first[2] = {s0, dSf};
     float* last[2] = {nullptr, dS0};
     if (s.seg_len) {
         LinearCarryParams c;
         memset(&c, 0, sizeof c);
         for (int i = 0; i < 2; ++i) {
-            s.dir[i].last = (float*)(ws + b.seg[i]);
+            s.dir[i].seg = (float*)(ws + b.seg[i]);
             s.dir[i].decay = (float*)(ws + b.decay[i]);
-            c.dir[i].s0 = first[i]; c.dir[i].state = s.dir[i].last; c.dir[i].decay = s.dir[i].decay;
-            c.dir[i].last = last[i]; c.dir[i].rev = i;
+            c.dir[i].s0 = first[i]; c.dir[i].seg = s.dir[i].seg; c.dir[i].decay = s.dir[i].decay; c.dir[i].rev = i;
         }
         c.cu = cu; c.T = T; c.N = N; c.H = cfg->H; c.seqlen = seqlen; c.seg_len = s.seg_len; c.elems = cfg->dk * cfg->dv;
-        KDA_TRY(launched(launch_linear_states(s, 2, cfg->in_dtype, cfg->dk, st)));
+        c.slots = (int32_t)linear_slots(T, N, s.seg_len);
+        KDA_TRY(launched(launch_linear_states(s, cfg->in_dtype, cfg->dk, st)));
         KDA_TRY(launched(launch_linear_carry(c, 2, st)));
-        for (int i = 0; i < 2; ++i) {
-            s.dir[i].s0 = s.dir[i].last;
-            s.dir[i].last = nullptr;
-            s.dir[i].decay = nullptr;
-        }
-    } else {
-        for (int i = 0; i < 2; ++i) {
-            s.dir[i].s0 = first[i];
-            s.dir[i].last = last[i];
-        }
+    }
+    for (int i = 0; i < 2; ++i) {
+        s.dir[i].s0 = first[i];
+        s.dir[i].last = last[i];
+        s.dir[i].decay = nullptr;
     }
     s.dir[0].border = ws + b.S;
     s.dir[1].border = ws + b.dS;
-    KDA_TRY(launched(launch_linear_states(s, 2, cfg->in_dtype, cfg->dk, st)));
+    KDA_TRY(launched(launch_linear_states(s, cfg->in_dtype, cfg->dk, st)));
 
     LinearBwdParams p;
     memset(&p, 0, sizeof p);

@@ -18,12 +18,11 @@ __device__ __forceinline__ int opaque(int x) {
 
 __device__ __forceinline__ f32x4 zero4() { return f32x4{0.f, 0.f, 0.f, 0.f}; }
 
-// Token range of piece j of document n; pieces of `piece` tokens, piece = 0 for the whole
-// document.  Every bound is clamped to [0, T], so a malformed cu cannot address memory
+// Token range of a piece of a document.  Every bound is clamped to [0, T], so a malformed cu cannot address memory
 // outside the buffers.
 struct Range {
     int64_t lo, hi, start, end;   // the piece and its document
-    int n, j;
+    int n;
 };
 __device__ __forceinline__ void doc_bounds(const int32_t* cu, int seqlen, int64_t T, int n, int64_t& s, int64_t& e) {
     s = cu ? (int64_t)cu[n] : (int64_t)n * seqlen;
@@ -53,22 +52,72 @@ __device__ __forceinline__ int piece_owner(const int32_t* cu, int N, int seqlen,
 }
 __device__ __forceinline__ Range piece_range(const int32_t* cu, int N, int seqlen, int64_t T, int64_t slot, int piece) {
     Range r;
-    if (piece == 0) {
-        r.n = (int)slot;
-        r.j = 0;
-        doc_bounds(cu, seqlen, T, r.n, r.start, r.end);
-        r.lo = r.start;
-        r.hi = r.end;
-        return r;
-    }
     r.n = piece_owner(cu, N, seqlen, slot, piece);
     doc_bounds(cu, seqlen, T, r.n, r.start, r.end);
-    r.j = (int)(slot - r.start / piece - r.n);
-    if (r.j < 0) r.j = 0;
-    r.lo = r.start + (int64_t)r.j * piece;
+    int64_t j = slot - r.start / piece - r.n;
+    if (j < 0) j = 0;
+    r.lo = r.start + j * piece;
     r.hi = r.lo + piece;
     if (r.lo > r.end) r.lo = r.end;
     if (r.hi > r.end) r.hi = r.end;
+    return r;
+}
+
+// Segments of seg_len tokens are numbered through the documents without gaps (an empty
+// document has one), so that the workgroups of a walk that have nothing to do are the last
+// ones: spread among the others they would leave some compute units with all of the work.
+// Every lane takes part, 64 documents at a time (at most kSegDocs of them).
+__device__ __forceinline__ int wave_scan_int(int x) {
+    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);
+    return x;
+}
+__device__ __forceinline__ int doc_segments(const int32_t* cu, int seqlen, int64_t T, int n, int seg_len) {
+    int64_t s, e;
+    doc_bounds(cu, seqlen, T, n, s, e);
+    const int c = (int)((e - s + seg_len - 1) / seg_len);
+    return c > 1 ? c : 1;
+}
+// The number of segments before document n.
+__device__ __forceinline__ int segments_before(const int32_t* cu, int seqlen, int64_t T, int seg_len, int n) {
+    const int l = threadIdx.x & 63;
+    int before = 0;
+    for (int n0 = 0; n0 < n; n0 += 64)
+        before += __builtin_amdgcn_readlane(wave_scan_int(n0 + l < n ? doc_segments(cu, seqlen, T, n0 + l, seg_len) : 0), 63);
+    return before;
+}
+// Segment k, or document k as a whole with seg_len = 0; r.n = N where there is none.
+__device__ __forceinline__ Range seg_range(const int32_t* cu, int N, int seqlen, int64_t T, int64_t k, int seg_len) {
+    Range r;
+    int64_t j = 0;
+    r.n = (int)k;
+    if (seg_len) {
+        const int l = threadIdx.x & 63;
+        int64_t left = k;
+        r.n = N;
+        for (int n0 = 0; n0 < N; n0 += 64) {
+            const int c = n0 + l < N ? doc_segments(cu, seqlen, T, n0 + l, seg_len) : 0;
+            const int upto = wave_scan_int(c), all = __builtin_amdgcn_readlane(upto, 63);
+            if (left < all) {
+                const int at = __ffsll((long long)__ballot(upto > left)) - 1;
+                r.n = n0 + at;
+                j = left - (__builtin_amdgcn_readlane(upto, at) - __builtin_amdgcn_readlane(c, at));
+                break;
+            }
+            left -= all;
+        }
+        if (r.n == N) {
+            r.lo = r.hi = r.start = r.end = 0;
+            return r;
+        }
+    }
+    doc_bounds(cu, seqlen, T, r.n, r.start, r.end);
+    r.lo = seg_len ? r.start + j * seg_len : r.start;
+    r.hi = seg_len && r.lo + seg_len < r.end ? r.lo + seg_len : r.end;
     return r;
 }
 
@@ -201,7 +250,10 @@ __device__ __forceinline__ float keep(float x, bool on) {
     return __builtin_bit_cast(float, __builtin_bit_cast(int, x) & (on ? -1 : 0));
 }
 
-__device__ __forceinline__ f32x8 widen8(bf16x8 x) { return __builtin_convertvector(x, f32x8); }
+// From the bits (unpack4), so that the compiler does not rebuild values by conversions.
+__device__ __forceinline__ f32x8 widen8(bf16x8 x) {
+    return join(unpack4(__builtin_shufflevector(x, x, 0, 1, 2, 3)), unpack4(__builtin_shufflevector(x, x, 4, 5, 6, 7)));
+}
 __device__ __forceinline__ f32x8 widen8(f32x8 x) { return x; }
 
 // An fp32 fragment as a product operand.  bf16: three bf16 terms (24 bits), so that fp32
@@ -212,9 +264,9 @@ template <> struct Split<bf16> {
     __device__ __forceinline__ Split() {}
     __device__ __forceinline__ explicit Split(f32x8 x) {
         h[0] = __builtin_convertvector(x, bf16x8);
-        x -= __builtin_convertvector(h[0], f32x8);
+        x -= widen8(h[0]);
         h[1] = __builtin_convertvector(x, bf16x8);
-        x -= __builtin_convertvector(h[1], f32x8);
+        x -= widen8(h[1]);
         h[2] = __builtin_convertvector(x, bf16x8);
     }
     template <bool IS_A> __device__ __forceinline__ f32x4 mma(f32x4 c, bf16x8 b) const {

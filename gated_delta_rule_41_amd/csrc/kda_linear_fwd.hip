@@ -18,8 +18,9 @@
 // linear_state_kernel: the state alone, forward or in reverse (the same sum with q, dO and
 // weights e^{G_i}), for the segments of long documents and for the backward.
 //
-// linear_carry_kernel: the states entering the segments of each document, from the
-// segments' own sums (a scalar decay composes as plain products).
+// linear_carry_kernel: the states entering the segments of each document after the first, from
+// the segments' own sums (a scalar decay composes as plain products).  In place: a segment's
+// slot holds its own sum before and its entering state after.
 #include "kda_linear_device.h"
 
 namespace kda {
@@ -57,14 +58,16 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void linear_out_k
     const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, cl = l & 15, qg = l >> 4;
     const int64_t slot = blockIdx.x / p.H;
     const int h = blockIdx.x % p.H, hk = h / (p.H / p.Hk);
-    const Range rg = piece_range(p.cu, p.N, p.seqlen, p.T, slot, p.seg_len);
+    const Range rg = seg_range(p.cu, p.N, p.seqlen, p.T, slot, p.seg_len);
     const int col = 16 * NC * w;
-    if (p.seg_len && rg.lo >= rg.hi) return;
+    if (rg.n >= p.N) return;
 
     // the state: block d of group c holds rows 16d + 4qg + i, column col + 16c + cl
     f32x4 S[NC][DK / 16];
     {
-        const float* s0 = p.s0 ? p.s0 + ((int64_t)(p.seg_len ? slot : rg.n) * p.H + h) * DK * DV + col + cl : nullptr;
+        // a document's first segment starts from its own state, the others from the carried ones
+        const float* s0 = rg.lo > rg.start ? p.seg_state + (slot * p.H + h) * DK * DV + col + cl
+                          : p.s0 ? p.s0 + ((int64_t)rg.n * p.H + h) * DK * DV + col + cl : nullptr;
 #pragma unroll
         for (int c = 0; c < NC; ++c)
 #pragma unroll
@@ -212,7 +215,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void linear_out_k
             }
         }
     }
-    if (p.sfinal && !p.seg_len) {
+    if (p.sfinal && rg.hi == rg.end) {
         float* sf = p.sfinal + ((int64_t)rg.n * p.H + h) * DK * DV + col + cl;
 #pragma unroll
         for (int c = 0; c < NC; ++c)
@@ -232,21 +235,30 @@ __global__ __launch_bounds__(kThreads, 2) void linear_state_kernel(LinearStatePa
     __shared__ __align__(32) T sB[C * DV];
     __shared__ __align__(32) Gates gates[2];
 
-    const LinearStateDir D = p.dir[blockIdx.y];
+    // The ways of a chain (directions, slices) are eight workgroups apart, on one XCD, whose L2
+    // serves the rows that they share; chains without work come last.
+    const int ways = p.dirs * (p.dv / DV), way = (int)(blockIdx.x / 8 % ways);
+    const int chain = (int)(blockIdx.x / (8 * ways) * 8 + (blockIdx.x & 7));
+    if (chain >= p.chains) return;
+    const LinearStateDir D = p.dir[way % p.dirs];
     const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, cl = l & 15, qg = l >> 4;
-    const int64_t slot = blockIdx.x / p.H;
-    const int h = blockIdx.x % p.H, hk = h / (p.H / p.Hk);
-    const Range rg = piece_range(p.cu, p.N, p.seqlen, p.T, slot, p.seg_len);
-    if (p.seg_len && rg.lo >= rg.hi) return;
-    const int col = 16 * NC * w, dv = p.dv, slice = blockIdx.z * DV;
+    const int64_t slot = chain / p.H;
+    const int h = chain % p.H, hk = h / (p.H / p.Hk);
+    const Range rg = seg_range(p.cu, p.N, p.seqlen, p.T, slot, p.seg_len);
+    if (rg.n >= p.N) return;
     const bool rev = D.rev != 0;
+    const bool head = rev ? rg.hi == rg.end : rg.lo == rg.start, tail = rev ? rg.lo == rg.start : rg.hi == rg.end;
+    if (D.decay && tail) return;   // a segment's own sum is for the segments that follow it
+    const int col = 16 * NC * w, dv = p.dv, slice = way / p.dirs * DV;
 
     // transposed against linear_out_kernel, for 16-byte stores: block d of group c holds state
     // row 16d + cl, value columns col + 16c + 4qg + i
     f32x4 S[NC][DK / 16];
     const int lane = cl * dv + slice + col + 4 * qg;
     {
-        const float* s0 = D.s0 ? D.s0 + ((int64_t)(p.seg_len ? slot : rg.n) * p.H + h) * DK * dv + lane : nullptr;
+        const float* s0 = D.decay ? nullptr
+                          : !head ? D.seg + (slot * p.H + h) * DK * dv + lane
+                          : D.s0 ? D.s0 + ((int64_t)rg.n * p.H + h) * DK * dv + lane : nullptr;
 #pragma unroll
         for (int c = 0; c < NC; ++c)
 #pragma unroll
@@ -318,8 +330,9 @@ __global__ __launch_bounds__(kThreads, 2) void linear_state_kernel(LinearStatePa
             }
         }
     }
-    if (D.last) {
-        float* s = D.last + ((int64_t)(p.seg_len ? slot : rg.n) * p.H + h) * DK * dv + lane;
+    float* s = D.decay ? D.seg + (slot * p.H + h) * DK * dv + lane
+               : D.last && tail ? D.last + ((int64_t)rg.n * p.H + h) * DK * dv + lane : nullptr;
+    if (s) {
 #pragma unroll
         for (int c = 0; c < NC; ++c)
 #pragma unroll
@@ -328,28 +341,43 @@ __global__ __launch_bounds__(kThreads, 2) void linear_state_kernel(LinearStatePa
     if (D.decay && slice == 0 && tid == 0) D.decay[slot * p.H + h] = fast_exp2((float)gsum);
 }
 
+// V vectors of four elements per thread.
+template <int V>
 __global__ __launch_bounds__(kThreads) void linear_carry_kernel(LinearCarryParams p) {
     const LinearCarryDir D = p.dir[blockIdx.y];
-    const int parts = p.elems / (4 * kThreads);
+    const int parts = p.elems / (4 * V * kThreads);
     const int part = blockIdx.x % parts;
     const int64_t nh = blockIdx.x / parts;
     const int n = (int)(nh / p.H), h = (int)(nh % p.H);
     int64_t s, e;
     doc_bounds(p.cu, p.seqlen, p.T, n, s, e);
     const int segs = (int)((e - s + p.seg_len - 1) / p.seg_len);
-    const int64_t first = s / p.seg_len + n, at = (int64_t)part * 4 * kThreads + 4 * threadIdx.x;
-    const int64_t step = (int64_t)p.H * p.elems;
-    f32x4 cur = D.s0 ? *reinterpret_cast<const f32x4*>(D.s0 + nh * p.elems + at) : zero4();
-    float* st = D.state + (first * p.H + h) * (int64_t)p.elems + at;
-    const float* dc = D.decay + first * p.H + h;
-    for (int x = 0; x < segs; ++x) {
-        const int j = D.rev ? segs - 1 - x : x;
-        const f32x4 own = *reinterpret_cast<const f32x4*>(st + j * step);
-        const float a = dc[(int64_t)j * p.H];
-        *reinterpret_cast<f32x4*>(st + j * step) = cur;
-        cur = a * cur + own;
+    if (segs < 2) return;
+    const int64_t first = segments_before(p.cu, p.seqlen, p.T, p.seg_len, n), at = ((int64_t)part * V * kThreads + threadIdx.x) * 4;
+    if (first + segs > p.slots) return;   // a malformed cu_seqlens only
+    const int64_t step = D.rev ? -(int64_t)p.H * p.elems : (int64_t)p.H * p.elems;
+    const int64_t from = first + (D.rev ? segs - 1 : 0);
+    float* st = D.seg + (from * p.H + h) * (int64_t)p.elems + at;
+    const float* dc = D.decay + from * p.H + h;
+    f32x4 cur[V], own[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        cur[i] = D.s0 ? *reinterpret_cast<const f32x4*>(D.s0 + nh * p.elems + at + i * 4 * kThreads) : zero4();
+        own[i] = *reinterpret_cast<const f32x4*>(st + i * 4 * kThreads);
     }
-    if (D.last) *reinterpret_cast<f32x4*>(D.last + nh * p.elems + at) = cur;
+    for (int x = 1; x < segs; ++x) {
+        st += step;
+        const float a = *dc;
+        dc += D.rev ? -p.H : p.H;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            f32x4* at_i = reinterpret_cast<f32x4*>(st + i * 4 * kThreads);
+            const f32x4 next = x + 1 < segs ? *at_i : zero4();
+            cur[i] = a * cur[i] + own[i];
+            *at_i = cur[i];
+            own[i] = next;
+        }
+    }
 }
 
 template <typename T> static hipError_t out_t(const LinearParams& p, int dk, hipStream_t stream) {
@@ -367,26 +395,30 @@ hipError_t launch_linear_out(const LinearParams& p, int in_dtype, int dk, hipStr
     return in_dtype == 1 ? out_t<bf16>(p, dk, stream) : out_t<float>(p, dk, stream);
 }
 
-template <typename T, int DK> static void states_d(const LinearStateParams& p, int dirs, hipStream_t stream) {
-    // 128 columns a workgroup halve the reads of `a` from LDS; 64 are for launches that would
-    // leave compute units with less than two workgroups
-    const bool wide = p.dv == 128 && (int64_t)p.chains * dirs >= kWalkTarget;
-    const dim3 grid((unsigned)p.chains, dirs, p.dv / (wide ? 128 : 64));
+template <typename T, int DK> static void states_d(const LinearStateParams& p, hipStream_t stream) {
+    // 128 columns a workgroup halve the reads of `a` from LDS (own sums of 131072 tokens x 16
+    // heads 340 -> 274 us); 64 are for launches that would leave compute units with less than
+    // two workgroups (4 documents x 32 heads, both directions: 650 -> 432 us)
+    const int64_t walks = p.seg_len && p.T / p.seg_len > p.N ? p.T / p.seg_len : p.N;
+    const bool wide = p.dv == 128 && walks * p.H * p.dirs >= kWalkTarget;
+    const dim3 grid((unsigned)(((int64_t)p.chains + 7) / 8 * 8 * p.dirs * (p.dv / (wide ? 128 : 64))));
     if (wide) hipLaunchKernelGGL((linear_state_kernel<T, DK, 2>), grid, dim3(kThreads), 0, stream, p);
     else hipLaunchKernelGGL((linear_state_kernel<T, DK, 1>), grid, dim3(kThreads), 0, stream, p);
 }
-template <typename T> static hipError_t states_t(const LinearStateParams& p, int dirs, int dk, hipStream_t stream) {
-    if (dk == 128) states_d<T, 128>(p, dirs, stream);
-    else states_d<T, 64>(p, dirs, stream);
+template <typename T> static hipError_t states_t(const LinearStateParams& p, int dk, hipStream_t stream) {
+    if (dk == 128) states_d<T, 128>(p, stream);
+    else states_d<T, 64>(p, stream);
     return hipGetLastError();
 }
-hipError_t launch_linear_states(const LinearStateParams& p, int dirs, int in_dtype, int dk, hipStream_t stream) {
-    return in_dtype == 1 ? states_t<bf16>(p, dirs, dk, stream) : states_t<float>(p, dirs, dk, stream);
+hipError_t launch_linear_states(const LinearStateParams& p, int in_dtype, int dk, hipStream_t stream) {
+    return in_dtype == 1 ? states_t<bf16>(p, dk, stream) : states_t<float>(p, dk, stream);
 }
 
 hipError_t launch_linear_carry(const LinearCarryParams& p, int dirs, hipStream_t stream) {
-    const dim3 grid((unsigned)((int64_t)p.N * p.H * (p.elems / (4 * kThreads))), dirs);
-    hipLaunchKernelGGL(linear_carry_kernel, grid, dim3(kThreads), 0, stream, p);
+    // many documents: most workgroups have nothing to do, so there are fewer of them
+    const int64_t nh = (int64_t)p.N * p.H, units = nh * (p.elems / (4 * kThreads));
+    if (nh < 256) hipLaunchKernelGGL(linear_carry_kernel<1>, dim3((unsigned)units, dirs), dim3(kThreads), 0, stream, p);
+    else hipLaunchKernelGGL(linear_carry_kernel<4>, dim3((unsigned)(units / 4), dirs), dim3(kThreads), 0, stream, p);
     return hipGetLastError();
 }
 

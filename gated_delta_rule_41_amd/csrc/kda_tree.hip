@@ -70,8 +70,8 @@ template <typename T> __device__ __forceinline__ f32x4 mma_split(f32x4 c, f32x8 
     if constexpr (sizeof(T) == 4) return mma_k32(c, a, b);
     else {
         const bf16x8 ah = __builtin_convertvector(a, bf16x8), bh = __builtin_convertvector(b, bf16x8);
-        const bf16x8 al = __builtin_convertvector(a - __builtin_convertvector(ah, f32x8), bf16x8);
-        const bf16x8 bl = __builtin_convertvector(b - __builtin_convertvector(bh, f32x8), bf16x8);
+        const bf16x8 al = __builtin_convertvector(a - widen8(ah), bf16x8);
+        const bf16x8 bl = __builtin_convertvector(b - widen8(bh), bf16x8);
         c = mma_k32(c, al, bh);
         c = mma_k32(c, ah, bl);
         return mma_k32(c, ah, bh);

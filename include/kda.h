@@ -309,9 +309,9 @@ typedef struct kda_linear_config {
 void kda_linear_config_init(kda_linear_config* cfg, int32_t H, int32_t Hk, int32_t dk, int32_t dv);
 
 /* Scratch for one call, in bytes (pure host functions; 0 for an invalid
- * config).  The forward's is non-zero when it cuts long documents into
- * segments (few documents and heads for the GPU; a rule on cfg and the sizes
- * only): each segment's own sum of k v^T, then the states entering the
+ * config).  The forward's is non-zero when it cuts documents into segments
+ * (those longer than an equal share of total_tokens * H; a rule on cfg and the
+ * sizes only): each segment's own sum of k v^T, then the states entering the
  * segments.  The backward's holds S and dL/dS at every 128-token block (input
  * type), per-token sums for dg, and the segments' states likewise. */
 size_t kda_linear_fwd_workspace_size(const kda_linear_config* cfg, int64_t total_tokens, int32_t num_seqs);

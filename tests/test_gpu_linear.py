@@ -137,37 +137,26 @@ def test_backward(lens, H, Hk, dk, dv, dtype, gate):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-def test_segments(dtype):
-    """Documents long enough to be cut into segments, ragged against the segments' and blocks' borders."""
+@pytest.mark.parametrize("lens,H,Hk,dk,dv,gate", [
+    ([1500, 1730], 2, 1, 64, 64, "token"),
+    ([0, 3, 2600, 130, 0, 1024, 512, 513, 0], 1, 1, 64, 64, "head"),
+    ([1100, 64], 2, 2, 128, 128, "token"),
+    ([700], 3, 1, 64, 128, "token"),
+])
+def test_segments(dtype, lens, H, Hk, dk, dv, gate):
+    """Documents long enough to be cut into segments (512 tokens at these sizes), among short and empty ones."""
     need_gpu()
-    lens, H, Hk, dk, dv = [1500, 1, 1729, 0], 2, 1, 64, 64
     _say(f"segments {lens} {dtype}")
-    d, h, cu = make(3, lens, H, Hk, dk, dv, dtype, "token", -3.0)
+    d, h, cu = make(3, lens, H, Hk, dk, dv, dtype, gate, -3.0)
     cfg = kda.linear._lib.make_linear_config(H, Hk, dk, dv)
-    assert kda.linear._lib.kda_linear_fwd_workspace_size(cfg, sum(lens), 2) > 0
-    lens2 = [1500, 1730]
-    cu2 = torch.tensor([0, 1500, 3230], dtype=torch.int32, device="cuda")
+    assert kda.linear._lib.kda_linear_fwd_workspace_size(cfg, sum(lens), len(lens)) > 0
+    check_fwd(d, h, cu, lens, dtype, torch.float32, 0.125)
+    check_bwd(d, h, cu, lens, dtype, torch.float32, 0.125)
     for n in ("s0", "dS"):
-        d[n], h[n] = d[n][:2].contiguous(), h[n][:2]
-    check_fwd(d, h, cu2, lens2, dtype, torch.float32, 0.125)
-    check_bwd(d, h, cu2, lens2, dtype, torch.float32, 0.125)
-
-
-def test_segments_with_uneven_documents():
-    """One long document among short and empty ones, the average long enough for segments."""
-    need_gpu()
-    lens = [0, 3, 2600, 130, 0, 2500]
-    _say(f"uneven {lens}")
-    d, h, cu = make(4, lens, 1, 1, 64, 64, "f32", "head")
-    # the plan goes by the average length: 6 documents need more tokens than this, 4 do not
-    cfg = kda.linear._lib.make_linear_config(1, 1, 64, 64)
-    lens4, keep = [3, 2600, 130, 2500], [1, 2, 3, 5]
-    assert kda.linear._lib.kda_linear_fwd_workspace_size(cfg, sum(lens4), 4) > 0
-    cu4 = torch.tensor(np.concatenate([[0], np.cumsum(lens4)]), dtype=torch.int32, device="cuda")
-    for n in ("s0", "dS"):
-        d[n], h[n] = d[n][keep].contiguous(), h[n][keep]
-    check_fwd(d, h, cu4, lens4, "f32", torch.float32, 0.125)
-    check_bwd(d, h, cu4, lens4, "f32", torch.float32, 0.125)
+        d[n] = h[n] = None
+    h["s0"] = h["dS"] = np.zeros((len(lens), H, dk, dv))
+    check_fwd(d, h, cu, lens, dtype, torch.float32, 0.125)
+    check_bwd(d, h, cu, lens, dtype, torch.float32, 0.125)
 
 
 def test_strong_and_infinite_gates():
