@@ -354,7 +354,7 @@ void kda_tree_config_init(kda_tree_config* cfg, int32_t rule, int32_t H, int32_t
 kda_status kda_tree(const kda_tree_config* cfg, int32_t N, const void* q, const void* k, const void* v, const void* g,
                     const void* beta, const int32_t* parent, const float* state, void* o, void* stream) {
     error_text()[0] = 0;
-    KDA_TRY(check_tree(cfg, N, 1024, 1));
+    KDA_TRY(check_tree(cfg, N, 512, 1));
     const bool delta = cfg->rule == KDA_RULE_DELTA;
     KDA_TRY(ptr(q, "q", N > 0));
     KDA_TRY(ptr(k, "k", N > 0));

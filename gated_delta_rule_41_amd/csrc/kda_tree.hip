@@ -10,10 +10,12 @@
 // between a node and an ancestor is the product of the factors e^g passed on the way up
 // (each at most 1, so any g <= 0 works), and only true ancestor pairs are visited.
 //
-// kda_tree_kernel: one workgroup per (sequence, head).  The state's loads are issued first
-// and are in flight while 16 lanes per node climb its path (A matrices, e^{G_i}); then one
-// matrix product of all rows with the state, then the triangular solve level by level of the
-// tree (nodes of one depth are independent), then the outputs.
+// kda_tree_kernel: one workgroup per (sequence, head), every load issued first.  16 lanes per
+// node climb its path (A matrices, e^{G_i}) while the state arrives; one matrix product of all
+// rows with the state, transposed, so that a wave keeps its 16 value columns of every node;
+// the triangular solve level by level of the tree (nodes of one depth are independent); then
+// each lane reads its own nodes' paths for the outputs.  Sums run over true ancestors only, so
+// nothing in another branch, NaN included, reaches a node.
 //
 // kda_tree_commit_kernel: the recurrence along the accepted path with the state in registers,
 // read and written once (kda_decode's layout).
@@ -45,6 +47,11 @@ __device__ __forceinline__ void climb(const int* par, int i, int L, u64& anc, in
     }
 }
 
+// A value that every lane holds, in scalar registers.
+__device__ __forceinline__ u64 uniform(u64 x) {
+    return (u64)(unsigned)__builtin_amdgcn_readfirstlane((int)x) | (u64)(unsigned)__builtin_amdgcn_readfirstlane((int)(x >> 32)) << 32;
+}
+
 __device__ __forceinline__ float sigmoidf(float b) { return 1.f / (1.f + __expf(-b)); }
 
 // Eight elements of a global row as fp32.
@@ -59,222 +66,311 @@ __device__ __forceinline__ float dot8(f32x8 a, f32x8 b) {
 }
 __device__ __forceinline__ f32x8 splat8(float x) { return f32x8{x, x, x, x, x, x, x, x}; }
 
-// Eight elements of an LDS row (16-byte aligned).
-__device__ __forceinline__ f32x8 row8(const float* p) {
-    return __builtin_shufflevector(*reinterpret_cast<const f32x4*>(p), *reinterpret_cast<const f32x4*>(p + 4), 0, 1, 2, 3, 4, 5, 6, 7);
+// An fp32 operand with fp32 accuracy in a product with another: bf16 inputs take two bf16 terms
+// each and three products (the fourth is below 2^-16 of the result), fp32 inputs the fp32 unit.
+template <typename T> struct Two;
+template <> struct Two<bf16> {
+    static constexpr int PLANES = 2;
+    bf16x8 h, l;
+    __device__ __forceinline__ void set(f32x8 x) {
+        h = __builtin_convertvector(x, bf16x8);
+        l = __builtin_convertvector(x - widen8(h), bf16x8);
+    }
+    template <int COLS> __device__ __forceinline__ void get(const Lane<bf16, COLS>& at, const bf16* t, int plane, int off, int y) {
+        h = at.row(t, off, y);
+        l = at.row(t + plane, off, y);
+    }
+};
+template <> struct Two<float> {
+    static constexpr int PLANES = 1;
+    f32x8 h;
+    __device__ __forceinline__ void set(f32x8 x) { h = x; }
+    template <int COLS> __device__ __forceinline__ void get(const Lane<float, COLS>& at, const float* t, int, int off, int y) { h = at.row(t, off, y); }
+};
+__device__ __forceinline__ f32x4 mma_two(f32x4 c, const Two<bf16>& a, const Two<bf16>& b) {
+    c = mma_k32(c, a.l, b.h);
+    c = mma_k32(c, a.h, b.l);
+    return mma_k32(c, a.h, b.h);
 }
+__device__ __forceinline__ f32x4 mma_two(f32x4 c, const Two<float>& a, const Two<float>& b) { return mma_k32(c, a.h, b.h); }
 
-// a * b in fp32 accuracy for bf16 inputs: both fp32 operands as two bf16 terms, three
-// products (the fourth is below 2^-16 of the result); fp32 inputs take the fp32 unit.
-template <typename T> __device__ __forceinline__ f32x4 mma_split(f32x4 c, f32x8 a, f32x8 b) {
-    if constexpr (sizeof(T) == 4) return mma_k32(c, a, b);
-    else {
-        const bf16x8 ah = __builtin_convertvector(a, bf16x8), bh = __builtin_convertvector(b, bf16x8);
-        const bf16x8 al = __builtin_convertvector(a - widen8(ah), bf16x8);
-        const bf16x8 bl = __builtin_convertvector(b - widen8(bh), bf16x8);
-        c = mma_k32(c, al, bh);
-        c = mma_k32(c, ah, bl);
-        return mma_k32(c, ah, bh);
+// A lane's E channels (8 or 4, at E cl) of a row in LDS.
+template <typename T, int E> __device__ __forceinline__ f32x8 get_row(const T* row, int cl) {
+    if constexpr (E == 4) {
+        const f32x4 x = unpack4(lds4(row + 4 * cl));
+        return f32x8{x[0], x[1], x[2], x[3], 0.f, 0.f, 0.f, 0.f};
+    } else if constexpr (sizeof(T) == 2) {
+        return widen8(*reinterpret_cast<const bf16x8*>(row + 8 * cl));
+    } else {   // fp32: the halves of all lanes apart, 16 bytes a lane each, for conflict-free reads
+        return join(lds4(row + 4 * cl), lds4(row + 64 + 4 * cl));
     }
 }
+template <int E> __device__ __forceinline__ void put_row(float* row, int cl, f32x8 x) {
+    *reinterpret_cast<f32x4*>(row + 4 * cl) = __builtin_shufflevector(x, x, 0, 1, 2, 3);
+    if constexpr (E == 8) *reinterpret_cast<f32x4*>(row + 64 + 4 * cl) = __builtin_shufflevector(x, x, 4, 5, 6, 7);
+}
+template <int E> __device__ __forceinline__ void put_row(bf16* row, int cl, f32x8 x) {   // exact: the values were bf16
+    const bf16x8 y = __builtin_convertvector(x, bf16x8);
+    if constexpr (E == 8) *reinterpret_cast<bf16x8*>(row + 8 * cl) = y;
+    else *reinterpret_cast<bf16x4*>(row + 4 * cl) = __builtin_shufflevector(y, y, 0, 1, 2, 3);
+}
+// The same channels of an operand tile (Swz), in planes.
+template <int E, int DK> __device__ __forceinline__ void put_planes(float* t, int, int row, int cl, f32x8 x) {
+    typedef Swz<float, DK> Z;
+    const f32x4 lo = __builtin_shufflevector(x, x, 0, 1, 2, 3), hi = __builtin_shufflevector(x, x, 4, 5, 6, 7);
+    *reinterpret_cast<f32x4*>(t + Z::at(row, E == 8 ? 2 * cl : cl)) = lo;
+    if constexpr (E == 8) *reinterpret_cast<f32x4*>(t + Z::at(row, 2 * cl + 1)) = hi;
+}
+template <int E, int DK> __device__ __forceinline__ void put_planes(bf16* t, int plane, int row, int cl, f32x8 x) {
+    typedef Swz<bf16, DK> Z;
+    Two<bf16> y;
+    y.set(x);
+    if constexpr (E == 8) {
+        *reinterpret_cast<bf16x8*>(t + Z::at(row, cl)) = y.h;
+        *reinterpret_cast<bf16x8*>(t + plane + Z::at(row, cl)) = y.l;
+    } else {
+        const int o = Z::at(row, cl >> 1) + 4 * (cl & 1);
+        *reinterpret_cast<bf16x4*>(t + o) = __builtin_shufflevector(y.h, y.h, 0, 1, 2, 3);
+        *reinterpret_cast<bf16x4*>(t + plane + o) = __builtin_shufflevector(y.l, y.l, 0, 1, 2, 3);
+    }
+}
+
+// LDS of a tree of up to NL nodes.  The first part is, one after the other: the keys and e^g
+// (climb), the rows that meet the state, u.
+template <typename T, bool DELTA, int NL, int DK, int DV> struct TreeShared {
+    static constexpr int LU = DV + 4, PLANE = NL * DK;
+    struct Climb {
+        T k[NL * DK];
+        float a[DELTA ? NL * DK : NL];
+    };
+    union {
+        __align__(32) char bytes[1];
+        Climb c;
+        T rows[Two<T>::PLANES * PLANE];
+        float u[NL * LU];
+    } x;
+    // node i's products with its path: entry i (i + 1) / 2 + d for the node d steps up
+    float kk[DELTA ? NL * (NL + 1) / 2 : 1], qk[NL * (NL + 1) / 2];
+    float beta[NL], norm[NL];
+    int par[64], depth[64], levels;
+    u64 anc[64], level[64];
+};
 
 // NL: the tree's size rounded up to 16, 32 or 64 nodes.
 template <typename T, bool DELTA, int NL, int DK, int DV>
-__global__ __launch_bounds__(NL * 16) void kda_tree_kernel(TreeParams p) {
-    constexpr int THREADS = NL * 16, WAVES = THREADS / 64, LK = DK + 4, LU = DV + 4, E = DK / 16, CG = DV / 16;
-    constexpr int ROWS = NL * (LK > LU ? LK : LU);
-    __shared__ __align__(32) float sK[ROWS];   // kh, then kh e^G, then u
-    __shared__ __align__(32) float sQ[ROWS];   // qh e^G, then S^T (qh e^G)
-    __shared__ __align__(32) float sA[DELTA ? NL * LK : NL];   // e^g
-    __shared__ float sKK[DELTA ? NL * (NL + 1) : 1], sQK[NL * (NL + 1)];
-    __shared__ float sB[NL];
-    __shared__ int sPar[64], sDepth[64];
-    __shared__ u64 sAnc[64], sLevel[64];
-    __shared__ int sLevels;
+__global__ __launch_bounds__(NL == 16 ? 256 : 512, sizeof(T) == 2 ? 4 : 2) void kda_tree_kernel(TreeParams p) {
+    constexpr int THREADS = NL == 16 ? 256 : 512, WAVES = THREADS / 64, E = DK / 16, CG = DV / 16, MT = NL / 16;
+    constexpr int NODES = THREADS / 16, ROUNDS = NL / NODES;   // nodes that climb at once
+    // column groups: COLS a wave, or shared by STEP waves that take every STEP-th tile of nodes
+    constexpr int STEP = WAVES > CG ? WAVES / CG : 1, COLS = WAVES < CG ? CG / WAVES : 1;
+    typedef TreeShared<T, DELTA, NL, DK, DV> Shared;
+    __shared__ __align__(32) Shared s;
 
     const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, cl = l & 15, qg = l >> 4;
     const int64_t nh = blockIdx.x, n = nh / p.H;
-    const int h = (int)(nh % p.H), hk = h / (p.H / p.Hk), L = p.L, dv = DV;
+    const int h = (int)(nh % p.H), hk = h / (p.H / p.Hk), L = p.L;
     const int64_t node0 = n * L;
 
-    // the state as product fragments: column 16 cg + cl, rows 32 s + 8 qg + j.  Waves share the
-    // columns' groups; the waves beyond the first CG of them take every STEP-th row tile.
-    constexpr int STEP = WAVES > CG ? WAVES / CG : 1, COLS = WAVES < CG ? CG / WAVES : 1;
-    f32x8 sf[COLS][DK / 32];
+    if (tid < 64) s.par[tid] = tid < L ? p.parent[node0 + tid] : -2;
+    f32x8 kv[ROUNDS], qv[ROUNDS], av[ROUNDS];
+    float bt[ROUNDS];
 #pragma unroll
-    for (int c = 0; c < COLS; ++c) {
-        const float* s = p.s_in + nh * DK * dv + 16 * (w % CG + c * WAVES) + cl;
-#pragma unroll
-        for (int x = 0; x < DK / 32; ++x)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) sf[c][x][j] = p.s_in ? s[(int64_t)(32 * x + 8 * qg + j) * dv] : 0.f;
-    }
-    if (tid < 64) sPar[tid] = tid < L ? p.parent[node0 + tid] : -2;
-
-    // 16 lanes per node, E channels each
-    const int i = tid >> 4;
-    f32x8 kv = splat8(0.f), qv = splat8(0.f), av = splat8(1.f);
-    const bool in = i < L;
-    const int64_t at = node0 + (in ? i : 0);
-    float bt = 0.f;
-    {
+    for (int r = 0; r < ROUNDS; ++r) {
+        const int i = (tid >> 4) + r * NODES;
+        const int64_t at = node0 + (i < L ? i : 0);
         const T* kp = (const T*)p.k + (at * p.Hk + hk) * DK + E * cl;
         const T* qp = (const T*)p.q + (at * p.Hk + hk) * DK + E * cl;
         if constexpr (E == 8) {
-            kv = load8f(kp);
-            qv = load8f(qp);
+            kv[r] = load8f(kp);
+            qv[r] = load8f(qp);
         } else {
-            const f32x4 a = unpack4(*reinterpret_cast<const typename V4<T>::t*>(kp));
-            const f32x4 b = unpack4(*reinterpret_cast<const typename V4<T>::t*>(qp));
-#pragma unroll
-            for (int j = 0; j < 4; ++j) { kv[j] = a[j]; qv[j] = b[j]; }
+            const f32x4 a = unpack4(*reinterpret_cast<const typename V4<T>::t*>(kp)), b = unpack4(*reinterpret_cast<const typename V4<T>::t*>(qp));
+            kv[r] = f32x8{a[0], a[1], a[2], a[3], 0.f, 0.f, 0.f, 0.f};
+            qv[r] = f32x8{b[0], b[1], b[2], b[3], 0.f, 0.f, 0.f, 0.f};
         }
+        bt[r] = 0.f;
         if constexpr (DELTA) {
             const T* gp = (const T*)p.g + (at * p.H + h) * DK + E * cl;
-#pragma unroll
-            for (int j = 0; j < E; ++j) av[j] = fast_exp2((float)gate_log2(to_f32(gp[j])));
-            bt = sigmoidf(to_f32(((const T*)p.beta)[at * p.H + h]));
-            const float nk = row16_sum(dot8(kv, kv)), nq = row16_sum(dot8(qv, qv));
-            kv *= splat8(1.f / sqrtf(nk + p.eps));
-            qv *= splat8(p.scale / sqrtf(nq + p.eps));
+            f32x8 g = splat8(0.f);
+            if constexpr (E == 8) g = load8f(gp);
+            else {
+                const f32x4 a = unpack4(*reinterpret_cast<const typename V4<T>::t*>(gp));
+                g = f32x8{a[0], a[1], a[2], a[3], 0.f, 0.f, 0.f, 0.f};
+            }
+            av[r] = g;
+            bt[r] = to_f32(((const T*)p.beta)[at * p.H + h]);
         } else {
-            const float g = ((const float*)p.g)[p.gate_head ? h : at * p.H + h];
-            av = splat8(fast_exp2((float)gate_log2(g)));
-            qv *= splat8(p.scale);
+            av[r] = splat8(((const float*)p.g)[p.gate_head ? h : at * p.H + h]);
         }
-        if (!in) { kv = splat8(0.f); qv = splat8(0.f); }
     }
+    // the state as product fragments: value column 16 cg + cl, rows 32 y + 8 qg + j
+    Two<T> st[COLS][DK / 32];
+    {
+        f32x8 x[COLS][DK / 32];
 #pragma unroll
-    for (int j = 0; j < E; ++j) {
-        sK[i * LK + E * cl + j] = kv[j];
-        if constexpr (DELTA) sA[i * LK + E * cl + j] = av[j];
-    }
-    if (cl == 0) {
-        if constexpr (!DELTA) sA[i] = av[0];
-        sB[i] = bt;
-    }
-    __syncthreads();
-    if (w == 0) {
-        u64 anc;
-        int depth;
-        climb(sPar, l, L, anc, depth);
-        sAnc[l] = anc;
-        sDepth[l] = depth;
-        int levels = 0;
-        for (; levels < 64; ++levels) {
-            const u64 m = __ballot(depth == levels);
-            if (!m) break;
-            if (l == 0) sLevel[levels] = m;
+        for (int c = 0; c < COLS; ++c) {
+            const float* sp = p.s_in + nh * DK * DV + 16 * (w % CG + c * WAVES) + cl;
+#pragma unroll
+            for (int y = 0; y < DK / 32; ++y)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[c][y][j] = p.s_in ? sp[(32 * y + 8 * qg + j) * DV] : 0.f;
         }
-        if (l == 0) sLevels = levels;
-    }
-    __syncthreads();
-
-    // climb: A rows of node i and e^{G_i}; av becomes the product of the factors passed
-    const bool live = sDepth[i] >= 0;
-    if (live) {
-        const float self = row16_sum(dot8(qv, kv));
-        if (cl == 0) sQK[i * (NL + 1) + i] = self;
-        for (int a = sPar[i]; a >= 0; a = sPar[a]) {
-            f32x8 ka = splat8(0.f), aa = splat8(1.f);
+        // norms, gates and the keys' rows meanwhile
 #pragma unroll
-            for (int j = 0; j < E; ++j) ka[j] = sK[a * LK + E * cl + j];
+        for (int r = 0; r < ROUNDS; ++r) {
+            const int i = (tid >> 4) + r * NODES;
+            put_row<E>(s.x.c.k + i * DK, cl, kv[r]);
             if constexpr (DELTA) {
+                const float rk = 1.f / sqrtf(row16_sum(dot8(kv[r], kv[r])) + p.eps);
+                const float rq = p.scale / sqrtf(row16_sum(dot8(qv[r], qv[r])) + p.eps);
+                kv[r] *= splat8(rk);
+                qv[r] *= splat8(rq);
 #pragma unroll
-                for (int j = 0; j < E; ++j) aa[j] = sA[a * LK + E * cl + j];
+                for (int j = 0; j < E; ++j) av[r][j] = fast_exp2((float)gate_log2(av[r][j]));
+                put_row<E>(s.x.c.a + i * DK, cl, av[r]);
+                if (cl == 0) {
+                    s.norm[i] = rk;
+                    s.beta[i] = sigmoidf(bt[r]);
+                }
             } else {
-                aa = splat8(sA[a]);
+                qv[r] *= splat8(p.scale);
+                av[r] = splat8(fast_exp2((float)gate_log2(av[r][0])));
+                if (cl == 0) s.x.c.a[i] = av[r][0];
             }
-            const f32x8 ke = ka * av;
-            const float qk = row16_sum(dot8(qv, ke));
-            if (cl == 0) sQK[i * (NL + 1) + a] = qk;
-            if constexpr (DELTA) {
-                const float kk = row16_sum(dot8(kv, ke));
-                if (cl == 0) sKK[i * (NL + 1) + a] = kk;
-            }
-            av *= aa;
         }
-    }
-    __syncthreads();   // every climb has read its kh
+        __syncthreads();
+        if (w == 0) {
+            u64 anc;
+            int depth;
+            climb(s.par, l, L, anc, depth);
+            s.anc[l] = anc;
+            s.depth[l] = depth;
+            int levels = 0;
+            for (; levels < 64; ++levels) {
+                const u64 m = __ballot(depth == levels);
+                if (!m) break;
+                if (l == 0) s.level[levels] = m;
+            }
+            if (l == 0) s.levels = levels;
+        }
+        __syncthreads();
+        // climb: node i's products with its path, and the product of the factors passed
 #pragma unroll
-    for (int j = 0; j < E; ++j) {
-        if constexpr (DELTA) sK[i * LK + E * cl + j] = kv[j] * av[j];
-        sQ[i * LK + E * cl + j] = qv[j] * av[j];
+        for (int r = 0; r < ROUNDS; ++r) {
+            const int i = (tid >> 4) + r * NODES;
+            if (s.depth[i] >= 0) {
+                const int t0 = i * (i + 1) / 2;
+                const float self = row16_sum(dot8(qv[r], kv[r]));
+                if (cl == 0) s.qk[t0] = self;
+                int d = t0;
+                for (int a = s.par[i]; a >= 0; a = s.par[a]) {
+                    f32x8 ke = get_row<T, E>(s.x.c.k + a * DK, cl) * av[r];
+                    if constexpr (DELTA) {
+                        ke *= splat8(s.norm[a]);
+                        av[r] *= get_row<float, E>(s.x.c.a + a * DK, cl);
+                    } else {
+                        av[r] *= splat8(s.x.c.a[a]);
+                    }
+                    ++d;
+                    const float qk = row16_sum(dot8(qv[r], ke));
+                    if constexpr (DELTA) {
+                        const float kk = row16_sum(dot8(kv[r], ke));
+                        if (cl == 0) s.kk[d] = kk;
+                    }
+                    if (cl == 0) s.qk[d] = qk;
+                }
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < COLS; ++c)
+#pragma unroll
+            for (int y = 0; y < DK / 32; ++y) st[c][y].set(x[c][y]);
     }
-    __syncthreads();
 
-    // rows times the state; accumulators: row = node 16 m + 4 qg + i, column = value column
-    constexpr int MT = NL / 16;
+    // rows times the state; row = value column 16 cg + 4 qg + i, column = node 16 m + cl
+    const Lane<T, DK> lane(cl, qg);
+    constexpr int R16 = 16 * DK * sizeof(T);
     f32x4 ks[COLS][MT], qs[COLS][MT];
 #pragma unroll
-    for (int c = 0; c < COLS; ++c)
+    for (int pass = DELTA ? 0 : 1; pass < 2; ++pass) {
+        __syncthreads();   // the last readers of this part of LDS are done
+#pragma unroll
+        for (int r = 0; r < ROUNDS; ++r)
+            put_planes<E, DK>(s.x.rows, Shared::PLANE, (tid >> 4) + r * NODES, cl, (pass ? qv[r] : kv[r]) * av[r]);
+        __syncthreads();
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-            ks[c][m] = qs[c][m] = zero4();
+            f32x4 x[COLS];
+#pragma unroll
+            for (int c = 0; c < COLS; ++c) x[c] = zero4();
             if ((STEP == 1 || (m % STEP) == w / CG) && 16 * m < L) {
 #pragma unroll
-                for (int x = 0; x < DK / 32; ++x) {
-                    const int r = (16 * m + cl) * LK + 32 * x + 8 * qg;
-                    qs[c][m] = mma_split<T>(qs[c][m], row8(sQ + r), sf[c][x]);
-                    if constexpr (DELTA) ks[c][m] = mma_split<T>(ks[c][m], row8(sK + r), sf[c][x]);
+                for (int y = 0; y < DK / 32; ++y) {
+                    Two<T> f;
+                    f.get(lane, s.x.rows, Shared::PLANE, m * R16, y);
+#pragma unroll
+                    for (int c = 0; c < COLS; ++c) x[c] = mma_two(x[c], st[c][y], f);
                 }
             }
+#pragma unroll
+            for (int c = 0; c < COLS; ++c) (pass ? qs : ks)[c][m] = x[c];
         }
-    __syncthreads();   // sK and sQ change their meaning
+    }
+    __syncthreads();
 #pragma unroll
     for (int c = 0; c < COLS; ++c) {
-        const int col = 16 * (w % CG + c * WAVES) + cl;
+        const int col = 16 * (w % CG + c * WAVES) + 4 * qg;
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-            if ((STEP == 1 || (m % STEP) == w / CG) && 16 * m < L) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int r = 16 * m + 4 * qg + e;
-                    const float v = r < L ? to_f32(((const T*)p.v)[((node0 + r) * p.H + h) * dv + col]) : 0.f;
-                    sK[r * LU + col] = DELTA ? sB[r] * (v - ks[c][m][e]) : v;
-                    sQ[r * LU + col] = qs[c][m][e];
-                }
+        for (int m = 0; m < MT; ++m) {
+            const int i = 16 * m + cl;
+            if ((STEP == 1 || (m % STEP) == w / CG) && i < L) {
+                f32x4 u = unpack4(*reinterpret_cast<const typename V4<T>::t*>((const T*)p.v + ((node0 + i) * p.H + h) * DV + col));
+                if constexpr (DELTA) u = s.beta[i] * (u - ks[c][m]);
+                *reinterpret_cast<f32x4*>(s.x.u + i * Shared::LU + col) = u;
             }
+        }
     }
     __syncthreads();
 
     // u, level by level: a wave takes a node, a lane DV / 64 columns
     constexpr int CPL = DV / 64;
     if constexpr (DELTA) {
-        const int levels = sLevels;
+        const int levels = s.levels;
         for (int d = 1; d < levels; ++d) {
-            u64 nodes = sLevel[d];
-            for (int x = 0; nodes; ++x) {
-                const int i2 = __ffsll((long long)nodes) - 1;
-                nodes &= nodes - 1;
+            u64 nodes = uniform(s.level[d]);
+            for (int x = 0; nodes; ++x, nodes &= nodes - 1) {
                 if (x % WAVES != w) continue;
+                const int i = __ffsll((long long)nodes) - 1;
+                const float* A = s.kk + i * (i + 1) / 2 + d;   // the path from the root down
                 float u[CPL] = {};
-                for (u64 m = sAnc[i2]; m; m &= m - 1) {
+                for (u64 m = uniform(s.anc[i]); m; m &= m - 1, --A) {
                     const int a = __ffsll((long long)m) - 1;
-                    const float A = sKK[i2 * (NL + 1) + a];
 #pragma unroll
-                    for (int c = 0; c < CPL; ++c) u[c] += A * sK[a * LU + l + 64 * c];
+                    for (int c = 0; c < CPL; ++c) u[c] += *A * s.x.u[a * Shared::LU + l + 64 * c];
                 }
 #pragma unroll
-                for (int c = 0; c < CPL; ++c) sK[i2 * LU + l + 64 * c] -= sB[i2] * u[c];
+                for (int c = 0; c < CPL; ++c) s.x.u[i * Shared::LU + l + 64 * c] -= s.beta[i] * u[c];
             }
             __syncthreads();
         }
     }
-    for (int i2 = w; i2 < L; i2 += WAVES) {
-        const bool on = sDepth[i2] >= 0;
-        float o[CPL];
+    // outputs: every lane follows its own nodes' paths
 #pragma unroll
-        for (int c = 0; c < CPL; ++c) o[c] = on ? sQ[i2 * LU + l + 64 * c] : 0.f;
-        if (on)
-            for (u64 m = sAnc[i2] | 1ull << i2; m; m &= m - 1) {
-                const int a = __ffsll((long long)m) - 1;
-                const float A = sQK[i2 * (NL + 1) + a];
+    for (int m = 0; m < MT; ++m) {
+        const int i = 16 * m + cl;
+        if ((STEP == 1 || (m % STEP) == w / CG) && i < L) {
+            const bool live = s.depth[i] >= 0;
+            int d = i * (i + 1) / 2;
+            for (int a = live ? i : -1; a >= 0; a = s.par[a], ++d) {
+                const float A = s.qk[d];
 #pragma unroll
-                for (int c = 0; c < CPL; ++c) o[c] += A * sK[a * LU + l + 64 * c];
+                for (int c = 0; c < COLS; ++c)
+                    qs[c][m] += A * *reinterpret_cast<const f32x4*>(s.x.u + a * Shared::LU + 16 * (w % CG + c * WAVES) + 4 * qg);
             }
 #pragma unroll
-        for (int c = 0; c < CPL; ++c) store1(p.o, ((node0 + i2) * p.H + h) * dv + l + 64 * c, o[c], p.out_bf16);
+            for (int c = 0; c < COLS; ++c)
+                store4(p.o, ((node0 + i) * p.H + h) * DV + 16 * (w % CG + c * WAVES) + 4 * qg, live ? qs[c][m] : zero4(), p.out_bf16);
+        }
     }
 }
 
@@ -375,8 +471,8 @@ __global__ __launch_bounds__(kThreads) void kda_tree_commit_kernel(TreeParams p)
 
 template <typename T, bool DELTA, int NL, int DK> static void tree_n(const TreeParams& p, hipStream_t stream) {
     const dim3 grid((unsigned)((int64_t)p.N * p.H));
-    if (p.dv == 128) hipLaunchKernelGGL((kda_tree_kernel<T, DELTA, NL, DK, 128>), grid, dim3(NL * 16), 0, stream, p);
-    else hipLaunchKernelGGL((kda_tree_kernel<T, DELTA, NL, DK, 64>), grid, dim3(NL * 16), 0, stream, p);
+    if (p.dv == 128) hipLaunchKernelGGL((kda_tree_kernel<T, DELTA, NL, DK, 128>), grid, dim3(NL == 16 ? 256 : 512), 0, stream, p);
+    else hipLaunchKernelGGL((kda_tree_kernel<T, DELTA, NL, DK, 64>), grid, dim3(NL == 16 ? 256 : 512), 0, stream, p);
 }
 template <typename T, bool DELTA, int DK> static void tree_t(const TreeParams& p, hipStream_t stream) {
     if (p.L <= 16) tree_n<T, DELTA, 16, DK>(p, stream);
