@@ -9,13 +9,17 @@ def torch_module():
     return torch
 
 
+_DT_CODES = {}
+
+
 def dt_code(dtype):
-    torch = torch_module()
-    if dtype == torch.bfloat16:
-        return KDA_BF16
-    if dtype == torch.float32:
-        return KDA_F32
-    raise TypeError(f"unsupported dtype {dtype}")
+    if not _DT_CODES:
+        torch = torch_module()
+        _DT_CODES.update({torch.bfloat16: KDA_BF16, torch.float32: KDA_F32})
+    code = _DT_CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}")
+    return code
 
 
 def ptr(t):
@@ -41,10 +45,12 @@ def launch(dev, call, *args):
     torch = torch_module()
     index = dev.index
     if index == torch.cuda.current_device():
-        lib_check(call(*args, _raw_stream(index)))
+        status = call(*args, _raw_stream(index))
     else:
         with torch.cuda.device(dev):
-            lib_check(call(*args, _raw_stream(index)))
+            status = call(*args, _raw_stream(index))
+    if status:
+        lib_check(status)
 
 
 def _raw_stream(index):

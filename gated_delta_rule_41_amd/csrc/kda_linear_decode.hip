@@ -35,7 +35,7 @@ __global__ __launch_bounds__(kThreads) void linear_decode_kernel(LinearDecodePar
         sq[tid] = to_f32(((const T*)p.q)[(n * p.Hk + hk) * DK + tid]) * p.scale;
         sk[tid] = to_f32(((const T*)p.k)[(n * p.Hk + hk) * DK + tid]);
     }
-    const float a = fast_exp2((float)gate_log2(g));
+    const float a = fast_exp(g);
     __syncthreads();
     f32x4 o = zero4();
 #pragma unroll

@@ -221,12 +221,12 @@ __global__ __launch_bounds__(NL == 16 ? 256 : 512, sizeof(T) == 2 ? 4 : 2) void 
             const int i = (tid >> 4) + r * NODES;
             put_row<E>(s.x.c.k + i * DK, cl, kv[r]);
             if constexpr (DELTA) {
-                const float rk = 1.f / sqrtf(row16_sum(dot8(kv[r], kv[r])) + p.eps);
-                const float rq = p.scale / sqrtf(row16_sum(dot8(qv[r], qv[r])) + p.eps);
+                const float rk = __builtin_amdgcn_rsqf(row16_sum(dot8(kv[r], kv[r])) + p.eps);
+                const float rq = p.scale * __builtin_amdgcn_rsqf(row16_sum(dot8(qv[r], qv[r])) + p.eps);
                 kv[r] *= splat8(rk);
                 qv[r] *= splat8(rq);
 #pragma unroll
-                for (int j = 0; j < E; ++j) av[r][j] = fast_exp2((float)gate_log2(av[r][j]));
+                for (int j = 0; j < E; ++j) av[r][j] = fast_exp(av[r][j]);
                 put_row<E>(s.x.c.a + i * DK, cl, av[r]);
                 if (cl == 0) {
                     s.norm[i] = rk;
@@ -234,7 +234,7 @@ __global__ __launch_bounds__(NL == 16 ? 256 : 512, sizeof(T) == 2 ? 4 : 2) void 
                 }
             } else {
                 qv[r] *= splat8(p.scale);
-                av[r] = splat8(fast_exp2((float)gate_log2(av[r][0])));
+                av[r] = splat8(fast_exp(av[r][0]));
                 if (cl == 0) s.x.c.a[i] = av[r][0];
             }
         }
@@ -264,17 +264,18 @@ __global__ __launch_bounds__(NL == 16 ? 256 : 512, sizeof(T) == 2 ? 4 : 2) void 
                 if (cl == 0) s.qk[t0] = self;
                 int d = t0;
                 for (int a = s.par[i]; a >= 0; a = s.par[a]) {
-                    f32x8 ke = get_row<T, E>(s.x.c.k + a * DK, cl) * av[r];
+                    const f32x8 ke = get_row<T, E>(s.x.c.k + a * DK, cl) * av[r];
+                    float norm = 1.f;
                     if constexpr (DELTA) {
-                        ke *= splat8(s.norm[a]);
+                        norm = s.norm[a];
                         av[r] *= get_row<float, E>(s.x.c.a + a * DK, cl);
                     } else {
                         av[r] *= splat8(s.x.c.a[a]);
                     }
                     ++d;
-                    const float qk = row16_sum(dot8(qv[r], ke));
+                    const float qk = row16_sum(dot8(qv[r], ke)) * norm;
                     if constexpr (DELTA) {
-                        const float kk = row16_sum(dot8(kv[r], ke));
+                        const float kk = row16_sum(dot8(kv[r], ke)) * norm;
                         if (cl == 0) s.kk[d] = kk;
                     }
                     if (cl == 0) s.qk[d] = qk;
@@ -420,18 +421,18 @@ __global__ __launch_bounds__(kThreads) void kda_tree_commit_kernel(TreeParams p)
             if constexpr (DELTA) {
 #pragma unroll
                 for (int x = 16; x >= 1; x >>= 1) sum += __shfl_xor(sum, x, 64);
-                r = 1.f / sqrtf(sum + p.eps);
+                r = __builtin_amdgcn_rsqf(sum + p.eps);
             }
             if (done) __syncthreads();   // the last batch's readers are done
 #pragma unroll
             for (int e = 0; e < DK / 32; ++e) {
                 sk[b][c + 32 * e] = kx[e] * r;
                 if constexpr (DELTA)
-                    sal[b][c + 32 * e] = fast_exp2((float)gate_log2(to_f32(((const T*)p.g)[(at * p.H + h) * DK + c + 32 * e])));
+                    sal[b][c + 32 * e] = fast_exp(to_f32(((const T*)p.g)[(at * p.H + h) * DK + c + 32 * e]));
             }
             if (c == 0) {
                 if constexpr (DELTA) sb[b] = sigmoidf(to_f32(((const T*)p.beta)[at * p.H + h]));
-                else sb[b] = fast_exp2((float)gate_log2(((const float*)p.g)[p.gate_head ? h : at * p.H + h]));
+                else sb[b] = fast_exp(((const float*)p.g)[p.gate_head ? h : at * p.H + h]);
             }
         }
         __syncthreads();

@@ -78,7 +78,7 @@ def kda_linear_fwd(q, k, v, g, cu_seqlens=None, initial_state=None, *, num_seqs:
     out_dtype = out_dtype or torch.float32
     _check(initial_state, "initial_state", (N, H, dk, dv), torch.float32, dev)
     config = (H, Hk, dk, dv, _dt_code(dt), _dt_code(out_dtype), gate, scale)
-    o = torch.empty((T, H, dv), dtype=out_dtype, device=dev)
+    o = torch.empty_like(v, dtype=out_dtype)
     sf = torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev) if output_final_state else None
     wsb = _linear_workspace(_lib.kda_linear_fwd_workspace_size, T, N, *config)
     ws = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
@@ -101,10 +101,10 @@ def kda_linear_bwd(q, k, v, g, dO, cu_seqlens=None, initial_state=None, dS_final
     _check(dS_final, "dS_final", (N, H, dk, dv), torch.float32, dev)
     config = (H, Hk, dk, dv, _dt_code(dt), _dt_code(out_dtype), gate, scale)
     out = {
-        "dq": torch.empty((T, Hk, dk), dtype=out_dtype, device=dev),
-        "dk": torch.empty((T, Hk, dk), dtype=out_dtype, device=dev),
-        "dv": torch.empty((T, H, dv), dtype=out_dtype, device=dev),
-        "dg": torch.empty(tuple(g.shape), dtype=out_dtype, device=dev),
+        "dq": torch.empty_like(q, dtype=out_dtype),
+        "dk": torch.empty_like(k, dtype=out_dtype),
+        "dv": torch.empty_like(v, dtype=out_dtype),
+        "dg": torch.empty_like(g, dtype=out_dtype),
         "dS0": torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev) if output_d_initial_state else None,
     }
     wsb = _linear_workspace(_lib.kda_linear_bwd_workspace_size, T, N, *config)
@@ -125,12 +125,12 @@ def kda_linear_decode(q, k, v, g, state=None, *, out_state=None, out_dtype=None,
     gate = _gate(g, (N,), H, dev)
     _check(state, "state", (N, H, dk, dv), torch.float32, dev)
     if out_state is None:
-        out_state = torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev)
+        out_state = torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev) if state is None else torch.empty_like(state)
     else:
         _check(out_state, "out_state", (N, H, dk, dv), torch.float32, dev)
     out_dtype = out_dtype or torch.float32
     cfg = _linear_config(H, Hk, dk, dv, _dt_code(dt), _dt_code(out_dtype), gate, scale)
-    o = torch.empty((N, H, dv), dtype=out_dtype, device=dev)
+    o = torch.empty_like(v, dtype=out_dtype)
     _launch(dev, _lib.kda_linear_decode_raw, cfg, N, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(state), _ptr(out_state), _ptr(o))
     return o, out_state
 
@@ -168,7 +168,7 @@ def kda_tree(q, k, v, g, beta, parent, state=None, *, out_dtype=None, eps: float
     torch = _torch()
     out_dtype = out_dtype or torch.float32
     cfg, N, L, H, dk, dv, dev = _tree_common(q, k, v, g, beta, parent, state, out_dtype, eps, scale)
-    o = torch.empty((N, L, H, dv), dtype=out_dtype, device=dev)
+    o = torch.empty_like(v, dtype=out_dtype)
     _launch(dev, _lib.kda_tree_raw, cfg, N, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(parent), _ptr(state), _ptr(o))
     return o
 
@@ -182,7 +182,7 @@ def kda_tree_commit(k, v, g, beta, parent, accept, state=None, *, out_state=None
     cfg, N, L, H, dk, dv, dev = _tree_common(None, k, v, g, beta, parent, state, torch.float32, eps, 1.0)
     _check(accept, "accept", (N,), torch.int32, dev)
     if out_state is None:
-        out_state = torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev)
+        out_state = torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev) if state is None else torch.empty_like(state)
     else:
         _check(out_state, "out_state", (N, H, dk, dv), torch.float32, dev)
     _launch(dev, _lib.kda_tree_commit_raw, cfg, N, _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(parent), _ptr(accept),
