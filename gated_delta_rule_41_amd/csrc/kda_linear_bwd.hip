@@ -135,14 +135,19 @@ __device__ __forceinline__ void dq_role(const LinearBwdParams& p, const Task& t,
         const float eq = fast_exp2((float)gq) * p.scale;
         float e = 0.f;   // q . dq through the state, then the row sums of A
 #pragma unroll
-        for (int m = 0; m < DK / 16; ++m) {
-            f32x4 x = zero4();
+        for (int m = 0; m < DK / 16; m += 2) {
+            f32x4 x[2] = {zero4(), zero4()};
 #pragma unroll
-            for (int y = 0; y < DV / 32; ++y) x = mma_k32(x, lv.row(s.b, m * RV, y), dof[y]);
-            x *= eq;
-            e += dot4(x, half4(qf[m / 2], m & 1));
-            dq[m] += x;
-            if (m & 1) __builtin_amdgcn_sched_barrier(0);   // keeps the reads ahead of it to two blocks' registers
+            for (int y = 0; y < DV / 32; ++y)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) x[u] = mma_k32(x[u], lv.row(s.b, (m + u) * RV, y), dof[y]);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                x[u] *= eq;
+                e += dot4(x[u], half4(qf[m / 2], u));
+                dq[m + u] += x[u];
+            }
+            __builtin_amdgcn_sched_barrier(0);   // keeps the reads ahead of it to two blocks' registers
         }
         lds_barrier();   // the last readers of the state are done
         tv.store(s.b, rows, tid);
@@ -155,16 +160,19 @@ __device__ __forceinline__ void dq_role(const LinearBwdParams& p, const Task& t,
             if (l + 64 * i < 16 * rb) s.F[w][l + 64 * i] = fast_exp2((float)(gref - s.G[l + 64 * i]));
         lds_barrier();
         for (int x = 0; x <= rb / 2; ++x) {
-            f32x4 a[2];
+            // the products of both blocks side by side, so that none waits for the one before it
+            f32x4 a[2] = {zero4(), zero4()}, b[2] = {zero4(), zero4()};
+#pragma unroll
+            for (int y = 0; y < DV / 32; ++y)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) a[u] = mma_k32(a[u], lv.row(s.b, (2 * x + u) * RV, y), dof[y]);
+#pragma unroll
+            for (int y = 0; y < DK / 32; ++y)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) b[u] = mma_k32(b[u], lk.perm(s.a, (2 * x + u) * RK, y), qf[y]);
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int n = 2 * x + u;
-                f32x4 b = zero4();
-                a[u] = zero4();
-#pragma unroll
-                for (int y = 0; y < DV / 32; ++y) a[u] = mma_k32(a[u], lv.row(s.b, n * RV, y), dof[y]);
-#pragma unroll
-                for (int y = 0; y < DK / 32; ++y) b = mma_k32(b, lk.perm(s.a, n * RK, y), qf[y]);
                 if (n < rb) {
                     a[u] *= lds4(&s.F[w][16 * n + 4 * qg]) * fq;
                 } else {
@@ -173,10 +181,10 @@ __device__ __forceinline__ void dq_role(const LinearBwdParams& p, const Task& t,
                         const int key = 16 * n + 4 * qg + i;
                         const bool on = key <= row;
                         a[u][i] = keep(a[u][i] * (fast_exp2((float)(gq - s.G[key])) * p.scale), on);
-                        b[i] = keep(b[i], on);
+                        b[u][i] = keep(b[u][i], on);
                     }
                 }
-                e += dot4(a[u], b);   // A_ij = dP_ij q_i . k_j
+                e += dot4(a[u], b[u]);   // A_ij = dP_ij q_i . k_j
             }
             const frag f = pack8<T>(a[0], a[1]);   // bf16 inputs: dP rounded to the products' type
 #pragma unroll
@@ -231,14 +239,19 @@ __device__ __forceinline__ void dk_role(const LinearBwdParams& p, const Task& t,
         const float wj = fast_exp2((float)(s.G[kB - 1] - gk));
         float f = 0.f;
 #pragma unroll
-        for (int m = 0; m < DK / 16; ++m) {
-            f32x4 x = zero4();
+        for (int m = 0; m < DK / 16; m += 2) {
+            f32x4 x[2] = {zero4(), zero4()};
 #pragma unroll
-            for (int y = 0; y < DV / 32; ++y) x = mma_k32(x, lv.row(s.b, m * RV, y), vf[y]);
-            x *= wj;
-            f += dot4(x, half4(kf[m / 2], m & 1));
-            dk[m] += x;
-            if (m & 1) __builtin_amdgcn_sched_barrier(0);
+            for (int y = 0; y < DV / 32; ++y)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) x[u] = mma_k32(x[u], lv.row(s.b, (m + u) * RV, y), vf[y]);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                x[u] *= wj;
+                f += dot4(x[u], half4(kf[m / 2], u));
+                dk[m + u] += x[u];
+            }
+            __builtin_amdgcn_sched_barrier(0);
         }
         f = qsum4(f);
         if (qg == 0 && key < rows) p.f[(int64_t)h * p.T + t.lo + key] = f;
@@ -253,16 +266,18 @@ __device__ __forceinline__ void dk_role(const LinearBwdParams& p, const Task& t,
         lds_barrier();
         float colsum = 0.f;
         for (int x = rb / 2; x < (rows + 31) / 32; ++x) {
-            f32x4 b[2];
+            f32x4 a[2] = {zero4(), zero4()}, b[2] = {zero4(), zero4()};
+#pragma unroll
+            for (int y = 0; y < DK / 32; ++y)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) a[u] = mma_k32(a[u], lk.perm(s.a, (2 * x + u) * RK, y), kf[y]);
+#pragma unroll
+            for (int y = 0; y < DV / 32; ++y)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) b[u] = mma_k32(b[u], lv.row(s.b, (2 * x + u) * RV, y), vf[y]);
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int n = 2 * x + u;
-                f32x4 a = zero4();
-                b[u] = zero4();
-#pragma unroll
-                for (int y = 0; y < DK / 32; ++y) a = mma_k32(a, lk.perm(s.a, n * RK, y), kf[y]);
-#pragma unroll
-                for (int y = 0; y < DV / 32; ++y) b[u] = mma_k32(b[u], lv.row(s.b, n * RV, y), vf[y]);
                 if (n > rb) {
                     b[u] *= lds4(&s.F[w][16 * n + 4 * qg]) * fk;
                 } else {
@@ -271,10 +286,10 @@ __device__ __forceinline__ void dk_role(const LinearBwdParams& p, const Task& t,
                         const int query = 16 * n + 4 * qg + i;
                         const bool on = key <= query;
                         b[u][i] = keep(b[u][i] * (fast_exp2((float)(s.G[query] - gk)) * p.scale), on);
-                        a[i] = keep(a[i], on);
+                        a[u][i] = keep(a[u][i], on);
                     }
                 }
-                colsum += dot4(a, b[u]);   // A_ij = q_i . k_j dP_ij
+                colsum += dot4(a[u], b[u]);   // A_ij = q_i . k_j dP_ij
             }
             const frag f = pack8<T>(b[0], b[1]);   // bf16 inputs: dP rounded to the products' type
 #pragma unroll
@@ -339,11 +354,14 @@ __device__ __forceinline__ void dv_role(const LinearBwdParams& p, const Task& t,
     const float wj = fast_exp2((float)(s.G[kB - 1] - gk));
     f32x4 dv[DV / 16];
 #pragma unroll
-    for (int m = 0; m < DV / 16; ++m) {
-        f32x4 x = zero4();
+    for (int m = 0; m < DV / 16; m += 2) {
+        f32x4 x[2] = {zero4(), zero4()};
 #pragma unroll
-        for (int y = 0; y < DK / 32; ++y) x = mma_k32(x, lv.col(s.b, 2 * y * RV, m), kf[y]);
-        dv[m] = x * wj;
+        for (int y = 0; y < DK / 32; ++y)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) x[u] = mma_k32(x[u], lv.col(s.b, 2 * y * RV, m + u), kf[y]);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) dv[m + u] = x[u] * wj;
     }
     lds_barrier();   // the last readers of dS are done
     tq.store(s.b, rows, tid);
@@ -354,13 +372,14 @@ __device__ __forceinline__ void dv_role(const LinearBwdParams& p, const Task& t,
         if (l + 64 * i >= 16 * rb + 16) s.F[w][l + 64 * i] = fast_exp2((float)(s.G[l + 64 * i] - gref));
     lds_barrier();
     for (int x = rb / 2; x < (rows + 31) / 32; ++x) {
-        f32x4 a[2];
+        f32x4 a[2] = {zero4(), zero4()};
+#pragma unroll
+        for (int y = 0; y < DK / 32; ++y)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) a[u] = mma_k32(a[u], lk.perm(s.b, (2 * x + u) * RK, y), kf[y]);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const int n = 2 * x + u;
-            a[u] = zero4();
-#pragma unroll
-            for (int y = 0; y < DK / 32; ++y) a[u] = mma_k32(a[u], lk.perm(s.b, n * RK, y), kf[y]);
             if (n > rb) {
                 a[u] *= lds4(&s.F[w][16 * n + 4 * qg]) * fk;
             } else {

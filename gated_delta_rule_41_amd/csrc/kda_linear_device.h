@@ -269,17 +269,17 @@ template <> struct Split<bf16> {
         x -= widen8(h[1]);
         h[2] = __builtin_convertvector(x, bf16x8);
     }
-    template <bool IS_A> __device__ __forceinline__ f32x4 mma(f32x4 c, bf16x8 b) const {
-#pragma unroll
-        for (int i = 2; i >= 0; --i) c = IS_A ? mma_k32(c, h[i], b) : mma_k32(c, b, h[i]);
-        return c;
+    static constexpr int TERMS = 3;
+    template <bool IS_A> __device__ __forceinline__ f32x4 mma(int i, f32x4 c, bf16x8 b) const {   // term i, smallest first
+        return IS_A ? mma_k32(c, h[2 - i], b) : mma_k32(c, b, h[2 - i]);
     }
 };
 template <> struct Split<float> {
     f32x8 x;
     __device__ __forceinline__ Split() {}
     __device__ __forceinline__ explicit Split(f32x8 y) : x(y) {}
-    template <bool IS_A> __device__ __forceinline__ f32x4 mma(f32x4 c, f32x8 b) const {
+    static constexpr int TERMS = 1;
+    template <bool IS_A> __device__ __forceinline__ f32x4 mma(int, f32x4 c, f32x8 b) const {
         return IS_A ? mma_k32(c, x, b) : mma_k32(c, b, x);
     }
 };

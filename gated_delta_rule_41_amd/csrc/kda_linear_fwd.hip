@@ -44,6 +44,24 @@ __device__ __forceinline__ float load_gate(const float* g, int stride, int t, in
     return g[(int64_t)(t + (l < rows ? l : rows - 1)) * stride];
 }
 
+// S += a u over 32 tokens, four blocks of rows at a time, the terms of u in the outer loop: a
+// product that adds to the result of the one before it would wait for it.
+template <bool U_IS_A, typename T, int NC, int D, typename F>
+__device__ __forceinline__ void add_outer(f32x4 (&S)[NC][D], const Split<T> (&u)[NC], F&& rows) {
+#pragma unroll
+    for (int d0 = 0; d0 < D; d0 += 4) {
+        typename V8<T>::t a[4];
+#pragma unroll
+        for (int d = 0; d < 4; ++d) a[d] = rows(d0 + d);
+#pragma unroll
+        for (int i = 0; i < Split<T>::TERMS; ++i)
+#pragma unroll
+            for (int d = 0; d < 4; ++d)
+#pragma unroll
+                for (int c = 0; c < NC; ++c) S[c][d0 + d] = u[c].template mma<U_IS_A>(i, S[c][d0 + d], a[d]);
+    }
+}
+
 template <typename T, int DK, int DV>
 __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void linear_out_kernel(LinearParams p) {
     constexpr int C = kLinChunk, NC = DV / 64;   // column groups of 16 per wave
@@ -131,20 +149,27 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void linear_out_k
             frag qf[DK / 32];
 #pragma unroll
             for (int s = 0; s < DK / 32; ++s) qf[s] = lk.row(sQ, w * RK, s);
+            // two blocks at a time, so that their products do not wait for each other
 #pragma unroll
-            for (int n = 0; n < 4; ++n)
-                if (n <= w) {
-                    f32x4 a = zero4();
+            for (int n0 = 0; n0 < 4; n0 += 2)
+                if (n0 <= w) {
+                    f32x4 a[2] = {zero4(), zero4()};
 #pragma unroll
-                    for (int s = 0; s < DK / 32; ++s) a = mma_k32(a, lk.row(sK, n * RK, s), qf[s]);
-                    if (n < w) {
-                        a *= lds4(&sF[w][16 * n + 4 * qg]) * fq;
-                    } else {
+                    for (int s = 0; s < DK / 32; ++s)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            a[i] = keep(a[i] * (fast_exp2((float)(gq - G.G[16 * w + 4 * qg + i])) * p.scale), 4 * qg + i <= cl);
+                        for (int n = 0; n < 2; ++n) a[n] = mma_k32(a[n], lk.row(sK, (n0 + n) * RK, s), qf[s]);
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        if (n0 + n > w) break;
+                        if (n0 + n < w) {
+                            a[n] *= lds4(&sF[w][16 * (n0 + n) + 4 * qg]) * fq;
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                a[n][i] = keep(a[n][i] * (fast_exp2((float)(gq - G.G[16 * w + 4 * qg + i])) * p.scale), 4 * qg + i <= cl);
+                        }
+                        put4<T, C>(sP, 16 * w + cl, n0 + n, qg, a[n]);   // bf16 inputs: P rounded to the products' type
                     }
-                    put4<T, C>(sP, 16 * w + cl, n, qg, a);   // bf16 inputs: P rounded to the products' type
                 }
         }
         if (w == 0 && rows > C) put_gates(gates[(t0 / C + 1) & 1], gn, rows - C, l, false, 0.f);
@@ -207,12 +232,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void linear_out_k
             Split<T> u[NC];
 #pragma unroll
             for (int c = 0; c < NC; ++c) u[c] = Split<T>(widen8(vf[c][kk]) * wt);
-#pragma unroll
-            for (int d = 0; d < DK / 16; ++d) {
-                const frag k = lk.col(sK, 2 * kk * RK, d);
-#pragma unroll
-                for (int c = 0; c < NC; ++c) S[c][d] = u[c].template mma<false>(S[c][d], k);
-            }
+            add_outer<false>(S, u, [&](int d) { return lk.col(sK, 2 * kk * RK, d); });
         }
     }
     if (p.sfinal && rg.hi == rg.end) {
@@ -273,22 +293,27 @@ __global__ __launch_bounds__(kThreads, 2) void linear_state_kernel(LinearStatePa
     // a block of the document keeps its slot whatever the segments are
     const int64_t block0 = rg.start / kLinBlock + rg.n + (rg.lo - rg.start) / kLinBlock;
 
-    Tile<T, C, DK, kThreads> ta;
-    Tile<T, C, DV, kThreads> tb;
+    // Rows are loaded two chunks ahead: a chunk takes about as long here as a load does when the
+    // memory is busy.
+    Tile<T, C, DK, kThreads> ta[2];
+    Tile<T, C, DV, kThreads> tb[2];
     float g = 0.f;
     double gsum = 0.0;
-    const int dir = rev ? -C : C;
-    int t0 = rev ? (chunks - 1) * C : 0;
+    const int dir = rev ? -C : C, first = rev ? (chunks - 1) * C : 0;
     if (chunks > 0) {
-        ta.load(ap + t0 * lda, lda, total - t0, tid);
-        tb.load(bp + t0 * ldb, ldb, total - t0, tid);
+        ta[0].load(ap + first * lda, lda, total - first, tid);
+        tb[0].load(bp + first * ldb, ldb, total - first, tid);
         if (w == 0) {
-            gsum += put_gates(gates[0], load_gate(gp, p.g_stride, t0, total - t0, l), total - t0, l, rev, p.scale);
-            if (chunks > 1) g = load_gate(gp, p.g_stride, t0 + dir, total - t0 - dir, l);
+            gsum += put_gates(gates[0], load_gate(gp, p.g_stride, first, total - first, l), total - first, l, rev, p.scale);
+            if (chunks > 1) g = load_gate(gp, p.g_stride, first + dir, total - first - dir, l);
+        }
+        if (chunks > 1) {
+            ta[1].load(ap + (first + dir) * lda, lda, total - first - dir, tid);
+            tb[1].load(bp + (first + dir) * ldb, ldb, total - first - dir, tid);
         }
     }
-    for (int x = 0; x < chunks; ++x, t0 += dir) {
-        const int rows = total - t0, c0 = t0 / C, cl = opaque(l & 15), qg = opaque(l >> 4);
+    auto step = [&](Tile<T, C, DK, kThreads>& ta, Tile<T, C, DV, kThreads>& tb, int x) __attribute__((always_inline)) {
+        const int t0 = first + x * dir, rows = total - t0, c0 = t0 / C, cl = opaque(l & 15), qg = opaque(l >> 4);
         const Gates& G = gates[x & 1];
         if (D.border && (rev ? ((c0 & 1) || x == 0) : !(c0 & 1))) {
             T* b = (T*)D.border + ((block0 + c0 / 2) * p.H + h) * DK * dv + lane;
@@ -297,15 +322,15 @@ __global__ __launch_bounds__(kThreads, 2) void linear_state_kernel(LinearStatePa
 #pragma unroll
                 for (int d = 0; d < DK / 16; ++d) *reinterpret_cast<typename V4<T>::t*>(b + 16 * d * dv + 16 * c) = pack4<T>(S[c][d]);
         }
-        lds_barrier();
+        lds_barrier();   // the last chunk's readers are done
         ta.store(sA, rows, tid);
         tb.store(sB, rows, tid);
         const float gn = g;
         const bool more = x + 1 < chunks;
-        if (more) {
-            ta.load(ap + (t0 + dir) * lda, lda, rows - dir, tid);
-            tb.load(bp + (t0 + dir) * ldb, ldb, rows - dir, tid);
-            if (w == 0 && x + 2 < chunks) g = load_gate(gp, p.g_stride, t0 + 2 * dir, rows - 2 * dir, l);
+        if (x + 2 < chunks) {
+            ta.load(ap + (t0 + 2 * dir) * lda, lda, rows - 2 * dir, tid);
+            tb.load(bp + (t0 + 2 * dir) * ldb, ldb, rows - 2 * dir, tid);
+            if (w == 0) g = load_gate(gp, p.g_stride, t0 + 2 * dir, rows - 2 * dir, l);
         }
         lds_barrier();
         const Lane<T, DK> la(cl, qg);
@@ -322,13 +347,12 @@ __global__ __launch_bounds__(kThreads, 2) void linear_state_kernel(LinearStatePa
             Split<T> u[NC];
 #pragma unroll
             for (int c = 0; c < NC; ++c) u[c] = Split<T>(widen8(lb.col(sB, 2 * kk * 16 * DV * (int)sizeof(T), w * NC + c)) * wt);
-#pragma unroll
-            for (int d = 0; d < DK / 16; ++d) {
-                const frag a = la.col(sA, 2 * kk * 16 * DK * (int)sizeof(T), d);
-#pragma unroll
-                for (int c = 0; c < NC; ++c) S[c][d] = u[c].template mma<true>(S[c][d], a);
-            }
+            add_outer<true>(S, u, [&](int d) { return la.col(sA, 2 * kk * 16 * DK * (int)sizeof(T), d); });
         }
+    };
+    for (int x = 0; x < chunks; x += 2) {
+        step(ta[0], tb[0], x);
+        if (x + 1 < chunks) step(ta[1], tb[1], x + 1);
     }
     float* s = D.decay ? D.seg + (slot * p.H + h) * DK * dv + lane
                : D.last && tail ? D.last + ((int64_t)rg.n * p.H + h) * DK * dv + lane : nullptr;
