@@ -55,24 +55,29 @@ __device__ __forceinline__ f32x4 half4(f32x8 x, int hi) {
 }
 __device__ __forceinline__ float dot4(f32x4 a, f32x4 b) { return a[0] * b[0] + a[1] * b[1] + a[2] * b[2] + a[3] * b[3]; }
 
-// Row `row` of a global matrix as product fragments (zeros where row >= rows).
-template <typename T, int D> __device__ __forceinline__ void row_frags(typename V8<T>::t (&f)[D / 32], const T* base, int64_t ld, int row, int rows, int qg) {
-    const T* p = base + (int64_t)(row < rows ? row : rows - 1) * ld + 8 * qg;
-#pragma unroll
-    for (int s = 0; s < D / 32; ++s) {
-        f[s] = *reinterpret_cast<const typename V8<T>::t*>(p + 32 * s);
-        if (row >= rows) f[s] = typename V8<T>::t{};
-    }
+// Eight elements at a byte offset, and two groups of four.
+template <typename T> __device__ __forceinline__ typename V8<T>::t load_halves(Buffer b, unsigned o0, unsigned o1) {
+    if constexpr (sizeof(T) == 2) return join(__builtin_bit_cast(bf16x4, load8(b, o0)), __builtin_bit_cast(bf16x4, load8(b, o1)));
+    else return join(__builtin_bit_cast(f32x4, load16(b, o0)), __builtin_bit_cast(f32x4, load16(b, o1)));
+}
+template <typename T> __device__ __forceinline__ typename V8<T>::t load_frag(Buffer b, unsigned o0, unsigned o1) {
+    if constexpr (sizeof(T) == 2) return __builtin_bit_cast(bf16x8, load16(b, o0));
+    else return load_halves<T>(b, o0, o1);
 }
 
+// Row `row` of a global matrix as product fragments (zeros where row >= rows).
+template <typename T, int D> __device__ __forceinline__ void row_frags(typename V8<T>::t (&f)[D / 32], const T* base, int64_t ld, int row, int rows, int qg) {
+    const Buffer b = rows_of(base, ld, rows, kB, D);
+    const unsigned off = ((unsigned)row * (unsigned)ld + 8 * qg) * sizeof(T);
+#pragma unroll
+    for (int s = 0; s < D / 32; ++s) f[s] = load_frag<T>(b, off + 32 * s * sizeof(T), off + (32 * s + 4) * sizeof(T));
+}
 // The same row in the k order of two stacked accumulator blocks.
 template <typename T, int D> __device__ __forceinline__ void row_perms(typename V8<T>::t (&f)[D / 32], const T* base, int64_t ld, int row, int rows, int qg) {
-    const T* p = base + (int64_t)(row < rows ? row : rows - 1) * ld + 4 * qg;
+    const Buffer b = rows_of(base, ld, rows, kB, D);
+    const unsigned off = ((unsigned)row * (unsigned)ld + 4 * qg) * sizeof(T);
 #pragma unroll
-    for (int s = 0; s < D / 32; ++s) {
-        f[s] = join(*reinterpret_cast<const typename V4<T>::t*>(p + 32 * s), *reinterpret_cast<const typename V4<T>::t*>(p + 32 * s + 16));
-        if (row >= rows) f[s] = typename V8<T>::t{};
-    }
+    for (int s = 0; s < D / 32; ++s) f[s] = load_halves<T>(b, off + 32 * s * sizeof(T), off + (32 * s + 16) * sizeof(T));
 }
 
 // What a role's workgroup knows of its block.
@@ -100,7 +105,7 @@ template <typename T, int DK, int DV, bool GROUPED>
 __device__ __forceinline__ void dq_role(const LinearBwdParams& p, const Task& t, GradTiles<T, DK, DV>& s) {
     typedef typename V8<T>::t frag;
     constexpr int RK = 16 * DK * sizeof(T), RV = 16 * DV * sizeof(T);   // bytes of 16 rows
-    const int w = threadIdx.x >> 6, rb = row_block(w), rows = t.rows;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), rb = row_block(w), rows = t.rows;
     const int64_t ldk = (int64_t)p.Hk * DK, ldv = (int64_t)p.H * DV;
     const T* q = (const T*)p.q + t.lo * ldk + t.hk * DK;
 
@@ -121,11 +126,11 @@ __device__ __forceinline__ void dq_role(const LinearBwdParams& p, const Task& t,
             Tile<T, kB, DK, kGradThreads> tk;
             tk.load((const T*)p.k + t.lo * ldk + t.hk * DK, ldk, rows, tid);
             if (w == 0) block_gates(s.G, p.g + (p.g_stride ? t.lo * p.g_stride : 0) + h, p.g_stride, rows, l);
-            ts.store(s.b, DK, tid);
-            tk.store(s.a, rows, tid);
+            ts.store(s.b, tid);
+            tk.store(s.a, tid);
         } else {
             if (w == 0) block_gates(s.G, p.g + (p.g_stride ? t.lo * p.g_stride : 0) + h, p.g_stride, rows, l);
-            ts.store(s.b, DK, tid);
+            ts.store(s.b, tid);
         }
         lds_barrier();
         // through the entering state; row = key channel 16m + 4qg + i, column = query
@@ -150,7 +155,7 @@ __device__ __forceinline__ void dq_role(const LinearBwdParams& p, const Task& t,
             __builtin_amdgcn_sched_barrier(0);   // keeps the reads ahead of it to two blocks' registers
         }
         lds_barrier();   // the last readers of the state are done
-        tv.store(s.b, rows, tid);
+        tv.store(s.b, tid);
         // Below the diagonal block the decay is split at the last key before the wave's
         // queries, both factors at most 1: two exponentials a lane instead of four a block.
         const double gref = s.G[rb ? 16 * rb - 1 : 0];
@@ -195,17 +200,16 @@ __device__ __forceinline__ void dq_role(const LinearBwdParams& p, const Task& t,
         lds_barrier();
     }
     const int l = threadIdx.x & 63, row = 16 * rb + (l & 15);
-    if (row < rows)
+    const Buffer out = out_rows(p.dq, t.lo * ldk + t.hk * DK, ldk, rows, kB, DK, p.out_bf16);
 #pragma unroll
-        for (int m = 0; m < DK / 16; ++m)
-            store4(p.dq, ((t.lo + row) * p.Hk + t.hk) * DK + 16 * m + 4 * (l >> 4), dq[m], p.out_bf16);
+    for (int m = 0; m < DK / 16; ++m) store4(out, row * (unsigned)ldk + 16 * m + 4 * (l >> 4), dq[m], p.out_bf16);
 }
 
 template <typename T, int DK, int DV, bool GROUPED>
 __device__ __forceinline__ void dk_role(const LinearBwdParams& p, const Task& t, GradTiles<T, DK, DV>& s) {
     typedef typename V8<T>::t frag;
     constexpr int RK = 16 * DK * sizeof(T), RV = 16 * DV * sizeof(T);
-    const int w = threadIdx.x >> 6, rb = row_block(w), rows = t.rows;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), rb = row_block(w), rows = t.rows;
     const int64_t ldk = (int64_t)p.Hk * DK, ldv = (int64_t)p.H * DV;
     const T* k = (const T*)p.k + t.lo * ldk + t.hk * DK;
 
@@ -225,11 +229,11 @@ __device__ __forceinline__ void dk_role(const LinearBwdParams& p, const Task& t,
             Tile<T, kB, DK, kGradThreads> tq;
             tq.load((const T*)p.q + t.lo * ldk + t.hk * DK, ldk, rows, tid);
             if (w == 0) block_gates(s.G, p.g + (p.g_stride ? t.lo * p.g_stride : 0) + h, p.g_stride, rows, l);
-            td.store(s.b, DK, tid);
-            tq.store(s.a, rows, tid);
+            td.store(s.b, tid);
+            tq.store(s.a, tid);
         } else {
             if (w == 0) block_gates(s.G, p.g + (p.g_stride ? t.lo * p.g_stride : 0) + h, p.g_stride, rows, l);
-            td.store(s.b, DK, tid);
+            td.store(s.b, tid);
         }
         lds_barrier();
         // through the state's gradient; row = key channel, column = key
@@ -256,7 +260,7 @@ __device__ __forceinline__ void dk_role(const LinearBwdParams& p, const Task& t,
         f = qsum4(f);
         if (qg == 0 && key < rows) p.f[(int64_t)h * p.T + t.lo + key] = f;
         lds_barrier();   // the last readers of dS are done
-        to.store(s.b, rows, tid);
+        to.store(s.b, tid);
         // Above the diagonal block the decay is split at the wave's last key.
         const double gref = s.G[16 * rb + 15];
         const float fk = fast_exp2((float)(gref - gk)) * p.scale;
@@ -300,17 +304,16 @@ __device__ __forceinline__ void dk_role(const LinearBwdParams& p, const Task& t,
         lds_barrier();
     }
     const int l = threadIdx.x & 63, key = 16 * rb + (l & 15);
-    if (key < rows)
+    const Buffer out = out_rows(p.dk_out, t.lo * ldk + t.hk * DK, ldk, rows, kB, DK, p.out_bf16);
 #pragma unroll
-        for (int m = 0; m < DK / 16; ++m)
-            store4(p.dk_out, ((t.lo + key) * p.Hk + t.hk) * DK + 16 * m + 4 * (l >> 4), dk[m], p.out_bf16);
+    for (int m = 0; m < DK / 16; ++m) store4(out, key * (unsigned)ldk + 16 * m + 4 * (l >> 4), dk[m], p.out_bf16);
 }
 
 template <typename T, int DK, int DV>
 __device__ __forceinline__ void dv_role(const LinearBwdParams& p, const Task& t, int h, GradTiles<T, DK, DV>& s) {
     typedef typename V8<T>::t frag;
     constexpr int RK = 16 * DK * sizeof(T), RV = 16 * DV * sizeof(T);
-    const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, cl = l & 15, qg = l >> 4;
+    const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, cl = l & 15, qg = l >> 4;
     const int rb = row_block(w), key = 16 * rb + cl, rows = t.rows;
     const int64_t ldk = (int64_t)p.Hk * DK, ldv = (int64_t)p.H * DV;
 
@@ -326,7 +329,7 @@ __device__ __forceinline__ void dv_role(const LinearBwdParams& p, const Task& t,
         Tile<T, kB, DV, kGradThreads> to;
         to.load((const T*)p.dO + t.lo * ldv + h * DV, ldv, rows, tid);
         if (w == 0) block_gates(s.G, p.g + (p.g_stride ? t.lo * p.g_stride : 0) + h, p.g_stride, rows, l);
-        td.store(s.b, DK, tid);
+        td.store(s.b, tid);
         float cross = 0.f;
 #pragma unroll
         for (int i = 0; i < Tile<T, DK, DV, kGradThreads>::PIECES; ++i) {
@@ -338,7 +341,7 @@ __device__ __forceinline__ void dv_role(const LinearBwdParams& p, const Task& t,
 #pragma unroll
         for (int m = 32; m >= 1; m >>= 1) cross += __shfl_xor(cross, m, 64);
         if (l == 0) s.sum[w] = cross;
-        to.store(s.a, rows, tid);
+        to.store(s.a, tid);
     }
     lds_barrier();
     if (tid == 0) {
@@ -364,7 +367,7 @@ __device__ __forceinline__ void dv_role(const LinearBwdParams& p, const Task& t,
         for (int u = 0; u < 2; ++u) dv[m + u] = x[u] * wj;
     }
     lds_barrier();   // the last readers of dS are done
-    tq.store(s.b, rows, tid);
+    tq.store(s.b, tid);
     const double gref = s.G[16 * rb + 15];
     const float fk = fast_exp2((float)(gref - gk)) * p.scale;
 #pragma unroll
@@ -394,10 +397,9 @@ __device__ __forceinline__ void dv_role(const LinearBwdParams& p, const Task& t,
 #pragma unroll
         for (int m = 0; m < DV / 16; ++m) dv[m] = mma_k32(dv[m], lv.col(s.a, 2 * x * RV, m), f);
     }
-    if (key < rows)
+    const Buffer out = out_rows(p.dv_out, t.lo * ldv + h * DV, ldv, rows, kB, DV, p.out_bf16);
 #pragma unroll
-        for (int m = 0; m < DV / 16; ++m)
-            store4(p.dv_out, ((t.lo + key) * p.H + h) * DV + 16 * m + 4 * qg, dv[m], p.out_bf16);
+    for (int m = 0; m < DV / 16; ++m) store4(out, key * (unsigned)ldv + 16 * m + 4 * qg, dv[m], p.out_bf16);
 }
 
 // GROUPED: several value heads to a key head.

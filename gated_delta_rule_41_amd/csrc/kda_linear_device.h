@@ -293,44 +293,48 @@ __device__ __forceinline__ void store1(void* base, int64_t at, float x, int out_
     else ((float*)base)[at] = x;
 }
 
-// A tile of ROWS x COLS (row-major in global with row stride `ld` elements) held in
-// registers between its loads and its stores to a Swz tile, 16 bytes a piece.  Rows at or
-// past `rows` are read from the last valid row and stored as zeros.  Addresses are a uniform
-// base and a 32-bit lane offset (ROWS rows of ld elements are below 2^31 bytes).
+// `rows` rows of `cols` elements with stride `ld`, as a buffer: reads past its end return zeros
+// and writes past it are dropped, so rows behind a document's end need no branches.  That
+// matters beyond the branches: a wait for one load must count the memory operations issued
+// after it, and around conditional ones the compiler can only wait for all of them.
+// At most 128 rows (checked on the host to be below 2^31 bytes); `base` and the counts are
+// the same for the whole wave.
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+typedef __amdgpu_buffer_rsrc_t Buffer;
+template <typename T> __device__ __forceinline__ Buffer rows_of(const T* base, int64_t ld, int rows, int most, int cols) {
+    const int n = rows < 0 ? 0 : rows < most ? rows : most;
+    const int bytes = n ? (int)((unsigned)((n - 1) * (int)ld + cols) * sizeof(T)) : 0;
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(base), 0, bytes, 0x00027000);
+}
+__device__ __forceinline__ u32x4 load16(Buffer b, unsigned off) { return __builtin_amdgcn_raw_buffer_load_b128(b, off, 0, 0); }
+__device__ __forceinline__ u32x2 load8(Buffer b, unsigned off) { return __builtin_amdgcn_raw_buffer_load_b64(b, off, 0, 0); }
+// Four values at element `at` of a buffer of bf16 or fp32.
+__device__ __forceinline__ void store4(Buffer b, unsigned at, f32x4 x, int out_bf16) {
+    if (out_bf16) __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, pack4<bf16>(x)), b, at * 2, 0, 0);
+    else __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), b, at * 4, 0, 0);
+}
+// `rows` rows of `cols` elements of an output of either type.
+__device__ __forceinline__ Buffer out_rows(void* base, int64_t at, int64_t ld, int rows, int most, int cols, int out_bf16) {
+    return out_bf16 ? rows_of((const bf16*)base + at, ld, rows, most, cols) : rows_of((const float*)base + at, ld, rows, most, cols);
+}
+
+// A tile of ROWS x COLS (row-major in global with row stride `ld` elements) held in registers
+// between its loads and its stores to a Swz tile, 16 bytes a piece.  Rows at or past `rows`
+// are zeros.
 template <typename T, int ROWS, int COLS, int THREADS> struct Tile {
     typedef Swz<T, COLS> Z;
     static constexpr int PIECES = ROWS * Z::PR / THREADS, STEP = THREADS / Z::PR;   // rows between a lane's pieces
     static_assert(ROWS * Z::PR % THREADS == 0, "tile pieces");
-    typedef unsigned u4 __attribute__((ext_vector_type(4)));
-    u4 r[PIECES];
+    u32x4 r[PIECES];
     __device__ __forceinline__ void load(const T* g, int64_t ld, int rows, int tid) {
-        const int row = tid / Z::PR;
-        const unsigned c = (tid % Z::PR) * 16u, step = (unsigned)ld * sizeof(T);
-        if (rows >= ROWS) {
-            const unsigned off = (unsigned)row * step + c;
+        const Buffer b = rows_of(g, ld, rows, ROWS, COLS);
+        const unsigned row = (unsigned)ld * sizeof(T), off = (unsigned)(tid / Z::PR) * row + (tid % Z::PR) * 16u;
 #pragma unroll
-            for (int i = 0; i < PIECES; ++i)
-                r[i] = *reinterpret_cast<const u4*>((const char*)(g + i * STEP * ld) + off);
-        } else {
-#pragma unroll
-            for (int i = 0; i < PIECES; ++i) {
-                const int x = row + i * STEP;
-                r[i] = *reinterpret_cast<const u4*>((const char*)g + ((unsigned)(x < rows ? x : rows - 1) * step + c));
-            }
-        }
+        for (int i = 0; i < PIECES; ++i) r[i] = load16(b, off + i * STEP * row);
     }
-    __device__ __forceinline__ void store(T* s, int rows, int tid) const {
-        const int row = tid / Z::PR, c = tid % Z::PR;
-        if (rows >= ROWS) {
+    __device__ __forceinline__ void store(T* s, int tid) const {
 #pragma unroll
-            for (int i = 0; i < PIECES; ++i) *reinterpret_cast<u4*>(s + Z::at(row + i * STEP, c)) = r[i];
-        } else {
-#pragma unroll
-            for (int i = 0; i < PIECES; ++i) {
-                const u4 z = {0u, 0u, 0u, 0u};
-                *reinterpret_cast<u4*>(s + Z::at(row + i * STEP, c)) = row + i * STEP < rows ? r[i] : z;
-            }
-        }
+        for (int i = 0; i < PIECES; ++i) *reinterpret_cast<u32x4*>(s + Z::at(tid / Z::PR + i * STEP, tid % Z::PR)) = r[i];
     }
 };
 

@@ -40,8 +40,11 @@ __device__ __forceinline__ double put_gates(Gates& s, float g, int rows, int l, 
     if (l == 0) s.E = fast_exp2((float)Gt);
     return Gt;
 }
-__device__ __forceinline__ float load_gate(const float* g, int stride, int t, int rows, int l) {
-    return g[(int64_t)(t + (l < rows ? l : rows - 1)) * stride];
+// The gate of token t + lane, for the wave that makes the gates; the other waves' loads read
+// nothing (see rows_of).
+__device__ __forceinline__ float load_gate(const float* g, int stride, int t, int rows, int l, bool mine) {
+    const Buffer b = rows_of(g + (int64_t)t * stride, stride, mine ? rows : 0, kLinChunk, 1);
+    return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(b, (unsigned)l * stride * 4u, 0, 0));
 }
 
 // S += a u over 32 tokens, four blocks of rows at a time, the terms of u in the outer loop: a
@@ -73,7 +76,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void linear_out_k
     __shared__ __align__(16) float sF[4][C];   // a wave's own decays
     __shared__ __align__(32) Gates gates[2];
 
-    const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, cl = l & 15, qg = l >> 4;
+    const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, cl = l & 15, qg = l >> 4;
     const int64_t slot = blockIdx.x / p.H;
     const int h = blockIdx.x % p.H, hk = h / (p.H / p.Hk);
     const Range rg = seg_range(p.cu, p.N, p.seqlen, p.T, slot, p.seg_len);
@@ -99,39 +102,31 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void linear_out_k
     const T* kp = (const T*)p.k + rg.lo * ldk + hk * DK;
     const T* vp = (const T*)p.v + rg.lo * ldv + h * DV;
     const float* gp = p.g + (p.g_stride ? rg.lo * p.g_stride : 0) + h;
-    const int total = (int)(rg.hi - rg.lo), es = p.out_bf16 ? 2 : 4;
-    char* op = (char*)p.o + (rg.lo * ldv + h * DV) * es;
-    const unsigned ooff = ((unsigned)cl * (unsigned)ldv + col + 4 * qg) * es;
+    const int total = (int)(rg.hi - rg.lo);
 
     // key blocks above the diagonal that a 32-wide product step still covers stay zero
     for (int x = tid; x < C * C; x += kThreads) sP[x] = (T)0.f;
 
     Tile<T, C, DK, kThreads> tq, tk;
     Tile<T, C, DV, kThreads> tv;
-    float g = 0.f;
-    if (total > 0) {
-        tq.load(qp, ldk, total, tid);
-        tk.load(kp, ldk, total, tid);
-        tv.load(vp, ldv, total, tid);
-        if (w == 0) {
-            put_gates(gates[0], load_gate(gp, p.g_stride, 0, total, l), total, l, false, 0.f);
-            if (total > C) g = load_gate(gp, p.g_stride, C, total - C, l);
-        }
-    }
+    tq.load(qp, ldk, total, tid);
+    tk.load(kp, ldk, total, tid);
+    tv.load(vp, ldv, total, tid);
+    const bool gw = w == 0;
+    if (gw) put_gates(gates[0], load_gate(gp, p.g_stride, 0, total, l, true), total, l, false, 0.f);
+    float g = load_gate(gp, p.g_stride, C, total - C, l, gw);
     for (int t0 = 0; t0 < total; t0 += C) {
         const int rows = total - t0, cl = opaque(l & 15), qg = opaque(l >> 4);
         const Gates& G = gates[(t0 / C) & 1];
         lds_barrier();   // the last chunk's readers are done
-        tq.store(sQ, rows, tid);
-        tk.store(sK, rows, tid);
-        tv.store(sV, rows, tid);
-        float gn = g;
-        if (rows > C) {
-            tq.load(qp + (t0 + C) * ldk, ldk, rows - C, tid);
-            tk.load(kp + (t0 + C) * ldk, ldk, rows - C, tid);
-            tv.load(vp + (t0 + C) * ldv, ldv, rows - C, tid);
-            if (w == 0 && rows > 2 * C) g = load_gate(gp, p.g_stride, t0 + 2 * C, rows - 2 * C, l);
-        }
+        tq.store(sQ, tid);
+        tk.store(sK, tid);
+        tv.store(sV, tid);
+        const float gn = g;
+        g = load_gate(gp, p.g_stride, t0 + 2 * C, rows - 2 * C, l, gw);
+        tq.load(qp + (t0 + C) * ldk, ldk, rows - C, tid);
+        tk.load(kp + (t0 + C) * ldk, ldk, rows - C, tid);
+        tv.load(vp + (t0 + C) * ldv, ldv, rows - C, tid);
         lds_barrier();
 
         const Lane<T, DK> lk(cl, qg);
@@ -172,7 +167,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void linear_out_k
                     }
                 }
         }
-        if (w == 0 && rows > C) put_gates(gates[(t0 / C + 1) & 1], gn, rows - C, l, false, 0.f);
+        if (gw) put_gates(gates[(t0 / C + 1) & 1], gn, rows - C, l, false, 0.f);
         // through the entering state; transposed: row = value column, column = token 16m + cl
         f32x4 O[NC][4];
 #pragma unroll
@@ -203,6 +198,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void linear_out_k
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk) vf[c][kk] = lv.col(sV, 2 * kk * RV, w * NC + c);
         lds_barrier();   // P is there
+        const Buffer out = out_rows(p.o, (rg.lo + t0) * ldv + h * DV, ldv, rows, C, DV, p.out_bf16);
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
 #pragma unroll
@@ -211,14 +207,8 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void linear_out_k
 #pragma unroll
                 for (int c = 0; c < NC; ++c) O[c][m] = mma_k32(O[c][m], vf[c][kk], f);
             }
-            if (16 * m + cl < rows) {
-                char* o = op + (int64_t)(t0 + 16 * m) * ldv * es;
 #pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    if (p.out_bf16) *reinterpret_cast<bf16x4*>(o + (ooff + 32u * c)) = pack4<bf16>(O[c][m]);
-                    else *reinterpret_cast<f32x4*>(o + (ooff + 64u * c)) = O[c][m];
-                }
-            }
+            for (int c = 0; c < NC; ++c) store4(out, (16 * m + cl) * (unsigned)ldv + col + 16 * c + 4 * qg, O[c][m], p.out_bf16);
         }
         // the state
         const float eC = G.E;
@@ -246,8 +236,9 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void linear_out_k
     }
 }
 
-// One workgroup per chain and 64 NC value columns (of a [DK][dv] state).
-template <typename T, int DK, int NC>
+// One workgroup per chain and 64 NC value columns (of a [DK][dv] state).  BORDER: the states at
+// the blocks' borders are written too.
+template <typename T, int DK, int NC, bool BORDER>
 __global__ __launch_bounds__(kThreads, 2) void linear_state_kernel(LinearStateParams p) {
     constexpr int C = kLinChunk, DV = 64 * NC;
     typedef typename V8<T>::t frag;
@@ -260,8 +251,8 @@ __global__ __launch_bounds__(kThreads, 2) void linear_state_kernel(LinearStatePa
     const int ways = p.dirs * (p.dv / DV), way = (int)(blockIdx.x / 8 % ways);
     const int chain = (int)(blockIdx.x / (8 * ways) * 8 + (blockIdx.x & 7));
     if (chain >= p.chains) return;
-    const LinearStateDir D = p.dir[way % p.dirs];
-    const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, cl = l & 15, qg = l >> 4;
+    const LinearStateDir D = way % p.dirs ? p.dir[1] : p.dir[0];
+    const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, cl = l & 15, qg = l >> 4;
     const int64_t slot = chain / p.H;
     const int h = chain % p.H, hk = h / (p.H / p.Hk);
     const Range rg = seg_range(p.cu, p.N, p.seqlen, p.T, slot, p.seg_len);
@@ -293,49 +284,49 @@ __global__ __launch_bounds__(kThreads, 2) void linear_state_kernel(LinearStatePa
     // a block of the document keeps its slot whatever the segments are
     const int64_t block0 = rg.start / kLinBlock + rg.n + (rg.lo - rg.start) / kLinBlock;
 
-    // Rows are loaded two chunks ahead: a chunk takes about as long here as a load does when the
-    // memory is busy.
+    // Chunks go in pairs, one block of the document, of which the second may be behind its end
+    // (it adds nothing); in reverse the second comes first.  Rows are loaded two chunks ahead: a
+    // chunk takes about as long here as a load does when the memory is busy.
     Tile<T, C, DK, kThreads> ta[2];
     Tile<T, C, DV, kThreads> tb[2];
-    float g = 0.f;
+    float g[2];   // the gates of the chunk after the current one, and of the next one after it
     double gsum = 0.0;
-    const int dir = rev ? -C : C, first = rev ? (chunks - 1) * C : 0;
-    if (chunks > 0) {
-        ta[0].load(ap + first * lda, lda, total - first, tid);
-        tb[0].load(bp + first * ldb, ldb, total - first, tid);
-        if (w == 0) {
-            gsum += put_gates(gates[0], load_gate(gp, p.g_stride, first, total - first, l), total - first, l, rev, p.scale);
-            if (chunks > 1) g = load_gate(gp, p.g_stride, first + dir, total - first - dir, l);
-        }
-        if (chunks > 1) {
-            ta[1].load(ap + (first + dir) * lda, lda, total - first - dir, tid);
-            tb[1].load(bp + (first + dir) * ldb, ldb, total - first - dir, tid);
-        }
-    }
-    auto step = [&](Tile<T, C, DK, kThreads>& ta, Tile<T, C, DV, kThreads>& tb, int x) __attribute__((always_inline)) {
-        const int t0 = first + x * dir, rows = total - t0, c0 = t0 / C, cl = opaque(l & 15), qg = opaque(l >> 4);
-        const Gates& G = gates[x & 1];
-        if (D.border && (rev ? ((c0 & 1) || x == 0) : !(c0 & 1))) {
-            T* b = (T*)D.border + ((block0 + c0 / 2) * p.H + h) * DK * dv + lane;
-#pragma unroll
-            for (int c = 0; c < NC; ++c)
-#pragma unroll
-                for (int d = 0; d < DK / 16; ++d) *reinterpret_cast<typename V4<T>::t*>(b + 16 * d * dv + 16 * c) = pack4<T>(S[c][d]);
-        }
+    const bool gw = w == 0;
+    const int pairs = (chunks + 1) / 2, dir = rev ? -C : C, first = rev ? (2 * pairs - 1) * C : 0;
+    // rows from token t on; none before the document (two chunks past the first in reverse, and
+    // in reverse all of an empty document's)
+    auto rows_at = [&](int t) { return t < 0 ? 0 : total - t; };
+    if (gw) gsum += put_gates(gates[0], load_gate(gp, p.g_stride, first, rows_at(first), l, true), rows_at(first), l, rev, p.scale);
+    ta[0].load(ap + first * lda, lda, rows_at(first), tid);
+    tb[0].load(bp + first * ldb, ldb, rows_at(first), tid);
+    g[1] = load_gate(gp, p.g_stride, first + dir, rows_at(first + dir), l, gw);
+    ta[1].load(ap + (first + dir) * lda, lda, rows_at(first + dir), tid);
+    tb[1].load(bp + (first + dir) * ldb, ldb, rows_at(first + dir), tid);
+    // t0: the chunk's first token; x: 0 for the first of a pair
+    auto step = [&](Tile<T, C, DK, kThreads>& ta, Tile<T, C, DV, kThreads>& tb, float& g, const float& gn, int t0, int x) __attribute__((always_inline)) {
+        const int cl = opaque(l & 15), qg = opaque(l >> 4);
+        const Gates& G = gates[x];
         lds_barrier();   // the last chunk's readers are done
-        ta.store(sA, rows, tid);
-        tb.store(sB, rows, tid);
-        const float gn = g;
-        const bool more = x + 1 < chunks;
-        if (x + 2 < chunks) {
-            ta.load(ap + (t0 + 2 * dir) * lda, lda, rows - 2 * dir, tid);
-            tb.load(bp + (t0 + 2 * dir) * ldb, ldb, rows - 2 * dir, tid);
-            if (w == 0) g = load_gate(gp, p.g_stride, t0 + 2 * dir, rows - 2 * dir, l);
-        }
+        ta.store(sA, tid);
+        tb.store(sB, tid);
+        if constexpr (BORDER)
+            if (x == 0) {
+                T* b = (T*)D.border + ((block0 + t0 / kLinBlock) * p.H + h) * DK * dv + lane;
+#pragma unroll
+                for (int c = 0; c < NC; ++c)
+#pragma unroll
+                    for (int d = 0; d < DK / 16; ++d) *reinterpret_cast<typename V4<T>::t*>(b + 16 * d * dv + 16 * c) = pack4<T>(S[c][d]);
+            }
+        const int t2 = t0 + 2 * dir, rows2 = rows_at(t2);
+        g = load_gate(gp, p.g_stride, t2, rows2, l, gw);
+        ta.load(ap + t2 * lda, lda, rows2, tid);
+        tb.load(bp + t2 * ldb, ldb, rows2, tid);
         lds_barrier();
         const Lane<T, DK> la(cl, qg);
         const Lane<T, DV> lb(cl, qg);
-        if (w == 0 && more) gsum += put_gates(gates[(x + 1) & 1], gn, rows - dir, l, rev, p.scale);
+        if (gw) {
+            gsum += put_gates(gates[1 - x], gn, rows_at(t0 + dir), l, rev, p.scale);
+        }
         const float eC = G.E;
 #pragma unroll
         for (int c = 0; c < NC; ++c)
@@ -350,9 +341,10 @@ __global__ __launch_bounds__(kThreads, 2) void linear_state_kernel(LinearStatePa
             add_outer<true>(S, u, [&](int d) { return la.col(sA, 2 * kk * 16 * DK * (int)sizeof(T), d); });
         }
     };
-    for (int x = 0; x < chunks; x += 2) {
-        step(ta[0], tb[0], x);
-        if (x + 1 < chunks) step(ta[1], tb[1], x + 1);
+    for (int y = 0; y < pairs; ++y) {
+        const int t0 = first + 2 * y * dir;
+        step(ta[0], tb[0], g[0], g[1], t0, 0);
+        step(ta[1], tb[1], g[1], g[0], t0 + dir, 1);
     }
     float* s = D.decay ? D.seg + (slot * p.H + h) * DK * dv + lane
                : D.last && tail ? D.last + ((int64_t)rg.n * p.H + h) * DK * dv + lane : nullptr;
@@ -426,8 +418,13 @@ template <typename T, int DK> static void states_d(const LinearStateParams& p, h
     const int64_t walks = p.seg_len && p.T / p.seg_len > p.N ? p.T / p.seg_len : p.N;
     const bool wide = p.dv == 128 && walks * p.H * p.dirs >= kWalkTarget;
     const dim3 grid((unsigned)(((int64_t)p.chains + 7) / 8 * 8 * p.dirs * (p.dv / (wide ? 128 : 64))));
-    if (wide) hipLaunchKernelGGL((linear_state_kernel<T, DK, 2>), grid, dim3(kThreads), 0, stream, p);
-    else hipLaunchKernelGGL((linear_state_kernel<T, DK, 1>), grid, dim3(kThreads), 0, stream, p);
+    if (wide) {
+        if (p.dir[0].border) hipLaunchKernelGGL((linear_state_kernel<T, DK, 2, true>), grid, dim3(kThreads), 0, stream, p);
+        else hipLaunchKernelGGL((linear_state_kernel<T, DK, 2, false>), grid, dim3(kThreads), 0, stream, p);
+    } else {
+        if (p.dir[0].border) hipLaunchKernelGGL((linear_state_kernel<T, DK, 1, true>), grid, dim3(kThreads), 0, stream, p);
+        else hipLaunchKernelGGL((linear_state_kernel<T, DK, 1, false>), grid, dim3(kThreads), 0, stream, p);
+    }
 }
 template <typename T> static hipError_t states_t(const LinearStateParams& p, int dk, hipStream_t stream) {
     if (dk == 128) states_d<T, 128>(p, stream);

@@ -166,7 +166,7 @@ __global__ __launch_bounds__(NL == 16 ? 256 : 512, sizeof(T) == 2 ? 4 : 2) void 
     typedef TreeShared<T, DELTA, NL, DK, DV> Shared;
     __shared__ __align__(32) Shared s;
 
-    const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, cl = l & 15, qg = l >> 4;
+    const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, cl = l & 15, qg = l >> 4;
     const int64_t nh = blockIdx.x, n = nh / p.H;
     const int h = (int)(nh % p.H), hk = h / (p.H / p.Hk), L = p.L;
     const int64_t node0 = n * L;
