@@ -255,12 +255,12 @@ def kda_linear_bwd_raw(cfg, total_tokens, num_seqs, q, k, v, g, cu_seqlens, init
 
 
 def kda_linear_decode_raw(cfg, num_seqs, q, k, v, g, state_in, state_out, o, stream) -> int:
-    return load().kda_linear_decode(ctypes.byref(cfg), num_seqs, q, k, v, g, state_in, state_out, o, stream)
+    return (_lib or load()).kda_linear_decode(cfg, num_seqs, q, k, v, g, state_in, state_out, o, stream)
 
 
 def kda_tree_raw(cfg, num_seqs, q, k, v, g, beta, parent, state, o, stream) -> int:
-    return load().kda_tree(ctypes.byref(cfg), num_seqs, q, k, v, g, beta, parent, state, o, stream)
+    return (_lib or load()).kda_tree(cfg, num_seqs, q, k, v, g, beta, parent, state, o, stream)
 
 
 def kda_tree_commit_raw(cfg, num_seqs, k, v, g, beta, parent, accept, state_in, state_out, stream) -> int:
-    return load().kda_tree_commit(ctypes.byref(cfg), num_seqs, k, v, g, beta, parent, accept, state_in, state_out, stream)
+    return (_lib or load()).kda_tree_commit(cfg, num_seqs, k, v, g, beta, parent, accept, state_in, state_out, stream)

@@ -4,21 +4,28 @@ from __future__ import annotations
 from ._lib import KDA_BF16, KDA_F32, check as lib_check
 
 
+_torch = None
+
+
 def torch_module():
-    import torch
-    return torch
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
 
 
 _DT_CODES = {}
 
 
 def dt_code(dtype):
-    if not _DT_CODES:
-        torch = torch_module()
-        _DT_CODES.update({torch.bfloat16: KDA_BF16, torch.float32: KDA_F32})
     code = _DT_CODES.get(dtype)
     if code is None:
-        raise TypeError(f"unsupported dtype {dtype}")
+        torch = torch_module()
+        _DT_CODES.update({torch.bfloat16: KDA_BF16, torch.float32: KDA_F32})
+        code = _DT_CODES.get(dtype)
+        if code is None:
+            raise TypeError(f"unsupported dtype {dtype}")
     return code
 
 

@@ -23,27 +23,29 @@ def _linear_workspace(size, T, N, *config):
 
 def _heads(q, k, v, lead_dims):
     """Shapes, device and dtype of q/k ``[..., Hk, dk]`` and v ``[..., H, dv]`` (q may be None)."""
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        if t is not None and t.dim() != lead_dims + 2:
-            raise ValueError(f"{name} must have {lead_dims + 2} dimensions, got shape {tuple(t.shape)}")
-    shape = tuple(k.shape)
-    lead, (Hk, dk), (H, dv) = shape[:-2], shape[-2:], tuple(v.shape[-2:])
-    dev, dt = k.device, k.dtype
-    if dev.type != "cuda":
+    shape, vshape = k.shape, v.shape
+    dims = lead_dims + 2
+    if len(shape) != dims or len(vshape) != dims or (q is not None and q.dim() != dims):
+        for name, t in (("q", q), ("k", k), ("v", v)):
+            if t is not None and t.dim() != dims:
+                raise ValueError(f"{name} must have {dims} dimensions, got shape {tuple(t.shape)}")
+    dev, dt, lead = k.device, k.dtype, tuple(shape[:-2])
+    if not k.is_cuda:
         raise ValueError("libkda runs on the GPU only: tensors must be on a cuda (HIP) device")
-    _check(q, "q", shape, dt, dev)
+    if q is not None:
+        _check(q, "q", shape, dt, dev)
     _check(k, "k", shape, dt, dev)
-    _check(v, "v", lead + (H, dv), dt, dev)
-    return lead, H, Hk, dk, dv, dev, dt
+    _check(v, "v", lead + vshape[-2:], dt, dev)
+    return lead, vshape[-2], shape[-2], shape[-1], vshape[-1], dev, dt
 
 
 def _gate(g, lead, H, dev):
     """fp32 gates ``[..., H]`` or ``[H]``."""
-    torch = _torch()
+    float32 = _torch().float32
     if g.dim() == 1:
-        _check(g, "g", (H,), torch.float32, dev)
+        _check(g, "g", (H,), float32, dev)
         return KDA_GATE_HEAD
-    _check(g, "g", lead + (H,), torch.float32, dev)
+    _check(g, "g", lead + (H,), float32, dev)
     return KDA_GATE_TOKEN
 
 
@@ -77,7 +79,7 @@ def kda_linear_fwd(q, k, v, g, cu_seqlens=None, initial_state=None, *, num_seqs:
     T, N, H, Hk, dk, dv, dev, dt, gate = _packed(q, k, v, g, cu_seqlens, num_seqs)
     out_dtype = out_dtype or torch.float32
     _check(initial_state, "initial_state", (N, H, dk, dv), torch.float32, dev)
-    config = (H, Hk, dk, dv, _dt_code(dt), _dt_code(out_dtype), gate, scale)
+    config = (H, Hk, dk, dv, _dt_code(dt), _dt_code(out_dtype), gate, float(scale))
     o = torch.empty_like(v, dtype=out_dtype)
     sf = torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev) if output_final_state else None
     wsb = _linear_workspace(_lib.kda_linear_fwd_workspace_size, T, N, *config)
@@ -99,7 +101,7 @@ def kda_linear_bwd(q, k, v, g, dO, cu_seqlens=None, initial_state=None, dS_final
     _check(dO, "dO", (T, H, dv), dt, dev)
     _check(initial_state, "initial_state", (N, H, dk, dv), torch.float32, dev)
     _check(dS_final, "dS_final", (N, H, dk, dv), torch.float32, dev)
-    config = (H, Hk, dk, dv, _dt_code(dt), _dt_code(out_dtype), gate, scale)
+    config = (H, Hk, dk, dv, _dt_code(dt), _dt_code(out_dtype), gate, float(scale))
     out = {
         "dq": torch.empty_like(q, dtype=out_dtype),
         "dk": torch.empty_like(k, dtype=out_dtype),
@@ -129,7 +131,7 @@ def kda_linear_decode(q, k, v, g, state=None, *, out_state=None, out_dtype=None,
     else:
         _check(out_state, "out_state", (N, H, dk, dv), torch.float32, dev)
     out_dtype = out_dtype or torch.float32
-    cfg = _linear_config(H, Hk, dk, dv, _dt_code(dt), _dt_code(out_dtype), gate, scale)
+    cfg = _linear_config(H, Hk, dk, dv, _dt_code(dt), _dt_code(out_dtype), gate, float(scale))
     o = torch.empty_like(v, dtype=out_dtype)
     _launch(dev, _lib.kda_linear_decode_raw, cfg, N, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(state), _ptr(out_state), _ptr(o))
     return o, out_state
@@ -151,7 +153,7 @@ def _tree_common(q, k, v, g, beta, parent, state, out_dtype, eps, scale):
         _check(beta, "beta", lead + (H,), dt, dev)
     _check(parent, "parent", (N, L), torch.int32, dev)
     _check(state, "state", (N, H, dk, dv), torch.float32, dev)
-    cfg = _tree_config(rule, H, Hk, dk, dv, L, _dt_code(dt), _dt_code(out_dtype), gate, eps, scale)
+    cfg = _tree_config(rule, H, Hk, dk, dv, L, _dt_code(dt), _dt_code(out_dtype), gate, float(eps), float(scale))
     return cfg, N, L, H, dk, dv, dev
 
 
