@@ -80,7 +80,9 @@ Plan walk_plan(const kda_linear_config* c, int64_t T, int32_t N, int ways, bool 
     if (ragged) share /= 2;
     int64_t L = (share + kLinBlock - 1) / kLinBlock * kLinBlock;
     if (L < kMinSegment) L = kMinSegment;
-    if (T <= L || N > kSegDocs) return p;
+    // up to two segments: summing the first one and then walking both takes as long as one walk
+    // (1003 tokens x 4 heads, fp32, backward: 52 us cut, 47 us whole)
+    if (T <= 2 * L || N > kSegDocs) return p;
     p.seg_len = (int32_t)L;
     p.chains = linear_slots(T, N, p.seg_len) * c->H;
     return p;
