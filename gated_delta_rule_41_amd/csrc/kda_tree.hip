@@ -12,10 +12,10 @@
 //
 // kda_tree_kernel: one workgroup per (sequence, head), every load issued first.  16 lanes per
 // node climb its path (A matrices, e^{G_i}) while the state arrives; one matrix product of all
-// rows with the state, transposed, so that a wave keeps its 16 value columns of every node;
-// the triangular solve level by level of the tree (nodes of one depth are independent); then
-// each lane reads its own nodes' paths for the outputs.  Sums run over true ancestors only, so
-// nothing in another branch, NaN included, reaches a node.
+// rows with the state, transposed, so that a wave keeps its 16 value columns of every node and
+// solves for them alone: level by level from the roots, every deeper node takes what its
+// ancestor of that level adds to u and o, one read of u for both.  Sums run over true ancestors
+// only, so nothing in another branch, NaN included, reaches a node.
 //
 // kda_tree_commit_kernel: the recurrence along the accepted path with the state in registers,
 // read and written once (kda_decode's layout).
@@ -27,29 +27,11 @@ using namespace lin;
 
 typedef unsigned long long u64;
 
-// Lane i of the calling wave takes node i: its strict ancestors as a bit mask and its depth,
-// depth -1 for an absent node.  A node is absent if its parent entry is below -1, is not
-// smaller than its own index, or names an absent node.  `par` is an LDS array of 64.
-__device__ __forceinline__ void climb(const int* par, int i, int L, u64& anc, int& depth) {
-    anc = 0;
-    depth = 0;
-    int a = i;
-    while (true) {
-        const int up = a < L ? par[a] : -2;
-        if (up < -1 || up >= a) {
-            depth = -1;
-            return;
-        }
-        if (up == -1) return;
-        anc |= 1ull << up;
-        ++depth;
-        a = up;
-    }
-}
-
-// A value that every lane holds, in scalar registers.
-__device__ __forceinline__ u64 uniform(u64 x) {
-    return (u64)(unsigned)__builtin_amdgcn_readfirstlane((int)x) | (u64)(unsigned)__builtin_amdgcn_readfirstlane((int)(x >> 32)) << 32;
+// The parent of node a of a tree: -1 for the state, below -1 if the node is absent (its entry
+// is below -1, or is not smaller than its own index).  `par` is an LDS array of 64.
+__device__ __forceinline__ int parent_of(const int* par, int a, int L) {
+    const int up = a < L ? par[a] : -2;
+    return up < a ? up : -2;
 }
 
 __device__ __forceinline__ float sigmoidf(float b) { return 1.f / (1.f + __expf(-b)); }
@@ -152,8 +134,8 @@ template <typename T, bool DELTA, int NL, int DK, int DV> struct TreeShared {
     // node i's products with its path: entry i (i + 1) / 2 + d for the node d steps up
     float kk[DELTA ? NL * (NL + 1) / 2 : 1], qk[NL * (NL + 1) / 2];
     float beta[NL], norm[NL];
-    int par[64], depth[64], levels;
-    u64 anc[64], level[64];
+    int par[64], depth[NL];   // depth: strict ancestors, -1 of an absent node
+    u64 anc[NL];              // strict ancestors as a bit mask
 };
 
 // NL: the tree's size rounded up to 16, 32 or 64 nodes.
@@ -239,47 +221,36 @@ __global__ __launch_bounds__(NL == 16 ? 256 : 512, sizeof(T) == 2 ? 4 : 2) void 
             }
         }
         __syncthreads();
-        if (w == 0) {
-            u64 anc;
-            int depth;
-            climb(s.par, l, L, anc, depth);
-            s.anc[l] = anc;
-            s.depth[l] = depth;
-            int levels = 0;
-            for (; levels < 64; ++levels) {
-                const u64 m = __ballot(depth == levels);
-                if (!m) break;
-                if (l == 0) s.level[levels] = m;
-            }
-            if (l == 0) s.levels = levels;
-        }
-        __syncthreads();
         // climb: node i's products with its path, and the product of the factors passed
 #pragma unroll
         for (int r = 0; r < ROUNDS; ++r) {
             const int i = (tid >> 4) + r * NODES;
-            if (s.depth[i] >= 0) {
-                const int t0 = i * (i + 1) / 2;
-                const float self = row16_sum(dot8(qv[r], kv[r]));
-                if (cl == 0) s.qk[t0] = self;
-                int d = t0;
-                for (int a = s.par[i]; a >= 0; a = s.par[a]) {
-                    const f32x8 ke = get_row<T, E>(s.x.c.k + a * DK, cl) * av[r];
-                    float norm = 1.f;
-                    if constexpr (DELTA) {
-                        norm = s.norm[a];
-                        av[r] *= get_row<float, E>(s.x.c.a + a * DK, cl);
-                    } else {
-                        av[r] *= splat8(s.x.c.a[a]);
-                    }
-                    ++d;
-                    const float qk = row16_sum(dot8(qv[r], ke)) * norm;
-                    if constexpr (DELTA) {
-                        const float kk = row16_sum(dot8(kv[r], ke)) * norm;
-                        if (cl == 0) s.kk[d] = kk;
-                    }
-                    if (cl == 0) s.qk[d] = qk;
+            const int t0 = i * (i + 1) / 2;
+            const float self = row16_sum(dot8(qv[r], kv[r]));
+            if (cl == 0) s.qk[t0] = self;
+            u64 anc = 0;
+            int d = 0, a = parent_of(s.par, i, L);
+            for (; a >= 0; a = parent_of(s.par, a, L)) {
+                const f32x8 ke = get_row<T, E>(s.x.c.k + a * DK, cl) * av[r];
+                float norm = 1.f;
+                if constexpr (DELTA) {
+                    norm = s.norm[a];
+                    av[r] *= get_row<float, E>(s.x.c.a + a * DK, cl);
+                } else {
+                    av[r] *= splat8(s.x.c.a[a]);
                 }
+                ++d;
+                anc |= 1ull << a;
+                const float qk = row16_sum(dot8(qv[r], ke)) * norm;
+                if constexpr (DELTA) {
+                    const float kk = row16_sum(dot8(kv[r], ke)) * norm;
+                    if (cl == 0) s.kk[t0 + d] = kk;
+                }
+                if (cl == 0) s.qk[t0 + d] = qk;
+            }
+            if (cl == 0) {
+                s.anc[i] = anc;
+                s.depth[i] = a < -1 ? -1 : d;
             }
         }
 #pragma unroll
@@ -288,6 +259,17 @@ __global__ __launch_bounds__(NL == 16 ? 256 : 512, sizeof(T) == 2 ? 4 : 2) void 
             for (int y = 0; y < DK / 32; ++y) st[c][y].set(x[c][y]);
     }
 
+    // v meanwhile; value columns 16 cg + 4 qg + i of node 16 m + cl, as the products below
+    auto mine = [&](int m) { return STEP == 1 || m % STEP == w / CG; };
+    auto column = [&](int c) { return 16 * (w % CG + c * WAVES) + 4 * qg; };
+    typename V4<T>::t v[COLS][MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        const int i = 16 * m + cl < L ? 16 * m + cl : 0;
+#pragma unroll
+        for (int c = 0; c < COLS; ++c)
+            if (mine(m)) v[c][m] = *reinterpret_cast<const typename V4<T>::t*>((const T*)p.v + ((node0 + i) * p.H + h) * DV + column(c));
+    }
     // rows times the state; row = value column 16 cg + 4 qg + i, column = node 16 m + cl
     const Lane<T, DK> lane(cl, qg);
     constexpr int R16 = 16 * DK * sizeof(T);
@@ -304,7 +286,7 @@ __global__ __launch_bounds__(NL == 16 ? 256 : 512, sizeof(T) == 2 ? 4 : 2) void 
             f32x4 x[COLS];
 #pragma unroll
             for (int c = 0; c < COLS; ++c) x[c] = zero4();
-            if ((STEP == 1 || (m % STEP) == w / CG) && 16 * m < L) {
+            if (mine(m) && 16 * m < L) {
 #pragma unroll
                 for (int y = 0; y < DK / 32; ++y) {
                     Two<T> f;
@@ -318,59 +300,75 @@ __global__ __launch_bounds__(NL == 16 ? 256 : 512, sizeof(T) == 2 ? 4 : 2) void 
         }
     }
     __syncthreads();
-#pragma unroll
-    for (int c = 0; c < COLS; ++c) {
-        const int col = 16 * (w % CG + c * WAVES) + 4 * qg;
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            const int i = 16 * m + cl;
-            if ((STEP == 1 || (m % STEP) == w / CG) && i < L) {
-                f32x4 u = unpack4(*reinterpret_cast<const typename V4<T>::t*>((const T*)p.v + ((node0 + i) * p.H + h) * DV + col));
-                if constexpr (DELTA) u = s.beta[i] * (u - ks[c][m]);
-                *reinterpret_cast<f32x4*>(s.x.u + i * Shared::LU + col) = u;
-            }
-        }
-    }
-    __syncthreads();
-
-    // u, level by level: a wave takes a node, a lane DV / 64 columns
-    constexpr int CPL = DV / 64;
-    if constexpr (DELTA) {
-        const int levels = s.levels;
-        for (int d = 1; d < levels; ++d) {
-            u64 nodes = uniform(s.level[d]);
-            for (int x = 0; nodes; ++x, nodes &= nodes - 1) {
-                if (x % WAVES != w) continue;
-                const int i = __ffsll((long long)nodes) - 1;
-                const float* A = s.kk + i * (i + 1) / 2 + d;   // the path from the root down
-                float u[CPL] = {};
-                for (u64 m = uniform(s.anc[i]); m; m &= m - 1, --A) {
-                    const int a = __ffsll((long long)m) - 1;
-#pragma unroll
-                    for (int c = 0; c < CPL; ++c) u[c] += *A * s.x.u[a * Shared::LU + l + 64 * c];
-                }
-#pragma unroll
-                for (int c = 0; c < CPL; ++c) s.x.u[i * Shared::LU + l + 64 * c] -= s.beta[i] * u[c];
-            }
-            __syncthreads();
-        }
-    }
-    // outputs: every lane follows its own nodes' paths
+    // Nodes of depth 0, 1, ...: their u is complete, and every deeper node takes its part of
+    // u and o from its ancestor of that depth.  A wave needs no other wave's columns, and a
+    // wave's LDS operations are done in order; only where waves share columns (STEP) they wait
+    // for each other.
+    u64 anc[MT];
+    int depth[MT], at[MT], levels = 0;   // at: the products with the next ancestor
+    float beta[MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
         const int i = 16 * m + cl;
-        if ((STEP == 1 || (m % STEP) == w / CG) && i < L) {
-            const bool live = s.depth[i] >= 0;
-            int d = i * (i + 1) / 2;
-            for (int a = live ? i : -1; a >= 0; a = s.par[a], ++d) {
-                const float A = s.qk[d];
+        depth[m] = s.depth[i];
+        anc[m] = s.anc[i];
+        at[m] = i * (i + 1) / 2 + (depth[m] > 0 ? depth[m] : 0);
+        beta[m] = DELTA ? s.beta[i] : 1.f;
+        while (__ballot(depth[m] >= levels)) ++levels;
 #pragma unroll
-                for (int c = 0; c < COLS; ++c)
-                    qs[c][m] += A * *reinterpret_cast<const f32x4*>(s.x.u + a * Shared::LU + 16 * (w % CG + c * WAVES) + 4 * qg);
+        for (int c = 0; c < COLS; ++c)
+            if (mine(m)) ks[c][m] = DELTA ? unpack4(v[c][m]) - ks[c][m] : unpack4(v[c][m]);
+    }
+    for (int d = 0; d < levels; ++d) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+            if (mine(m) && depth[m] == d) {
+                const int i = 16 * m + cl;
+                const float self = s.qk[i * (i + 1) / 2];
+#pragma unroll
+                for (int c = 0; c < COLS; ++c) {
+                    const f32x4 u = beta[m] * ks[c][m];
+                    qs[c][m] += self * u;
+                    *reinterpret_cast<f32x4*>(s.x.u + i * Shared::LU + column(c)) = u;
+                }
+            }
+        if (d + 1 == levels) break;
+        if constexpr (STEP > 1) __syncthreads();
+        else asm volatile("" ::: "memory");
+        // reads without branches, so that those of all nodes are in flight together
+        float kk[MT], qk[MT];
+        f32x4 u[COLS][MT];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+            if (mine(m)) {
+                const int a = anc[m] ? __ffsll((long long)anc[m]) - 1 : 0;
+                if constexpr (DELTA) kk[m] = s.kk[at[m]];
+                qk[m] = s.qk[at[m]];
+#pragma unroll
+                for (int c = 0; c < COLS; ++c) u[c][m] = *reinterpret_cast<const f32x4*>(s.x.u + a * Shared::LU + column(c));
             }
 #pragma unroll
+        for (int m = 0; m < MT; ++m)
+            if (mine(m)) {
+                const bool on = depth[m] > d;
+#pragma unroll
+                for (int c = 0; c < COLS; ++c)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if constexpr (DELTA) ks[c][m][e] -= keep(kk[m] * u[c][m][e], on);
+                        qs[c][m][e] += keep(qk[m] * u[c][m][e], on);
+                    }
+                at[m] -= on;
+                anc[m] &= anc[m] - 1;
+            }
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        const int i = 16 * m + cl;
+        if (mine(m) && i < L) {
+#pragma unroll
             for (int c = 0; c < COLS; ++c)
-                store4(p.o, ((node0 + i) * p.H + h) * DV + 16 * (w % CG + c * WAVES) + 4 * qg, live ? qs[c][m] : zero4(), p.out_bf16);
+                store4(p.o, ((node0 + i) * p.H + h) * DV + column(c), depth[m] >= 0 ? qs[c][m] : zero4(), p.out_bf16);
         }
     }
 }
@@ -398,9 +396,9 @@ __global__ __launch_bounds__(kThreads) void kda_tree_commit_kernel(TreeParams p)
     // the path as a bit mask: a parent's index is below its child's, so ascending bits run from the root
     u64 path = 0;
     if (leaf >= 0 && leaf < p.L) {
-        int depth;
-        climb(sPar, leaf, p.L, path, depth);
-        path = depth < 0 ? 0 : path | 1ull << leaf;
+        int a = leaf;
+        for (; a >= 0; a = parent_of(sPar, a, p.L)) path |= 1ull << a;
+        if (a < -1) path = 0;   // an absent node
     }
     for (int done = 0; path;) {
         const int count = __popcll(path) < BATCH ? __popcll(path) : BATCH;
