@@ -192,8 +192,15 @@ def kda_tree_commit(k, v, g, beta, parent, accept, state=None, *, out_state=None
     return out_state
 
 
+def _upstream(grad):
+    """A gradient as the kernels take it: autograd may hand over a view of a larger tensor."""
+    grad = grad.contiguous()
+    return grad if grad.data_ptr() % 16 == 0 else grad.clone()
+
+
 def _autograd_function():
     torch = _torch()
+    from torch.autograd.function import once_differentiable
 
     class LinearFunction(torch.autograd.Function):
         """Autograd glue: the backward runs from the inputs, so nothing else is saved.
@@ -207,10 +214,11 @@ def _autograd_function():
             return o, sf
 
         @staticmethod
+        @once_differentiable
         def backward(ctx, d_o, d_sf):
             q, k, v, g, cu_seqlens, s0 = ctx.saved_tensors
-            d_o = (d_o if d_o is not None else torch.zeros_like(v)).to(q.dtype).contiguous()
-            d_sf = d_sf.contiguous() if d_sf is not None else None
+            d_o = _upstream((d_o if d_o is not None else torch.zeros_like(v)).to(q.dtype))
+            d_sf = _upstream(d_sf) if d_sf is not None else None
             gr = kda_linear_bwd(q, k, v, g, d_o, cu_seqlens, s0, d_sf, num_seqs=ctx.num_seqs, out_dtype=q.dtype,
                                 scale=ctx.scale, output_d_initial_state=s0 is not None)
             return gr["dq"], gr["dk"], gr["dv"], gr["dg"].to(g.dtype), None, gr["dS0"], None, None
@@ -225,7 +233,7 @@ def kda_linear(q, k, v, g, cu_seqlens=None, initial_state=None, *, num_seqs: Opt
     """kda_linear_fwd as a differentiable torch op: returns ``(o, final_state)``
     (fp32) and, under autograd, back-propagates through kda_linear_bwd.  The
     upstream gradient of o is cast to the input dtype, and the gradients of q,
-    k, v and g are rounded to it."""
+    k, v and g are rounded to it.  A second differentiation is refused."""
     global _FN
     if _FN is None:
         _FN = _autograd_function()

@@ -141,7 +141,7 @@ def test_backward(lens, H, Hk, dk, dv, dtype, gate):
     ([1500, 1730], 2, 1, 64, 64, "token"),
     ([0, 3, 2600, 130, 0, 1024, 512, 513, 0], 1, 1, 64, 64, "head"),
     ([1100, 64], 2, 2, 128, 128, "token"),
-    ([700], 3, 1, 64, 128, "token"),
+    ([1700], 3, 1, 64, 128, "token"),
 ])
 def test_segments(dtype, lens, H, Hk, dk, dv, gate):
     """Documents long enough to be cut into segments (512 tokens at these sizes), among short and empty ones."""
@@ -157,6 +157,50 @@ def test_segments(dtype, lens, H, Hk, dk, dv, gate):
     h["s0"] = h["dS"] = np.zeros((len(lens), H, dk, dv))
     check_fwd(d, h, cu, lens, dtype, torch.float32, 0.125)
     check_bwd(d, h, cu, lens, dtype, torch.float32, 0.125)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("short,long", [([0, 1, 2, 5, 9], [1290]), ([4, 3, 0, 2], [])])
+def test_many_documents(dtype, short, long):
+    """131 documents, one of them in segments, and 600 (more than are cut): looked up 64 at a time."""
+    need_gpu()
+    lens = (short * 65)[:70] + long + (short * 65)[:60] if long else short * 150
+    _say(f"{len(lens)} documents {dtype}")
+    d, h, cu = make(20, lens, 2, 1, 64, 64, dtype)
+    sizes = kda.linear._lib.make_linear_config(2, 1, 64, 64), sum(lens), len(lens)
+    assert sum(lens) > 1024 and (kda.linear._lib.kda_linear_fwd_workspace_size(*sizes) > 0) == bool(long)
+    check_fwd(d, h, cu, lens, dtype, torch.float32, 0.125)
+    check_bwd(d, h, cu, lens, dtype, torch.float32, 0.125)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("lens,H", [([129, 1, 200, 64, 0, 130, 65, 63], 32), ([8192], 64), ([2900] + [73, 64, 1] * 5, 16)])
+def test_many_heads(dtype, lens, H):
+    """Enough walks that a workgroup of the state kernel takes 128 value columns; some heads are compared, each with the
+    reference and with a call for it alone."""
+    need_gpu()
+    _say(f"{H} heads {lens[:2]}... {dtype}")
+    d, h, cu = make(21, lens, H, H, 64, 128, dtype)
+    o, sf = kda.kda_linear_fwd(d["q"], d["k"], d["v"], d["g"], cu, d["s0"], scale=0.125)
+    gr = kda.kda_linear_bwd(d["q"], d["k"], d["v"], d["g"], d["dO"], cu, d["s0"], d["dS"], scale=0.125)
+    torch.cuda.synchronize()
+    for x in (o, sf, *gr.values()):
+        assert bool(torch.isfinite(x).all())
+    heads = [0, H // 2 + 1, H - 1] if sum(lens) < 1024 else [H - 1]
+    for head in heads:
+        # the same head alone: another plan, other kernels
+        e = {n: t[:, head:head + 1].contiguous() for n, t in d.items()}
+        eh = {n: t[:, head:head + 1] for n, t in h.items()}
+        o1, sf1 = check_fwd(e, eh, cu, lens, dtype, torch.float32, 0.125)
+        gr1 = check_bwd(e, eh, cu, lens, dtype, torch.float32, 0.125)
+        # The inputs are independent, so the norm of sqrt(V) is about the output's own.  bf16: each side rounds P (or dP)
+        # and the state once, 2^-8 each.
+        for n, a, b in [("o", o, o1), ("final", sf, sf1)] + [(n, gr[n], gr1[n]) for n in ("dq", "dk", "dv", "dg", "dS0")]:
+            a = a[:, head:head + 1].double()
+            off, size = float((a - b.double()).norm()), float(b.double().norm())
+            most = STEPS + (0 if dtype == "f32" or n in ("final", "dS0") else 4 * BF16)
+            _say(f"  head {head} {n}: {off / size:.2e} of its norm from the head alone, at most {most:.2e}")
+            assert off <= most * size, n
 
 
 def test_strong_and_infinite_gates():
@@ -352,6 +396,38 @@ def test_autograd_matches_direct_calls():
         o, sf = kda.kda_linear(leaves["q"], d["k"], d["v"], d["g"], cu, scale=0.125)
         sf.sum().backward()
         assert torch.equal(leaves["q"].grad, torch.zeros_like(d["q"]))
+
+
+def test_autograd_upstream_views_and_second_order():
+    """Upstream gradients that are odd views of larger tensors; a second differentiation raises."""
+    need_gpu()
+    lens = [40, 9]
+    d, h, cu = make(15, lens, 2, 2, 64, 64, "f32")
+    gr = kda.kda_linear_bwd(d["q"], d["k"], d["v"], d["g"], d["dO"], cu, d["s0"], d["dS"], scale=0.125)
+    leaves = {n: d[n].clone().requires_grad_(True) for n in ("q", "k", "v", "g", "s0")}
+    o, sf = kda.kda_linear(leaves["q"], leaves["k"], leaves["v"], leaves["g"], cu, leaves["s0"], scale=0.125)
+    one = torch.zeros(1, device="cuda", requires_grad=True)
+    w = torch.cat([torch.zeros(1, device="cuda"), d["dO"].flatten(), d["dS"].flatten()])
+    (torch.cat([one, o.flatten(), sf.flatten()]) * w).sum().backward()
+    torch.cuda.synchronize()
+    for n, gn in (("q", "dq"), ("k", "dk"), ("v", "dv"), ("g", "dg"), ("s0", "dS0")):
+        assert torch.equal(leaves[n].grad, gr[gn]), n
+    o, _ = kda.kda_linear(leaves["q"], d["k"], d["v"], d["g"], cu, scale=0.125)
+    (dq,) = torch.autograd.grad(o.square().sum(), leaves["q"], create_graph=True)
+    with pytest.raises(RuntimeError):
+        dq.sum().backward()
+
+
+def test_scale_is_read_at_each_call():
+    """A tensor as scale: its value counts, not its identity."""
+    need_gpu()
+    d, _, cu = make(16, [20], 1, 1, 64, 64, "f32")
+    scale = torch.tensor(0.5)
+    a, _ = kda.kda_linear_fwd(d["q"], d["k"], d["v"], d["g"], cu, d["s0"], scale=scale)
+    scale.mul_(2)
+    b, _ = kda.kda_linear_fwd(d["q"], d["k"], d["v"], d["g"], cu, d["s0"], scale=scale)
+    torch.cuda.synchronize()
+    assert torch.equal(2 * a, b)
 
 
 def test_repeatable_graph_streams():
