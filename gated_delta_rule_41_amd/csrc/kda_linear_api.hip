@@ -5,6 +5,8 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <algorithm>
+
 #include "../../include/kda.h"
 #include "kda_internal.h"
 #include "kda_linear.h"
@@ -65,7 +67,21 @@ bool grid_fits(int64_t workgroups, int threads) {
 // is a host function; cu_seqlens is on the device, so any document may have all the tokens.
 // More than kSegDocs documents even out by their number (and finding a segment would take a
 // workgroup longer).
-constexpr int64_t kMinSegment = 512;     // tokens: below, a segment's state outweighs its rows
+// Equal shares of small streams would be too short: a segment costs its state four moves
+// through memory (T H dk dv / L elements over all of them) and a step of its document's carry
+// (T / L of them in a row), against 2 L tokens of walking.  The two square roots are where those
+// are equal, with factors from these times (us; forward, 128 x 128, L a floor under the share),
+// taken at powers of two as the floor is:
+//     tokens x heads         128   256   512  1024
+//     2048 x 8                35    40    58   130
+//     8192 x 8                70    57    65
+//     32768 x 4              108   107    87   110
+//     32768 x 8, 16 documents     154   124   127
+//     32768 x 1              103    73    75   108
+//     131072 x 1             211   211   140   136
+// Up to two segments, or eight chunks, are walked whole: summing the first and then walking both
+// takes as long as one walk (1003 tokens x 4 heads, fp32, backward: 52 us in two, 48 whole).
+constexpr int64_t kWholeTokens = 8 * kLinChunk;
 
 struct Plan {
     int32_t seg_len;   // 0: whole documents
@@ -76,13 +92,13 @@ struct Plan {
 // heads: 263 -> 244 us; one document of 131072 tokens x 16 heads would lose: 787 -> 820 us).
 Plan walk_plan(const kda_linear_config* c, int64_t T, int32_t N, int ways, bool ragged) {
     Plan p = {0, (int64_t)N * c->H};
-    int64_t share = T * c->H / kWalkTarget * ways;
-    if (ragged) share /= 2;
-    int64_t L = (share + kLinBlock - 1) / kLinBlock * kLinBlock;
-    if (L < kMinSegment) L = kMinSegment;
-    // up to two segments: summing the first one and then walking both takes as long as one walk
-    // (1003 tokens x 4 heads, fp32, backward: 52 us cut, 47 us whole)
-    if (T <= 2 * L || N > kSegDocs) return p;
+    const double even = ragged ? 0.5 : 1.0, rows = even * T * c->H;
+    const int64_t share = (int64_t)(rows * ways / kWalkTarget);
+    const double least = std::max(0.9 * sqrt(rows * c->dk * c->dv) / 128.0, 1.4 * sqrt((double)T));
+    int64_t floor = kLinBlock;
+    while (floor < least) floor *= 2;
+    const int64_t L = std::max(floor, (share + kLinBlock - 1) / kLinBlock * kLinBlock);
+    if (T <= 2 * L || T <= kWholeTokens || N > kSegDocs) return p;
     p.seg_len = (int32_t)L;
     p.chains = linear_slots(T, N, p.seg_len) * c->H;
     return p;
@@ -137,10 +153,9 @@ BwdLayout bwd_layout(const kda_linear_config* c, int64_t T, int32_t N) {
     return b;
 }
 
-kda_status check_sizes(const kda_linear_config* c, int64_t T, int32_t N, const int32_t* cu) {
+kda_status check_sizes(const kda_linear_config* c, int64_t T, int32_t N) {
     if (T < 0 || T >= ((int64_t)1 << 31)) return fail(KDA_ERR_INVALID_ARG, "total_tokens must be in [0, 2^31)%s");
     if (N < 1) return fail(KDA_ERR_INVALID_ARG, "num_seqs must be >= 1%s");
-    if (!cu && T % N) return fail(KDA_ERR_INVALID_ARG, "cu_seqlens is NULL but total_tokens is not a multiple of num_seqs%s");
     // the kernels address a block's rows with 32-bit byte offsets from a 64-bit base
     if ((int64_t)kLinBlock * c->H * 128 * 4 >= ((int64_t)1 << 31)) return fail(KDA_ERR_UNSUPPORTED, "H too large%s");
     // the largest launches: the walks' chains, the a block's gradients in at most three roles a head, the carry
@@ -148,6 +163,12 @@ kda_status check_sizes(const kda_linear_config* c, int64_t T, int32_t N, const i
         !grid_fits((int64_t)N * c->H * (c->dk * c->dv / (4 * kThreads)), kThreads))
         return fail(KDA_ERR_UNSUPPORTED, "num_seqs, H or total_tokens too large for one launch%s");
     return KDA_OK;
+}
+kda_status check_stream(const kda_linear_config* c, int64_t T, int32_t N, const int32_t* cu) {
+    KDA_TRY(check_config(c));
+    KDA_TRY(check_sizes(c, T, N));
+    if (!cu && T % N) return fail(KDA_ERR_INVALID_ARG, "cu_seqlens is NULL but total_tokens is not a multiple of num_seqs%s");
+    return ptr(cu, "cu_seqlens", false);
 }
 
 bool overlap(const void* a, const void* b, size_t bytes) {
@@ -193,12 +214,12 @@ void kda_linear_config_init(kda_linear_config* cfg, int32_t H, int32_t Hk, int32
 }
 
 size_t kda_linear_fwd_workspace_size(const kda_linear_config* cfg, int64_t T, int32_t N) {
-    if (check_config(cfg) != KDA_OK || T < 0 || N < 1) return 0;
+    if (check_config(cfg) != KDA_OK || check_sizes(cfg, T, N) != KDA_OK) return 0;
     return fwd_layout(cfg, T, N).total;
 }
 
 size_t kda_linear_bwd_workspace_size(const kda_linear_config* cfg, int64_t T, int32_t N) {
-    if (check_config(cfg) != KDA_OK || T < 0 || N < 1) return 0;
+    if (check_config(cfg) != KDA_OK || check_sizes(cfg, T, N) != KDA_OK) return 0;
     return bwd_layout(cfg, T, N).total;
 }
 
@@ -206,14 +227,12 @@ kda_status kda_linear_fwd(const kda_linear_config* cfg, int64_t T, int32_t N, co
                           const float* g, const int32_t* cu, const float* s0, void* o, float* sfinal, void* workspace,
                           size_t workspace_bytes, void* stream) {
     error_text()[0] = 0;
-    KDA_TRY(check_config(cfg));
-    KDA_TRY(check_sizes(cfg, T, N, cu));
+    KDA_TRY(check_stream(cfg, T, N, cu));
     KDA_TRY(ptr(q, "q", T > 0));
     KDA_TRY(ptr(k, "k", T > 0));
     KDA_TRY(ptr(v, "v", T > 0));
     KDA_TRY(ptr(g, "g", T > 0));
     KDA_TRY(ptr(o, "o", T > 0));
-    KDA_TRY(ptr(cu, "cu_seqlens", false));
     KDA_TRY(ptr(s0, "initial_state", false));
     KDA_TRY(ptr(sfinal, "final_state", false));
     const FwdLayout f = fwd_layout(cfg, T, N);
@@ -254,8 +273,7 @@ kda_status kda_linear_bwd(const kda_linear_config* cfg, int64_t T, int32_t N, co
                           const float* g, const int32_t* cu, const float* s0, const void* dO, const float* dSf, void* dq,
                           void* dk, void* dv, void* dg, float* dS0, void* workspace, size_t workspace_bytes, void* stream) {
     error_text()[0] = 0;
-    KDA_TRY(check_config(cfg));
-    KDA_TRY(check_sizes(cfg, T, N, cu));
+    KDA_TRY(check_stream(cfg, T, N, cu));
     const bool any = T > 0;
     KDA_TRY(ptr(q, "q", any));
     KDA_TRY(ptr(k, "k", any));
@@ -266,7 +284,6 @@ kda_status kda_linear_bwd(const kda_linear_config* cfg, int64_t T, int32_t N, co
     KDA_TRY(ptr(dk, "dk", any));
     KDA_TRY(ptr(dv, "dv", any));
     KDA_TRY(ptr(dg, "dg", any || cfg->gate == KDA_GATE_HEAD));
-    KDA_TRY(ptr(cu, "cu_seqlens", false));
     KDA_TRY(ptr(s0, "initial_state", false));
     KDA_TRY(ptr(dSf, "dS_final", false));
     KDA_TRY(ptr(dS0, "d_initial_state", false));

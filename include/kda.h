@@ -291,7 +291,10 @@ kda_status kda_decode(const kda_config* cfg, int32_t num_seqs, const void* q, co
  * bf16 inputs: products on bf16 operands with fp32 accumulation; P, dP and the
  * state as it is read are rounded to bf16 once; the states themselves, their
  * gradients and their updates keep fp32 accuracy.  fp32 inputs: fp32
- * throughout.  Sums of g are kept in 64 bits.  Results are deterministic. */
+ * throughout.  Sums of g are kept in 64 bits.  Results are deterministic.
+ * H below 2^15 (the kernels address a 128-token block's rows with 32-bit
+ * offsets), and four workgroups of 512 threads per 128-token block, document
+ * and head in one launch: (total_tokens/128 + num_seqs + 8) * H below 2^21. */
 typedef enum kda_gate { KDA_GATE_TOKEN = 0, KDA_GATE_HEAD = 1 } kda_gate;
 
 typedef struct kda_linear_config {
@@ -309,10 +312,10 @@ typedef struct kda_linear_config {
 void kda_linear_config_init(kda_linear_config* cfg, int32_t H, int32_t Hk, int32_t dk, int32_t dv);
 
 /* Scratch for one call, in bytes (pure host functions; 0 for an invalid
- * config).  The forward's is non-zero when it cuts documents into segments
- * (those longer than an equal share of total_tokens * H; a rule on cfg and the
- * sizes only): each segment's own sum of k v^T, then the states entering the
- * segments.  The backward's holds S and dL/dS at every 128-token block (input
+ * config or sizes).  The forward's is non-zero when it cuts documents into
+ * segments (those longer than an equal share of total_tokens * H, where that
+ * pays; at most 512 documents; a rule on cfg and the sizes only): each
+ * segment's own sum of k v^T, then the states entering the segments.  The backward's holds S and dL/dS at every 128-token block (input
  * type), per-token sums for dg, and the segments' states likewise. */
 size_t kda_linear_fwd_workspace_size(const kda_linear_config* cfg, int64_t total_tokens, int32_t num_seqs);
 size_t kda_linear_bwd_workspace_size(const kda_linear_config* cfg, int64_t total_tokens, int32_t num_seqs);

@@ -144,7 +144,7 @@ def test_backward(lens, H, Hk, dk, dv, dtype, gate):
     ([1700], 3, 1, 64, 128, "token"),
 ])
 def test_segments(dtype, lens, H, Hk, dk, dv, gate):
-    """Documents long enough to be cut into segments (512 tokens at these sizes), among short and empty ones."""
+    """Documents long enough to be cut into segments (128 tokens at these sizes), among short and empty ones."""
     need_gpu()
     _say(f"segments {lens} {dtype}")
     d, h, cu = make(3, lens, H, Hk, dk, dv, dtype, gate, -3.0)

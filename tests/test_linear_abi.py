@@ -126,6 +126,11 @@ def test_forward_and_backward_refuse_bad_arguments():
     assert fwd(cfg, T=8192, ws=0, wsb=need) == KDA_ERR_INVALID_ARG
     assert _lib.kda_linear_fwd_workspace_size(lin(H=1024, Hk=1024), 8192, 1) == 0
     assert _lib.kda_linear_fwd_workspace_size(cfg, 128, 1) == 0
+    # sizes that the calls refuse need no workspace either
+    for T, N in ((-1, 1), (1 << 31, 1), (1 << 62, 1), ((1 << 31) - 64, 1), (128, 0), (128, -1)):
+        assert _lib.kda_linear_fwd_workspace_size(cfg, T, N) == 0 and _lib.kda_linear_bwd_workspace_size(cfg, T, N) == 0
+    big = lin(H=1 << 30, Hk=1 << 30)
+    assert _lib.kda_linear_bwd_workspace_size(big, 1 << 20, 1) == 0 and fwd(big) == KDA_ERR_UNSUPPORTED
 
 
 def test_decode_refuses_bad_arguments():
