@@ -200,9 +200,7 @@ __device__ __forceinline__ void dq_role(const LinearBwdParams& p, const Task& t,
         lds_barrier();
     }
     const int l = threadIdx.x & 63, row = 16 * rb + (l & 15);
-    const Buffer out = out_rows(p.dq, t.lo * ldk + t.hk * DK, ldk, rows, kB, DK, p.out_bf16);
-#pragma unroll
-    for (int m = 0; m < DK / 16; ++m) store4(out, row * (unsigned)ldk + 16 * m + 4 * (l >> 4), dq[m], p.out_bf16);
+    store_row<DK>(p.dq, t.lo * ldk + t.hk * DK, ldk, rows, kB, row, l >> 4, dq, p.out_bf16);
 }
 
 template <typename T, int DK, int DV, bool GROUPED>
@@ -304,9 +302,7 @@ __device__ __forceinline__ void dk_role(const LinearBwdParams& p, const Task& t,
         lds_barrier();
     }
     const int l = threadIdx.x & 63, key = 16 * rb + (l & 15);
-    const Buffer out = out_rows(p.dk_out, t.lo * ldk + t.hk * DK, ldk, rows, kB, DK, p.out_bf16);
-#pragma unroll
-    for (int m = 0; m < DK / 16; ++m) store4(out, key * (unsigned)ldk + 16 * m + 4 * (l >> 4), dk[m], p.out_bf16);
+    store_row<DK>(p.dk_out, t.lo * ldk + t.hk * DK, ldk, rows, kB, key, l >> 4, dk, p.out_bf16);
 }
 
 template <typename T, int DK, int DV>
@@ -397,9 +393,7 @@ __device__ __forceinline__ void dv_role(const LinearBwdParams& p, const Task& t,
 #pragma unroll
         for (int m = 0; m < DV / 16; ++m) dv[m] = mma_k32(dv[m], lv.col(s.a, 2 * x * RV, m), f);
     }
-    const Buffer out = out_rows(p.dv_out, t.lo * ldv + h * DV, ldv, rows, kB, DV, p.out_bf16);
-#pragma unroll
-    for (int m = 0; m < DV / 16; ++m) store4(out, key * (unsigned)ldv + 16 * m + 4 * qg, dv[m], p.out_bf16);
+    store_row<DV>(p.dv_out, t.lo * ldv + h * DV, ldv, rows, kB, key, qg, dv, p.out_bf16);
 }
 
 // GROUPED: several value heads to a key head.

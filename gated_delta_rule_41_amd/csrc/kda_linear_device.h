@@ -308,14 +308,23 @@ template <typename T> __device__ __forceinline__ Buffer rows_of(const T* base, i
 }
 __device__ __forceinline__ u32x4 load16(Buffer b, unsigned off) { return __builtin_amdgcn_raw_buffer_load_b128(b, off, 0, 0); }
 __device__ __forceinline__ u32x2 load8(Buffer b, unsigned off) { return __builtin_amdgcn_raw_buffer_load_b64(b, off, 0, 0); }
-// Four values at element `at` of a buffer of bf16 or fp32.
-__device__ __forceinline__ void store4(Buffer b, unsigned at, f32x4 x, int out_bf16) {
-    if (out_bf16) __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, pack4<bf16>(x)), b, at * 2, 0, 0);
+// Four values at element `at` of a buffer of O.
+template <typename O> __device__ __forceinline__ void store4(Buffer b, unsigned at, f32x4 x) {
+    if constexpr (sizeof(O) == 2) __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, pack4<bf16>(x)), b, at * 2, 0, 0);
     else __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), b, at * 4, 0, 0);
 }
-// `rows` rows of `cols` elements of an output of either type.
-__device__ __forceinline__ Buffer out_rows(void* base, int64_t at, int64_t ld, int rows, int most, int cols, int out_bf16) {
-    return out_bf16 ? rows_of((const bf16*)base + at, ld, rows, most, cols) : rows_of((const float*)base + at, ld, rows, most, cols);
+// Row `row` of D columns, four values at 16 m + 4 qg for every m, to a block's output of either
+// type: one branch.
+template <int D> __device__ __forceinline__ void store_row(void* base, int64_t at, int64_t ld, int rows, int most, int row, int qg, const f32x4 (&x)[D / 16], int out_bf16) {
+    if (out_bf16) {
+        const Buffer b = rows_of((bf16*)base + at, ld, rows, most, D);
+#pragma unroll
+        for (int m = 0; m < D / 16; ++m) store4<bf16>(b, row * (unsigned)ld + 16 * m + 4 * qg, x[m]);
+    } else {
+        const Buffer b = rows_of((float*)base + at, ld, rows, most, D);
+#pragma unroll
+        for (int m = 0; m < D / 16; ++m) store4<float>(b, row * (unsigned)ld + 16 * m + 4 * qg, x[m]);
+    }
 }
 
 // A tile of ROWS x COLS (row-major in global with row stride `ld` elements) held in registers

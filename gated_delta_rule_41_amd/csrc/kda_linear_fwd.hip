@@ -65,7 +65,9 @@ __device__ __forceinline__ void add_outer(f32x4 (&S)[NC][D], const Split<T> (&u)
     }
 }
 
-template <typename T, int DK, int DV>
+// O: the type of o.  (As an argument it made a branch around every store, which kept the
+// products of a chunk from being scheduled across them.)
+template <typename T, typename O, int DK, int DV>
 __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void linear_out_kernel(LinearParams p) {
     constexpr int C = kLinChunk, NC = DV / 64;   // column groups of 16 per wave
     typedef typename V8<T>::t frag;
@@ -169,11 +171,11 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void linear_out_k
         }
         if (gw) put_gates(gates[(t0 / C + 1) & 1], gn, rows - C, l, false, 0.f);
         // through the entering state; transposed: row = value column, column = token 16m + cl
-        f32x4 O[NC][4];
+        f32x4 out[NC][4];
 #pragma unroll
         for (int c = 0; c < NC; ++c)
 #pragma unroll
-            for (int m = 0; m < 4; ++m) O[c][m] = zero4();
+            for (int m = 0; m < 4; ++m) out[c][m] = zero4();
 #pragma unroll
         for (int s = 0; s < DK / 32; ++s) {
             frag sf[NC];
@@ -183,14 +185,14 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void linear_out_k
             for (int m = 0; m < 4; ++m) {
                 const frag q = lk.perm(sQ, m * RK, s);
 #pragma unroll
-                for (int c = 0; c < NC; ++c) O[c][m] = mma_k32(O[c][m], sf[c], q);
+                for (int c = 0; c < NC; ++c) out[c][m] = mma_k32(out[c][m], sf[c], q);
             }
         }
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
             const float e = fast_exp2((float)G.G[16 * m + cl]) * p.scale;
 #pragma unroll
-            for (int c = 0; c < NC; ++c) O[c][m] *= e;
+            for (int c = 0; c < NC; ++c) out[c][m] *= e;
         }
         frag vf[NC][2];
 #pragma unroll
@@ -198,17 +200,17 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void linear_out_k
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk) vf[c][kk] = lv.col(sV, 2 * kk * RV, w * NC + c);
         lds_barrier();   // P is there
-        const Buffer out = out_rows(p.o, (rg.lo + t0) * ldv + h * DV, ldv, rows, C, DV, p.out_bf16);
+        const Buffer to = rows_of((O*)p.o + (rg.lo + t0) * ldv + h * DV, ldv, rows, C, DV);
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
 #pragma unroll
             for (int kk = 0; kk <= m / 2; ++kk) {
                 const frag f = lp.perm(sP, m * RP, kk);
 #pragma unroll
-                for (int c = 0; c < NC; ++c) O[c][m] = mma_k32(O[c][m], vf[c][kk], f);
+                for (int c = 0; c < NC; ++c) out[c][m] = mma_k32(out[c][m], vf[c][kk], f);
             }
 #pragma unroll
-            for (int c = 0; c < NC; ++c) store4(out, (16 * m + cl) * (unsigned)ldv + col + 16 * c + 4 * qg, O[c][m], p.out_bf16);
+            for (int c = 0; c < NC; ++c) store4<O>(to, (16 * m + cl) * (unsigned)ldv + col + 16 * c + 4 * qg, out[c][m]);
         }
         // the state
         const float eC = G.E;
@@ -396,19 +398,20 @@ __global__ __launch_bounds__(kThreads) void linear_carry_kernel(LinearCarryParam
     }
 }
 
-template <typename T> static hipError_t out_t(const LinearParams& p, int dk, hipStream_t stream) {
+template <typename T, typename O> static hipError_t out_t(const LinearParams& p, int dk, hipStream_t stream) {
     const dim3 grid((unsigned)p.chains);
     if (dk == 128) {
-        if (p.dv == 128) hipLaunchKernelGGL((linear_out_kernel<T, 128, 128>), grid, dim3(kThreads), 0, stream, p);
-        else hipLaunchKernelGGL((linear_out_kernel<T, 128, 64>), grid, dim3(kThreads), 0, stream, p);
+        if (p.dv == 128) hipLaunchKernelGGL((linear_out_kernel<T, O, 128, 128>), grid, dim3(kThreads), 0, stream, p);
+        else hipLaunchKernelGGL((linear_out_kernel<T, O, 128, 64>), grid, dim3(kThreads), 0, stream, p);
     } else {
-        if (p.dv == 128) hipLaunchKernelGGL((linear_out_kernel<T, 64, 128>), grid, dim3(kThreads), 0, stream, p);
-        else hipLaunchKernelGGL((linear_out_kernel<T, 64, 64>), grid, dim3(kThreads), 0, stream, p);
+        if (p.dv == 128) hipLaunchKernelGGL((linear_out_kernel<T, O, 64, 128>), grid, dim3(kThreads), 0, stream, p);
+        else hipLaunchKernelGGL((linear_out_kernel<T, O, 64, 64>), grid, dim3(kThreads), 0, stream, p);
     }
     return hipGetLastError();
 }
 hipError_t launch_linear_out(const LinearParams& p, int in_dtype, int dk, hipStream_t stream) {
-    return in_dtype == 1 ? out_t<bf16>(p, dk, stream) : out_t<float>(p, dk, stream);
+    if (in_dtype == 1) return p.out_bf16 ? out_t<bf16, bf16>(p, dk, stream) : out_t<bf16, float>(p, dk, stream);
+    return p.out_bf16 ? out_t<float, bf16>(p, dk, stream) : out_t<float, float>(p, dk, stream);
 }
 
 template <typename T, int DK> static void states_d(const LinearStateParams& p, hipStream_t stream) {
