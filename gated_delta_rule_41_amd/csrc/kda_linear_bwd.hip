@@ -119,9 +119,9 @@ __device__ __forceinline__ void dq_role(const LinearBwdParams& p, const Task& t,
         ts.load((const T*)p.S + (t.slot * p.H + h) * DK * DV, DV, DK, tid);
         frag dof[DV / 32], qf[DK / 32];
         row_frags<T, DV>(dof, (const T*)p.dO + t.lo * ldv + h * DV, ldv, row, rows, qg);
-        row_perms<T, DK>(qf, q, ldk, row, rows, qg);
+        if constexpr (!GROUPED) row_perms<T, DK>(qf, q, ldk, row, rows, qg);
         Tile<T, kB, DV, kGradThreads> tv;
-        tv.load((const T*)p.v + t.lo * ldv + h * DV, ldv, rows, tid);
+        if constexpr (!GROUPED) tv.load((const T*)p.v + t.lo * ldv + h * DV, ldv, rows, tid);
         if (r == 0) {
             Tile<T, kB, DK, kGradThreads> tk;
             tk.load((const T*)p.k + t.lo * ldk + t.hk * DK, ldk, rows, tid);
@@ -132,6 +132,7 @@ __device__ __forceinline__ void dq_role(const LinearBwdParams& p, const Task& t,
             if (w == 0) block_gates(s.G, p.g + (p.g_stride ? t.lo * p.g_stride : 0) + h, p.g_stride, rows, l);
             ts.store(s.b, tid);
         }
+        if constexpr (GROUPED) row_perms<T, DK>(qf, q, ldk, row, rows, qg);
         lds_barrier();
         // through the entering state; row = key channel 16m + 4qg + i, column = query
         const Lane<T, DK> lk(cl, qg);
@@ -154,6 +155,8 @@ __device__ __forceinline__ void dq_role(const LinearBwdParams& p, const Task& t,
             }
             __builtin_amdgcn_sched_barrier(0);   // keeps the reads ahead of it to two blocks' registers
         }
+        // with the gradient of the heads before in registers there is no room for it earlier
+        if constexpr (GROUPED) tv.load((const T*)p.v + t.lo * ldv + h * DV, ldv, rows, tid);
         lds_barrier();   // the last readers of the state are done
         tv.store(s.b, tid);
         // Below the diagonal block the decay is split at the last key before the wave's
@@ -220,9 +223,9 @@ __device__ __forceinline__ void dk_role(const LinearBwdParams& p, const Task& t,
         td.load((const T*)p.dS + (t.slot * p.H + h) * DK * DV, DV, DK, tid);
         frag vf[DV / 32], kf[DK / 32];
         row_frags<T, DV>(vf, (const T*)p.v + t.lo * ldv + h * DV, ldv, key, rows, qg);
-        row_perms<T, DK>(kf, k, ldk, key, rows, qg);
+        if constexpr (!GROUPED) row_perms<T, DK>(kf, k, ldk, key, rows, qg);
         Tile<T, kB, DV, kGradThreads> to;
-        to.load((const T*)p.dO + t.lo * ldv + h * DV, ldv, rows, tid);
+        if constexpr (!GROUPED) to.load((const T*)p.dO + t.lo * ldv + h * DV, ldv, rows, tid);
         if (r == 0) {
             Tile<T, kB, DK, kGradThreads> tq;
             tq.load((const T*)p.q + t.lo * ldk + t.hk * DK, ldk, rows, tid);
@@ -233,6 +236,7 @@ __device__ __forceinline__ void dk_role(const LinearBwdParams& p, const Task& t,
             if (w == 0) block_gates(s.G, p.g + (p.g_stride ? t.lo * p.g_stride : 0) + h, p.g_stride, rows, l);
             td.store(s.b, tid);
         }
+        if constexpr (GROUPED) row_perms<T, DK>(kf, k, ldk, key, rows, qg);
         lds_barrier();
         // through the state's gradient; row = key channel, column = key
         const Lane<T, DK> lk(cl, qg);
@@ -257,6 +261,7 @@ __device__ __forceinline__ void dk_role(const LinearBwdParams& p, const Task& t,
         }
         f = qsum4(f);
         if (qg == 0 && key < rows) p.f[(int64_t)h * p.T + t.lo + key] = f;
+        if constexpr (GROUPED) to.load((const T*)p.dO + t.lo * ldv + h * DV, ldv, rows, tid);
         lds_barrier();   // the last readers of dS are done
         to.store(s.b, tid);
         // Above the diagonal block the decay is split at the wave's last key.
@@ -305,117 +310,119 @@ __device__ __forceinline__ void dk_role(const LinearBwdParams& p, const Task& t,
     store_row<DK>(p.dk_out, t.lo * ldk + t.hk * DK, ldk, rows, kB, key, l >> 4, dk, p.out_bf16);
 }
 
-template <typename T, int DK, int DV>
-__device__ __forceinline__ void dv_role(const LinearBwdParams& p, const Task& t, int h, GradTiles<T, DK, DV>& s) {
+template <typename T, int DK, int DV, bool GROUPED>
+__device__ __forceinline__ void dv_role(const LinearBwdParams& p, const Task& t, GradTiles<T, DK, DV>& s) {
     typedef typename V8<T>::t frag;
     constexpr int RK = 16 * DK * sizeof(T), RV = 16 * DV * sizeof(T);
-    const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, cl = l & 15, qg = l >> 4;
-    const int rb = row_block(w), key = 16 * rb + cl, rows = t.rows;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), rb = row_block(w), rows = t.rows;
     const int64_t ldk = (int64_t)p.Hk * DK, ldv = (int64_t)p.H * DV;
 
-    // the keys in the k order of the state's columns as they are read here
-    frag kf[DK / 32];
-    row_perms<T, DK>(kf, (const T*)p.k + t.lo * ldk + t.hk * DK, ldk, key, rows, qg);
-    Tile<T, kB, DK, kGradThreads> tq;
-    tq.load((const T*)p.q + t.lo * ldk + t.hk * DK, ldk, rows, tid);
-    {
-        Tile<T, DK, DV, kGradThreads> td, ts;
-        td.load((const T*)p.dS + (t.slot * p.H + h) * DK * DV, DV, DK, tid);
-        ts.load((const T*)p.S + (t.slot * p.H + h) * DK * DV, DV, DK, tid);
+    for (int r = 0; r < (GROUPED ? t.R : 1); ++r) {
+        const int h = GROUPED ? t.hk * t.R + r : t.hk, tid = GROUPED ? opaque(threadIdx.x) : threadIdx.x, l = tid & 63, cl = l & 15, qg = l >> 4, key = 16 * rb + cl;
+        // the keys in the k order of the state's columns as they are read here
+        frag kf[DK / 32];
+        row_perms<T, DK>(kf, (const T*)p.k + t.lo * ldk + t.hk * DK, ldk, key, rows, qg);
         Tile<T, kB, DV, kGradThreads> to;
         to.load((const T*)p.dO + t.lo * ldv + h * DV, ldv, rows, tid);
-        if (w == 0) block_gates(s.G, p.g + (p.g_stride ? t.lo * p.g_stride : 0) + h, p.g_stride, rows, l);
-        td.store(s.b, tid);
-        float cross = 0.f;
+        {
+            Tile<T, DK, DV, kGradThreads> td, ts;
+            td.load((const T*)p.dS + (t.slot * p.H + h) * DK * DV, DV, DK, tid);
+            ts.load((const T*)p.S + (t.slot * p.H + h) * DK * DV, DV, DK, tid);
+            Tile<T, kB, DK, kGradThreads> tq;
+            if (r == 0) tq.load((const T*)p.q + t.lo * ldk + t.hk * DK, ldk, rows, tid);
+            if (w == 0) block_gates(s.G, p.g + (p.g_stride ? t.lo * p.g_stride : 0) + h, p.g_stride, rows, l);
+            td.store(s.b, tid);
+            float cross = 0.f;
 #pragma unroll
-        for (int i = 0; i < Tile<T, DK, DV, kGradThreads>::PIECES; ++i) {
-            typedef T piece __attribute__((ext_vector_type(16 / sizeof(T))));
-            const piece x = __builtin_bit_cast(piece, ts.r[i]), y = __builtin_bit_cast(piece, td.r[i]);
+            for (int i = 0; i < Tile<T, DK, DV, kGradThreads>::PIECES; ++i) {
+                typedef T piece __attribute__((ext_vector_type(16 / sizeof(T))));
+                const piece x = __builtin_bit_cast(piece, ts.r[i]), y = __builtin_bit_cast(piece, td.r[i]);
 #pragma unroll
-            for (int j = 0; j < (int)(16 / sizeof(T)); ++j) cross += to_f32(x[j]) * to_f32(y[j]);
+                for (int j = 0; j < (int)(16 / sizeof(T)); ++j) cross += to_f32(x[j]) * to_f32(y[j]);
+            }
+#pragma unroll
+            for (int m = 32; m >= 1; m >>= 1) cross += __shfl_xor(cross, m, 64);
+            if (l == 0) s.sum[w] = cross;
+            if (r == 0) tq.store(s.a, tid);
         }
+        lds_barrier();
+        if (tid == 0) {
+            float x = 0.f;
 #pragma unroll
-        for (int m = 32; m >= 1; m >>= 1) cross += __shfl_xor(cross, m, 64);
-        if (l == 0) s.sum[w] = cross;
-        to.store(s.a, tid);
-    }
-    lds_barrier();
-    if (tid == 0) {
-        float x = 0.f;
+            for (int i = 0; i < 8; ++i) x += s.sum[i];
+            p.cross[t.slot * p.H + h] = x * fast_exp2((float)s.G[kB - 1]);
+        }
+        // through the state's gradient; row = value channel, column = key
+        const Lane<T, DK> lk(cl, qg);
+        const Lane<T, DV> lv(cl, qg);
+        const double gk = s.G[key];
+        const float wj = fast_exp2((float)(s.G[kB - 1] - gk));
+        f32x4 dv[DV / 16];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x += s.sum[i];
-        p.cross[t.slot * p.H + h] = x * fast_exp2((float)s.G[kB - 1]);
-    }
-    // through the state's gradient; row = value channel, column = key
-    const Lane<T, DK> lk(cl, qg);
-    const Lane<T, DV> lv(cl, qg);
-    const double gk = s.G[key];
-    const float wj = fast_exp2((float)(s.G[kB - 1] - gk));
-    f32x4 dv[DV / 16];
+        for (int m = 0; m < DV / 16; m += 2) {
+            f32x4 x[2] = {zero4(), zero4()};
 #pragma unroll
-    for (int m = 0; m < DV / 16; m += 2) {
-        f32x4 x[2] = {zero4(), zero4()};
+            for (int y = 0; y < DK / 32; ++y)
 #pragma unroll
-        for (int y = 0; y < DK / 32; ++y)
+                for (int u = 0; u < 2; ++u) x[u] = mma_k32(x[u], lv.col(s.b, 2 * y * RV, m + u), kf[y]);
 #pragma unroll
-            for (int u = 0; u < 2; ++u) x[u] = mma_k32(x[u], lv.col(s.b, 2 * y * RV, m + u), kf[y]);
+            for (int u = 0; u < 2; ++u) dv[m + u] = x[u] * wj;
+        }
+        lds_barrier();   // the last readers of dS are done
+        to.store(s.b, tid);
+        const double gref = s.G[16 * rb + 15];
+        const float fk = fast_exp2((float)(gref - gk)) * p.scale;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) dv[m + u] = x[u] * wj;
-    }
-    lds_barrier();   // the last readers of dS are done
-    tq.store(s.b, tid);
-    const double gref = s.G[16 * rb + 15];
-    const float fk = fast_exp2((float)(gref - gk)) * p.scale;
+        for (int i = 0; i < 2; ++i)
+            if (l + 64 * i >= 16 * rb + 16) s.F[w][l + 64 * i] = fast_exp2((float)(s.G[l + 64 * i] - gref));
+        lds_barrier();
+        for (int x = rb / 2; x < (rows + 31) / 32; ++x) {
+            f32x4 a[2] = {zero4(), zero4()};
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-        if (l + 64 * i >= 16 * rb + 16) s.F[w][l + 64 * i] = fast_exp2((float)(s.G[l + 64 * i] - gref));
-    lds_barrier();
-    for (int x = rb / 2; x < (rows + 31) / 32; ++x) {
-        f32x4 a[2] = {zero4(), zero4()};
+            for (int y = 0; y < DK / 32; ++y)
 #pragma unroll
-        for (int y = 0; y < DK / 32; ++y)
+                for (int u = 0; u < 2; ++u) a[u] = mma_k32(a[u], lk.perm(s.a, (2 * x + u) * RK, y), kf[y]);
 #pragma unroll
-            for (int u = 0; u < 2; ++u) a[u] = mma_k32(a[u], lk.perm(s.b, (2 * x + u) * RK, y), kf[y]);
+            for (int u = 0; u < 2; ++u) {
+                const int n = 2 * x + u;
+                if (n > rb) {
+                    a[u] *= lds4(&s.F[w][16 * n + 4 * qg]) * fk;
+                } else {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int n = 2 * x + u;
-            if (n > rb) {
-                a[u] *= lds4(&s.F[w][16 * n + 4 * qg]) * fk;
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int query = 16 * n + 4 * qg + i;
-                    a[u][i] = keep(a[u][i] * (fast_exp2((float)(s.G[query] - gk)) * p.scale), key <= query);
+                    for (int i = 0; i < 4; ++i) {
+                        const int query = 16 * n + 4 * qg + i;
+                        a[u][i] = keep(a[u][i] * (fast_exp2((float)(s.G[query] - gk)) * p.scale), key <= query);
+                    }
                 }
             }
-        }
-        const frag f = pack8<T>(a[0], a[1]);   // bf16 inputs: P rounded to the products' type
+            const frag f = pack8<T>(a[0], a[1]);   // bf16 inputs: P rounded to the products' type
 #pragma unroll
-        for (int m = 0; m < DV / 16; ++m) dv[m] = mma_k32(dv[m], lv.col(s.a, 2 * x * RV, m), f);
+            for (int m = 0; m < DV / 16; ++m) dv[m] = mma_k32(dv[m], lv.col(s.b, 2 * x * RV, m), f);
+        }
+        store_row<DV>(p.dv_out, t.lo * ldv + h * DV, ldv, rows, kB, key, qg, dv, p.out_bf16);
+        if constexpr (GROUPED) lds_barrier();   // the last readers of this head's tiles are done
     }
-    store_row<DV>(p.dv_out, t.lo * ldv + h * DV, ldv, rows, kB, key, qg, dv, p.out_bf16);
 }
 
 // GROUPED: several value heads to a key head.
 template <typename T, int DK, int DV, bool GROUPED>
 __global__ __launch_bounds__(kGradThreads, sizeof(T) == 2 ? 4 : 2) void linear_grads_kernel(LinearBwdParams p) {
     __shared__ GradTiles<T, DK, DV> s;
-    const int R = GROUPED ? p.H / p.Hk : 1, roles = 2 + R;
-    const int64_t group = blockIdx.x / (8 * roles);
-    const int x = (int)(blockIdx.x % (8 * roles)), role = x >> 3;
+    const int64_t group = blockIdx.x / 24;
+    const int x = (int)(blockIdx.x % 24), role = x >> 3;
     const int64_t task = group * 8 + (x & 7);
     Task t;
     t.slot = task / p.Hk;
     if (t.slot >= p.blocks) return;
     t.hk = (int)(task % p.Hk);
-    t.R = R;
+    t.R = p.H / p.Hk;
     const Range rg = piece_range(p.cu, p.N, p.seqlen, p.T, t.slot, kB);
     t.lo = rg.lo;
     t.rows = (int)(rg.hi - rg.lo);
     if (t.rows <= 0) return;
     if (role == 0) dq_role<T, DK, DV, GROUPED>(p, t, s);
     else if (role == 1) dk_role<T, DK, DV, GROUPED>(p, t, s);
-    else dv_role<T, DK, DV>(p, t, t.hk * R + role - 2, s);
+    else dv_role<T, DK, DV, GROUPED>(p, t, s);
 }
 
 // dg of a block, one wave per (block, head): lane l holds tokens l and l + 64.  64-bit sums.
@@ -480,7 +487,7 @@ __global__ __launch_bounds__(kThreads) void linear_dg_head_kernel(LinearBwdParam
 
 template <typename T, int DK, int DV> static void grads_t(const LinearBwdParams& p, hipStream_t stream) {
     const int64_t tasks = (p.blocks * p.Hk + 7) / 8 * 8;
-    const dim3 grid((unsigned)(tasks * (2 + p.H / p.Hk)));
+    const dim3 grid((unsigned)(tasks * 3));
     if (p.H == p.Hk) hipLaunchKernelGGL((linear_grads_kernel<T, DK, DV, false>), grid, dim3(kGradThreads), 0, stream, p);
     else hipLaunchKernelGGL((linear_grads_kernel<T, DK, DV, true>), grid, dim3(kGradThreads), 0, stream, p);
 }
