@@ -81,13 +81,14 @@ struct LinearBwdParams {
     float* a;              // [H,T] column sums of A
     float* f;              // [H,T] k . dk through dS
     float* cross;          // [blocks,H] e^{G} <S, dS>
+    float* sums;           // [2][parts,T,Hk,dk] dq and dk summed over a part's value heads (parts > 1)
     float* dg_part;        // [blocks,H] sum of dg over the block (gate per head), or nullptr
     void* dq;
     void* dk_out;
     void* dv_out;
     void* dg;
     int64_t T, blocks;
-    int32_t N, H, Hk, dv, seqlen, g_stride, out_bf16;
+    int32_t N, H, Hk, dv, seqlen, g_stride, out_bf16, parts;   // parts divides H / Hk
     float scale;
 };
 

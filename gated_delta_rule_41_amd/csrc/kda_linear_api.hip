@@ -123,13 +123,27 @@ FwdLayout fwd_layout(const kda_linear_config* c, int64_t T, int32_t N) {
 struct BwdLayout {
     Plan plan;
     int64_t blocks;
-    size_t S, dS, e, a, f, cross, part, seg[2], decay[2], total;
+    int32_t parts;
+    size_t S, dS, e, a, f, cross, part, sums, seg[2], decay[2], total;
 };
+// A key head's value heads are divided among so many workgroups: the smallest divisor of their
+// number that gives kGradTarget workgroups (three roles a block), so that short streams do not
+// wait for one workgroup's value heads in turn.  Backward in us, whole and divided for 256, 512
+// and 1024 workgroups: 134 tokens x 8 heads on 2: 44, 27, 27, 27; 1024 x 32 on 8: 87, 87, 77,
+// 81; 4096 x 16 on 4: 130, 130, 139, 143; 4096 x 32 on 1: 354, 192, 189, 186.
+constexpr int64_t kGradTarget = 512;
+int32_t grad_parts(const kda_linear_config* c, int64_t blocks) {
+    const int32_t R = c->H / c->Hk;
+    int32_t parts = 1;
+    while (parts < R && (3 * blocks * c->Hk * parts < kGradTarget || R % parts)) ++parts;
+    return parts;
+}
 BwdLayout bwd_layout(const kda_linear_config* c, int64_t T, int32_t N) {
     BwdLayout b;
     memset(&b, 0, sizeof b);
     b.plan = walk_plan(c, T, N, 2 * (c->dv / 64), false);
     b.blocks = linear_slots(T, N, kLinBlock);
+    b.parts = grad_parts(c, b.blocks);
     size_t at = 0;
     auto take = [&at](size_t bytes) {
         const size_t x = at;
@@ -144,6 +158,7 @@ BwdLayout bwd_layout(const kda_linear_config* c, int64_t T, int32_t N) {
     b.f = take(rows);
     b.cross = take((size_t)b.blocks * c->H * sizeof(float));
     b.part = take(c->gate == KDA_GATE_HEAD ? (size_t)b.blocks * c->H * sizeof(float) : 0);
+    b.sums = take(b.parts > 1 ? (size_t)2 * b.parts * T * c->Hk * c->dk * sizeof(float) : 0);
     if (b.plan.seg_len)
         for (int i = 0; i < 2; ++i) {
             b.seg[i] = take((size_t)b.plan.chains * state_elems(c) * sizeof(float));
@@ -330,6 +345,7 @@ kda_status kda_linear_bwd(const kda_linear_config* cfg, int64_t T, int32_t N, co
     p.S = ws + b.S; p.dS = ws + b.dS;
     p.e = (float*)(ws + b.e); p.a = (float*)(ws + b.a); p.f = (float*)(ws + b.f); p.cross = (float*)(ws + b.cross);
     p.dg_part = cfg->gate == KDA_GATE_HEAD ? (float*)(ws + b.part) : nullptr;
+    p.sums = (float*)(ws + b.sums); p.parts = b.parts;
     p.dq = dq; p.dk_out = dk; p.dv_out = dv; p.dg = dg;
     p.T = T; p.blocks = T > 0 ? b.blocks : 0; p.N = N; p.H = cfg->H; p.Hk = cfg->Hk; p.dv = cfg->dv; p.seqlen = seqlen;
     p.g_stride = g_stride; p.out_bf16 = cfg->out_dtype == KDA_BF16;

@@ -12,17 +12,23 @@
 // column sums of A are fp32 products), unlike the sum of q . dq - k . dk to the end of the
 // document, whose rounding grows with its length.
 //
-// linear_grads_kernel: one workgroup (8 waves) per block, head and role: dq (with e and the
-// row sums of A), dk (with f and its column sums) or dv (with <S, dS>), wave w a 16-row block of queries or keys.  dq and dk belong to
-// a key head and loop over its value heads, so the gradients of shared heads add up in
-// registers in a fixed order.  A wave forms its own rows of P or dP in the transposed
-// orientation, in which the accumulators are at once the operand of the next product: no
-// exchange between waves, at the price of forming dP twice and P twice.  One role needs two
-// 128-row tiles in LDS and fits 128 registers, so two workgroups share a compute unit and one
-// computes while the other loads; the three roles of a block are issued eight workgroups
-// apart, on one XCD, whose L2 serves the rows that they share.  (One kernel for dk and dv at
-// 255 registers, one workgroup per compute unit, took 620 us at 4 x 8192 tokens x 32 heads,
-// and dq beside it 461 us.)  linear_dg_kernel finishes dg.
+// linear_grads_kernel: one workgroup (8 waves) per block, key head and role: dq (with e and the
+// row sums of A), dk (with f and its column sums) or dv (with <S, dS>), wave w a 16-row block
+// of queries or keys.  Each role loops over the key head's value heads in the same order, so
+// that the L2 still has what another role has read (with dv's value heads side by side instead
+// 32768 tokens x 32 heads on 16 key heads took 1495 us, now 1221), and the gradients of shared
+// heads add up in registers in a fixed order.  Where that leaves too few workgroups, the value
+// heads are divided among `parts` of them, whose sums linear_parts_kernel adds, again in a
+// fixed order.  A wave forms its own rows of P or dP in the transposed orientation, in which the
+// accumulators are at once the operand of the next product: no exchange between waves, at the
+// price of forming dP twice and P twice.  One role needs two 128-row tiles in LDS and fits 128
+// registers, so two workgroups share a compute unit and one computes while the other loads;
+// the three roles of a block are issued eight workgroups apart, on one XCD, whose L2 serves the
+// rows that they share.  At 4 x 8192 tokens x 32 heads, bf16, it takes 730 us and moves 2.47 GB
+// (3.4 TB/s; the matrix units are busy 15% of the time, LDS 23%): memory bounds it, at two
+// thirds of a copy's rate, with loads and sums of two workgroups in turn.  (One kernel for dk and
+// dv at 255 registers, one workgroup a compute unit, took 620 us, and dq beside it 461.)
+// linear_dg_kernel finishes dg.
 #include "kda_linear_device.h"
 
 namespace kda {
@@ -83,7 +89,9 @@ template <typename T, int D> __device__ __forceinline__ void row_perms(typename 
 // What a role's workgroup knows of its block.
 struct Task {
     int64_t slot, lo;
-    int rows, hk, R;
+    int rows, hk;
+    int h0, h1;        // its value heads
+    float* sums;       // where dq or dk goes if other workgroups have the key head's other value heads
 };
 
 // LDS of a role: two tiles of 128 rows (the second one also holds the state), the gates, and
@@ -112,8 +120,9 @@ __device__ __forceinline__ void dq_role(const LinearBwdParams& p, const Task& t,
     f32x4 dq[DK / 16];
 #pragma unroll
     for (int m = 0; m < DK / 16; ++m) dq[m] = zero4();
-    for (int r = 0; r < (GROUPED ? t.R : 1); ++r) {
-        const int h = GROUPED ? t.hk * t.R + r : t.hk, tid = GROUPED ? opaque(threadIdx.x) : threadIdx.x, l = tid & 63, cl = l & 15, qg = l >> 4, row = 16 * rb + cl;
+    for (int h = t.h0; h < (GROUPED ? t.h1 : t.h0 + 1); ++h) {
+        const bool first = !GROUPED || h == t.h0;
+        const int tid = GROUPED ? opaque(threadIdx.x) : threadIdx.x, l = tid & 63, cl = l & 15, qg = l >> 4, row = 16 * rb + cl;
         // every load of the step is issued before the first wait
         Tile<T, DK, DV, kGradThreads> ts;
         ts.load((const T*)p.S + (t.slot * p.H + h) * DK * DV, DV, DK, tid);
@@ -122,7 +131,7 @@ __device__ __forceinline__ void dq_role(const LinearBwdParams& p, const Task& t,
         if constexpr (!GROUPED) row_perms<T, DK>(qf, q, ldk, row, rows, qg);
         Tile<T, kB, DV, kGradThreads> tv;
         if constexpr (!GROUPED) tv.load((const T*)p.v + t.lo * ldv + h * DV, ldv, rows, tid);
-        if (r == 0) {
+        if (first) {
             Tile<T, kB, DK, kGradThreads> tk;
             tk.load((const T*)p.k + t.lo * ldk + t.hk * DK, ldk, rows, tid);
             if (w == 0) block_gates(s.G, p.g + (p.g_stride ? t.lo * p.g_stride : 0) + h, p.g_stride, rows, l);
@@ -203,7 +212,8 @@ __device__ __forceinline__ void dq_role(const LinearBwdParams& p, const Task& t,
         lds_barrier();
     }
     const int l = threadIdx.x & 63, row = 16 * rb + (l & 15);
-    store_row<DK>(p.dq, t.lo * ldk + t.hk * DK, ldk, rows, kB, row, l >> 4, dq, p.out_bf16);
+    if (GROUPED && t.sums) store_row<DK>(t.sums, t.lo * ldk + t.hk * DK, ldk, rows, kB, row, l >> 4, dq, 0);
+    else store_row<DK>(p.dq, t.lo * ldk + t.hk * DK, ldk, rows, kB, row, l >> 4, dq, p.out_bf16);
 }
 
 template <typename T, int DK, int DV, bool GROUPED>
@@ -217,8 +227,9 @@ __device__ __forceinline__ void dk_role(const LinearBwdParams& p, const Task& t,
     f32x4 dk[DK / 16];
 #pragma unroll
     for (int m = 0; m < DK / 16; ++m) dk[m] = zero4();
-    for (int r = 0; r < (GROUPED ? t.R : 1); ++r) {
-        const int h = GROUPED ? t.hk * t.R + r : t.hk, tid = GROUPED ? opaque(threadIdx.x) : threadIdx.x, l = tid & 63, cl = l & 15, qg = l >> 4, key = 16 * rb + cl;
+    for (int h = t.h0; h < (GROUPED ? t.h1 : t.h0 + 1); ++h) {
+        const bool first = !GROUPED || h == t.h0;
+        const int tid = GROUPED ? opaque(threadIdx.x) : threadIdx.x, l = tid & 63, cl = l & 15, qg = l >> 4, key = 16 * rb + cl;
         Tile<T, DK, DV, kGradThreads> td;
         td.load((const T*)p.dS + (t.slot * p.H + h) * DK * DV, DV, DK, tid);
         frag vf[DV / 32], kf[DK / 32];
@@ -226,7 +237,7 @@ __device__ __forceinline__ void dk_role(const LinearBwdParams& p, const Task& t,
         if constexpr (!GROUPED) row_perms<T, DK>(kf, k, ldk, key, rows, qg);
         Tile<T, kB, DV, kGradThreads> to;
         if constexpr (!GROUPED) to.load((const T*)p.dO + t.lo * ldv + h * DV, ldv, rows, tid);
-        if (r == 0) {
+        if (first) {
             Tile<T, kB, DK, kGradThreads> tq;
             tq.load((const T*)p.q + t.lo * ldk + t.hk * DK, ldk, rows, tid);
             if (w == 0) block_gates(s.G, p.g + (p.g_stride ? t.lo * p.g_stride : 0) + h, p.g_stride, rows, l);
@@ -307,7 +318,8 @@ __device__ __forceinline__ void dk_role(const LinearBwdParams& p, const Task& t,
         lds_barrier();
     }
     const int l = threadIdx.x & 63, key = 16 * rb + (l & 15);
-    store_row<DK>(p.dk_out, t.lo * ldk + t.hk * DK, ldk, rows, kB, key, l >> 4, dk, p.out_bf16);
+    if (GROUPED && t.sums) store_row<DK>(t.sums, t.lo * ldk + t.hk * DK, ldk, rows, kB, key, l >> 4, dk, 0);
+    else store_row<DK>(p.dk_out, t.lo * ldk + t.hk * DK, ldk, rows, kB, key, l >> 4, dk, p.out_bf16);
 }
 
 template <typename T, int DK, int DV, bool GROUPED>
@@ -317,8 +329,9 @@ __device__ __forceinline__ void dv_role(const LinearBwdParams& p, const Task& t,
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), rb = row_block(w), rows = t.rows;
     const int64_t ldk = (int64_t)p.Hk * DK, ldv = (int64_t)p.H * DV;
 
-    for (int r = 0; r < (GROUPED ? t.R : 1); ++r) {
-        const int h = GROUPED ? t.hk * t.R + r : t.hk, tid = GROUPED ? opaque(threadIdx.x) : threadIdx.x, l = tid & 63, cl = l & 15, qg = l >> 4, key = 16 * rb + cl;
+    for (int h = t.h0; h < (GROUPED ? t.h1 : t.h0 + 1); ++h) {
+        const bool first = !GROUPED || h == t.h0;
+        const int tid = GROUPED ? opaque(threadIdx.x) : threadIdx.x, l = tid & 63, cl = l & 15, qg = l >> 4, key = 16 * rb + cl;
         // the keys in the k order of the state's columns as they are read here
         frag kf[DK / 32];
         row_perms<T, DK>(kf, (const T*)p.k + t.lo * ldk + t.hk * DK, ldk, key, rows, qg);
@@ -329,7 +342,7 @@ __device__ __forceinline__ void dv_role(const LinearBwdParams& p, const Task& t,
             td.load((const T*)p.dS + (t.slot * p.H + h) * DK * DV, DV, DK, tid);
             ts.load((const T*)p.S + (t.slot * p.H + h) * DK * DV, DV, DK, tid);
             Tile<T, kB, DK, kGradThreads> tq;
-            if (r == 0) tq.load((const T*)p.q + t.lo * ldk + t.hk * DK, ldk, rows, tid);
+            if (first) tq.load((const T*)p.q + t.lo * ldk + t.hk * DK, ldk, rows, tid);
             if (w == 0) block_gates(s.G, p.g + (p.g_stride ? t.lo * p.g_stride : 0) + h, p.g_stride, rows, l);
             td.store(s.b, tid);
             float cross = 0.f;
@@ -343,7 +356,7 @@ __device__ __forceinline__ void dv_role(const LinearBwdParams& p, const Task& t,
 #pragma unroll
             for (int m = 32; m >= 1; m >>= 1) cross += __shfl_xor(cross, m, 64);
             if (l == 0) s.sum[w] = cross;
-            if (r == 0) tq.store(s.a, tid);
+            if (first) tq.store(s.a, tid);
         }
         lds_barrier();
         if (tid == 0) {
@@ -411,11 +424,16 @@ __global__ __launch_bounds__(kGradThreads, sizeof(T) == 2 ? 4 : 2) void linear_g
     const int64_t group = blockIdx.x / 24;
     const int x = (int)(blockIdx.x % 24), role = x >> 3;
     const int64_t task = group * 8 + (x & 7);
+    const int units = GROUPED ? p.Hk * p.parts : p.Hk, unit = (int)(task % units), part = GROUPED ? unit % p.parts : 0;
     Task t;
-    t.slot = task / p.Hk;
+    t.slot = task / units;
     if (t.slot >= p.blocks) return;
-    t.hk = (int)(task % p.Hk);
-    t.R = p.H / p.Hk;
+    t.hk = GROUPED ? unit / p.parts : unit;
+    const int R = p.H / p.Hk;
+    t.h0 = GROUPED ? t.hk * R + part * (R / p.parts) : t.hk;
+    t.h1 = GROUPED ? t.h0 + R / p.parts : t.hk + 1;
+    t.sums = nullptr;
+    if (GROUPED && p.parts > 1) t.sums = p.sums + (int64_t)(role * p.parts + part) * p.T * p.Hk * DK;   // dv has none
     const Range rg = piece_range(p.cu, p.N, p.seqlen, p.T, t.slot, kB);
     t.lo = rg.lo;
     t.rows = (int)(rg.hi - rg.lo);
@@ -423,6 +441,23 @@ __global__ __launch_bounds__(kGradThreads, sizeof(T) == 2 ? 4 : 2) void linear_g
     if (role == 0) dq_role<T, DK, DV, GROUPED>(p, t, s);
     else if (role == 1) dk_role<T, DK, DV, GROUPED>(p, t, s);
     else dv_role<T, DK, DV, GROUPED>(p, t, s);
+}
+
+// dq (blockIdx.y 0) and dk of some rows of a block and key head from the sums of its
+// parts, in their order.
+template <int DK>
+__global__ __launch_bounds__(kThreads) void linear_parts_kernel(LinearBwdParams p) {
+    constexpr int LANES = DK / 4, ROWS = kThreads / LANES, PIECES = kB / ROWS;
+    const int64_t id = blockIdx.x / PIECES, slot = id / p.Hk;
+    const int hk = (int)(id % p.Hk), row = blockIdx.x % PIECES * ROWS + threadIdx.x / LANES;
+    const Range rg = piece_range(p.cu, p.N, p.seqlen, p.T, slot, kB);
+    if (row >= rg.hi - rg.lo) return;
+    const int64_t plane = p.T * p.Hk * DK, at = ((rg.lo + row) * p.Hk + hk) * DK + threadIdx.x % LANES * 4;
+    const float* from = p.sums + blockIdx.y * p.parts * plane + at;
+    f32x4 sum = lds4(from);
+#pragma unroll 4
+    for (int i = 1; i < p.parts; ++i) sum += lds4(from + i * plane);
+    store4(blockIdx.y ? p.dk_out : p.dq, at, sum, p.out_bf16);
 }
 
 // dg of a block, one wave per (block, head): lane l holds tokens l and l + 64.  64-bit sums.
@@ -486,10 +521,11 @@ __global__ __launch_bounds__(kThreads) void linear_dg_head_kernel(LinearBwdParam
 }
 
 template <typename T, int DK, int DV> static void grads_t(const LinearBwdParams& p, hipStream_t stream) {
-    const int64_t tasks = (p.blocks * p.Hk + 7) / 8 * 8;
+    const int64_t tasks = (p.blocks * p.Hk * p.parts + 7) / 8 * 8;
     const dim3 grid((unsigned)(tasks * 3));
     if (p.H == p.Hk) hipLaunchKernelGGL((linear_grads_kernel<T, DK, DV, false>), grid, dim3(kGradThreads), 0, stream, p);
     else hipLaunchKernelGGL((linear_grads_kernel<T, DK, DV, true>), grid, dim3(kGradThreads), 0, stream, p);
+    if (p.parts > 1) hipLaunchKernelGGL(linear_parts_kernel<DK>, dim3((unsigned)(p.blocks * p.Hk * (kB * DK / (4 * kThreads))), 2), dim3(kThreads), 0, stream, p);
 }
 template <typename T> static void grads_d(const LinearBwdParams& p, int dk, hipStream_t stream) {
     if (dk == 128) {

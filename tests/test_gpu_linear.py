@@ -203,6 +203,17 @@ def test_many_heads(dtype, lens, H):
             assert off <= most * size, n
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("lens,H,Hk,dk,dv", [([130, 5], 8, 1, 64, 64), ([150], 9, 3, 128, 128), ([3] * 100 + [70], 6, 1, 64, 128)])
+def test_divided_value_heads(dtype, lens, H, Hk, dk, dv):
+    """A key head's value heads in several workgroups: 8 or 3 parts of one head, and 2 parts of three."""
+    need_gpu()
+    _say(f"{H}/{Hk} heads, {len(lens)} documents {dtype}")
+    d, h, cu = make(22, lens, H, Hk, dk, dv, dtype)
+    for out in (torch.float32, torch.bfloat16):
+        check_bwd(d, h, cu, lens, dtype, out, 0.125)
+
+
 def test_strong_and_infinite_gates():
     """Gates of -8 a token, and -inf, which restarts the state at its token."""
     need_gpu()
