@@ -414,20 +414,23 @@ hipError_t launch_linear_out(const LinearParams& p, int in_dtype, int dk, hipStr
     return p.out_bf16 ? out_t<float, bf16>(p, dk, stream) : out_t<float, float>(p, dk, stream);
 }
 
+template <typename T, int DK, int NC> static void states_n(const LinearStateParams& p, hipStream_t stream) {
+    const dim3 grid((unsigned)(((int64_t)p.chains + 7) / 8 * 8 * p.dirs * (p.dv / (64 * NC))));
+    if (p.dir[0].border) hipLaunchKernelGGL((linear_state_kernel<T, DK, NC, true>), grid, dim3(kThreads), 0, stream, p);
+    else hipLaunchKernelGGL((linear_state_kernel<T, DK, NC, false>), grid, dim3(kThreads), 0, stream, p);
+}
 template <typename T, int DK> static void states_d(const LinearStateParams& p, hipStream_t stream) {
-    // 128 columns a workgroup halve the reads of `a` from LDS (own sums of 131072 tokens x 16
-    // heads 340 -> 274 us); 64 are for launches that would leave compute units with less than
-    // two workgroups (4 documents x 32 heads, both directions: 650 -> 432 us)
-    const int64_t walks = p.seg_len && p.T / p.seg_len > p.N ? p.T / p.seg_len : p.N;
-    const bool wide = p.dv == 128 && walks * p.H * p.dirs >= kWalkTarget;
-    const dim3 grid((unsigned)(((int64_t)p.chains + 7) / 8 * 8 * p.dirs * (p.dv / (wide ? 128 : 64))));
-    if (wide) {
-        if (p.dir[0].border) hipLaunchKernelGGL((linear_state_kernel<T, DK, 2, true>), grid, dim3(kThreads), 0, stream, p);
-        else hipLaunchKernelGGL((linear_state_kernel<T, DK, 2, false>), grid, dim3(kThreads), 0, stream, p);
-    } else {
-        if (p.dir[0].border) hipLaunchKernelGGL((linear_state_kernel<T, DK, 1, true>), grid, dim3(kThreads), 0, stream, p);
-        else hipLaunchKernelGGL((linear_state_kernel<T, DK, 1, false>), grid, dim3(kThreads), 0, stream, p);
+    // bf16: 128 columns a workgroup halve the reads of `a` from LDS (forward of 131083 tokens x 16
+    // heads 814 -> 771 us, backward of 4 documents x 32 heads 1161 -> 1135), as long as whole
+    // documents give a workgroup a compute unit, or segments two (backward of 8192 tokens x 8
+    // heads with one: 116 -> 119).  fp32: the matrix unit bounds it, and its 128 columns leave
+    // room for fewer workgroups (backward of 8 documents x 32 heads 1064 -> 1117).
+    if constexpr (sizeof(T) == 2) {
+        const bool cut = p.seg_len && p.T / p.seg_len > p.N;
+        const int64_t walks = (cut ? p.T / p.seg_len : p.N) * p.H * p.dirs;
+        if (p.dv == 128 && walks >= (cut ? kWalkTarget : kWalkTarget / 2)) return states_n<T, DK, 2>(p, stream);
     }
+    states_n<T, DK, 1>(p, stream);
 }
 template <typename T> static hipError_t states_t(const LinearStateParams& p, int dk, hipStream_t stream) {
     if (dk == 128) states_d<T, 128>(p, stream);
