@@ -131,11 +131,13 @@ template <typename T, bool DELTA, int NL, int DK, int DV> struct TreeShared {
         T rows[Two<T>::PLANES * PLANE];
         float u[NL * LU];
     } x;
-    // node i's products with its path: entry i (i + 1) / 2 + d for the node d steps up
-    float kk[DELTA ? NL * (NL + 1) / 2 : 1], qk[NL * (NL + 1) / 2];
-    float beta[NL], norm[NL];
-    int par[64], depth[NL];   // depth: strict ancestors, -1 of an absent node
-    u64 anc[NL];              // strict ancestors as a bit mask
+    // node i's path and its products with it: entry i (i + 1) / 2 + d for the node d steps up.
+    // Entry 0 is node i itself with products of zero, where a node waits once its path is used up.
+    static constexpr int ENTRIES = NL * (NL + 1) / 2;
+    float kk[DELTA ? ENTRIES : 1], qk[ENTRIES];
+    unsigned char node[ENTRIES];
+    float self[NL], beta[NL], norm[NL];   // self: q_i . k_i
+    int par[64], depth[NL];               // depth: strict ancestors, -1 of an absent node
 };
 
 // NL: the tree's size rounded up to 16, 32 or 64 nodes.
@@ -227,8 +229,12 @@ __global__ __launch_bounds__(NL == 16 ? 256 : 512, sizeof(T) == 2 ? 4 : 2) void 
             const int i = (tid >> 4) + r * NODES;
             const int t0 = i * (i + 1) / 2;
             const float self = row16_sum(dot8(qv[r], kv[r]));
-            if (cl == 0) s.qk[t0] = self;
-            u64 anc = 0;
+            if (cl == 0) {
+                s.self[i] = self;
+                s.node[t0] = (unsigned char)i;
+                s.qk[t0] = 0.f;
+                if constexpr (DELTA) s.kk[t0] = 0.f;
+            }
             int d = 0, a = parent_of(s.par, i, L);
             for (; a >= 0; a = parent_of(s.par, a, L)) {
                 const f32x8 ke = get_row<T, E>(s.x.c.k + a * DK, cl) * av[r];
@@ -240,18 +246,17 @@ __global__ __launch_bounds__(NL == 16 ? 256 : 512, sizeof(T) == 2 ? 4 : 2) void 
                     av[r] *= splat8(s.x.c.a[a]);
                 }
                 ++d;
-                anc |= 1ull << a;
                 const float qk = row16_sum(dot8(qv[r], ke)) * norm;
                 if constexpr (DELTA) {
                     const float kk = row16_sum(dot8(kv[r], ke)) * norm;
                     if (cl == 0) s.kk[t0 + d] = kk;
                 }
-                if (cl == 0) s.qk[t0 + d] = qk;
+                if (cl == 0) {
+                    s.qk[t0 + d] = qk;
+                    s.node[t0 + d] = (unsigned char)a;
+                }
             }
-            if (cl == 0) {
-                s.anc[i] = anc;
-                s.depth[i] = a < -1 ? -1 : d;
-            }
+            if (cl == 0) s.depth[i] = a < -1 ? -1 : d;
         }
 #pragma unroll
         for (int c = 0; c < COLS; ++c)
@@ -304,16 +309,16 @@ __global__ __launch_bounds__(NL == 16 ? 256 : 512, sizeof(T) == 2 ? 4 : 2) void 
     // u and o from its ancestor of that depth.  A wave needs no other wave's columns, and a
     // wave's LDS operations are done in order; only where waves share columns (STEP) they wait
     // for each other.
-    u64 anc[MT];
-    int depth[MT], at[MT], levels = 0;   // at: the products with the next ancestor
-    float beta[MT];
+    int depth[MT], at[MT], a[MT], levels = 0;   // at: the entry of the next ancestor, a
+    float beta[MT], self[MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
         const int i = 16 * m + cl;
         depth[m] = s.depth[i];
-        anc[m] = s.anc[i];
         at[m] = i * (i + 1) / 2 + (depth[m] > 0 ? depth[m] : 0);
+        a[m] = s.node[at[m]];
         beta[m] = DELTA ? s.beta[i] : 1.f;
+        self[m] = s.self[i];
         while (__ballot(depth[m] >= levels)) ++levels;
 #pragma unroll
         for (int c = 0; c < COLS; ++c)
@@ -323,43 +328,32 @@ __global__ __launch_bounds__(NL == 16 ? 256 : 512, sizeof(T) == 2 ? 4 : 2) void 
 #pragma unroll
         for (int m = 0; m < MT; ++m)
             if (mine(m) && depth[m] == d) {
-                const int i = 16 * m + cl;
-                const float self = s.qk[i * (i + 1) / 2];
 #pragma unroll
                 for (int c = 0; c < COLS; ++c) {
                     const f32x4 u = beta[m] * ks[c][m];
-                    qs[c][m] += self * u;
-                    *reinterpret_cast<f32x4*>(s.x.u + i * Shared::LU + column(c)) = u;
+                    qs[c][m] += self[m] * u;
+                    *reinterpret_cast<f32x4*>(s.x.u + (16 * m + cl) * Shared::LU + column(c)) = u;
                 }
             }
         if (d + 1 == levels) break;
         if constexpr (STEP > 1) __syncthreads();
         else asm volatile("" ::: "memory");
-        // reads without branches, so that those of all nodes are in flight together
-        float kk[MT], qk[MT];
-        f32x4 u[COLS][MT];
+        // without branches, so that the reads of all nodes are in flight together; a node whose
+        // path is used up adds zero times its own u
 #pragma unroll
         for (int m = 0; m < MT; ++m)
             if (mine(m)) {
-                const int a = anc[m] ? __ffsll((long long)anc[m]) - 1 : 0;
-                if constexpr (DELTA) kk[m] = s.kk[at[m]];
-                qk[m] = s.qk[at[m]];
+                float kk = 0.f;
+                if constexpr (DELTA) kk = s.kk[at[m]];
+                const float qk = s.qk[at[m]];
 #pragma unroll
-                for (int c = 0; c < COLS; ++c) u[c][m] = *reinterpret_cast<const f32x4*>(s.x.u + a * Shared::LU + column(c));
-            }
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-            if (mine(m)) {
-                const bool on = depth[m] > d;
-#pragma unroll
-                for (int c = 0; c < COLS; ++c)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if constexpr (DELTA) ks[c][m][e] -= keep(kk[m] * u[c][m][e], on);
-                        qs[c][m][e] += keep(qk[m] * u[c][m][e], on);
-                    }
-                at[m] -= on;
-                anc[m] &= anc[m] - 1;
+                for (int c = 0; c < COLS; ++c) {
+                    const f32x4 u = *reinterpret_cast<const f32x4*>(s.x.u + a[m] * Shared::LU + column(c));
+                    if constexpr (DELTA) ks[c][m] -= kk * u;
+                    qs[c][m] += qk * u;
+                }
+                at[m] -= depth[m] > d;
+                a[m] = s.node[at[m]];
             }
     }
 #pragma unroll
