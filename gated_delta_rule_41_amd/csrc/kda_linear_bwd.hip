@@ -24,9 +24,10 @@
 // price of forming dP twice and P twice.  One role needs two 128-row tiles in LDS and fits 128
 // registers, so two workgroups share a compute unit and one computes while the other loads;
 // the three roles of a block are issued eight workgroups apart, on one XCD, whose L2 serves the
-// rows that they share.  At 4 x 8192 tokens x 32 heads, bf16, it takes 730 us and moves 2.47 GB
-// (3.4 TB/s; the matrix units are busy 15% of the time, LDS 23%): memory bounds it, at two
-// thirds of a copy's rate, with loads and sums of two workgroups in turn.  (One kernel for dk and
+// rows that they share.  At 4 x 8192 tokens x 32 heads, bf16, it takes 735 us and moves 2.47 GB
+// (3.4 TB/s; matrix instructions issue 17% of the time, vector instructions 34%, LDS is busy
+// 25%): memory bounds it, at two thirds of a copy's rate, with loads and sums of two
+// workgroups in turn.  (One kernel for dk and
 // dv at 255 registers, one workgroup a compute unit, took 620 us, and dq beside it 461.)
 // linear_dg_kernel finishes dg.
 #include "kda_linear_device.h"
