@@ -7,7 +7,6 @@
 namespace kda {
 namespace lin {
 
-typedef double f64x2 __attribute__((ext_vector_type(2)));
 
 // A lane value the compiler cannot see through: LDS offsets made from it stay inside the loop
 // (a few integer operations) instead of being kept in registers across it.

@@ -214,6 +214,88 @@ def test_divided_value_heads(dtype, lens, H, Hk, dk, dv):
         check_bwd(d, h, cu, lens, dtype, out, 0.125)
 
 
+def big(seed, T, N, H, Hk, dk, dv):
+    """bf16 inputs made on the GPU, for sizes that numpy would take long over."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+
+    def rounded(*shape):
+        return torch.randn(shape, generator=gen, device="cuda", dtype=torch.bfloat16)
+
+    d = {"q": rounded(T, Hk, dk), "k": rounded(T, Hk, dk), "v": rounded(T, H, dv), "dO": rounded(T, H, dv)}
+    d["g"] = -torch.nn.functional.softplus(torch.randn((T, H), generator=gen, device="cuda") - 2)
+    d["s0"], d["dS"] = (0.1 * torch.randn((N, H, dk, dv), generator=gen, device="cuda") for _ in range(2))
+    return d
+
+
+def part(d, rows, docs, heads, keys):
+    """The inputs of some rows, documents and heads, contiguous."""
+    e = {n: d[n][rows][:, keys].contiguous() for n in ("q", "k")}
+    e.update({n: d[n][rows][:, heads].contiguous() for n in ("v", "dO", "g")})
+    e.update({n: d[n][docs][:, heads].contiguous() for n in ("s0", "dS")})
+    return e, {n: host(t) for n, t in e.items()}
+
+
+def test_most_heads():
+    """32767 heads, the most there are: 32-bit row offsets of almost 2^31 bytes in the fp32 outputs."""
+    need_gpu()
+    T, H, dk, dv = 129, 32767, 64, 128
+    d = big(31, T, 1, H, H, dk, dv)
+    _say("most heads")
+    o, sf = kda.kda_linear_fwd(d["q"], d["k"], d["v"], d["g"], None, d["s0"], scale=0.125)
+    gr = kda.kda_linear_bwd(d["q"], d["k"], d["v"], d["g"], d["dO"], None, d["s0"], d["dS"], scale=0.125)
+    torch.cuda.synchronize()
+    heads = [0, 20001, 32766]
+    e, h = part(d, slice(0, T), slice(0, 1), heads, heads)
+    cu = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    o1, sf1 = check_fwd(e, h, cu, [T], "bf16", torch.float32, 0.125)
+    gr1 = check_bwd(e, h, cu, [T], "bf16", torch.float32, 0.125)
+    # the plans differ only in the segments, which 129 tokens do not have: the same sums in the same order
+    for n, a, b in [("o", o, o1), ("final", sf, sf1)] + [(n, gr[n], gr1[n]) for n in gr]:
+        assert torch.equal(a[:, heads], b), n
+
+
+def test_long_offsets():
+    """131072 tokens x 128 heads of 128: more than 2^31 elements of v, o, dO and dv.  The last document is compared."""
+    need_gpu()
+    lens, H, Hk, dk, dv = [131000, 72], 128, 1, 64, 128
+    d = big(32, sum(lens), 2, H, Hk, dk, dv)
+    cu = torch.tensor([0, lens[0], sum(lens)], dtype=torch.int32, device="cuda")
+    _say("long offsets")
+    o, sf = kda.kda_linear_fwd(d["q"], d["k"], d["v"], d["g"], cu, d["s0"], scale=0.125, out_dtype=torch.bfloat16)
+    gr = kda.kda_linear_bwd(d["q"], d["k"], d["v"], d["g"], d["dO"], cu, d["s0"], d["dS"], scale=0.125,
+                            out_dtype=torch.bfloat16)
+    torch.cuda.synchronize()
+    rows = slice(lens[0], sum(lens))
+    e, h = part(d, rows, slice(1, 2), slice(0, H), slice(0, 1))
+    one = torch.tensor([0, lens[1]], dtype=torch.int32, device="cuda")
+    o1, sf1 = check_fwd(e, h, one, lens[1:], "bf16", torch.bfloat16, 0.125)
+    assert torch.equal(o[rows], o1) and torch.equal(sf[1:], sf1)
+    gr1 = check_bwd(e, h, one, lens[1:], "bf16", torch.bfloat16, 0.125)
+    for n in ("dv", "dg"):
+        assert torch.equal(gr[n][rows], gr1[n]), n
+    assert torch.equal(gr["dS0"][1:], gr1["dS0"])
+    # the value heads of the one key head are divided among workgroups for 72 tokens, not for 131072: sums of 128 heads
+    # in another order, then one rounding each
+    for n in ("dq", "dk"):
+        a, b = gr[n][rows].double(), gr1[n].double()
+        assert float((a - b).norm()) <= (2 * BF16 + STEPS) * float(b.norm()), n
+
+
+def test_decode_long_offsets():
+    """More than 2^31 elements of state, in place."""
+    need_gpu()
+    N, H, d = 530, 256, 128
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    q, k, v = (torch.randn((N, H, d), generator=gen, device="cuda") for _ in range(3))
+    g = -torch.rand((N, H), generator=gen, device="cuda")
+    s = torch.randn((N, H, d, d), generator=gen, device="cuda")
+    _say("decode, long offsets")
+    want = [x[-1:] for x in kda.kda_linear_decode(*(x[-1:].clone() for x in (q, k, v, g)), s[-1:].clone())]
+    o, s2 = kda.kda_linear_decode(q, k, v, g, s, out_state=s)
+    torch.cuda.synchronize()
+    assert s2 is s and torch.equal(o[-1:], want[0]) and torch.equal(s[-1:], want[1])
+
+
 def test_strong_and_infinite_gates():
     """Gates of -8 a token, and -inf, which restarts the state at its token."""
     need_gpu()

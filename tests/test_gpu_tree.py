@@ -210,6 +210,28 @@ def test_strong_and_infinite_gates(rule):
 
 
 @pytest.mark.parametrize("rule", ["delta", "linear"])
+def test_long_offsets(rule):
+    """More than 2^31 elements of state: the last sequence as in a call of its own."""
+    need_gpu()
+    N, L, H, d = 530, 3, 256, 128
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    q, k, v = (torch.randn((N, L, H, d), generator=gen, device="cuda", dtype=torch.bfloat16) for _ in range(3))
+    g = -torch.rand((N, L, H, d) if rule == "delta" else (N, L, H), generator=gen, device="cuda")
+    g = g.bfloat16() if rule == "delta" else g
+    beta = torch.randn((N, L, H), generator=gen, device="cuda").bfloat16() if rule == "delta" else None
+    s = torch.randn((N, H, d, d), generator=gen, device="cuda")
+    par = torch.tensor([[-1, 0, 0]] * N, dtype=torch.int32, device="cuda")
+    acc = torch.full((N,), 2, dtype=torch.int32, device="cuda")
+    last = [None if x is None else x[-1:].clone() for x in (q, k, v, g, beta, par, acc, s)]
+    _say(f"long offsets {rule}")
+    want = kda.kda_tree(*last[:6], last[7]), kda.kda_tree_commit(*last[1:])
+    o = kda.kda_tree(q, k, v, g, beta, par, s)
+    assert kda.kda_tree_commit(k, v, g, beta, par, acc, s, out_state=s) is s
+    torch.cuda.synchronize()
+    assert torch.equal(o[-1:], want[0]) and torch.equal(s[-1:], want[1])
+
+
+@pytest.mark.parametrize("rule", ["delta", "linear"])
 def test_chain_equals_decode_steps(rule):
     """A chain's outputs and committed states are those of one decode step per token."""
     need_gpu()
