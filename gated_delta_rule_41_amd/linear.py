@@ -233,7 +233,11 @@ def kda_linear(q, k, v, g, cu_seqlens=None, initial_state=None, *, num_seqs: Opt
     """kda_linear_fwd as a differentiable torch op: returns ``(o, final_state)``
     (fp32) and, under autograd, back-propagates through kda_linear_bwd.  The
     upstream gradient of o is cast to the input dtype, and the gradients of q,
-    k, v and g are rounded to it.  A second differentiation is refused."""
+    k, v and g are rounded to it.  A second differentiation is refused.
+
+    In a captured graph use torch.autograd.grad, or leaves of which no eager graph
+    is alive: torch ties a leaf's gradient accumulation to the stream of its first
+    graph."""
     global _FN
     if _FN is None:
         _FN = _autograd_function()

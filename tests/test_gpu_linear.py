@@ -560,3 +560,37 @@ def test_repeatable_graph_streams():
         torch.cuda.synchronize()
         assert torch.isfinite(junk)
         assert all(torch.equal(a, b) for a, b in zip(outs, ref_)), rep
+
+
+def test_captured_autograd():
+    """kda_linear and its backward in a graph: every replay equals the eager call, with eager calls in between."""
+    need_gpu()
+    lens = [300, 41]
+    d, _, cu = make(17, lens, 4, 2, 64, 64, "bf16")
+    e, _, _ = make(18, lens, 4, 2, 64, 64, "bf16")
+    names = ("q", "k", "v", "g", "s0")
+
+    def call(x, up):
+        leaves = [x[n].detach().requires_grad_(True) for n in names]
+        o, sf = kda.kda_linear(*leaves[:4], cu, leaves[4], scale=0.125)
+        return [o.detach(), sf.detach()] + list(torch.autograd.grad([o, sf], leaves, up))
+
+    up = [d["dO"].float(), d["dS"]]
+    want = {id(x): call(x, up) for x in (d, e)}
+    x = {n: d[n].clone() for n in names}
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call(x, up)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = call(x, up)
+    for src in (d, e, e, d):
+        for n in names:
+            x[n].copy_(src[n])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want[id(src)]))
+        assert all(torch.equal(a, b) for a, b in zip(call(src, up), want[id(src)]))
