@@ -127,15 +127,17 @@ struct BwdLayout {
     size_t S, dS, e, a, f, cross, part, sums, seg[2], decay[2], total;
 };
 // A key head's value heads are divided among so many workgroups: the smallest divisor of their
-// number that gives kGradTarget workgroups (three roles a block), so that short streams do not
-// wait for one workgroup's value heads in turn.  Backward in us, whole and divided for 256, 512
+// number that gives kGradTarget workgroups (three roles a block), or the largest that does not,
+// so that short streams do not wait for one workgroup's value heads in turn.  Backward in us, whole and divided for 256, 512
 // and 1024 workgroups: 134 tokens x 8 heads on 2: 44, 27, 27, 27; 1024 x 32 on 8: 87, 87, 77,
 // 81; 4096 x 16 on 4: 130, 130, 139, 143; 4096 x 32 on 1: 354, 192, 189, 186.
 constexpr int64_t kGradTarget = 512;
 int32_t grad_parts(const kda_linear_config* c, int64_t blocks) {
     const int32_t R = c->H / c->Hk;
+    const int64_t groups = 3 * blocks * c->Hk;
     int32_t parts = 1;
-    while (parts < R && (3 * blocks * c->Hk * parts < kGradTarget || R % parts)) ++parts;
+    for (int32_t x = 2; x <= R && groups * parts < kGradTarget && x <= kGradTarget; ++x)
+        if (R % x == 0 && groups * x < 2 * kGradTarget) parts = x;
     return parts;
 }
 BwdLayout bwd_layout(const kda_linear_config* c, int64_t T, int32_t N) {

@@ -315,8 +315,11 @@ void kda_linear_config_init(kda_linear_config* cfg, int32_t H, int32_t Hk, int32
  * config or sizes).  The forward's is non-zero when it cuts documents into
  * segments (those longer than an equal share of total_tokens * H, where that
  * pays; at most 512 documents; a rule on cfg and the sizes only): each
- * segment's own sum of k v^T, then the states entering the segments.  The backward's holds S and dL/dS at every 128-token block (input
- * type), per-token sums for dg, and the segments' states likewise. */
+ * segment's own sum of k v^T, then the states entering the segments.  The
+ * backward's holds S and dL/dS at every 128-token block (input type),
+ * per-token sums for dg, the segments' states likewise, and for short streams
+ * with shared key heads partial sums of dq and dk.  Calls that may run at the
+ * same time, replays of captured ones included, need a workspace each. */
 size_t kda_linear_fwd_workspace_size(const kda_linear_config* cfg, int64_t total_tokens, int32_t num_seqs);
 size_t kda_linear_bwd_workspace_size(const kda_linear_config* cfg, int64_t total_tokens, int32_t num_seqs);
 

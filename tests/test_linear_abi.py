@@ -129,6 +129,10 @@ def test_forward_and_backward_refuse_bad_arguments():
     # sizes that the calls refuse need no workspace either
     for T, N in ((-1, 1), (1 << 31, 1), (1 << 62, 1), ((1 << 31) - 64, 1), (128, 0), (128, -1)):
         assert _lib.kda_linear_fwd_workspace_size(cfg, T, N) == 0 and _lib.kda_linear_bwd_workspace_size(cfg, T, N) == 0
+    # many value heads on one key head: the partial gradients stay a few times the gradients themselves
+    for H in (8192, 8191):
+        shared = _lib.kda_linear_bwd_workspace_size(lin(H=H, Hk=1), 256, 1)
+        assert 0 < shared <= 1.05 * _lib.kda_linear_bwd_workspace_size(lin(H=H, Hk=H), 256, 1)
     big = lin(H=1 << 30, Hk=1 << 30)
     assert _lib.kda_linear_bwd_workspace_size(big, 1 << 20, 1) == 0 and fwd(big) == KDA_ERR_UNSUPPORTED
 
