@@ -131,7 +131,7 @@ struct BwdLayout {
 // so that short streams do not wait for one workgroup's value heads in turn.  Backward in us, whole and divided for 256, 512
 // and 1024 workgroups: 134 tokens x 8 heads on 2: 44, 27, 27, 27; 1024 x 32 on 8: 87, 87, 77,
 // 81; 4096 x 16 on 4: 130, 130, 139, 143; 4096 x 32 on 1: 354, 192, 189, 186.
-constexpr int64_t kGradTarget = 512;
+constexpr int64_t kGradTarget = 384;   // 288 workgroups gain from it (1024 x 32 on 8), 408 lose (4096 x 16 on 4)
 int32_t grad_parts(const kda_linear_config* c, int64_t blocks) {
     const int32_t R = c->H / c->Hk;
     const int64_t groups = 3 * blocks * c->Hk;
