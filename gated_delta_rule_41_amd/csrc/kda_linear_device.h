@@ -312,18 +312,29 @@ template <typename O> __device__ __forceinline__ void store4(Buffer b, unsigned 
     if constexpr (sizeof(O) == 2) __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, pack4<bf16>(x)), b, at * 2, 0, 0);
     else __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), b, at * 4, 0, 0);
 }
+// Two accumulator blocks side by side (x: four values at column 4 qg of a row's first 16, y: of
+// its second) to 32 columns of a row from `at`.  bf16: lanes 16 apart trade halves, so that each
+// stores 16 bytes and a row 64 in a piece, where 8 and 32 of them would be.
+template <typename O> __device__ __forceinline__ void store8(Buffer b, unsigned at, int qg, f32x4 x, f32x4 y) {
+    if constexpr (sizeof(O) == 2) {
+        const u32x2 p = __builtin_bit_cast(u32x2, pack4<bf16>(x)), q = __builtin_bit_cast(u32x2, pack4<bf16>(y));
+        const auto lo = __builtin_amdgcn_permlane16_swap(p[0], q[0], false, false), hi = __builtin_amdgcn_permlane16_swap(p[1], q[1], false, false);
+        __builtin_amdgcn_raw_buffer_store_b128(u32x4{lo[0], hi[0], lo[1], hi[1]}, b, (at + 16 * (qg & 1) + 8 * (qg >> 1)) * 2, 0, 0);
+    } else {
+        store4<O>(b, at + 4 * qg, x);
+        store4<O>(b, at + 16 + 4 * qg, y);
+    }
+}
 // Row `row` of D columns, four values at 16 m + 4 qg for every m, to a block's output of either
 // type: one branch.
+template <typename O, int D> __device__ __forceinline__ void store_row(O* base, int64_t ld, int rows, int most, int row, int qg, const f32x4 (&x)[D / 16]) {
+    const Buffer b = rows_of(base, ld, rows, most, D);
+#pragma unroll
+    for (int m = 0; m < D / 16; m += 2) store8<O>(b, row * (unsigned)ld + 16 * m, qg, x[m], x[m + 1]);
+}
 template <int D> __device__ __forceinline__ void store_row(void* base, int64_t at, int64_t ld, int rows, int most, int row, int qg, const f32x4 (&x)[D / 16], int out_bf16) {
-    if (out_bf16) {
-        const Buffer b = rows_of((bf16*)base + at, ld, rows, most, D);
-#pragma unroll
-        for (int m = 0; m < D / 16; ++m) store4<bf16>(b, row * (unsigned)ld + 16 * m + 4 * qg, x[m]);
-    } else {
-        const Buffer b = rows_of((float*)base + at, ld, rows, most, D);
-#pragma unroll
-        for (int m = 0; m < D / 16; ++m) store4<float>(b, row * (unsigned)ld + 16 * m + 4 * qg, x[m]);
-    }
+    if (out_bf16) store_row<bf16, D>((bf16*)base + at, ld, rows, most, row, qg, x);
+    else store_row<float, D>((float*)base + at, ld, rows, most, row, qg, x);
 }
 
 // A tile of ROWS x COLS (row-major in global with row stride `ld` elements) held in registers

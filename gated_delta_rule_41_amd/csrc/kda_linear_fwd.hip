@@ -218,8 +218,9 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void linear_out_k
 #pragma unroll
                 for (int c = 0; c < NC; ++c) out[c][m] = mma_k32(out[c][m], vf[c][kk], f);
             }
-#pragma unroll
-            for (int c = 0; c < NC; ++c) store4<O>(to, (16 * m + cl) * (unsigned)ldv + col + 16 * c + 4 * qg, out[c][m]);
+            const unsigned at = (16 * m + cl) * (unsigned)ldv + col;
+            if constexpr (NC == 2) store8<O>(to, at, qg, out[0][m], out[1][m]);
+            else store4<O>(to, at + 4 * qg, out[0][m]);
         }
         // the state
         const float eC = G.E;
