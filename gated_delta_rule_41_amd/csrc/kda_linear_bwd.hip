@@ -62,14 +62,10 @@ __device__ __forceinline__ f32x4 half4(f32x8 x, int hi) {
 }
 __device__ __forceinline__ float dot4(f32x4 a, f32x4 b) { return a[0] * b[0] + a[1] * b[1] + a[2] * b[2] + a[3] * b[3]; }
 
-// Eight elements at a byte offset, and two groups of four.
-template <typename T> __device__ __forceinline__ typename V8<T>::t load_halves(Buffer b, unsigned o0, unsigned o1) {
-    if constexpr (sizeof(T) == 2) return join(__builtin_bit_cast(bf16x4, load8(b, o0)), __builtin_bit_cast(bf16x4, load8(b, o1)));
-    else return join(__builtin_bit_cast(f32x4, load16(b, o0)), __builtin_bit_cast(f32x4, load16(b, o1)));
-}
-template <typename T> __device__ __forceinline__ typename V8<T>::t load_frag(Buffer b, unsigned o0, unsigned o1) {
-    if constexpr (sizeof(T) == 2) return __builtin_bit_cast(bf16x8, load16(b, o0));
-    else return load_halves<T>(b, o0, o1);
+// Eight elements at a byte offset.
+template <typename T> __device__ __forceinline__ typename V8<T>::t load_frag(Buffer b, unsigned off) {
+    if constexpr (sizeof(T) == 2) return __builtin_bit_cast(bf16x8, load16(b, off));
+    else return join(__builtin_bit_cast(f32x4, load16(b, off)), __builtin_bit_cast(f32x4, load16(b, off + 16)));
 }
 
 // Row `row` of a global matrix as product fragments (zeros where row >= rows).
@@ -77,14 +73,23 @@ template <typename T, int D> __device__ __forceinline__ void row_frags(typename 
     const Buffer b = rows_of(base, ld, rows, kB, D);
     const unsigned off = ((unsigned)row * (unsigned)ld + 8 * qg) * sizeof(T);
 #pragma unroll
-    for (int s = 0; s < D / 32; ++s) f[s] = load_frag<T>(b, off + 32 * s * sizeof(T), off + (32 * s + 4) * sizeof(T));
+    for (int s = 0; s < D / 32; ++s) f[s] = load_frag<T>(b, off + 32 * s * sizeof(T));
 }
 // The same row in the k order of two stacked accumulator blocks.
 template <typename T, int D> __device__ __forceinline__ void row_perms(typename V8<T>::t (&f)[D / 32], const T* base, int64_t ld, int row, int rows, int qg) {
     const Buffer b = rows_of(base, ld, rows, kB, D);
-    const unsigned off = ((unsigned)row * (unsigned)ld + 4 * qg) * sizeof(T);
+    if constexpr (sizeof(T) == 2) {
+        const unsigned off = ((unsigned)row * (unsigned)ld + trade_col(qg)) * 2;
 #pragma unroll
-    for (int s = 0; s < D / 32; ++s) f[s] = load_halves<T>(b, off + 32 * s * sizeof(T), off + (32 * s + 16) * sizeof(T));
+        for (int s = 0; s < D / 32; ++s) {
+            const u32x4 x = load16(b, off + 64 * s);
+            f[s] = __builtin_bit_cast(bf16x8, trade(u32x2{x[0], x[1]}, u32x2{x[2], x[3]}));
+        }
+    } else {
+        const unsigned off = ((unsigned)row * (unsigned)ld + 4 * qg) * 4;
+#pragma unroll
+        for (int s = 0; s < D / 32; ++s) f[s] = join(__builtin_bit_cast(f32x4, load16(b, off + 128 * s)), __builtin_bit_cast(f32x4, load16(b, off + 128 * s + 64)));
+    }
 }
 
 // What a role's workgroup knows of its block.

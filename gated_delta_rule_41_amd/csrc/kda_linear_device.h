@@ -306,20 +306,28 @@ template <typename T> __device__ __forceinline__ Buffer rows_of(const T* base, i
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(base), 0, bytes, 0x00027000);
 }
 __device__ __forceinline__ u32x4 load16(Buffer b, unsigned off) { return __builtin_amdgcn_raw_buffer_load_b128(b, off, 0, 0); }
-__device__ __forceinline__ u32x2 load8(Buffer b, unsigned off) { return __builtin_amdgcn_raw_buffer_load_b64(b, off, 0, 0); }
 // Four values at element `at` of a buffer of O.
 template <typename O> __device__ __forceinline__ void store4(Buffer b, unsigned at, f32x4 x) {
     if constexpr (sizeof(O) == 2) __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, pack4<bf16>(x)), b, at * 2, 0, 0);
     else __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), b, at * 4, 0, 0);
 }
+// Rows 0 and 1 of 16 lanes, and 2 and 3, trade: what lane qg of a has of the first 16 columns
+// (4 qg ..) and of b of the second becomes 8 columns in a row, from trade_col(qg) on; and back.
+__device__ __forceinline__ u32x4 trade(u32x2 a, u32x2 b) {
+    const auto lo = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false), hi = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+    return u32x4{lo[0], hi[0], lo[1], hi[1]};
+}
+__device__ __forceinline__ int trade_col(int qg) { return 16 * (qg & 1) + 8 * (qg >> 1); }
+__device__ __forceinline__ u32x4 trade_bf16(f32x4 x, f32x4 y) {
+    return trade(__builtin_bit_cast(u32x2, pack4<bf16>(x)), __builtin_bit_cast(u32x2, pack4<bf16>(y)));
+}
 // Two accumulator blocks side by side (x: four values at column 4 qg of a row's first 16, y: of
-// its second) to 32 columns of a row from `at`.  bf16: lanes 16 apart trade halves, so that each
-// stores 16 bytes and a row 64 in a piece, where 8 and 32 of them would be.
+// its second) to 32 columns of a row from `at`.  bf16: each lane stores 16 bytes and a row 64 in
+// a piece, where 8 and 32 of them would be (memory takes pieces of rows worse the smaller they
+// are: 735 -> 670 us of gradients).
 template <typename O> __device__ __forceinline__ void store8(Buffer b, unsigned at, int qg, f32x4 x, f32x4 y) {
     if constexpr (sizeof(O) == 2) {
-        const u32x2 p = __builtin_bit_cast(u32x2, pack4<bf16>(x)), q = __builtin_bit_cast(u32x2, pack4<bf16>(y));
-        const auto lo = __builtin_amdgcn_permlane16_swap(p[0], q[0], false, false), hi = __builtin_amdgcn_permlane16_swap(p[1], q[1], false, false);
-        __builtin_amdgcn_raw_buffer_store_b128(u32x4{lo[0], hi[0], lo[1], hi[1]}, b, (at + 16 * (qg & 1) + 8 * (qg >> 1)) * 2, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(trade_bf16(x, y), b, (at + trade_col(qg)) * 2, 0, 0);
     } else {
         store4<O>(b, at + 4 * qg, x);
         store4<O>(b, at + 16 + 4 * qg, y);

@@ -323,11 +323,15 @@ __global__ __launch_bounds__(kThreads, 2) void linear_state_kernel(LinearStatePa
         tb.store(sB, tid);
         if constexpr (BORDER)
             if (x == 0) {
-                T* b = (T*)D.border + ((block0 + t0 / kLinBlock) * p.H + h) * DK * dv + lane;
+                T* b = (T*)D.border + ((block0 + t0 / kLinBlock) * p.H + h) * DK * dv;
 #pragma unroll
-                for (int c = 0; c < NC; ++c)
+                for (int d = 0; d < DK / 16; ++d) {
+                    if constexpr (sizeof(T) == 2 && NC == 2)
+                        *reinterpret_cast<u32x4*>(b + (16 * d + cl) * dv + slice + col + trade_col(qg)) = trade_bf16(S[0][d], S[1][d]);
+                    else
 #pragma unroll
-                    for (int d = 0; d < DK / 16; ++d) *reinterpret_cast<typename V4<T>::t*>(b + 16 * d * dv + 16 * c) = pack4<T>(S[c][d]);
+                        for (int c = 0; c < NC; ++c) *reinterpret_cast<typename V4<T>::t*>(b + lane + 16 * d * dv + 16 * c) = pack4<T>(S[c][d]);
+                }
             }
         const int t2 = t0 + 2 * dir, rows2 = rows_at(t2);
         g = load_gate(gp, p.g_stride, t2, rows2, l, gw);
