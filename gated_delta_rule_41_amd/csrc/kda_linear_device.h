@@ -324,7 +324,7 @@ __device__ __forceinline__ u32x4 trade_bf16(f32x4 x, f32x4 y) {
 // Two accumulator blocks side by side (x: four values at column 4 qg of a row's first 16, y: of
 // its second) to 32 columns of a row from `at`.  bf16: each lane stores 16 bytes and a row 64 in
 // a piece, where 8 and 32 of them would be (memory takes pieces of rows worse the smaller they
-// are: 735 -> 670 us of gradients).
+// are: gradients of 4 x 8192 x 32 heads 753 -> 664 us).
 template <typename O> __device__ __forceinline__ void store8(Buffer b, unsigned at, int qg, f32x4 x, f32x4 y) {
     if constexpr (sizeof(O) == 2) {
         __builtin_amdgcn_raw_buffer_store_b128(trade_bf16(x, y), b, (at + trade_col(qg)) * 2, 0, 0);

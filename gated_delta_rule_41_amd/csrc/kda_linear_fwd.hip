@@ -15,16 +15,15 @@
 // The next chunk's rows are loaded into registers while this one runs, and its gates are
 // summed by wave 0, which has the least of P.
 //
-// 131083 tokens x 16 heads of 128, bf16, 512 segments: 496 us, 2.19 GB, 4.4 TB/s (a copy: 5.2).
+// 131083 tokens x 16 heads of 128, bf16, 512 segments: 472 us, 2.19 GB, 4.6 TB/s (a copy: 5.2).
 // Two waves a SIMD issue vector instructions 43% and matrix instructions 33% of that time; at
-// 32768 x 32 heads on 8, with a third less to read, it takes 251 us against 275 on 32: near both
+// 32768 x 32 heads on 8, with a third less to read, it took 251 us against 275 on 32: near both
 // bounds.  64 tokens a step are what two workgroups' LDS allows.
 //
 // linear_state_kernel: the state alone, forward or in reverse (the same sum with q, dO and
 // weights e^{G_i}), for the segments of long documents and for the backward.  Own sums of the
-// same segments: 256 us, 1.1 GB, 4.3 TB/s.  Both directions of 4 x 8192 x 32 heads with the
-// states at the blocks' borders: 404 us, 1.7 GB, 4.2 TB/s (without its products 361 us, without
-// the borders' stores 293).
+// same segments: 250 us, 1.1 GB, 4.4 TB/s.  Both directions of 4 x 8192 x 32 heads with the
+// states at the blocks' borders: 371 us, 1.7 GB, 4.6 TB/s.
 //
 // linear_carry_kernel: the states entering the segments of each document after the first, from
 // the segments' own sums (a scalar decay composes as plain products).  In place: a segment's
