@@ -323,13 +323,19 @@ __global__ __launch_bounds__(kThreads, 2) void linear_state_kernel(LinearStatePa
         if constexpr (BORDER)
             if (x == 0) {
                 T* b = (T*)D.border + ((block0 + t0 / kLinBlock) * p.H + h) * DK * dv;
+                if constexpr (sizeof(T) == 4) {
 #pragma unroll
-                for (int d = 0; d < DK / 16; ++d) {
-                    if constexpr (sizeof(T) == 2 && NC == 2)
+                    for (int c = 0; c < NC; ++c)
+#pragma unroll
+                        for (int d = 0; d < DK / 16; ++d) *reinterpret_cast<f32x4*>(b + lane + 16 * d * dv + 16 * c) = S[c][d];
+                } else if constexpr (NC == 2) {
+#pragma unroll
+                    for (int d = 0; d < DK / 16; ++d)
                         *reinterpret_cast<u32x4*>(b + (16 * d + cl) * dv + slice + col + trade_col(qg)) = trade_bf16(S[0][d], S[1][d]);
-                    else
+                } else {   // one group of columns: the trade is between two blocks of rows
 #pragma unroll
-                        for (int c = 0; c < NC; ++c) *reinterpret_cast<typename V4<T>::t*>(b + lane + 16 * d * dv + 16 * c) = pack4<T>(S[c][d]);
+                    for (int d = 0; d < DK / 16; d += 2)
+                        *reinterpret_cast<u32x4*>(b + (16 * (d + (qg & 1)) + cl) * dv + slice + col + 8 * (qg >> 1)) = trade_bf16(S[0][d], S[0][d + 1]);
                 }
             }
         const int t2 = t0 + 2 * dir, rows2 = rows_at(t2);
