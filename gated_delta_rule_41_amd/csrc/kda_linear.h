@@ -28,7 +28,7 @@ struct LinearParams {
     void* o;               // [T,H,dv] out dtype
     float* sfinal;         // [N,H,dk,dv] or nullptr
     int64_t T;
-    int32_t N, H, Hk, dv, seqlen, g_stride, seg_len, out_bf16, chains;
+    int32_t N, H, Hk, dv, seqlen, g_stride, seg_len, out_bf16, chains, longest_first;
     float scale;
 };
 

@@ -120,6 +120,48 @@ __device__ __forceinline__ Range seg_range(const int32_t* cu, int N, int seqlen,
     return r;
 }
 
+// The k-th longest segment of up to 64 documents: all full ones in the documents' order, then
+// their rests from the longest on (an empty document's is empty), so that a launch of unlike
+// walks ends evenly.  `slot` is the segment's number as in seg_range.  A rest's key holds its
+// length in 1024ths of a segment and its document, and the wanted one is found bit by bit: the
+// largest key that more than k - (full segments) rests reach.
+__device__ __forceinline__ Range longest_range(const int32_t* cu, int N, int seqlen, int64_t T, int64_t k, int seg_len, int64_t& slot) {
+    const int l = threadIdx.x & 63;
+    Range r;
+    int full = 0, key = 0, segments = 0;
+    if (l < N) {
+        int64_t s, e;
+        doc_bounds(cu, seqlen, T, l, s, e);
+        full = (int)((e - s) / seg_len);
+        const int64_t rest = (e - s) - (int64_t)full * seg_len;
+        const bool any = rest || s == e;
+        if (any) key = (int)(rest * 1024 / seg_len << 6 | (63 - l)) + 1;
+        segments = full + any;
+    }
+    const int upto = wave_scan_int(full), all = __builtin_amdgcn_readlane(upto, 63);
+    int64_t j;
+    if (k < all) {
+        r.n = __ffsll((long long)__ballot(upto > k)) - 1;
+        j = k - (__builtin_amdgcn_readlane(upto, r.n) - __builtin_amdgcn_readlane(full, r.n));
+    } else {
+        int found = 0;
+        for (int bit = 1 << 16; bit; bit >>= 1)
+            if (__popcll(__ballot(key >= (found | bit))) > k - all) found |= bit;
+        if (!found) {
+            r.lo = r.hi = r.start = r.end = 0;
+            r.n = N;
+            return r;
+        }
+        r.n = 63 - ((found - 1) & 63);
+        j = __builtin_amdgcn_readlane(full, r.n);
+    }
+    doc_bounds(cu, seqlen, T, r.n, r.start, r.end);
+    r.lo = r.start + j * seg_len;
+    r.hi = r.lo + seg_len < r.end ? r.lo + seg_len : r.end;
+    slot = __builtin_amdgcn_readlane(wave_scan_int(segments) - segments, r.n) + j;
+    return r;
+}
+
 // A token's gate in log2 units.  Below -128 e^g is zero in fp32 either way (the smallest
 // fp32 value is e^-103), so such gates, -inf among them, count as -128: every difference of
 // sums stays finite.  NaN stays NaN.

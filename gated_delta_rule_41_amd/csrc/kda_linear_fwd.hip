@@ -87,11 +87,12 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void linear_out_k
     __shared__ __align__(32) Gates gates[2];
 
     const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, cl = l & 15, qg = l >> 4;
-    const int64_t slot = blockIdx.x / p.H;
+    int64_t slot = blockIdx.x / p.H;
     const int h = blockIdx.x % p.H, hk = h / (p.H / p.Hk);
-    const Range rg = seg_range(p.cu, p.N, p.seqlen, p.T, slot, p.seg_len);
+    const Range rg = p.longest_first ? longest_range(p.cu, p.N, p.seqlen, p.T, slot, p.seg_len, slot)
+                                     : seg_range(p.cu, p.N, p.seqlen, p.T, slot, p.seg_len);
     const int col = 16 * NC * w;
-    if (rg.n >= p.N) return;
+    if (rg.n >= p.N || slot * p.H >= p.chains) return;   // the latter with a malformed cu_seqlens only
 
     // the state: block d of group c holds rows 16d + 4qg + i, column col + 16c + cl
     f32x4 S[NC][DK / 16];
