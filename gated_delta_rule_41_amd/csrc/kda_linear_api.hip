@@ -87,14 +87,14 @@ struct Plan {
     int32_t seg_len;   // 0: whole documents
     int64_t chains;    // (document or segment slot, head) pairs
 };
-// ways: workgroups that share a chain (directions, slices of the value columns).  ragged: half
-// shares, as walks of unlike lengths end together better (37 ragged documents, 16411 tokens, 32
-// heads: 263 -> 244 us; one document of 131072 tokens x 16 heads would lose: 787 -> 820 us).
-Plan walk_plan(const kda_linear_config* c, int64_t T, int32_t N, int ways, bool ragged) {
+// ways: workgroups that share a chain (directions, slices of the value columns).  Half shares for
+// several documents, which end more evenly in the documents' order, lose to whole ones with the
+// longest first (37 ragged documents, 16411 tokens, 32 heads: 223 against 207 us; 4 equal ones,
+// 32768, 32: 427, 386).
+Plan walk_plan(const kda_linear_config* c, int64_t T, int32_t N, int ways) {
     Plan p = {0, (int64_t)N * c->H};
-    const double even = ragged ? 0.5 : 1.0, rows = even * T * c->H;
-    const int64_t share = (int64_t)(rows * ways / kWalkTarget);
-    const double least = std::max(0.9 * sqrt(rows * c->dk * c->dv) / 128.0, 1.4 * sqrt((double)T));
+    const int64_t share = T * c->H * ways / kWalkTarget;
+    const double least = std::max(0.8 * sqrt((double)T * c->H * c->dk * c->dv) / 128.0, 1.4 * sqrt((double)T));
     int64_t floor = kLinBlock;
     while (floor < least) floor *= 2;
     const int64_t L = std::max(floor, (share + kLinBlock - 1) / kLinBlock * kLinBlock);
@@ -112,7 +112,7 @@ struct FwdLayout {
     size_t state, decay, total;
 };
 FwdLayout fwd_layout(const kda_linear_config* c, int64_t T, int32_t N) {
-    FwdLayout f = {walk_plan(c, T, N, 1, N > 1), 0, 0, 0};
+    FwdLayout f = {walk_plan(c, T, N, 1), 0, 0, 0};
     if (f.plan.seg_len) {
         f.decay = align256((size_t)f.plan.chains * state_elems(c) * sizeof(float));
         f.total = f.decay + align256((size_t)f.plan.chains * sizeof(float));
@@ -143,7 +143,7 @@ int32_t grad_parts(const kda_linear_config* c, int64_t blocks) {
 BwdLayout bwd_layout(const kda_linear_config* c, int64_t T, int32_t N) {
     BwdLayout b;
     memset(&b, 0, sizeof b);
-    b.plan = walk_plan(c, T, N, 2 * (c->dv / 64), false);
+    b.plan = walk_plan(c, T, N, 2 * (c->dv / 64));
     b.blocks = linear_slots(T, N, kLinBlock);
     b.parts = grad_parts(c, b.blocks);
     size_t at = 0;
