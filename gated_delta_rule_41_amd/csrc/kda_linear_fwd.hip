@@ -28,7 +28,7 @@
 // linear_carry_kernel: the states entering the segments of each document after the first, from
 // the segments' own sums (a scalar decay composes as plain products).  In place: a segment's
 // slot holds its own sum before and its entering state after.  16 us for 32 segments x 16 heads,
-// 20 for 37 documents x 32 heads, about half of it reading and writing the states.
+// 8 for 37 documents x 32 heads, about half of it reading and writing the states.
 #include "kda_linear_device.h"
 
 namespace kda {
