@@ -50,7 +50,7 @@ struct LinearStateParams {
     const float* g;
     const int32_t* cu;
     int64_t T;
-    int32_t N, H, Hk, dv, seqlen, g_stride, seg_len, chains, dirs;
+    int32_t N, H, Hk, dv, seqlen, g_stride, seg_len, whole_len, chains, dirs;   // whole_len: see segment_length
     float scale;
 };
 
@@ -65,7 +65,7 @@ struct LinearCarryParams {
     LinearCarryDir dir[2];
     const int32_t* cu;
     int64_t T;
-    int32_t N, H, seqlen, seg_len, elems, slots;   // elems = dk * dv; slots: room for segments
+    int32_t N, H, seqlen, seg_len, whole_len, elems, slots;   // elems = dk * dv; slots: room for segments
 };
 
 struct LinearBwdParams {

@@ -84,22 +84,26 @@ bool grid_fits(int64_t workgroups, int threads) {
 constexpr int64_t kWholeTokens = 8 * kLinChunk;
 
 struct Plan {
-    int32_t seg_len;   // 0: whole documents
-    int64_t chains;    // (document or segment slot, head) pairs
+    int32_t seg_len;     // 0: whole documents
+    int32_t whole_len;   // see segment_length
+    int64_t chains;      // (document or segment slot, head) pairs
 };
-// ways: workgroups that share a chain (directions, slices of the value columns).  Half shares for
-// several documents, which end more evenly in the documents' order, lose to whole ones with the
-// longest first (37 ragged documents, 16411 tokens, 32 heads: 223 against 207 us; 4 equal ones,
-// 32768, 32: 427, 386).
-Plan walk_plan(const kda_linear_config* c, int64_t T, int32_t N, int ways) {
-    Plan p = {0, (int64_t)N * c->H};
-    const int64_t share = T * c->H * ways / kWalkTarget;
-    const double least = std::max(0.8 * sqrt((double)T * c->H * c->dk * c->dv) / 128.0, 1.4 * sqrt((double)T));
+// dirs: directions walked, each by dv / 64 workgroups in the backward.  Several documents take half
+// shares there unless none of them is longer than a share: 4 ragged documents of 32768 tokens x 32
+// heads 1576 -> 1296 us, but equal ones 1036 -> 1229 if cut like that.  The forward has its longest
+// segments first instead (37 ragged documents, 16411 tokens, 32 heads with half shares 223 us, whole
+// ones 208).
+Plan walk_plan(const kda_linear_config* c, int64_t T, int32_t N, int dirs) {
+    Plan p = {0, 0, (int64_t)N * c->H};
+    const int64_t share = T * c->H * (dirs == 2 ? 2 * (c->dv / 64) : 1) / kWalkTarget;
+    const double least = std::max(0.8 * dirs * sqrt((double)T * c->H * c->dk * c->dv) / 128.0, 1.4 * sqrt((double)T));
     int64_t floor = kLinBlock;
     while (floor < least) floor *= 2;
-    const int64_t L = std::max(floor, (share + kLinBlock - 1) / kLinBlock * kLinBlock);
-    if (T <= 2 * L || T <= kWholeTokens || N > kSegDocs) return p;
-    p.seg_len = (int32_t)L;
+    auto length = [floor](int64_t share) { return std::max(floor, (share + kLinBlock - 1) / kLinBlock * kLinBlock); };
+    const int64_t whole = length(share);
+    if (T <= 2 * whole || T <= kWholeTokens || N > kSegDocs) return p;
+    p.seg_len = (int32_t)(dirs == 2 && N > 1 ? length(share / 2) : whole);
+    p.whole_len = p.seg_len == whole ? 0 : (int32_t)whole;
     p.chains = linear_slots(T, N, p.seg_len) * c->H;
     return p;
 }
@@ -143,7 +147,7 @@ int32_t grad_parts(const kda_linear_config* c, int64_t blocks) {
 BwdLayout bwd_layout(const kda_linear_config* c, int64_t T, int32_t N) {
     BwdLayout b;
     memset(&b, 0, sizeof b);
-    b.plan = walk_plan(c, T, N, 2 * (c->dv / 64));
+    b.plan = walk_plan(c, T, N, 2);
     b.blocks = linear_slots(T, N, kLinBlock);
     b.parts = grad_parts(c, b.blocks);
     size_t at = 0;
@@ -320,7 +324,7 @@ kda_status kda_linear_bwd(const kda_linear_config* cfg, int64_t T, int32_t N, co
     s.dir[0].a = k; s.dir[0].b = v;
     s.dir[1].a = q; s.dir[1].b = dO; s.dir[1].rev = 1;
     s.g = g; s.cu = cu; s.T = T; s.N = N; s.H = cfg->H; s.Hk = cfg->Hk; s.dv = cfg->dv; s.seqlen = seqlen;
-    s.g_stride = g_stride; s.seg_len = b.plan.seg_len; s.chains = (int32_t)b.plan.chains; s.dirs = 2; s.scale = cfg->scale;
+    s.g_stride = g_stride; s.seg_len = b.plan.seg_len; s.whole_len = b.plan.whole_len; s.chains = (int32_t)b.plan.chains; s.dirs = 2; s.scale = cfg->scale;
     const float* first[2] = {s0, dSf};
     float* last[2] = {nullptr, dS0};
     if (s.seg_len) {
@@ -331,7 +335,7 @@ kda_status kda_linear_bwd(const kda_linear_config* cfg, int64_t T, int32_t N, co
             s.dir[i].decay = (float*)(ws + b.decay[i]);
             c.dir[i].s0 = first[i]; c.dir[i].seg = s.dir[i].seg; c.dir[i].decay = s.dir[i].decay; c.dir[i].rev = i;
         }
-        c.cu = cu; c.T = T; c.N = N; c.H = cfg->H; c.seqlen = seqlen; c.seg_len = s.seg_len; c.elems = cfg->dk * cfg->dv;
+        c.cu = cu; c.T = T; c.N = N; c.H = cfg->H; c.seqlen = seqlen; c.seg_len = s.seg_len; c.whole_len = s.whole_len; c.elems = cfg->dk * cfg->dv;
         c.slots = (int32_t)linear_slots(T, N, s.seg_len);
         KDA_TRY(launched(launch_linear_states(s, cfg->in_dtype, cfg->dk, st)));
         KDA_TRY(launched(launch_linear_carry(c, 2, st)));

@@ -120,6 +120,20 @@ __device__ __forceinline__ Range seg_range(const int32_t* cu, int N, int seqlen,
     return r;
 }
 
+// Documents of up to whole_len tokens each stay whole; if one is longer, all are cut into seg_len.
+// (A launch's walks end together with documents alike, and cutting them would only cost; with
+// documents unlike, the shorter segments even them out.)
+__device__ __forceinline__ int segment_length(const int32_t* cu, int N, int seqlen, int64_t T, int seg_len, int whole_len) {
+    const int l = threadIdx.x & 63;
+    if (!whole_len) return seg_len;
+    for (int n0 = 0; n0 < N; n0 += 64) {
+        int64_t s = 0, e = 0;
+        if (n0 + l < N) doc_bounds(cu, seqlen, T, n0 + l, s, e);
+        if (__ballot(e - s > whole_len)) return seg_len;
+    }
+    return whole_len;
+}
+
 // The k-th longest segment of up to 64 documents: all full ones in the documents' order, then
 // their rests from the longest on (an empty document's is empty), so that a launch of unlike
 // walks ends evenly.  `slot` is the segment's number as in seg_range.  A rest's key holds its

@@ -267,7 +267,8 @@ __global__ __launch_bounds__(kThreads, 2) void linear_state_kernel(LinearStatePa
     const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, cl = l & 15, qg = l >> 4;
     const int64_t slot = chain / p.H;
     const int h = chain % p.H, hk = h / (p.H / p.Hk);
-    const Range rg = seg_range(p.cu, p.N, p.seqlen, p.T, slot, p.seg_len);
+    const int seg_len = segment_length(p.cu, p.N, p.seqlen, p.T, p.seg_len, p.whole_len);
+    const Range rg = seg_range(p.cu, p.N, p.seqlen, p.T, slot, seg_len);
     if (rg.n >= p.N) return;
     const bool rev = D.rev != 0;
     const bool head = rev ? rg.hi == rg.end : rg.lo == rg.start, tail = rev ? rg.lo == rg.start : rg.hi == rg.end;
@@ -389,9 +390,10 @@ __global__ __launch_bounds__(kThreads) void linear_carry_kernel(LinearCarryParam
     const int n = (int)(nh / p.H), h = (int)(nh % p.H);
     int64_t s, e;
     doc_bounds(p.cu, p.seqlen, p.T, n, s, e);
-    const int segs = (int)((e - s + p.seg_len - 1) / p.seg_len);
+    const int seg_len = segment_length(p.cu, p.N, p.seqlen, p.T, p.seg_len, p.whole_len);
+    const int segs = (int)((e - s + seg_len - 1) / seg_len);
     if (segs < 2) return;
-    const int64_t first = segments_before(p.cu, p.seqlen, p.T, p.seg_len, n), at = ((int64_t)part * V * kThreads + threadIdx.x) * 4;
+    const int64_t first = segments_before(p.cu, p.seqlen, p.T, seg_len, n), at = ((int64_t)part * V * kThreads + threadIdx.x) * 4;
     if (first + segs > p.slots) return;   // a malformed cu_seqlens only
     const int64_t step = D.rev ? -(int64_t)p.H * p.elems : (int64_t)p.H * p.elems;
     const int64_t from = first + (D.rev ? segs - 1 : 0);

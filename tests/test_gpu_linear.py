@@ -175,10 +175,12 @@ def test_many_documents(dtype, short, long):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("lens,H", [([129, 1, 200, 64, 0, 130, 65, 63], 32), ([8192], 64), ([2900] + [73, 64, 1] * 5, 16),
-                                    ([256, 0, 128, 300, 1, 0, 384, 77], 64), ([40] * 50 + [0] * 13 + [700], 32)])
+                                    ([256, 0, 128, 300, 1, 0, 384, 77], 64), ([40] * 50 + [0] * 13 + [700], 32),
+                                    ([1024] * 8, 16), ([1024] * 3 + [1025, 1023] + [1024] * 3, 16)])
 def test_many_heads(dtype, lens, H):
     """Enough walks that a workgroup of the state kernel takes 128 value columns, and that the forward's come in the order
-    of their lengths (full segments, rests, equal ones, empty documents); some heads are compared, each with the
+    of their lengths (full segments, rests, equal ones, empty documents), and documents that the backward leaves whole
+    until one is a token longer; some heads are compared, each with the
     reference and with a call for it alone."""
     need_gpu()
     _say(f"{H} heads {lens[:2]}... {dtype}")
