@@ -194,7 +194,12 @@ kda_status check_stream(const kda_linear_config* c, int64_t T, int32_t N, const 
 
 bool overlap(const void* a, const void* b, size_t bytes) {
     const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-    return a && a != b && x < y + bytes && y < x + bytes;
+    return a && b && x < y + bytes && y < x + bytes;
+}
+// A step reads and writes each part of the state in one workgroup, so it may run in place.
+kda_status check_step(const float* in, const float* out, size_t bytes) {
+    if (in != out && overlap(in, out, bytes)) return fail(KDA_ERR_INVALID_ARG, "state_in and state_out overlap without being equal%s");
+    return KDA_OK;
 }
 
 kda_status check_tree(const kda_tree_config* c, int32_t N, int threads, int64_t per_head) {
@@ -256,6 +261,9 @@ kda_status kda_linear_fwd(const kda_linear_config* cfg, int64_t T, int32_t N, co
     KDA_TRY(ptr(o, "o", T > 0));
     KDA_TRY(ptr(s0, "initial_state", false));
     KDA_TRY(ptr(sfinal, "final_state", false));
+    // A document's last segment may write its state before the first has read its own.
+    if (overlap(s0, sfinal, (size_t)N * cfg->H * state_elems(cfg) * sizeof(float)))
+        return fail(KDA_ERR_INVALID_ARG, "final_state overlaps initial_state%s");
     const FwdLayout f = fwd_layout(cfg, T, N);
     if (workspace_bytes < f.total) return fail(KDA_ERR_WORKSPACE, "workspace too small%s");
     KDA_TRY(ptr(workspace, "workspace", f.total > 0));
@@ -312,6 +320,10 @@ kda_status kda_linear_bwd(const kda_linear_config* cfg, int64_t T, int32_t N, co
     KDA_TRY(ptr(s0, "initial_state", false));
     KDA_TRY(ptr(dSf, "dS_final", false));
     KDA_TRY(ptr(dS0, "d_initial_state", false));
+    // One launch walks both ways: the reverse walk's end writes what either walk's start may still have to read.
+    const size_t states = (size_t)N * cfg->H * state_elems(cfg) * sizeof(float);
+    if (overlap(dS0, s0, states)) return fail(KDA_ERR_INVALID_ARG, "d_initial_state overlaps initial_state%s");
+    if (overlap(dS0, dSf, states)) return fail(KDA_ERR_INVALID_ARG, "d_initial_state overlaps dS_final%s");
     const BwdLayout b = bwd_layout(cfg, T, N);
     if (workspace_bytes < b.total) return fail(KDA_ERR_WORKSPACE, "workspace too small%s");
     KDA_TRY(ptr(workspace, "workspace", b.total > 0));
@@ -377,8 +389,7 @@ kda_status kda_linear_decode(const kda_linear_config* cfg, int32_t N, const void
     KDA_TRY(ptr(state_in, "state_in", false));
     KDA_TRY(ptr(state_out, "state_out", N > 0));
     KDA_TRY(ptr(o, "o", N > 0));
-    if (overlap(state_in, state_out, (size_t)N * cfg->H * state_elems(cfg) * sizeof(float)))
-        return fail(KDA_ERR_INVALID_ARG, "state_in and state_out overlap without being equal%s");
+    KDA_TRY(check_step(state_in, state_out, (size_t)N * cfg->H * state_elems(cfg) * sizeof(float)));
     LinearDecodeParams p;
     memset(&p, 0, sizeof p);
     p.q = q; p.k = k; p.v = v; p.g = g; p.s_in = state_in; p.s_out = state_out; p.o = o;
@@ -431,8 +442,7 @@ kda_status kda_tree_commit(const kda_tree_config* cfg, int32_t N, const void* k,
     KDA_TRY(ptr(accept, "accept", N > 0));
     KDA_TRY(ptr(state_in, "state_in", false));
     KDA_TRY(ptr(state_out, "state_out", N > 0));
-    if (overlap(state_in, state_out, (size_t)N * cfg->H * cfg->dk * cfg->dv * sizeof(float)))
-        return fail(KDA_ERR_INVALID_ARG, "state_in and state_out overlap without being equal%s");
+    KDA_TRY(check_step(state_in, state_out, (size_t)N * cfg->H * cfg->dk * cfg->dv * sizeof(float)));
     TreeParams p = tree_params(cfg, N);
     p.k = k; p.v = v; p.g = g; p.beta = beta; p.parent = parent; p.accept = accept;
     p.s_in = state_in; p.s_out = state_out;

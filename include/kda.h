@@ -323,8 +323,9 @@ void kda_linear_config_init(kda_linear_config* cfg, int32_t H, int32_t Hk, int32
 size_t kda_linear_fwd_workspace_size(const kda_linear_config* cfg, int64_t total_tokens, int32_t num_seqs);
 size_t kda_linear_bwd_workspace_size(const kda_linear_config* cfg, int64_t total_tokens, int32_t num_seqs);
 
-/* Forward.  initial_state and final_state as for kda_fwd (either may be NULL).
- * workspace may be NULL when kda_linear_fwd_workspace_size() is 0. */
+/* Forward.  initial_state and final_state as for kda_fwd (either may be NULL);
+ * they must not overlap, equal pointers included (KDA_ERR_INVALID_ARG: the
+ * segments of a document run at the same time).  workspace may be NULL when kda_linear_fwd_workspace_size() is 0. */
 kda_status kda_linear_fwd(const kda_linear_config* cfg, int64_t total_tokens, int32_t num_seqs, const void* q,
                           const void* k, const void* v, const float* g, const int32_t* cu_seqlens,
                           const float* initial_state, void* o, float* final_state, void* workspace,
@@ -335,7 +336,8 @@ kda_status kda_linear_fwd(const kda_linear_config* cfg, int64_t total_tokens, in
  * ([total_tokens, H, dv], in_dtype) and dS_final (fp32 or NULL = 0).  Outputs:
  * dq, dk [total_tokens, Hk, dk] (summed over the value heads that share them),
  * dv [total_tokens, H, dv], dg (the shape of g; [H] sums over all tokens), all
- * in out_dtype, and d_initial_state, fp32 or NULL. */
+ * in out_dtype, and d_initial_state, fp32 or NULL, which must not overlap
+ * initial_state or dS_final (KDA_ERR_INVALID_ARG). */
 kda_status kda_linear_bwd(const kda_linear_config* cfg, int64_t total_tokens, int32_t num_seqs, const void* q,
                           const void* k, const void* v, const float* g, const int32_t* cu_seqlens,
                           const float* initial_state, const void* dO, const float* dS_final, void* dq, void* dk,

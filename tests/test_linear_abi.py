@@ -137,6 +137,20 @@ def test_forward_and_backward_refuse_bad_arguments():
     assert _lib.kda_linear_bwd_workspace_size(big, 1 << 20, 1) == 0 and fwd(big) == KDA_ERR_UNSUPPORTED
 
 
+def test_packed_calls_refuse_overlapping_states():
+    """The walks read and write states in one launch, so none of these may share memory, in place included."""
+    cfg = lin()
+    state, nbytes = 1 << 30, 3 * 2 * 64 * 64 * 4
+    for other in (state, state + 16, state + nbytes - 16, state - nbytes + 16):
+        for T in (129, 12288):   # whole documents and cut ones
+            size = _lib.kda_linear_fwd_workspace_size(cfg, T, 3)
+            assert fwd(cfg, T=T, N=3, s0=state, sf=other, ws=FAKE, wsb=size) == KDA_ERR_INVALID_ARG
+            assert "overlap" in _err()
+            for name in ("s0", "dS"):
+                assert bwd(cfg, T=T, N=3, dS0=state, **{name: other}) == KDA_ERR_INVALID_ARG, name
+                assert "overlap" in _err()
+
+
 def test_decode_refuses_bad_arguments():
     cfg = lin()
     assert decode(cfg, N=-1) == KDA_ERR_INVALID_ARG
