@@ -179,9 +179,9 @@ kda_status check_sizes(const kda_linear_config* c, int64_t T, int32_t N) {
     if (N < 1) return fail(KDA_ERR_INVALID_ARG, "num_seqs must be >= 1%s");
     // the kernels address a block's rows with 32-bit byte offsets from a 64-bit base
     if ((int64_t)kLinBlock * c->H * 128 * 4 >= ((int64_t)1 << 31)) return fail(KDA_ERR_UNSUPPORTED, "H too large%s");
-    // the largest launches: the walks' chains, the a block's gradients in at most three roles a head, the carry
-    if (!grid_fits((linear_slots(T, N, kLinBlock) + 8) * 4 * (int64_t)c->H, kGradThreads) ||
-        !grid_fits((int64_t)N * c->H * (c->dk * c->dv / (4 * kThreads)), kThreads))
+    // the largest launches: the walks' chains in at most four ways of kThreads, a block's gradients in at most three roles
+    // a head, and the carry's at most four workgroups of kThreads for each of N * H states
+    if (!grid_fits((linear_slots(T, N, kLinBlock) + 8) * 4 * (int64_t)c->H, kGradThreads))
         return fail(KDA_ERR_UNSUPPORTED, "num_seqs, H or total_tokens too large for one launch%s");
     return KDA_OK;
 }

@@ -151,6 +151,18 @@ def test_packed_calls_refuse_overlapping_states():
                 assert "overlap" in _err()
 
 
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128)])
+def test_sizes_up_to_the_documented_limit(dk, dv):
+    """(total_tokens / 128 + num_seqs + 8) * H below 2^21, whatever the head sizes."""
+    cfg = lin(dk=dk, dv=dv)
+    N = 1 << 19
+    T = ((1 << 20) - 1 - 8 - N) * 128
+    assert _lib.kda_linear_bwd_workspace_size(cfg, T, N) > 0
+    assert _lib.kda_linear_bwd_workspace_size(cfg, T + 128, N) == 0 and "too large" in _err()
+    assert _lib.kda_linear_bwd_workspace_size(cfg, 600000, 600000) > 0
+    assert fwd(cfg, T=T + 128, N=N) == KDA_ERR_UNSUPPORTED and bwd(cfg, T=T + 128, N=N) == KDA_ERR_UNSUPPORTED
+
+
 def test_decode_refuses_bad_arguments():
     cfg = lin()
     assert decode(cfg, N=-1) == KDA_ERR_INVALID_ARG
