@@ -38,6 +38,7 @@ class KdaConfig(ctypes.Structure):
 
 
 KDA_GATE_TOKEN, KDA_GATE_HEAD = 0, 1
+KDA_GATE_GRAD_F32 = 0x100
 KDA_RULE_DELTA, KDA_RULE_LINEAR = 0, 1
 KDA_TREE_MAX_NODES = 64
 

@@ -88,7 +88,7 @@ struct LinearBwdParams {
     void* dv_out;
     void* dg;
     int64_t T, blocks;
-    int32_t N, H, Hk, dv, seqlen, g_stride, out_bf16, parts;   // parts divides H / Hk
+    int32_t N, H, Hk, dv, seqlen, g_stride, out_bf16, dg_bf16, parts;   // parts divides H / Hk
     float scale;
 };
 

@@ -48,9 +48,10 @@ kda_status check_heads(int32_t H, int32_t Hk, int32_t dk, int32_t dv, int32_t in
     if (!isfinite(scale)) return fail(KDA_ERR_INVALID_ARG, "scale must be finite%s");
     return KDA_OK;
 }
+int32_t gate_of(const kda_linear_config* c) { return c->gate & ~KDA_GATE_GRAD_F32; }
 kda_status check_config(const kda_linear_config* c) {
     if (!c) return fail(KDA_ERR_INVALID_ARG, "config is NULL%s");
-    return check_heads(c->H, c->Hk, c->dk, c->dv, c->in_dtype, c->out_dtype, c->gate, c->scale);
+    return check_heads(c->H, c->Hk, c->dk, c->dv, c->in_dtype, c->out_dtype, gate_of(c), c->scale);
 }
 
 // One launch covers at most 2^32 - 1 work-items along x.
@@ -163,7 +164,7 @@ BwdLayout bwd_layout(const kda_linear_config* c, int64_t T, int32_t N) {
     b.a = take(rows);
     b.f = take(rows);
     b.cross = take((size_t)b.blocks * c->H * sizeof(float));
-    b.part = take(c->gate == KDA_GATE_HEAD ? (size_t)b.blocks * c->H * sizeof(float) : 0);
+    b.part = take(gate_of(c) == KDA_GATE_HEAD ? (size_t)b.blocks * c->H * sizeof(float) : 0);
     b.sums = take(b.parts > 1 ? (size_t)2 * b.parts * T * c->Hk * c->dk * sizeof(float) : 0);
     if (b.plan.seg_len)
         for (int i = 0; i < 2; ++i) {
@@ -274,7 +275,7 @@ kda_status kda_linear_fwd(const kda_linear_config* cfg, int64_t T, int32_t N, co
     p.q = q; p.k = k; p.v = v; p.g = g; p.cu = cu; p.s0 = s0; p.o = o; p.sfinal = sfinal;
     p.T = T; p.N = N; p.H = cfg->H; p.Hk = cfg->Hk; p.dv = cfg->dv;
     p.seqlen = cu ? 0 : (int32_t)(T / N);
-    p.g_stride = cfg->gate == KDA_GATE_TOKEN ? cfg->H : 0;
+    p.g_stride = gate_of(cfg) == KDA_GATE_TOKEN ? cfg->H : 0;
     p.out_bf16 = cfg->out_dtype == KDA_BF16;
     p.scale = cfg->scale;
     p.seg_len = f.plan.seg_len;
@@ -316,7 +317,7 @@ kda_status kda_linear_bwd(const kda_linear_config* cfg, int64_t T, int32_t N, co
     KDA_TRY(ptr(dq, "dq", any));
     KDA_TRY(ptr(dk, "dk", any));
     KDA_TRY(ptr(dv, "dv", any));
-    KDA_TRY(ptr(dg, "dg", any || cfg->gate == KDA_GATE_HEAD));
+    KDA_TRY(ptr(dg, "dg", any || gate_of(cfg) == KDA_GATE_HEAD));
     KDA_TRY(ptr(s0, "initial_state", false));
     KDA_TRY(ptr(dSf, "dS_final", false));
     KDA_TRY(ptr(dS0, "d_initial_state", false));
@@ -330,7 +331,7 @@ kda_status kda_linear_bwd(const kda_linear_config* cfg, int64_t T, int32_t N, co
 
     hipStream_t st = (hipStream_t)stream;
     char* ws = (char*)workspace;
-    const int32_t seqlen = cu ? 0 : (int32_t)(T / N), g_stride = cfg->gate == KDA_GATE_TOKEN ? cfg->H : 0;
+    const int32_t seqlen = cu ? 0 : (int32_t)(T / N), g_stride = gate_of(cfg) == KDA_GATE_TOKEN ? cfg->H : 0;
     LinearStateParams s;
     memset(&s, 0, sizeof s);
     s.dir[0].a = k; s.dir[0].b = v;
@@ -366,11 +367,12 @@ kda_status kda_linear_bwd(const kda_linear_config* cfg, int64_t T, int32_t N, co
     p.q = q; p.k = k; p.v = v; p.g = g; p.cu = cu; p.dO = dO;
     p.S = ws + b.S; p.dS = ws + b.dS;
     p.e = (float*)(ws + b.e); p.a = (float*)(ws + b.a); p.f = (float*)(ws + b.f); p.cross = (float*)(ws + b.cross);
-    p.dg_part = cfg->gate == KDA_GATE_HEAD ? (float*)(ws + b.part) : nullptr;
+    p.dg_part = gate_of(cfg) == KDA_GATE_HEAD ? (float*)(ws + b.part) : nullptr;
     p.sums = (float*)(ws + b.sums); p.parts = b.parts;
     p.dq = dq; p.dk_out = dk; p.dv_out = dv; p.dg = dg;
     p.T = T; p.blocks = T > 0 ? b.blocks : 0; p.N = N; p.H = cfg->H; p.Hk = cfg->Hk; p.dv = cfg->dv; p.seqlen = seqlen;
     p.g_stride = g_stride; p.out_bf16 = cfg->out_dtype == KDA_BF16;
+    p.dg_bf16 = p.out_bf16 && !(cfg->gate & KDA_GATE_GRAD_F32);
     p.scale = cfg->scale;
     return launched(launch_linear_grads(p, cfg->in_dtype, cfg->dk, st));
 }
@@ -394,7 +396,7 @@ kda_status kda_linear_decode(const kda_linear_config* cfg, int32_t N, const void
     memset(&p, 0, sizeof p);
     p.q = q; p.k = k; p.v = v; p.g = g; p.s_in = state_in; p.s_out = state_out; p.o = o;
     p.N = N; p.H = cfg->H; p.Hk = cfg->Hk; p.dv = cfg->dv;
-    p.g_stride = cfg->gate == KDA_GATE_TOKEN ? cfg->H : 0;
+    p.g_stride = gate_of(cfg) == KDA_GATE_TOKEN ? cfg->H : 0;
     p.out_bf16 = cfg->out_dtype == KDA_BF16;
     p.scale = cfg->scale;
     return launched(launch_linear_decode(p, cfg->in_dtype, cfg->dk, (hipStream_t)stream));

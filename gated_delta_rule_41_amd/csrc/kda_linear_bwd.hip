@@ -518,7 +518,7 @@ __global__ __launch_bounds__(1024) void linear_dg_kernel(LinearBwdParams p) {
     __syncthreads();
     const int h = h0 + tid % kDgHeads;
     if (h < p.H)
-        for (int t = tid / kDgHeads; t < rows; t += 1024 / kDgHeads) store1(p.dg, (rg.lo + t) * p.H + h, out[t][tid % kDgHeads], p.out_bf16);
+        for (int t = tid / kDgHeads; t < rows; t += 1024 / kDgHeads) store1(p.dg, (rg.lo + t) * p.H + h, out[t][tid % kDgHeads], p.dg_bf16);
 }
 
 // Gate per head: dg[h] is the sum over the blocks, in a fixed order.  One workgroup per head.
@@ -533,7 +533,7 @@ __global__ __launch_bounds__(kThreads) void linear_dg_head_kernel(LinearBwdParam
         if (tid < m) s[tid] += s[tid + m];
         __syncthreads();
     }
-    if (tid == 0) store1(p.dg, h, (float)s[0], p.out_bf16);
+    if (tid == 0) store1(p.dg, h, (float)s[0], p.dg_bf16);
 }
 
 template <typename T, int DK, int DV> static void grads_t(const LinearBwdParams& p, hipStream_t stream) {

@@ -8,7 +8,7 @@ from functools import lru_cache
 from typing import Optional
 
 from . import _lib
-from ._lib import KDA_GATE_HEAD, KDA_GATE_TOKEN, KDA_RULE_DELTA, KDA_RULE_LINEAR, KDA_TREE_MAX_NODES
+from ._lib import KDA_GATE_GRAD_F32, KDA_GATE_HEAD, KDA_GATE_TOKEN, KDA_RULE_DELTA, KDA_RULE_LINEAR, KDA_TREE_MAX_NODES
 from ._tensors import check as _check, dt_code as _dt_code, launch as _launch, ptr as _ptr, torch_module as _torch
 
 # Configs and workspace sizes depend on their arguments alone; made once for each set of them.
@@ -65,6 +65,11 @@ def _packed(q, k, v, g, cu_seqlens, num_seqs):
     return T, N, H, Hk, dk, dv, dev, dt, gate
 
 
+def _check_dg_dtype(dg_dtype, out_dtype):
+    if dg_dtype not in (None, out_dtype, _torch().float32):
+        raise ValueError(f"dg_dtype must be torch.float32 or {out_dtype}, got {dg_dtype}")
+
+
 def kda_linear_fwd(q, k, v, g, cu_seqlens=None, initial_state=None, *, num_seqs: Optional[int] = None, out_dtype=None,
                    scale: float = 1.0, output_final_state: bool = True):
     """Linear attention with a decay for each head, over packed documents:
@@ -90,14 +95,19 @@ def kda_linear_fwd(q, k, v, g, cu_seqlens=None, initial_state=None, *, num_seqs:
 
 
 def kda_linear_bwd(q, k, v, g, dO, cu_seqlens=None, initial_state=None, dS_final=None, *, num_seqs: Optional[int] = None,
-                   out_dtype=None, scale: float = 1.0, output_d_initial_state: bool = True):
+                   out_dtype=None, dg_dtype=None, scale: float = 1.0, output_d_initial_state: bool = True):
     """Backward of kda_linear_fwd for the loss <dO, o> + <dS_final, final_state>,
     from the forward's inputs alone.  Returns a dict with dq, dk, dv, dg (the
     shapes of q, k, v, g; fp32 unless ``out_dtype`` says otherwise) and dS0
-    (fp32, None unless requested)."""
+    (fp32, None unless requested).  ``dg_dtype=torch.float32`` keeps dg in g's own
+    type beside a bf16 ``out_dtype``."""
     torch = _torch()
     T, N, H, Hk, dk, dv, dev, dt, gate = _packed(q, k, v, g, cu_seqlens, num_seqs)
     out_dtype = out_dtype or torch.float32
+    dg_dtype = dg_dtype or out_dtype
+    if dg_dtype != out_dtype:
+        _check_dg_dtype(dg_dtype, out_dtype)
+        gate |= KDA_GATE_GRAD_F32
     _check(dO, "dO", (T, H, dv), dt, dev)
     _check(initial_state, "initial_state", (N, H, dk, dv), torch.float32, dev)
     _check(dS_final, "dS_final", (N, H, dk, dv), torch.float32, dev)
@@ -106,7 +116,7 @@ def kda_linear_bwd(q, k, v, g, dO, cu_seqlens=None, initial_state=None, dS_final
         "dq": torch.empty_like(q, dtype=out_dtype),
         "dk": torch.empty_like(k, dtype=out_dtype),
         "dv": torch.empty_like(v, dtype=out_dtype),
-        "dg": torch.empty_like(g, dtype=out_dtype),
+        "dg": torch.empty_like(g, dtype=dg_dtype),
         "dS0": torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev) if output_d_initial_state else None,
     }
     wsb = _linear_workspace(_lib.kda_linear_bwd_workspace_size, T, N, *config)
@@ -207,10 +217,10 @@ def _autograd_function():
         Gradients flow to q, k, v, g and initial_state."""
 
         @staticmethod
-        def forward(ctx, q, k, v, g, cu_seqlens, initial_state, num_seqs, scale):
+        def forward(ctx, q, k, v, g, cu_seqlens, initial_state, num_seqs, scale, dg_dtype):
             o, sf = kda_linear_fwd(q, k, v, g, cu_seqlens, initial_state, num_seqs=num_seqs, scale=scale)
             ctx.save_for_backward(q, k, v, g, cu_seqlens, initial_state)
-            ctx.num_seqs, ctx.scale = num_seqs, scale
+            ctx.num_seqs, ctx.scale, ctx.dg_dtype = num_seqs, scale, dg_dtype
             return o, sf
 
         @staticmethod
@@ -220,8 +230,8 @@ def _autograd_function():
             d_o = _upstream((d_o if d_o is not None else torch.zeros_like(v)).to(q.dtype))
             d_sf = _upstream(d_sf) if d_sf is not None else None
             gr = kda_linear_bwd(q, k, v, g, d_o, cu_seqlens, s0, d_sf, num_seqs=ctx.num_seqs, out_dtype=q.dtype,
-                                scale=ctx.scale, output_d_initial_state=s0 is not None)
-            return gr["dq"], gr["dk"], gr["dv"], gr["dg"].to(g.dtype), None, gr["dS0"], None, None
+                                dg_dtype=ctx.dg_dtype, scale=ctx.scale, output_d_initial_state=s0 is not None)
+            return gr["dq"], gr["dk"], gr["dv"], gr["dg"].to(g.dtype), None, gr["dS0"], None, None, None
 
     return LinearFunction
 
@@ -229,16 +239,20 @@ def _autograd_function():
 _FN = None
 
 
-def kda_linear(q, k, v, g, cu_seqlens=None, initial_state=None, *, num_seqs: Optional[int] = None, scale: float = 1.0):
+def kda_linear(q, k, v, g, cu_seqlens=None, initial_state=None, *, num_seqs: Optional[int] = None, scale: float = 1.0,
+               dg_dtype=None):
     """kda_linear_fwd as a differentiable torch op: returns ``(o, final_state)``
     (fp32) and, under autograd, back-propagates through kda_linear_bwd.  The
     upstream gradient of o is cast to the input dtype, and the gradients of q,
-    k, v and g are rounded to it.  A second differentiation is refused.
+    k, v and g are rounded to it; ``dg_dtype=torch.float32`` keeps g's as it is
+    summed, which a fixed decay's gradient, a sum over all tokens, needs beside
+    bf16 inputs.  A second differentiation is refused.
 
     In a captured graph use torch.autograd.grad, or leaves of which no eager graph
     is alive: torch ties a leaf's gradient accumulation to the stream of its first
     graph."""
     global _FN
+    _check_dg_dtype(dg_dtype, q.dtype)
     if _FN is None:
         _FN = _autograd_function()
-    return _FN.apply(q, k, v, g, cu_seqlens, initial_state, num_seqs, scale)
+    return _FN.apply(q, k, v, g, cu_seqlens, initial_state, num_seqs, scale, dg_dtype)

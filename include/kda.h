@@ -297,6 +297,10 @@ kda_status kda_decode(const kda_config* cfg, int32_t num_seqs, const void* q, co
  * and head in one launch: (total_tokens/128 + num_seqs + 8) * H below 2^21. */
 typedef enum kda_gate { KDA_GATE_TOKEN = 0, KDA_GATE_HEAD = 1 } kda_gate;
 
+/* Or'ed into kda_linear_config.gate: kda_linear_bwd stores dg in fp32, the type
+ * of g, whatever out_dtype is.  The other linear calls take it and ignore it. */
+#define KDA_GATE_GRAD_F32 0x100
+
 typedef struct kda_linear_config {
     int32_t H;         /* value heads                                  */
     int32_t Hk;        /* query / key heads; divides H                 */
@@ -304,7 +308,7 @@ typedef struct kda_linear_config {
     int32_t dv;        /* value head dim (64 or 128)                   */
     int32_t in_dtype;  /* kda_dtype of q, k, v, dO                     */
     int32_t out_dtype; /* kda_dtype of o, dq, dk, dv, dg               */
-    int32_t gate;      /* kda_gate                                     */
+    int32_t gate;      /* kda_gate, perhaps with KDA_GATE_GRAD_F32     */
     float scale;       /* multiplies the query (1.0)                   */
 } kda_linear_config;
 
@@ -336,7 +340,7 @@ kda_status kda_linear_fwd(const kda_linear_config* cfg, int64_t total_tokens, in
  * ([total_tokens, H, dv], in_dtype) and dS_final (fp32 or NULL = 0).  Outputs:
  * dq, dk [total_tokens, Hk, dk] (summed over the value heads that share them),
  * dv [total_tokens, H, dv], dg (the shape of g; [H] sums over all tokens), all
- * in out_dtype, and d_initial_state, fp32 or NULL, which must not overlap
+ * in out_dtype (dg in fp32 under KDA_GATE_GRAD_F32), and d_initial_state, fp32 or NULL, which must not overlap
  * initial_state or dS_final (KDA_ERR_INVALID_ARG). */
 kda_status kda_linear_bwd(const kda_linear_config* cfg, int64_t total_tokens, int32_t num_seqs, const void* q,
                           const void* k, const void* v, const float* g, const int32_t* cu_seqlens,

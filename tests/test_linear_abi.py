@@ -163,6 +163,23 @@ def test_sizes_up_to_the_documented_limit(dk, dv):
     assert fwd(cfg, T=T + 128, N=N) == KDA_ERR_UNSUPPORTED and bwd(cfg, T=T + 128, N=N) == KDA_ERR_UNSUPPORTED
 
 
+def test_dg_in_fp32_is_a_bit_of_the_gate():
+    flag = _lib.KDA_GATE_GRAD_F32
+    for gate in (0, KDA_GATE_HEAD):
+        a, b = lin(gate=gate), lin(gate=gate | flag)
+        for T, N in ((128, 1), (8192, 3)):
+            assert _lib.kda_linear_bwd_workspace_size(b, T, N) == _lib.kda_linear_bwd_workspace_size(a, T, N) > 0
+            assert _lib.kda_linear_fwd_workspace_size(b, T, N) == _lib.kda_linear_fwd_workspace_size(a, T, N)
+        # each call gets as far as its pointers
+        for call in (fwd, bwd, decode):
+            assert call(b, q=0) == KDA_ERR_INVALID_ARG and _err().startswith("q ")
+    for gate in (2 | flag, flag << 1, -1):
+        for call in (fwd, bwd, decode):
+            assert call(lin(gate=gate)) == KDA_ERR_INVALID_ARG and "gate" in _err()
+    for call in (tree, commit):
+        assert call(tree_cfg(KDA_RULE_LINEAR, gate=flag)) == KDA_ERR_INVALID_ARG
+
+
 def test_decode_refuses_bad_arguments():
     cfg = lin()
     assert decode(cfg, N=-1) == KDA_ERR_INVALID_ARG
