@@ -220,6 +220,7 @@ def _autograd_function():
         def forward(ctx, q, k, v, g, cu_seqlens, initial_state, num_seqs, scale, dg_dtype):
             o, sf = kda_linear_fwd(q, k, v, g, cu_seqlens, initial_state, num_seqs=num_seqs, scale=scale)
             ctx.save_for_backward(q, k, v, g, cu_seqlens, initial_state)
+            ctx.set_materialize_grads(False)   # an output that the loss does not use has no gradient, not one of zeros
             ctx.num_seqs, ctx.scale, ctx.dg_dtype = num_seqs, scale, dg_dtype
             return o, sf
 
