@@ -15,6 +15,8 @@ __device__ __forceinline__ int opaque(int x) {
     return x;
 }
 
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned u32x8 __attribute__((ext_vector_type(8)));
 __device__ __forceinline__ f32x4 zero4() { return f32x4{0.f, 0.f, 0.f, 0.f}; }
 
 // Token range of a piece of a document.  Every bound is clamped to [0, T], so a malformed cu cannot address memory
@@ -311,8 +313,34 @@ __device__ __forceinline__ f32x8 widen8(bf16x8 x) {
 }
 __device__ __forceinline__ f32x8 widen8(f32x8 x) { return x; }
 
+// Infinities and NaN.  A result that depends on one is never finite again, but the zeros of a
+// causal mask times one would be NaN too.  So where a tile holds any, products behind a mask take
+// the finite values alone, and the results that the others reach become NaN.
+
+// All ones where a value is infinite or NaN.
+__device__ __forceinline__ u16x8 not_finite(bf16x8 x) { return (u16x8)((__builtin_bit_cast(u16x8, x) & (unsigned short)0x7f80) == (unsigned short)0x7f80); }
+__device__ __forceinline__ u32x8 not_finite(f32x8 x) { return (u32x8)((__builtin_bit_cast(u32x8, x) & 0x7f800000u) == 0x7f800000u); }
+// The finite values, zeros in the place of the others.
+template <typename V> __device__ __forceinline__ V finite_part(V x) {
+    const auto m = not_finite(x);
+    return __builtin_bit_cast(V, __builtin_bit_cast(decltype(not_finite(x)), x) & ~m);
+}
+// For a transposed tile's fragment x (32 rows in the k order of Lane::col): in the accumulator
+// layout, how many values of each of its columns are infinite or NaN among the rows that reach(row).
+template <typename V, typename F> __device__ __forceinline__ f32x4 odd_count(V x, int qg, F&& reach) {
+    const auto m = not_finite(x);
+    V odd, mask;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        odd[e] = m[e] ? 1.f : 0.f;
+        mask[e] = reach((e < 4 ? 0 : 12) + 4 * qg + e) ? 1.f : 0.f;
+    }
+    return mma_k32(zero4(), odd, mask);
+}
+
 // An fp32 fragment as a product operand.  bf16: three bf16 terms (24 bits), so that fp32
-// states and state gradients keep fp32 accuracy; fp32: itself.
+// states and state gradients keep fp32 accuracy; fp32: itself.  (The terms of an infinity are
+// one and NaN.)
 template <typename T> struct Split;
 template <> struct Split<bf16> {
     bf16x8 h[3];
@@ -354,7 +382,6 @@ __device__ __forceinline__ void store1(void* base, int64_t at, float x, int out_
 // after it, and around conditional ones the compiler can only wait for all of them.
 // At most 128 rows (checked on the host to be below 2^31 bytes); `base` and the counts are
 // the same for the whole wave.
-typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 typedef __amdgpu_buffer_rsrc_t Buffer;
 template <typename T> __device__ __forceinline__ Buffer rows_of(const T* base, int64_t ld, int rows, int most, int cols) {
     const int n = rows < 0 ? 0 : rows < most ? rows : most;
