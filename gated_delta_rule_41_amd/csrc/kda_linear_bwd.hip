@@ -109,7 +109,56 @@ template <typename T, int DK, int DV> struct GradTiles {
     __align__(16) double G[kB];
     __align__(16) float F[8][kB];
     float sum[8];
+    __align__(16) unsigned odd[8];   // whether a wave's part of the masked tile holds infinities or NaN
 };
+
+// Infinities and NaN of the tile whose rows a mask keeps from some of a block's results.  The zeros of
+// the mask times one of them would be NaN, so the tile gets its finite values alone (put_finite), and
+// in the end what the others reach becomes NaN (odd_results).  Both are rare, and the second reads
+// memory again rather than keep anything in between.  Looking for them costs 4 x 8192 tokens x 32 heads
+// 1006 -> 1017 us, 32 heads on 16 1084 -> 1099 (looked for and taken out of LDS after the barrier: 1124).
+template <typename S, typename T, int COLS>
+__device__ __forceinline__ void put_finite(S& s, const Tile<T, kB, COLS, kGradThreads>& t, T* tile, int tid, int w) {
+    t.store(tile, tid);
+    float x = 0.f;
+#pragma unroll
+    for (int i = 0; i < t.PIECES; ++i) x = probe<T>(t.r[i], x);
+    const bool any = __ballot(x != 0.f) != 0;
+    s.odd[w] = any;   // by every lane: no branch
+    if (any) {
+        Tile<T, kB, COLS, kGradThreads> f;
+#pragma unroll
+        for (int i = 0; i < t.PIECES; ++i) f.r[i] = finite_piece<T>(t.r[i]);
+        f.store(tile, tid);
+    }
+}
+// After a barrier; the same for the whole workgroup.
+template <typename S> __device__ __forceinline__ bool any_odd(const S& s) {
+    const u32x4 o = *reinterpret_cast<const u32x4*>(s.odd) | *reinterpret_cast<const u32x4*>(s.odd + 4);
+    return __builtin_amdgcn_readfirstlane(o[0] | o[1] | o[2] | o[3]) != 0;
+}
+// NaN in the results (in the accumulator layout, column = the lane's row of the block) that the rows
+// 32 x0 .. 32 x1 - 1 of `base` reach; returns how many reach the lane's row.
+template <typename T, int COLS, typename F>
+__device__ __forceinline__ float odd_results(f32x4 (&y)[COLS / 16], const T* base, int64_t ld, int rows, int x0, int x1, int cl, int qg, F&& reach) {
+    const Buffer b = rows_of(base, ld, rows, kB, COLS);
+    float all = 0.f;
+#pragma unroll
+    for (int m = 0; m < COLS / 16; ++m) {
+        f32x4 n = zero4();
+#pragma unroll 1
+        for (int x = x0; x < x1; ++x) {
+            typename V8<T>::t f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = load_one<T>(b, (32 * x + (e < 4 ? 0 : 12) + 4 * qg + e) * (unsigned)ld + 16 * m + cl);
+            n += odd_count(f, qg, [&](int row) { return reach(32 * x + row); });
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[m][i] = n[i] > 0.f ? __builtin_nanf("") : y[m][i];
+        all += (n[0] + n[1]) + (n[2] + n[3]);
+    }
+    return qsum4(all);
+}
 
 // Wave w's 16 rows of a block: row blocks are given out so that the waves of one SIMD (w and
 // w + 4) share the causal work evenly.
@@ -142,7 +191,7 @@ __device__ __forceinline__ void dq_role(const LinearBwdParams& p, const Task& t,
             tk.load((const T*)p.k + t.lo * ldk + t.hk * DK, ldk, rows, tid);
             if (w == 0) block_gates(s.G, p.g + (p.g_stride ? t.lo * p.g_stride : 0) + h, p.g_stride, rows, l);
             ts.store(s.b, tid);
-            tk.store(s.a, tid);
+            put_finite(s, tk, s.a, tid, w);
         } else {
             if (w == 0) block_gates(s.G, p.g + (p.g_stride ? t.lo * p.g_stride : 0) + h, p.g_stride, rows, l);
             ts.store(s.b, tid);
@@ -218,6 +267,11 @@ __device__ __forceinline__ void dq_role(const LinearBwdParams& p, const Task& t,
         lds_barrier();
     }
     const int l = threadIdx.x & 63, row = 16 * rb + (l & 15);
+    if (any_odd(s)) {
+        const float n = odd_results<T, DK>(dq, (const T*)p.k + t.lo * ldk + t.hk * DK, ldk, rows, 0, rb / 2 + 1, l & 15, l >> 4, [&](int key) { return key <= row; });
+        if (n > 0.f && row < rows)   // their A as well
+            for (int h = t.h0; h < t.h1; ++h) p.e[(int64_t)h * p.T + t.lo + row] = NAN;
+    }
     if (GROUPED && t.sums) store_row<DK>(t.sums, t.lo * ldk + t.hk * DK, ldk, rows, kB, row, l >> 4, dq, 0);
     else store_row<DK>(p.dq, t.lo * ldk + t.hk * DK, ldk, rows, kB, row, l >> 4, dq, p.out_bf16);
 }
@@ -248,7 +302,7 @@ __device__ __forceinline__ void dk_role(const LinearBwdParams& p, const Task& t,
             tq.load((const T*)p.q + t.lo * ldk + t.hk * DK, ldk, rows, tid);
             if (w == 0) block_gates(s.G, p.g + (p.g_stride ? t.lo * p.g_stride : 0) + h, p.g_stride, rows, l);
             td.store(s.b, tid);
-            tq.store(s.a, tid);
+            put_finite(s, tq, s.a, tid, w);
         } else {
             if (w == 0) block_gates(s.G, p.g + (p.g_stride ? t.lo * p.g_stride : 0) + h, p.g_stride, rows, l);
             td.store(s.b, tid);
@@ -324,6 +378,11 @@ __device__ __forceinline__ void dk_role(const LinearBwdParams& p, const Task& t,
         lds_barrier();
     }
     const int l = threadIdx.x & 63, key = 16 * rb + (l & 15);
+    if (any_odd(s)) {
+        const float n = odd_results<T, DK>(dk, (const T*)p.q + t.lo * ldk + t.hk * DK, ldk, rows, rb / 2, kB / 32, l & 15, l >> 4, [&](int query) { return key <= query; });
+        if (n > 0.f && key < rows)
+            for (int h = t.h0; h < t.h1; ++h) p.a[(int64_t)h * p.T + t.lo + key] = NAN;
+    }
     if (GROUPED && t.sums) store_row<DK>(t.sums, t.lo * ldk + t.hk * DK, ldk, rows, kB, key, l >> 4, dk, 0);
     else store_row<DK>(p.dk_out, t.lo * ldk + t.hk * DK, ldk, rows, kB, key, l >> 4, dk, p.out_bf16);
 }
@@ -388,7 +447,7 @@ __device__ __forceinline__ void dv_role(const LinearBwdParams& p, const Task& t,
             for (int u = 0; u < 2; ++u) dv[m + u] = x[u] * wj;
         }
         lds_barrier();   // the last readers of dS are done
-        to.store(s.b, tid);
+        put_finite(s, to, s.b, tid, w);
         const double gref = s.G[16 * rb + 15];
         const float fk = fast_exp2((float)(gref - gk)) * p.scale;
 #pragma unroll
@@ -418,6 +477,7 @@ __device__ __forceinline__ void dv_role(const LinearBwdParams& p, const Task& t,
 #pragma unroll
             for (int m = 0; m < DV / 16; ++m) dv[m] = mma_k32(dv[m], lv.col(s.b, 2 * x * RV, m), f);
         }
+        if (any_odd(s)) odd_results<T, DV>(dv, (const T*)p.dO + t.lo * ldv + h * DV, ldv, rows, rb / 2, kB / 32, cl, qg, [&](int query) { return key <= query; });
         store_row<DV>(p.dv_out, t.lo * ldv + h * DV, ldv, rows, kB, key, qg, dv, p.out_bf16);
         if constexpr (GROUPED) lds_barrier();   // the last readers of this head's tiles are done
     }

@@ -317,6 +317,18 @@ __device__ __forceinline__ f32x8 widen8(f32x8 x) { return x; }
 // causal mask times one would be NaN too.  So where a tile holds any, products behind a mask take
 // the finite values alone, and the results that the others reach become NaN.
 
+// t, which is 0, or NaN where one of 16 bytes' values is infinite or NaN: zero times it is not zero.
+template <typename T> __device__ __forceinline__ float probe(u32x4 x, float t) {
+    if constexpr (sizeof(T) == 2) {
+        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, (unsigned)x[i]), bf16x2{0, 0}, t, false);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t = __builtin_fmaf(__uint_as_float(x[i]), 0.f, t);
+    }
+    return t;
+}
 // All ones where a value is infinite or NaN.
 __device__ __forceinline__ u16x8 not_finite(bf16x8 x) { return (u16x8)((__builtin_bit_cast(u16x8, x) & (unsigned short)0x7f80) == (unsigned short)0x7f80); }
 __device__ __forceinline__ u32x8 not_finite(f32x8 x) { return (u32x8)((__builtin_bit_cast(u32x8, x) & 0x7f800000u) == 0x7f800000u); }
@@ -324,6 +336,10 @@ __device__ __forceinline__ u32x8 not_finite(f32x8 x) { return (u32x8)((__builtin
 template <typename V> __device__ __forceinline__ V finite_part(V x) {
     const auto m = not_finite(x);
     return __builtin_bit_cast(V, __builtin_bit_cast(decltype(not_finite(x)), x) & ~m);
+}
+template <typename T> __device__ __forceinline__ u32x4 finite_piece(u32x4 x) {
+    if constexpr (sizeof(T) == 2) return __builtin_bit_cast(u32x4, finite_part(__builtin_bit_cast(bf16x8, x)));
+    else return x & ~(u32x4)((x & 0x7f800000u) == 0x7f800000u);
 }
 // For a transposed tile's fragment x (32 rows in the k order of Lane::col): in the accumulator
 // layout, how many values of each of its columns are infinite or NaN among the rows that reach(row).
@@ -336,6 +352,16 @@ template <typename V, typename F> __device__ __forceinline__ f32x4 odd_count(V x
         mask[e] = reach((e < 4 ? 0 : 12) + 4 * qg + e) ? 1.f : 0.f;
     }
     return mma_k32(zero4(), odd, mask);
+}
+
+// c + x y for a transposed tile's fragment x and weights y that are zero in the columns that a row
+// does not reach: x's infinities and NaN make NaN of what their row reaches, and nothing of the rest.
+template <typename V, typename F> __device__ __forceinline__ f32x4 mma_reaching(f32x4 c, V x, V y, int qg, F&& reach) {
+    c = mma_k32(c, finite_part(x), y);
+    const f32x4 odd = odd_count(x, qg, reach);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = odd[i] > 0.f ? __builtin_nanf("") : c[i];
+    return c;
 }
 
 // An fp32 fragment as a product operand.  bf16: three bf16 terms (24 bits), so that fp32
@@ -389,6 +415,10 @@ template <typename T> __device__ __forceinline__ Buffer rows_of(const T* base, i
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(base), 0, bytes, 0x00027000);
 }
 __device__ __forceinline__ u32x4 load16(Buffer b, unsigned off) { return __builtin_amdgcn_raw_buffer_load_b128(b, off, 0, 0); }
+template <typename T> __device__ __forceinline__ T load_one(Buffer b, unsigned at) {
+    if constexpr (sizeof(T) == 2) return __builtin_bit_cast(bf16, (unsigned short)__builtin_amdgcn_raw_buffer_load_b16(b, at * 2, 0, 0));
+    else return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(b, at * 4, 0, 0));
+}
 // Four values at element `at` of a buffer of O.
 template <typename O> __device__ __forceinline__ void store4(Buffer b, unsigned at, f32x4 x) {
     if constexpr (sizeof(O) == 2) __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, pack4<bf16>(x)), b, at * 2, 0, 0);

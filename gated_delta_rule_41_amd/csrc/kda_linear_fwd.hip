@@ -246,10 +246,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void linear_out_k
                     o[c] *= e;
                     for (int kk = 0; kk <= m / 2; ++kk) {
                         const frag x = lv.col(sV, 2 * kk * RV, w * NC + c);
-                        o[c] = mma_k32(o[c], finite_part(x), lp.perm(sP, m * RP, kk));
-                        const f32x4 odd = odd_count(x, qg, [&](int key) { return 32 * kk + key <= 16 * m + cl; });
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) o[c][i] = odd[i] > 0.f ? NAN : o[c][i];
+                        o[c] = mma_reaching(o[c], x, lp.perm(sP, m * RP, kk), qg, [&](int key) { return 32 * kk + key <= 16 * m + cl; });
                     }
                 }
                 store(m, o[0], o[NC - 1]);

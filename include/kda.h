@@ -294,9 +294,11 @@ kda_status kda_decode(const kda_config* cfg, int32_t num_seqs, const void* q, co
  * throughout.  Sums of g are kept in 64 bits.  Results are deterministic.
  * Infinities and NaN reach what depends on them by the recurrence and nothing
  * else: the token's own output and later ones of its document, through v in
- * its column alone.  Such a result is infinite or NaN; the packed calls
- * do not say which (chunks add up in another order), decode keeps a state's
- * infinities.
+ * its column alone; likewise the gradients of earlier tokens through q and dO,
+ * of later ones through k and v.  (In the token's own 128-token block and head
+ * dg is not held to that, nor is any gradient with a NaN gate.)  Such a result
+ * is infinite or NaN; the packed calls do not say which (chunks add up in
+ * another order), decode keeps a state's infinities.
  * H below 2^15 (the kernels address a 128-token block's rows with 32-bit
  * offsets), and four workgroups of 512 threads per 128-token block, document
  * and head in one launch: (total_tokens/128 + num_seqs + 8) * H below 2^21. */
