@@ -61,8 +61,12 @@ template <typename T> struct Two;
 template <> struct Two<bf16> {
     static constexpr int PLANES = 2;
     bf16x8 h, l;
+    // bf16's largest value in the first term where x is larger or infinite: what is left is x's then
     __device__ __forceinline__ void set(f32x8 x) {
-        h = __builtin_convertvector(x, bf16x8);
+        f32x8 y;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = __builtin_amdgcn_fmed3f(x[j], -0x1.fep127f, 0x1.fep127f);
+        h = __builtin_convertvector(y, bf16x8);
         l = __builtin_convertvector(x - widen8(h), bf16x8);
     }
     template <int COLS> __device__ __forceinline__ void get(const Lane<bf16, COLS>& at, const bf16* t, int plane, int off, int y) {
