@@ -135,14 +135,16 @@ struct BwdLayout {
 // number that gives kGradTarget workgroups (three roles a block), or the largest that does not,
 // so that short streams do not wait for one workgroup's value heads in turn.  Backward in us, whole and divided for 256, 512
 // and 1024 workgroups: 134 tokens x 8 heads on 2: 44, 27, 27, 27; 1024 x 32 on 8: 87, 87, 77,
-// 81; 4096 x 16 on 4: 130, 130, 139, 143; 4096 x 32 on 1: 354, 192, 189, 186.
+// 81; 4096 x 16 on 4: 130, 130, 139, 143; 4096 x 32 on 1: 354, 192, 189, 186.  A prime number of
+// value heads is divided into single ones, whole and so: 1152 x 28 on 4: 116, 97; 2048 x 28 on 4:
+// 134, 131; 1024 x 127 on 1: 1144, 205.  (Workspace: two rows of dk fp32 a token and part.)
 constexpr int64_t kGradTarget = 384;   // 288 workgroups gain from it (1024 x 32 on 8), 408 lose (4096 x 16 on 4)
 int32_t grad_parts(const kda_linear_config* c, int64_t blocks) {
     const int32_t R = c->H / c->Hk;
     const int64_t groups = 3 * blocks * c->Hk;
     int32_t parts = 1;
     for (int32_t x = 2; x <= R && groups * parts < kGradTarget && x <= kGradTarget; ++x)
-        if (R % x == 0 && groups * x < 2 * kGradTarget) parts = x;
+        if (R % x == 0) parts = x;
     return parts;
 }
 BwdLayout bwd_layout(const kda_linear_config* c, int64_t T, int32_t N) {

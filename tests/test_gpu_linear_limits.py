@@ -8,6 +8,29 @@ import gated_delta_rule_41_amd as kda
 pytestmark = pytest.mark.gpu
 
 
+@pytest.mark.parametrize("T,H,Hk", [(1152, 28, 4), (1024, 127, 1)])
+def test_prime_numbers_of_value_heads(T, H, Hk):
+    """7 and 127 value heads to a key head, each in a workgroup of its own: dq and dk are the sums of what every value head
+    gives with a key head of its own.  fp32: both sides add the same terms, 32 half steps of the root of their squares
+    each (tests/linear_ref.py), which for independent inputs is the result's norm; dv and dg do not change."""
+    need_gpu()
+    R = H // Hk
+    gen = torch.Generator(device="cuda").manual_seed(42)
+    q, k = (torch.randn((T, Hk, 64), generator=gen, device="cuda") for _ in range(2))
+    v, dO = (torch.randn((T, H, 64), generator=gen, device="cuda") for _ in range(2))
+    g = -0.1 * torch.rand((T, H), generator=gen, device="cuda")
+    print(f"[gpu-linear] {T} tokens, {H} heads on {Hk}", flush=True)
+    got = kda.kda_linear_bwd(q, k, v, g, dO, scale=0.125)
+    one = kda.kda_linear_bwd(q.repeat_interleave(R, 1), k.repeat_interleave(R, 1), v, g, dO, scale=0.125)
+    torch.cuda.synchronize()
+    assert torch.equal(got["dv"], one["dv"]) and torch.equal(got["dg"], one["dg"])
+    for n in ("dq", "dk"):
+        want = one[n].double().view(T, Hk, R, 64).sum(2)
+        off = float((got[n].double() - want).norm() / want.norm())
+        print(f"[gpu-linear]   {n}: {off:.2e}", flush=True)
+        assert off <= 2 * 32 * 2.0 ** -24, n
+
+
 def test_many_documents_of_one_token():
     """530000 documents x 2 heads of 128 x 128, more than 2^20 states: with no state before, o = scale (q . k) v,
     dv = scale (q . k) dO and dg = 0.  bf16 products are exact in fp32, and 128 of them add up with at most 128 half steps

@@ -163,6 +163,13 @@ def test_sizes_up_to_the_documented_limit(dk, dv):
     assert fwd(cfg, T=T + 128, N=N) == KDA_ERR_UNSUPPORTED and bwd(cfg, T=T + 128, N=N) == KDA_ERR_UNSUPPORTED
 
 
+def test_prime_numbers_of_value_heads_are_divided():
+    """Few workgroups' worth of tokens with 7 or 127 value heads to a key head: partial sums of dq and dk for each."""
+    for T, H, Hk in ((1152, 28, 4), (1024, 127, 1)):
+        whole = _lib.kda_linear_bwd_workspace_size(lin(H=H, Hk=H), T, 1)
+        assert _lib.kda_linear_bwd_workspace_size(lin(H=H, Hk=Hk), T, 1) == whole + 2 * T * H * 64 * 4, (T, H)
+
+
 def test_dg_in_fp32_is_a_bit_of_the_gate():
     flag = _lib.KDA_GATE_GRAD_F32
     for gate in (0, KDA_GATE_HEAD):
