@@ -66,8 +66,9 @@ bool grid_fits(int64_t workgroups, int threads) {
 // entering them, the walks from those.  Documents that fit one segment take no part in the
 // first two.  The plan depends on the config and the sizes alone, so that the workspace size
 // is a host function; cu_seqlens is on the device, so any document may have all the tokens.
-// More than kSegDocs documents even out by their number (and finding a segment would take a
-// workgroup longer).
+// More than kSegDocs documents are walked whole.  Short ones even out by their number, but a long one
+// among them does not: one of 131072 tokens x 16 heads with 511 documents of one token takes 1.1 ms
+// forward and 3.7 backward, with 512 of them 9.0 and 7.3.
 // Equal shares of small streams would be too short: a segment costs its state four moves
 // through memory (T H dk dv / L elements over all of them) and a step of its document's carry
 // (T / L of them in a row), against 2 L tokens of walking.  The two square roots are where those
@@ -80,8 +81,11 @@ bool grid_fits(int64_t workgroups, int threads) {
 //     32768 x 8, 16 documents     154   124   127
 //     32768 x 1              103    73    75   108
 //     131072 x 1             211   211   140   136
-// Up to two segments, or eight chunks, are walked whole: summing the first and then walking both
-// takes as long as one walk (1003 tokens x 4 heads, fp32, backward: 52 us in two, 48 whole).
+// Up to two segments, or eight chunks, are walked whole.  For the backward that is as good: 256 tokens
+// x 4 heads of 64, fp32, 35 us whole and 42 cut, 512 tokens 45 and 43; 256 x 8 of 128, bf16, 25 and
+// 34, 512 tokens 33 and 37.  The forward takes 26 us whole and 27 cut for 256 of the first, 22 and 25 of
+// the second, but 49 and 28, 38 and 26 for 512: the eight chunks cost it that much, and spare calls
+// so short a workspace.
 constexpr int64_t kWholeTokens = 8 * kLinChunk;
 
 struct Plan {
@@ -91,7 +95,9 @@ struct Plan {
 };
 // dirs: directions walked, each by dv / 64 workgroups in the backward.  Several documents take half
 // shares there unless none of them is longer than a share: 4 ragged documents of 32768 tokens x 32
-// heads 1576 -> 1296 us, but equal ones 1036 -> 1229 if cut like that.  The forward has its longest
+// heads 1576 -> 1296 us, but equal ones 1020 -> 1234 if cut like that.  The limit has no slack: four
+// equal documents x 32 heads are just a share long, and one token more in one of them cuts all (8193,
+// 8191, 8192, 8192 tokens: 1234; three documents are always cut, 1284).  The forward has its longest
 // segments first instead (37 ragged documents, 16411 tokens, 32 heads with half shares 223 us, whole
 // ones 208).
 Plan walk_plan(const kda_linear_config* c, int64_t T, int32_t N, int dirs) {
@@ -299,7 +305,7 @@ kda_status kda_linear_fwd(const kda_linear_config* cfg, int64_t T, int32_t N, co
         p.seg_state = state;
         // Longest first where workgroups follow one another (37 ragged documents, 16411 tokens, 32
         // heads: 236 -> 226 us; 64, 16384, 16: 158 -> 142).  Where all run at once it only costs (25,
-        // 6229, 4: 36 -> 40), and more documents even out by their number.
+        // 6229, 4: 36 -> 40).  A wave looks for the order among its lanes, so at most 64 documents.
         p.longest_first = N > 1 && N <= 64 && f.plan.chains > kWalkTarget;
     }
     return launched(launch_linear_out(p, cfg->in_dtype, cfg->dk, st));

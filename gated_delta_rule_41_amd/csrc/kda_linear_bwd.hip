@@ -16,7 +16,7 @@
 // row sums of A), dk (with f and its column sums) or dv (with <S, dS>), wave w a 16-row block
 // of queries or keys.  Each role loops over the key head's value heads in the same order, so
 // that the L2 still has what another role has read (with dv's value heads side by side instead
-// 32768 tokens x 32 heads on 16 key heads took 1495 us, so 1237), and the gradients of shared
+// 32768 tokens x 32 heads on 16 key heads took 1495 us, like this 1237), and the gradients of shared
 // heads add up in registers in a fixed order.  Where that leaves too few workgroups, the value
 // heads are divided among `parts` of them, whose sums linear_parts_kernel adds, again in a
 // fixed order.  A wave forms its own rows of P or dP in the transposed orientation, in which the
@@ -24,9 +24,10 @@
 // price of forming dP twice and P twice.  One role needs two 128-row tiles in LDS and fits 128
 // registers, so two workgroups share a compute unit and one computes while the other loads;
 // the three roles of a block are issued eight workgroups apart, on one XCD, whose L2 serves the
-// rows that they share.  At 4 x 8192 tokens x 32 heads, bf16, it takes 664 us and moves 2.47 GB
-// (3.7 TB/s; matrix instructions issue 20% of the time, vector instructions 41%, LDS is busy
-// 31%): memory bounds it, at 72% of a copy's rate, with loads and sums of two workgroups in turn.
+// rows that they share.  At 4 x 8192 tokens x 32 heads, bf16, it takes 655 us and moves 2.46 GB
+// (3.8 TB/s, 73% of a copy's rate; matrix instructions issue 20% of the time, vector instructions
+// 43%, LDS is busy 31%).  None of them is at its limit: latency bounds it, two workgroups in turn
+// through loads, products and stores.
 // (One kernel for dk and dv at 255 registers, one workgroup a compute unit, took 620 us, and dq
 // beside it 461.)
 // linear_dg_kernel finishes dg.

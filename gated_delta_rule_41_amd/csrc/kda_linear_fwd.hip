@@ -15,15 +15,15 @@
 // The next chunk's rows are loaded into registers while this one runs, and its gates are
 // summed by wave 0, which has the least of P.
 //
-// 131083 tokens x 16 heads of 128, bf16, 512 segments: 472 us, 2.19 GB, 4.6 TB/s (a copy: 5.2).
-// Two waves a SIMD issue vector instructions 43% and matrix instructions 33% of that time; at
+// 131083 tokens x 16 heads of 128, bf16, 512 segments: 491 us, 2.19 GB, 4.5 TB/s (a copy: 5.2).
+// Two waves a SIMD issue vector instructions 44% and matrix instructions 33% of that time; at
 // 32768 x 32 heads on 8, with a third less to read, it took 251 us against 275 on 32: near both
 // bounds.  64 tokens a step are what two workgroups' LDS allows.
 //
 // linear_state_kernel: the state alone, forward or in reverse (the same sum with q, dO and
 // weights e^{G_i}), for the segments of long documents and for the backward.  Own sums of the
-// same segments: 250 us, 1.1 GB, 4.4 TB/s.  Both directions of 4 x 8192 x 32 heads with the
-// states at the blocks' borders: 371 us, 1.7 GB, 4.6 TB/s.
+// same segments: 255 us, 1.1 GB, 4.3 TB/s.  Both directions of 4 x 8192 x 32 heads with the
+// states at the blocks' borders: 355 us, 1.7 GB, 4.8 TB/s.
 //
 // linear_carry_kernel: the states entering the segments of each document after the first, from
 // the segments' own sums (a scalar decay composes as plain products).  In place: a segment's
@@ -226,10 +226,10 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void linear_out_k
             store(m, out[0][m], out[NC - 1][m]);
         }
         // An infinity or NaN of v is in the last rows, which reach every key, and through the zeros of P in
-        // rows before its own: then all rows again, from v's finite values.  (Looking at v itself, or going
-        // over the whole document again where its state ends up infinite or NaN, took as long: 131083 tokens
-        // x 16 heads 740 us without this, 758 with it, 764 and 745 those ways, 37 documents, 16411 tokens,
-        // 32 heads on 8 208.7, 209.7, 209.5 and 214.8.)
+        // rows before its own: then all rows again, from v's finite values.  131083 tokens x 16 heads take
+        // 740 us without this and 758 with it, 37 documents, 16411 tokens, 32 heads on 8 208.7 and 209.7;
+        // looking at v itself 764 and 209.5, going over the whole document again where its state ends up
+        // infinite or NaN 745 and 214.8.
         f32x4 last = out[0][3];
         if constexpr (NC == 2) last += out[1][3];
         if (__ballot(!(fabsf((last[0] + last[1]) + (last[2] + last[3])) < INFINITY))) {

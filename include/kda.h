@@ -385,6 +385,8 @@ kda_status kda_linear_decode(const kda_linear_config* cfg, int32_t num_seqs, con
  * (int32 [num_seqs]); an accept[n] below 0, not below `nodes`, or of an absent
  * node accepts nothing and copies the state.  state_out may be state_in
  * itself and must not otherwise overlap it.
+ * bf16 inputs: the products with the state take two bf16 terms of each side,
+ * 2^-16 of their terms; everything else, and all of fp32 inputs, is fp32.
  * A chain (parent[n][i] = i - 1) equals a run of kda_decode /
  * kda_linear_decode calls up to rounding.  num_seqs = 0 enqueues nothing. */
 #define KDA_TREE_MAX_NODES 64
