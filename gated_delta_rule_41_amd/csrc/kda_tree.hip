@@ -217,8 +217,8 @@ __global__ __launch_bounds__(NL == 16 ? 256 : 512, sizeof(T) == 2 ? 4 : 2) void 
             const int i = (tid >> 4) + r * NODES;
             put_row<E>(s.x.c.k + i * DK, cl, kv[r]);
             if constexpr (DELTA) {
-                const float rk = __builtin_amdgcn_rsqf(row16_sum(dot8(kv[r], kv[r])) + p.eps);
-                const float rq = p.scale * __builtin_amdgcn_rsqf(row16_sum(dot8(qv[r], qv[r])) + p.eps);
+                const float rk = 1.f / sqrtf(row16_sum(dot8(kv[r], kv[r])) + p.eps);   // as kda_decode's, down to the smallest sums
+                const float rq = p.scale / sqrtf(row16_sum(dot8(qv[r], qv[r])) + p.eps);
                 kv[r] *= splat8(rk);
                 qv[r] *= splat8(rq);
 #pragma unroll
@@ -425,7 +425,7 @@ __global__ __launch_bounds__(kThreads) void kda_tree_commit_kernel(TreeParams p)
             if constexpr (DELTA) {
 #pragma unroll
                 for (int x = 16; x >= 1; x >>= 1) sum += __shfl_xor(sum, x, 64);
-                r = __builtin_amdgcn_rsqf(sum + p.eps);
+                r = 1.f / sqrtf(sum + p.eps);
             }
             if (done) __syncthreads();   // the last batch's readers are done
 #pragma unroll
