@@ -44,6 +44,14 @@ __device__ __forceinline__ int parent_of(const int* par, int a, int L) {
 
 __device__ __forceinline__ float sigmoidf(float b) { return 1.f / (1.f + __expf(-b)); }
 
+// 1 / sqrt(x) by the hardware's instruction, which is off by a unit in the last place at most but
+// takes x below fp32's smallest normal number for zero: such sums are scaled up first.  (Division
+// and square root as the compiler makes them: 64 trees of 61 nodes x 32 heads 98.1 us, this 97.1.)
+__device__ __forceinline__ float inv_sqrt(float x) {
+    const bool tiny = x < 0x1p-100f;
+    return __builtin_amdgcn_rsqf(tiny ? x * 0x1p96f : x) * (tiny ? 0x1p48f : 1.f);
+}
+
 // Eight elements of a global row as fp32.
 template <typename T> __device__ __forceinline__ f32x8 load8f(const T* p) {
     return widen8(*reinterpret_cast<const typename V8<T>::t*>(p));
@@ -217,8 +225,8 @@ __global__ __launch_bounds__(NL == 16 ? 256 : 512, sizeof(T) == 2 ? 4 : 2) void 
             const int i = (tid >> 4) + r * NODES;
             put_row<E>(s.x.c.k + i * DK, cl, kv[r]);
             if constexpr (DELTA) {
-                const float rk = 1.f / sqrtf(row16_sum(dot8(kv[r], kv[r])) + p.eps);   // as kda_decode's, down to the smallest sums
-                const float rq = p.scale / sqrtf(row16_sum(dot8(qv[r], qv[r])) + p.eps);
+                const float rk = inv_sqrt(row16_sum(dot8(kv[r], kv[r])) + p.eps);
+                const float rq = p.scale * inv_sqrt(row16_sum(dot8(qv[r], qv[r])) + p.eps);
                 kv[r] *= splat8(rk);
                 qv[r] *= splat8(rq);
 #pragma unroll
@@ -425,7 +433,7 @@ __global__ __launch_bounds__(kThreads) void kda_tree_commit_kernel(TreeParams p)
             if constexpr (DELTA) {
 #pragma unroll
                 for (int x = 16; x >= 1; x >>= 1) sum += __shfl_xor(sum, x, 64);
-                r = 1.f / sqrtf(sum + p.eps);
+                r = inv_sqrt(sum + p.eps);
             }
             if (done) __syncthreads();   // the last batch's readers are done
 #pragma unroll
