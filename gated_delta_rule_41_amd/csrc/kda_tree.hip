@@ -17,10 +17,10 @@
 // ancestor of that level adds to u and o, one read of u for both.  Sums run over true ancestors
 // only, so nothing in another branch, NaN included, reaches a node.
 //
-// 64 trees of 61 nodes x 32 heads of 128, bf16, delta rule: 90 us, 0.29 GB at 3.3 TB/s; vector
+// 64 trees of 61 nodes x 32 heads of 128, bf16, delta rule: 91 to 97 us, 0.29 GB at 3.1 TB/s; vector
 // instructions issue 71% of the time, two workgroups a compute unit in turn through load (a third
 // of a workgroup's time), climb, products, solve.  One workgroup with the solve level by level
-// across waves took 247 us, two 119, each wave for itself 100.  Linear rule, 32 nodes: 42.7 us,
+// across waves took 247 us, two 119, each wave for itself 100.  Linear rule, 32 nodes: 43.0 us,
 // 4.1 TB/s.  fp32 inputs: 186 us at 128 x 128, where one workgroup fits a compute unit, 67 at 64 x 64,
 // the linear rule 52.
 //
