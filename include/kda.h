@@ -295,7 +295,7 @@ kda_status kda_decode(const kda_config* cfg, int32_t num_seqs, const void* q, co
  * Infinities and NaN reach what depends on them by the recurrence and nothing
  * else: the token's own output and later ones of its document, through v in
  * its column alone; likewise the gradients of earlier tokens through q and dO,
- * of later ones through k and v.  (In the token's own 128-token block and head
+ * of later ones through k and v.  (In the token's own 128-token block and heads
  * dg is not held to that, nor is any gradient with a NaN gate.)  Such a result
  * is infinite or NaN; the packed calls do not say which (chunks add up in
  * another order), decode keeps a state's infinities.
@@ -336,7 +336,8 @@ size_t kda_linear_bwd_workspace_size(const kda_linear_config* cfg, int64_t total
 
 /* Forward.  initial_state and final_state as for kda_fwd (either may be NULL);
  * they must not overlap, equal pointers included (KDA_ERR_INVALID_ARG: the
- * segments of a document run at the same time).  workspace may be NULL when kda_linear_fwd_workspace_size() is 0. */
+ * segments of a document run at the same time).  workspace may be NULL when
+ * kda_linear_fwd_workspace_size() is 0. */
 kda_status kda_linear_fwd(const kda_linear_config* cfg, int64_t total_tokens, int32_t num_seqs, const void* q,
                           const void* k, const void* v, const float* g, const int32_t* cu_seqlens,
                           const float* initial_state, void* o, float* final_state, void* workspace,
@@ -347,8 +348,9 @@ kda_status kda_linear_fwd(const kda_linear_config* cfg, int64_t total_tokens, in
  * ([total_tokens, H, dv], in_dtype) and dS_final (fp32 or NULL = 0).  Outputs:
  * dq, dk [total_tokens, Hk, dk] (summed over the value heads that share them),
  * dv [total_tokens, H, dv], dg (the shape of g; [H] sums over all tokens), all
- * in out_dtype (dg in fp32 under KDA_GATE_GRAD_F32), and d_initial_state, fp32 or NULL, which must not overlap
- * initial_state or dS_final (KDA_ERR_INVALID_ARG). */
+ * in out_dtype (dg in fp32 under KDA_GATE_GRAD_F32), and d_initial_state, fp32
+ * or NULL, which must not overlap initial_state or dS_final
+ * (KDA_ERR_INVALID_ARG). */
 kda_status kda_linear_bwd(const kda_linear_config* cfg, int64_t total_tokens, int32_t num_seqs, const void* q,
                           const void* k, const void* v, const float* g, const int32_t* cu_seqlens,
                           const float* initial_state, const void* dO, const float* dS_final, void* dq, void* dk,
