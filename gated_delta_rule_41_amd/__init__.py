@@ -19,9 +19,13 @@ from . import _lib
 from ._tensors import check as _check, dt_code as _dt_code, ptr as _ptr, torch_module as _torch
 from ._lib import (KDA_BF16, KDA_F32, KDA_FLAG_SAVE_FOR_BWD, KDA_FLAG_SEQUENTIAL, KdaConfig, KdaError, kda_bwd_workspace_size,
                    kda_fwd_workspace_size, kda_saved_size, make_config)
+from .layer import (kda_conv, kda_conv_bwd, kda_conv_decode, kda_conv_fwd, kda_norm, kda_norm_bwd, kda_norm_fwd, kda_selective,
+                    kda_selective_bwd, kda_selective_decode, kda_selective_fwd)
 from .linear import kda_linear, kda_linear_bwd, kda_linear_decode, kda_linear_fwd, kda_tree, kda_tree_commit
 
-__all__ = ["kda_linear", "kda_linear_fwd", "kda_linear_bwd", "kda_linear_decode", "kda_tree", "kda_tree_commit",
+__all__ = ["kda_norm", "kda_norm_fwd", "kda_norm_bwd", "kda_conv", "kda_conv_fwd", "kda_conv_bwd", "kda_conv_decode",
+           "kda_selective", "kda_selective_fwd", "kda_selective_bwd", "kda_selective_decode",
+           "kda_linear", "kda_linear_fwd", "kda_linear_bwd", "kda_linear_decode", "kda_tree", "kda_tree_commit",
            "kda", "kda_fwd", "kda_fwd_staged", "kda_bwd", "kda_decode", "kda_saved_size", "kda_fwd_workspace_size", "kda_bwd_workspace_size",
            "make_config", "KdaConfig", "KdaError", "KDA_F32", "KDA_BF16", "KDA_FLAG_SAVE_FOR_BWD",
            "KDA_FLAG_SEQUENTIAL"]

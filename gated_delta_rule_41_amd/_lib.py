@@ -41,6 +41,10 @@ KDA_GATE_TOKEN, KDA_GATE_HEAD = 0, 1
 KDA_GATE_GRAD_F32 = 0x100
 KDA_RULE_DELTA, KDA_RULE_LINEAR = 0, 1
 KDA_TREE_MAX_NODES = 64
+KDA_I8, KDA_E4M3 = 2, 3   # outputs of kda_norm_fwd
+KDA_NORM_MAX_CHANNELS = 32768
+KDA_ACT_NONE, KDA_ACT_SILU = 0, 1
+KDA_SELECTIVE_SOFTPLUS = 1
 
 
 class KdaLinearConfig(ctypes.Structure):
@@ -69,6 +73,45 @@ class KdaTreeConfig(ctypes.Structure):
         ("gate", ctypes.c_int32),
         ("l2_eps", ctypes.c_float),
         ("scale", ctypes.c_float),
+    ]
+
+
+class KdaNormConfig(ctypes.Structure):
+    _fields_ = [
+        ("C", ctypes.c_int32),
+        ("in_dtype", ctypes.c_int32),
+        ("res_dtype", ctypes.c_int32),
+        ("weight_dtype", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+    ]
+
+
+class KdaConvConfig(ctypes.Structure):
+    _fields_ = [
+        ("C", ctypes.c_int32),
+        ("width", ctypes.c_int32),
+        ("in_dtype", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int32),
+        ("weight_dtype", ctypes.c_int32),
+        ("activation", ctypes.c_int32),
+        ("x_stride", ctypes.c_int64),
+    ]
+
+
+class KdaSelectiveConfig(ctypes.Structure):
+    _fields_ = [
+        ("C", ctypes.c_int32),
+        ("S", ctypes.c_int32),
+        ("G", ctypes.c_int32),
+        ("in_dtype", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int32),
+        ("flags", ctypes.c_uint32),
+        ("x_stride", ctypes.c_int64),
+        ("dt_stride", ctypes.c_int64),
+        ("z_stride", ctypes.c_int64),
+        ("b_stride", ctypes.c_int64),
+        ("c_stride", ctypes.c_int64),
     ]
 
 
@@ -143,6 +186,24 @@ def load():
     lib.kda_tree_commit.argtypes = [treecfg, i32] + [_vp] * 9
     for name in ("kda_linear_fwd", "kda_linear_bwd", "kda_linear_decode", "kda_tree", "kda_tree_commit"):
         getattr(lib, name).restype = ctypes.c_int
+    i64, norm, conv, sel = ctypes.c_int64, *(ctypes.POINTER(c) for c in (KdaNormConfig, KdaConvConfig, KdaSelectiveConfig))
+    for name, res, args in (
+            ("kda_norm_config_init", None, [norm, i32]),
+            ("kda_norm_fwd", i32, [norm, i64] + [_vp] * 7),
+            ("kda_norm_bwd_workspace_size", size, [norm, i64]),
+            ("kda_norm_bwd", i32, [norm, i64] + [_vp] * 7 + [size, _vp]),
+            ("kda_conv_config_init", None, [conv, i32, i32]),
+            ("kda_conv_fwd", i32, [conv, i64, i32] + [_vp] * 8),
+            ("kda_conv_bwd_workspace_size", size, [conv, i64, i32]),
+            ("kda_conv_bwd", i32, [conv, i64, i32] + [_vp] * 12 + [size, _vp]),
+            ("kda_conv_decode", i32, [conv, i32] + [_vp] * 7),
+            ("kda_selective_config_init", None, [sel, i32, i32, i32]),
+            ("kda_selective_fwd_workspace_size", size, [sel, i64, i32]),
+            ("kda_selective_bwd_workspace_size", size, [sel, i64, i32]),
+            ("kda_selective_fwd", i32, [sel, i64, i32] + [_vp] * 13 + [size, _vp]),
+            ("kda_selective_bwd", i32, [sel, i64, i32] + [_vp] * 22 + [size, _vp]),
+            ("kda_selective_decode", i32, [sel, i32] + [_vp] * 12)):
+        getattr(lib, name).restype, getattr(lib, name).argtypes = res, args
     lib.kda_status_string.argtypes = [ctypes.c_int]
     lib.kda_status_string.restype = ctypes.c_char_p
     lib.kda_last_error.argtypes = []
@@ -265,3 +326,82 @@ def kda_tree_raw(cfg, num_seqs, q, k, v, g, beta, parent, state, o, stream) -> i
 
 def kda_tree_commit_raw(cfg, num_seqs, k, v, g, beta, parent, accept, state_in, state_out, stream) -> int:
     return (_lib or load()).kda_tree_commit(cfg, num_seqs, k, v, g, beta, parent, accept, state_in, state_out, stream)
+
+
+# ---- the norm, the short convolution and the selective scan: direct calls with integer device addresses (0 = NULL)
+def make_norm_config(C, in_dtype=KDA_BF16, res_dtype=KDA_BF16, weight_dtype=KDA_BF16, out_dtype=KDA_BF16, eps=1e-6):
+    cfg = KdaNormConfig()
+    load().kda_norm_config_init(ctypes.byref(cfg), C)
+    cfg.in_dtype, cfg.res_dtype, cfg.weight_dtype, cfg.out_dtype, cfg.eps = in_dtype, res_dtype, weight_dtype, out_dtype, eps
+    return cfg
+
+
+def make_conv_config(C, width, in_dtype=KDA_BF16, out_dtype=KDA_BF16, weight_dtype=KDA_BF16, activation=KDA_ACT_SILU, x_stride=0):
+    cfg = KdaConvConfig()
+    load().kda_conv_config_init(ctypes.byref(cfg), C, width)
+    cfg.in_dtype, cfg.out_dtype, cfg.weight_dtype, cfg.activation, cfg.x_stride = in_dtype, out_dtype, weight_dtype, activation, x_stride
+    return cfg
+
+
+def make_selective_config(C, S, G=1, in_dtype=KDA_BF16, out_dtype=KDA_BF16, flags=KDA_SELECTIVE_SOFTPLUS, x_stride=0, dt_stride=0,
+                          z_stride=0, b_stride=0, c_stride=0):
+    cfg = KdaSelectiveConfig()
+    load().kda_selective_config_init(ctypes.byref(cfg), C, S, G)
+    cfg.in_dtype, cfg.out_dtype, cfg.flags, cfg.x_stride, cfg.dt_stride = in_dtype, out_dtype, flags, x_stride, dt_stride
+    cfg.z_stride, cfg.b_stride, cfg.c_stride = z_stride, b_stride, c_stride
+    return cfg
+
+
+def kda_norm_bwd_workspace_size(cfg: KdaNormConfig, rows: int) -> int:
+    return int(load().kda_norm_bwd_workspace_size(cfg, rows))
+
+
+def kda_conv_bwd_workspace_size(cfg: KdaConvConfig, total_tokens: int, num_seqs: int) -> int:
+    return int(load().kda_conv_bwd_workspace_size(cfg, total_tokens, num_seqs))
+
+
+def kda_selective_fwd_workspace_size(cfg: KdaSelectiveConfig, total_tokens: int, num_seqs: int) -> int:
+    return int(load().kda_selective_fwd_workspace_size(cfg, total_tokens, num_seqs))
+
+
+def kda_selective_bwd_workspace_size(cfg: KdaSelectiveConfig, total_tokens: int, num_seqs: int) -> int:
+    return int(load().kda_selective_bwd_workspace_size(cfg, total_tokens, num_seqs))
+
+
+def kda_norm_fwd_raw(cfg, rows, x, residual, weight, y, s, scale, stream) -> int:
+    return (_lib or load()).kda_norm_fwd(cfg, rows, x, residual, weight, y, s, scale, stream)
+
+
+def kda_norm_bwd_raw(cfg, rows, s, weight, dy, ds, dx, dweight, workspace, workspace_bytes, stream) -> int:
+    return (_lib or load()).kda_norm_bwd(cfg, rows, s, weight, dy, ds, dx, dweight, workspace, workspace_bytes, stream)
+
+
+def kda_conv_fwd_raw(cfg, total_tokens, num_seqs, x, weight, bias, cu_seqlens, initial_state, y, final_state, stream) -> int:
+    return (_lib or load()).kda_conv_fwd(cfg, total_tokens, num_seqs, x, weight, bias, cu_seqlens, initial_state, y, final_state, stream)
+
+
+def kda_conv_bwd_raw(cfg, total_tokens, num_seqs, x, weight, bias, cu_seqlens, initial_state, dy, d_final_state, dx, dweight, dbias,
+                     d_initial_state, workspace, workspace_bytes, stream) -> int:
+    return (_lib or load()).kda_conv_bwd(cfg, total_tokens, num_seqs, x, weight, bias, cu_seqlens, initial_state, dy, d_final_state, dx,
+                                         dweight, dbias, d_initial_state, workspace, workspace_bytes, stream)
+
+
+def kda_conv_decode_raw(cfg, num_seqs, x, weight, bias, state_in, state_out, y, stream) -> int:
+    return (_lib or load()).kda_conv_decode(cfg, num_seqs, x, weight, bias, state_in, state_out, y, stream)
+
+
+def kda_selective_fwd_raw(cfg, total_tokens, num_seqs, x, dt, A, B, C, D, z, dt_bias, cu_seqlens, initial_state, y, final_state,
+                          workspace, workspace_bytes, stream) -> int:
+    return (_lib or load()).kda_selective_fwd(cfg, total_tokens, num_seqs, x, dt, A, B, C, D, z, dt_bias, cu_seqlens, initial_state, y,
+                                              final_state, workspace, workspace_bytes, stream)
+
+
+def kda_selective_bwd_raw(cfg, total_tokens, num_seqs, x, dt, A, B, C, D, z, dt_bias, cu_seqlens, initial_state, dy, dS_final, dx, ddt,
+                          dA, dB, dC, dD, dz, ddt_bias, d_initial_state, workspace, workspace_bytes, stream) -> int:
+    return (_lib or load()).kda_selective_bwd(cfg, total_tokens, num_seqs, x, dt, A, B, C, D, z, dt_bias, cu_seqlens, initial_state, dy,
+                                              dS_final, dx, ddt, dA, dB, dC, dD, dz, ddt_bias, d_initial_state, workspace,
+                                              workspace_bytes, stream)
+
+
+def kda_selective_decode_raw(cfg, num_seqs, x, dt, A, B, C, D, z, dt_bias, state_in, state_out, y, stream) -> int:
+    return (_lib or load()).kda_selective_decode(cfg, num_seqs, x, dt, A, B, C, D, z, dt_bias, state_in, state_out, y, stream)

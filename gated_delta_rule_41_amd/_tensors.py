@@ -46,6 +46,12 @@ def check(t, name, shape, dtype, device):
         raise ValueError(f"{name} must be contiguous")
 
 
+def upstream(grad):
+    """A gradient as the kernels take it: autograd may hand over a view of a larger tensor."""
+    grad = grad.contiguous()
+    return grad if grad.data_ptr() % 16 == 0 else grad.clone()
+
+
 def launch(dev, call, *args):
     """call(*args, stream) with `dev` current, on its current stream; raises on a bad status.  The device is switched only
     where it is another one, and the stream is asked for as its handle: both cost more than the checks of a small call."""

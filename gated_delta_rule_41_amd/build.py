@@ -12,7 +12,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libkda.so")
 SOURCES = ["kda_api.hip", "kda_fwd.hip", "kda_fwd16.hip", "kda_bwd.hip", "kda_decode.hip", "kda_split.hip", "kda_exact.hip", "kda_scan16.hip",
-           "kda_staged.hip", "kda_linear_api.hip", "kda_linear_fwd.hip", "kda_linear_bwd.hip", "kda_linear_decode.hip", "kda_tree.hip"]
+           "kda_staged.hip", "kda_linear_api.hip", "kda_linear_fwd.hip", "kda_linear_bwd.hip", "kda_linear_decode.hip", "kda_tree.hip", "kda_layer_api.hip",
+           "kda_norm.hip", "kda_conv.hip", "kda_selective_states.hip", "kda_selective_fwd.hip", "kda_selective_bwd.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

@@ -1,0 +1,74 @@
+// kda_selective.h -- device code shared by the selective scan's kernels.
+//
+// A lane holds one channel with all its S state entries in registers, a wave 64 channels of
+// one group, so B_t and C_t are the same for the whole wave: they come through the scalar
+// cache and enter the products as scalar operands, and the sums over the state's entries stay
+// in a lane.  An entry and token costs a multiply and an exponential for the decay (the
+// exponential a quarter of the rate), a multiply and a multiply-add for the state and a
+// multiply-add for the output: 8 issue slots, which bound these kernels.
+#pragma once
+#include "kda_layer.h"
+
+namespace kda {
+
+constexpr float kLn2 = 0.693147181f;
+
+// A row of B or C on its way (uniform), and as fp32.
+template <typename T, int S> struct UniformRow {
+    static constexpr int kWords = S * sizeof(T) / 4;
+    typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+    unsigned w[kWords];
+    __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+        for (int i = 0; i < kWords; i += 4) {
+            const u32x4 x = uniform_load<u32x4>(reinterpret_cast<const unsigned*>(p) + i);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[i + j] = x[j];
+        }
+    }
+    __device__ __forceinline__ float operator[](int n) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[n]);
+        else return __uint_as_float(n & 1 ? w[n >> 1] & 0xffff0000u : w[n >> 1] << 16);
+    }
+};
+
+// A wave's channels: `c` of a lane is clamped to its group, `valid` says whether it is its own.
+struct Channels {
+    int group, c;
+    bool valid;
+    __device__ __forceinline__ Channels(const SelectiveParams& p, int wave) {
+        const int per = p.C / p.G, in = (wave % p.group_waves) * 64 + (int)(threadIdx.x & 63);
+        group = wave / p.group_waves;
+        valid = in < per;
+        c = group * per + (valid ? in : per - 1);
+    }
+};
+
+template <int S> __device__ __forceinline__ void load_entries(float (&v)[S], const float* p) {
+#pragma unroll
+    for (int n = 0; n < S; n += 4) {
+        const f32x4 x = *reinterpret_cast<const f32x4*>(p + n);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[n + j] = x[j];
+    }
+}
+template <int S> __device__ __forceinline__ void store_entries(float* p, const float (&v)[S]) {
+#pragma unroll
+    for (int n = 0; n < S; n += 4) {
+        const f32x4 x = {v[n], v[n + 1], v[n + 2], v[n + 3]};
+        *reinterpret_cast<f32x4*>(p + n) = x;
+    }
+}
+// A in units of log 2, so that a decay is one multiply and one exponential.
+template <int S> __device__ __forceinline__ void load_A(float (&A2)[S], const float* A) {
+    load_entries<S>(A2, A);
+#pragma unroll
+    for (int n = 0; n < S; ++n) A2[n] *= kLog2e;
+}
+
+__device__ __forceinline__ float step_size(float raw, float bias, bool soft) {
+    const float v = raw + bias;
+    return soft ? softplus(v) : v;
+}
+
+}  // namespace kda

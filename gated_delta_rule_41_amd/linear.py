@@ -9,7 +9,7 @@ from typing import Optional
 
 from . import _lib
 from ._lib import KDA_GATE_GRAD_F32, KDA_GATE_HEAD, KDA_GATE_TOKEN, KDA_RULE_DELTA, KDA_RULE_LINEAR, KDA_TREE_MAX_NODES
-from ._tensors import check as _check, dt_code as _dt_code, launch as _launch, ptr as _ptr, torch_module as _torch
+from ._tensors import check as _check, dt_code as _dt_code, launch as _launch, ptr as _ptr, torch_module as _torch, upstream as _upstream
 
 # Configs and workspace sizes depend on their arguments alone; made once for each set of them.
 _linear_config = lru_cache(maxsize=256)(_lib.make_linear_config)
@@ -200,12 +200,6 @@ def kda_tree_commit(k, v, g, beta, parent, accept, state=None, *, out_state=None
     _launch(dev, _lib.kda_tree_commit_raw, cfg, N, _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(parent), _ptr(accept),
             _ptr(state), _ptr(out_state))
     return out_state
-
-
-def _upstream(grad):
-    """A gradient as the kernels take it: autograd may hand over a view of a larger tensor."""
-    grad = grad.contiguous()
-    return grad if grad.data_ptr() % 16 == 0 else grad.clone()
 
 
 def _autograd_function():

@@ -420,6 +420,174 @@ kda_status kda_tree_commit(const kda_tree_config* cfg, int32_t num_seqs, const v
                            const void* g, const void* beta, const int32_t* parent, const int32_t* accept,
                            const float* state_in, float* state_out, void* stream);
 
+/* ------------------------------------------------------------------------
+ * What stands around the recurrences in a layer: the norm with the residual's
+ * addition, the short causal convolution, and the selective scan (a recurrence
+ * with a decay for each channel and state entry).  The conventions at the top
+ * of this file hold (packed documents, cu_seqlens, pointers, streams, errors,
+ * re-entrancy); channels are the inner index.  Arguments called strides are the
+ * elements from one row to the next, so that an input may be a part of a wider
+ * projection's rows; 0 means rows without gaps.  Results are deterministic.
+ * Calls that may run at the same time, replays of captured ones included, need
+ * a workspace each. */
+
+/* Output types of kda_norm_fwd beside kda_dtype's. */
+#define KDA_I8 2   /* signed 8-bit integers in [-127, 127]                     */
+#define KDA_E4M3 3 /* 8-bit floats, 4 exponent and 3 mantissa bits, largest 448 */
+
+#define KDA_NORM_MAX_CHANNELS 32768
+
+typedef struct kda_norm_config {
+    int32_t C;            /* channels, 1 .. KDA_NORM_MAX_CHANNELS              */
+    int32_t in_dtype;     /* kda_dtype of x and dy                             */
+    int32_t res_dtype;    /* kda_dtype of residual, s and ds                   */
+    int32_t weight_dtype; /* kda_dtype of weight                               */
+    int32_t out_dtype;    /* forward: y (kda_dtype, KDA_I8 or KDA_E4M3); backward: dx (kda_dtype) */
+    float eps;            /* added to the mean of the squares (1e-6)           */
+} kda_norm_config;
+
+/* Fill *cfg with defaults: fp32 throughout, eps 1e-6. */
+void kda_norm_config_init(kda_norm_config* cfg, int32_t C);
+
+/* Root-mean-square norm of rows, with the residual's addition:
+ *     s = x + residual,   y = s weight / sqrt(mean(s^2) + eps)
+ * s is rounded to res_dtype once and the norm is of the rounded row, so that a
+ * backward from the stored s is that of this forward.
+ *   x, y : [rows, C]    residual, s : [rows, C]    weight : [C] or NULL (ones)
+ * residual NULL: s = x (res_dtype must be in_dtype then) and `s` is not written.
+ * s NULL: the sum is not kept.  s may be residual or x themselves, y may be x,
+ * where their types are equal; other overlaps of outputs with anything are
+ * refused (KDA_ERR_INVALID_ARG).
+ * KDA_I8, KDA_E4M3: a row's fp32 products p = s weight, m = max|p| and its code
+ * limit Q (127, 448) give the codes, p Q / m rounded to the nearest of the type
+ * (ties to even; exactly, so codes do not depend on the order of any sum), and
+ * scale[row] = m / (Q sqrt(mean(s^2) + eps)), fp32 [rows]: y = code * scale.  A
+ * row of zeros has zero codes and scale 0; one with an infinity or NaN has
+ * scale NaN and unspecified codes.  scale is NULL for the other types.
+ * rows = 0 enqueues nothing. */
+kda_status kda_norm_fwd(const kda_norm_config* cfg, int64_t rows, const void* x, const void* residual,
+                        const void* weight, void* y, void* s, float* scale, void* stream);
+
+/* Backward of kda_norm_fwd (of its unquantised y) for the loss <dy, y> +
+ * <ds, s>: from the stored s (res_dtype; x itself without a residual), dy
+ * (in_dtype) and ds (res_dtype or NULL = 0) to dx (out_dtype; the gradient of x
+ * and of the residual alike) and dweight (fp32 [C], or NULL).  dx may be dy or
+ * ds themselves where their types are equal.  workspace:
+ * kda_norm_bwd_workspace_size bytes (0 for an invalid config or sizes, and
+ * where dweight is not asked for none is needed). */
+size_t kda_norm_bwd_workspace_size(const kda_norm_config* cfg, int64_t rows);
+kda_status kda_norm_bwd(const kda_norm_config* cfg, int64_t rows, const void* s, const void* weight, const void* dy,
+                        const void* ds, void* dx, float* dweight, void* workspace, size_t workspace_bytes,
+                        void* stream);
+
+typedef enum kda_activation { KDA_ACT_NONE = 0, KDA_ACT_SILU = 1 } kda_activation;
+
+typedef struct kda_conv_config {
+    int32_t C;            /* channels                                          */
+    int32_t width;        /* taps: 2, 3 or 4                                   */
+    int32_t in_dtype;     /* kda_dtype of x, dy and the states                 */
+    int32_t out_dtype;    /* kda_dtype of y, dx                                */
+    int32_t weight_dtype; /* kda_dtype of weight and bias                      */
+    int32_t activation;   /* kda_activation                                    */
+    int64_t x_stride;     /* of x's rows; 0: C                                 */
+} kda_conv_config;
+
+/* Fill *cfg with defaults: fp32 throughout, SiLU, rows without gaps. */
+void kda_conv_config_init(kda_conv_config* cfg, int32_t C, int32_t width);
+
+/* Causal convolution of every channel with its own taps, over documents:
+ *     pre_t = bias + sum_j weight[j] x_{t - width + 1 + j},   y_t = act(pre_t)
+ * Rows before a document are its initial state's: the width - 1 rows that came
+ * before it, oldest first; the final state is the last width - 1 rows of both.
+ *   x, y, dy, dx : [total_tokens, C]    weight : [C, width]    bias : [C] or NULL
+ *   states : [num_seqs, width - 1, C] in in_dtype (NULL: zero / not kept)
+ * initial_state and final_state must not overlap, nor y and x.  Any C; rows of
+ * 8 channels at 16-byte addresses (C and x_stride multiples of 8) are faster. */
+kda_status kda_conv_fwd(const kda_conv_config* cfg, int64_t total_tokens, int32_t num_seqs, const void* x,
+                        const void* weight, const void* bias, const int32_t* cu_seqlens, const void* initial_state,
+                        void* y, void* final_state, void* stream);
+
+/* Backward of kda_conv_fwd for the loss <dy, y> + <d_final_state, final_state>,
+ * from the forward's inputs: dx (out_dtype), dweight (fp32 [C, width]), dbias
+ * (fp32 [C], or NULL) and d_initial_state (in_dtype, or NULL). */
+size_t kda_conv_bwd_workspace_size(const kda_conv_config* cfg, int64_t total_tokens, int32_t num_seqs);
+kda_status kda_conv_bwd(const kda_conv_config* cfg, int64_t total_tokens, int32_t num_seqs, const void* x,
+                        const void* weight, const void* bias, const int32_t* cu_seqlens, const void* initial_state,
+                        const void* dy, const void* d_final_state, void* dx, float* dweight, float* dbias,
+                        void* d_initial_state, void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token per sequence: x, y [num_seqs, C]; state_out is the state after the
+ * token and may be state_in itself (NULL: zero), but must not otherwise overlap
+ * it.  num_seqs = 0 enqueues nothing. */
+kda_status kda_conv_decode(const kda_conv_config* cfg, int32_t num_seqs, const void* x, const void* weight,
+                           const void* bias, const void* state_in, void* state_out, void* y, void* stream);
+
+/* kda_selective_config.flags */
+#define KDA_SELECTIVE_SOFTPLUS 1u /* dt = softplus(dt + dt_bias), else dt + dt_bias */
+
+typedef struct kda_selective_config {
+    int32_t C;         /* channels                                             */
+    int32_t S;         /* state entries of a channel: 8, 16 or 32              */
+    int32_t G;         /* groups of channels with B and C of their own; divides C */
+    int32_t in_dtype;  /* kda_dtype of x, dt, B, C, z, dy                      */
+    int32_t out_dtype; /* kda_dtype of y, dx, ddt, dB, dC, dz                  */
+    uint32_t flags;    /* KDA_SELECTIVE_*                                      */
+    int64_t x_stride;  /* of the rows of x, dt, z: 0: C                        */
+    int64_t dt_stride;
+    int64_t z_stride;
+    int64_t b_stride;  /* of the rows of B, C: 0: G S; 16-byte multiples       */
+    int64_t c_stride;
+} kda_selective_config;
+
+/* Fill *cfg with defaults: fp32/fp32, softplus, rows without gaps. */
+void kda_selective_config_init(kda_selective_config* cfg, int32_t C, int32_t S, int32_t G);
+
+/* Selective scan.  Per document and channel, with a state h of S fp32 entries:
+ *     dt_t = softplus(dt_t + dt_bias)                      (KDA_SELECTIVE_SOFTPLUS)
+ *     h_t  = exp(dt_t A) h_{t-1} + dt_t x_t B_t
+ *     y_t  = (sum_n C_t[n] h_t[n] + D x_t) silu(z_t)
+ *   x, dt, z, y : [total_tokens, C]  (z NULL: no gate)
+ *   B, C   : [total_tokens, G, S]; channel c reads group c / (C / G)
+ *   A      : fp32 [C, S]      D, dt_bias : fp32 [C] or NULL (0)
+ *   states : fp32 [num_seqs, C, S]
+ * dt A <= 0 is meant (decays); larger ones work as long as the decays over a
+ * document stay in range.  Everything inside is fp32.  Infinities and NaN reach
+ * what depends on them by the recurrence and nothing else (dA, dD and dt_bias's
+ * gradient are sums over all tokens); which of the two a result is, is open.
+ * Documents are cut into segments where that fills the GPU (a rule on the config
+ * and the sizes): own sums first, then a carry, then the walks; the workspace
+ * holds the segments' states (0 bytes where nothing is cut, or for an invalid
+ * config or sizes).  initial_state and final_state must not overlap. */
+size_t kda_selective_fwd_workspace_size(const kda_selective_config* cfg, int64_t total_tokens, int32_t num_seqs);
+size_t kda_selective_bwd_workspace_size(const kda_selective_config* cfg, int64_t total_tokens, int32_t num_seqs);
+kda_status kda_selective_fwd(const kda_selective_config* cfg, int64_t total_tokens, int32_t num_seqs, const void* x,
+                             const void* dt, const float* A, const void* B, const void* C, const float* D,
+                             const void* z, const float* dt_bias, const int32_t* cu_seqlens,
+                             const float* initial_state, void* y, float* final_state, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/* Backward of kda_selective_fwd for the loss <dy, y> + <dS_final, final_state>,
+ * from the forward's inputs.  dy : [total_tokens, C], in_dtype.  Outputs: dx,
+ * ddt (of dt as given), dz [total_tokens, C] and dB, dC [total_tokens, G, S] in
+ * out_dtype; dA [C, S], dD [C], ddt_bias [C] in fp32 (dD, ddt_bias may be NULL; dz
+ * is not used without z); d_initial_state fp32 or NULL, which must not overlap
+ * initial_state or dS_final. */
+kda_status kda_selective_bwd(const kda_selective_config* cfg, int64_t total_tokens, int32_t num_seqs, const void* x,
+                             const void* dt, const float* A, const void* B, const void* C, const float* D,
+                             const void* z, const float* dt_bias, const int32_t* cu_seqlens,
+                             const float* initial_state, const void* dy, const float* dS_final, void* dx, void* ddt,
+                             float* dA, void* dB, void* dC, float* dD, void* dz, float* ddt_bias,
+                             float* d_initial_state, void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token per sequence on a resident state, as kda_decode: x, dt, z, y
+ * [num_seqs, C], B, C [num_seqs, G, S]; state_in (NULL: zero), state_out (may be
+ * state_in itself, must not otherwise overlap it).  num_seqs = 0 enqueues
+ * nothing. */
+kda_status kda_selective_decode(const kda_selective_config* cfg, int32_t num_seqs, const void* x, const void* dt,
+                                const float* A, const void* B, const void* C, const float* D, const void* z,
+                                const float* dt_bias, const float* state_in, float* state_out, void* y,
+                                void* stream);
+
 /* Static description of a status code. */
 const char* kda_status_string(kda_status s);
 /* Thread-local description of the last failure on this thread ("" if none). */
