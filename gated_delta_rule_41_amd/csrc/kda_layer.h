@@ -7,7 +7,10 @@
 namespace kda {
 
 constexpr int kLayerThreads = 256;   // 4 wave64
-constexpr int selective_kept(int S) { return S == 32 ? 4 : 8; }   // tokens whose states a lane of the selective backward holds
+// Tokens between the states that the selective backward keeps, whose own states a lane then holds: S x (6 + 1) registers
+// at S = 16; 7 and 8 spill, 4 with the decays kept beside the states moves half as much again (1182 us a call for
+// 4 x 4096 tokens x 4096 channels, where 6 take 1109).
+constexpr int selective_kept(int S) { return S == 32 ? 4 : 6; }
 
 // ---------------------------------------------------------------- norm
 struct NormParams {
@@ -59,16 +62,16 @@ struct SelectiveParams {
     void* y;
     float* sfinal;          // [N,C,S] or nullptr
     // segments: own sums, replaced by the entering states; sums of dt
-    float* seg;             // [slots,C,S]
+    float* seg;             // [slots,S/4,C,4]
     float* sdt;             // [slots,C]
     // backward
     const void* dy;
     const float* dsf;       // [N,C,S] or nullptr
-    float* rseg;            // [slots,C,S]: likewise from the ends, gradients of the states
-    float* border;          // [borders,C,S] own states before every kept block of tokens
+    float* rseg;            // [slots,S/4,C,4]: likewise from the ends, gradients of the states
+    float* border;          // [borders,S/4,C,4] own states before every kept block of tokens
     float* bdt;             // [borders,C] sums of dt up to there
     float* bc_part;         // [T,waves,2,S] a wave's share of dB, dC
-    float* par_part;        // [slots,C,S+2] a segment's dA, dD, dbias
+    float* par_part;        // [slots,S+2,C] a segment's dA, dD, dbias
     void* dx;
     void* ddt;
     float* dA;

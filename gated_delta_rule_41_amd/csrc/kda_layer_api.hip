@@ -131,9 +131,14 @@ kda_status check_selective(const kda_selective_config* c) {
 }
 int32_t group_waves(const kda_selective_config* c) { return (c->C / c->G + 63) / 64; }
 
-// Waves that a launch aims for: two a SIMD.
-constexpr int64_t kSelectiveWaves = 2048;
-constexpr int64_t kSelectiveLeast = 64;     // tokens; a multiple of the kept blocks
+// Segments are short: their waves even out over the compute units, and a document's latency is a segment's
+// walk and the steps of its carry.  Tokens a segment and us (37 ragged documents, 16411 tokens x 4096 channels;
+// 131083 x 512; backward of 4 x 4096 x 4096):  48: 488, 490, 1429;  96: 467, 458, 1389;  144: 500, 494, 1484;
+// 528: 822, 605, 2572.  kSelectiveWaves makes that about 96.  Short streams: a backward of 1003 tokens x 200
+// channels takes 64 us at 12, 82 at 24 and 129 at 48; the root is where a token's walk (0.8 us alone) and its
+// share of the carry (0.05 us a segment) are equal.
+constexpr int64_t kSelectiveWaves = 10922;
+constexpr int64_t kSelectiveUnit = 12;      // tokens; a multiple of the kept blocks
 struct SelectivePlan {
     int64_t len, slots, borders;
     bool cut;
@@ -143,9 +148,9 @@ struct SelectivePlan {
 SelectivePlan selective_plan(const kda_selective_config* c, int64_t T, int32_t N, bool backward) {
     SelectivePlan p;
     memset(&p, 0, sizeof p);
-    auto up = [](int64_t x) { return std::max(kSelectiveLeast, (x + kSelectiveLeast - 1) / kSelectiveLeast * kSelectiveLeast); };
+    auto up = [](int64_t x) { return std::max(kSelectiveUnit, (x + kSelectiveUnit - 1) / kSelectiveUnit * kSelectiveUnit); };
     const int64_t waves = (int64_t)group_waves(c) * c->G;
-    p.len = up(T * waves / kSelectiveWaves);
+    p.len = up(std::max(T * waves / kSelectiveWaves, (int64_t)sqrt((double)T / 16)));
     p.cut = T > p.len;
     if (!p.cut) p.len = up(T);
     p.slots = layer_slots(T, N, (int32_t)p.len);

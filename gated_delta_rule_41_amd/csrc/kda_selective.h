@@ -32,15 +32,41 @@ template <typename T, int S> struct UniformRow {
     }
 };
 
+// Rows of B (or C) one after another from `p`, `step` elements apart; the last of `left` rows is not passed.  Rows that fit
+// eight scalar registers are loaded one token ahead; longer ones would push others out.
+template <typename T, int S> struct UniformRows {
+    static constexpr bool kAhead = S * sizeof(T) <= 32;
+    const T* p;
+    int64_t step;
+    UniformRow<T, S> row;
+    __device__ __forceinline__ UniformRows(const T* first, int64_t step_) : p(first), step(step_) {
+        if constexpr (kAhead) row.load(p);
+    }
+    __device__ __forceinline__ UniformRow<T, S> next(bool more) {
+        UniformRow<T, S> now;
+        if constexpr (kAhead) {
+            now = row;
+            if (more) p += step;
+            row.load(p);
+        } else {
+            now.load(p);
+            if (more) p += step;
+        }
+        return now;
+    }
+};
+
 // A wave's channels: `c` of a lane is clamped to its group, `valid` says whether it is its own.
 struct Channels {
-    int group, c;
+    int group;
+    unsigned c;
     bool valid;
     __device__ __forceinline__ Channels(const SelectiveParams& p, int wave) {
         const int per = p.C / p.G, in = (wave % p.group_waves) * 64 + (int)(threadIdx.x & 63);
         group = wave / p.group_waves;
         valid = in < per;
         c = group * per + (valid ? in : per - 1);
+        __builtin_assume(c < (1u << 20));     // the host's limit: offsets of a lane fit 32 bits
     }
 };
 
@@ -59,6 +85,22 @@ template <int S> __device__ __forceinline__ void store_entries(float* p, const f
         *reinterpret_cast<f32x4*>(p + n) = x;
     }
 }
+// States between launches lie four entries of all channels side by side, [S / 4][C][4], so that a wave moves whole lines.
+template <int S> __device__ __forceinline__ void load_kept(float (&v)[S], const float* p, int64_t slot, int C, unsigned c) {
+#pragma unroll
+    for (int n = 0; n < S; n += 4) {
+        const f32x4 x = reinterpret_cast<const f32x4*>(p + (slot * (S / 4) + n / 4) * C * 4)[c];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[n + j] = x[j];
+    }
+}
+template <int S> __device__ __forceinline__ void store_kept(float* p, int64_t slot, int C, unsigned c, const float (&v)[S]) {
+#pragma unroll
+    for (int n = 0; n < S; n += 4) {
+        const f32x4 x = {v[n], v[n + 1], v[n + 2], v[n + 3]};
+        reinterpret_cast<f32x4*>(p + (slot * (S / 4) + n / 4) * C * 4)[c] = x;
+    }
+}
 // A in units of log 2, so that a decay is one multiply and one exponential.
 template <int S> __device__ __forceinline__ void load_A(float (&A2)[S], const float* A) {
     load_entries<S>(A2, A);
@@ -66,9 +108,18 @@ template <int S> __device__ __forceinline__ void load_A(float (&A2)[S], const fl
     for (int n = 0; n < S; ++n) A2[n] *= kLog2e;
 }
 
+// Element c of a row at a uniform address: one scalar base, a 32-bit offset a lane.
+template <typename T> __device__ __forceinline__ T row_at(const T* row, unsigned c) { return row[c]; }
+__device__ __forceinline__ void row_put(void* base, int64_t row_start, unsigned c, float x, bool as_bf16) {
+    if (as_bf16) ((bf16*)base + row_start)[c] = (bf16)x;
+    else ((float*)base + row_start)[c] = x;
+}
+
 __device__ __forceinline__ float step_size(float raw, float bias, bool soft) {
     const float v = raw + bias;
-    return soft ? softplus(v) : v;
+    float s = softplus(v);
+    asm("" : "+v"(s));                        // a select instead of a branch
+    return soft ? s : v;
 }
 
 }  // namespace kda

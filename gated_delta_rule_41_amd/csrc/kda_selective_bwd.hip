@@ -3,15 +3,23 @@
 //     dx_t = dt_t (e_t . B_t) + D dy'_t,              dB_t = sum_c dt_t x_t e_t,  dC_t = sum_c dy'_t h_t
 //     d(dt_t) = x_t (e_t . B_t) + A . m_t,            m_t = e^{dt_t A} e_t h_{t-1},  dA = sum_t dt_t m_t
 // A wave walks a segment backwards in blocks of K tokens: from the kept state before the block
-// it forms the block's states in registers, then goes back over them with e.  A channel is a
+// it forms the block's states in registers, then goes back over them with e.  In a block that the
+// document ends in, the tokens behind it are its last with dt = dy = 0, which move neither h nor e,
+// and whose outputs are dropped; there is no branch around a token.  A channel is a
 // lane (kda_selective.h), so sums over the state's entries stay in a lane, and dB and dC are sums
 // over the lanes of a wave; the waves' shares are added by a last launch.
 #include "kda_selective.h"
 
 namespace kda {
 
-__device__ __forceinline__ void swap32(float& a, float& b) { asm("s_nop 1\n\tv_permlane32_swap_b32 %0, %1" : "+v"(a), "+v"(b)); }
-__device__ __forceinline__ void swap16(float& a, float& b) { asm("s_nop 1\n\tv_permlane16_swap_b32 %0, %1" : "+v"(a), "+v"(b)); }
+// Exchanges the upper 32 lanes of a[i] with the lower of b[i] (or odd rows of 16 with even ones), for two pairs; the wait
+// is for the values' own instructions.
+__device__ __forceinline__ void swap32(float& a0, float& b0, float& a1, float& b1) {
+    asm("s_nop 1\n\tv_permlane32_swap_b32 %0, %1\n\tv_permlane32_swap_b32 %2, %3" : "+v"(a0), "+v"(b0), "+v"(a1), "+v"(b1));
+}
+__device__ __forceinline__ void swap16(float& a0, float& b0, float& a1, float& b1) {
+    asm("s_nop 1\n\tv_permlane16_swap_b32 %0, %1\n\tv_permlane16_swap_b32 %2, %3" : "+v"(a0), "+v"(b0), "+v"(a1), "+v"(b1));
+}
 
 // One halving: lanes with `bit` set take the sums of the upper half of v, the others of the lower;
 // CTRL pairs each lane with one whose bit differs.
@@ -27,14 +35,16 @@ template <int V, int CTRL> __device__ __forceinline__ void halve(float (&v)[V], 
 // Sums of S values over the 64 lanes: lane l returns the one of value l S / 64.
 template <int S> __device__ __forceinline__ float lane_sums(float (&v)[S]) {
 #pragma unroll
-    for (int i = 0; i < S / 2; ++i) {
-        swap32(v[i], v[i + S / 2]);
+    for (int i = 0; i < S / 2; i += 2) {
+        swap32(v[i], v[i + S / 2], v[i + 1], v[i + 1 + S / 2]);
         v[i] += v[i + S / 2];
+        v[i + 1] += v[i + 1 + S / 2];
     }
 #pragma unroll
-    for (int i = 0; i < S / 4; ++i) {
-        swap16(v[i], v[i + S / 4]);
+    for (int i = 0; i < S / 4; i += 2) {
+        swap16(v[i], v[i + S / 4], v[i + 1], v[i + 1 + S / 4]);
         v[i] += v[i + S / 4];
+        v[i + 1] += v[i + 1 + S / 4];
     }
     halve<S, 0x140>(v, S / 4, 8);                 // mirrored in 16 lanes
     if constexpr (S >= 16) halve<S, 0x141>(v, S / 8, 4);   // mirrored in 8
@@ -44,9 +54,19 @@ template <int S> __device__ __forceinline__ float lane_sums(float (&v)[S]) {
     return v[0] + dpp<0xb1>(v[0]);                // lanes 1, 0, 3, 2
 }
 
-template <typename T, int S>
+// The kernel's parameters, read again where they are used: held in scalar registers from the start, they would push
+// out others.
+typedef const __attribute__((address_space(4))) SelectiveParams* ParamsAgain;
+__device__ __forceinline__ ParamsAgain params_again() {
+    ParamsAgain q = (ParamsAgain)__builtin_amdgcn_kernarg_segment_ptr();
+    asm("" : "+s"(q));
+    return q;
+}
+
+template <typename T, int S, bool GATED>
 __global__ __launch_bounds__(kLayerThreads, S == 32 ? 1 : 2) void selective_grads_kernel(SelectiveParams p) {
     constexpr int K = selective_kept(S);
+    __shared__ f32x4 enters[4 * (S / 4) * 64];    // the states that enter the waves' segments
     const Segment s = find_segment(p.cu, p.N, p.seqlen, p.T, p.len, blockIdx.x);
     const int wave = __builtin_amdgcn_readfirstlane((int)(blockIdx.y * 4 + (threadIdx.x >> 6)));
     if (wave >= p.waves) return;
@@ -54,77 +74,89 @@ __global__ __launch_bounds__(kLayerThreads, S == 32 ? 1 : 2) void selective_grad
     const int lane = threadIdx.x & 63;
     float A2[S], g[S], dA[S], dD = 0.f, dbias = 0.f;
     load_A<S>(A2, p.A + (int64_t)ch.c * S);
-    const int64_t state = ((int64_t)s.n * p.C + ch.c) * S, slot = ((int64_t)blockIdx.x * p.C + ch.c) * S;
+    const int64_t state = ((int64_t)s.n * p.C + ch.c) * S;
 #pragma unroll
     for (int n = 0; n < S; ++n) { g[n] = 0.f; dA[n] = 0.f; }
-    const float* enter = s.j > 0 ? p.seg + slot : p.s0 ? p.s0 + state : nullptr;
-    const float* leave = !s.last ? p.rseg + slot : p.dsf ? p.dsf + state : nullptr;
     if (s.begin < s.end || s.last) {
-        if (leave) load_entries<S>(g, leave);
+        if (!s.last) load_kept<S>(g, p.rseg, blockIdx.x, p.C, ch.c);
+        else if (p.dsf) load_entries<S>(g, p.dsf + state);
         const float bias = p.bias ? p.bias[ch.c] : 0.f, skip = p.D ? p.D[ch.c] : 0.f;
-        const T* x = (const T*)p.x + ch.c;
-        const T* dt = (const T*)p.dt + ch.c;
-        const T* dy = (const T*)p.dy + ch.c;
-        const T* z = p.z ? (const T*)p.z + ch.c : dy;
-        const int64_t z_stride = p.z ? p.z_stride : p.C;
-        const T* B = (const T*)p.B + (int64_t)ch.group * S;
-        const T* C = (const T*)p.Cm + (int64_t)ch.group * S;
-        const int64_t blocks = (s.end - s.begin + K - 1) / K, first = s.lo / K + s.n + (s.begin - s.lo) / K;
-        for (int64_t i = blocks - 1; i >= 0; --i) {
-            const int64_t t0 = s.begin + i * K;
-            const int count = (int)(s.end - t0 < K ? s.end - t0 : K);
+        // What a block's forward walk begins with, asked for while the block before it is on its way back and
+        // most of that one's states are no longer needed.  Nothing is kept before a segment's first block.
+        T nx[K], nd[K];
+        float own[S], own_dt;
+        auto ahead = [&](const int64_t t0, const int count) {
+            const ParamsAgain q = params_again();
+            const T* x = (const T*)q->x + t0 * q->x_stride;
+            const T* dt = (const T*)q->dt + t0 * q->dt_stride;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                nx[k] = row_at(x, ch.c);
+                nd[k] = row_at(dt, ch.c);
+                if (k + 1 < count) { x += q->x_stride; dt += q->dt_stride; }
+            }
+            const int64_t at = s.lo / K + s.n + (t0 - s.lo) / K;
+            load_kept<S>(own, q->border, at, q->C, ch.c);
+            own_dt = (q->bdt + at * q->C)[ch.c];
+        };
+        f32x4* const enter = enters + (threadIdx.x >> 6) * (S / 4) * 64 + lane;
+        // the block of `count` tokens from t0 on
+        auto block = [&](auto whole, const int64_t t0, const int count) {
             float h[K + 1][S], d[K];
             T tx[K], td[K], tg[K], tz[K];
+            {
+                const ParamsAgain q = params_again();
+                const T* dy = (const T*)q->dy + t0 * q->C;
+                const T* z = GATED ? (const T*)q->z + t0 * q->z_stride : dy;
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    tx[k] = nx[k];
+                    td[k] = nd[k];
+                    tg[k] = row_at(dy, ch.c);
+                    if (GATED) tz[k] = row_at(z, ch.c);
+                    if (whole.value || k + 1 < count) { dy += q->C; z += GATED ? q->z_stride : 0; }
+                }
+            }
+            const bool kept = t0 > s.begin;       // own state, and what is left of the entering one
+#pragma unroll
+            for (int n = 0; n < S; ++n) {
+                const float e = enter[n / 4 * 64][n & 3];
+                h[0][n] = kept ? __builtin_fmaf(fast_exp2(own_dt * A2[n]), e, own[n]) : e;
+            }
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                const int64_t t = t0 + (k < count ? k : count - 1);
-                tx[k] = x[t * p.x_stride];
-                td[k] = dt[t * p.dt_stride];
-                tg[k] = dy[t * p.C];
-                tz[k] = z[t * z_stride];
-            }
-            if (enter) load_entries<S>(h[0], enter);
-            else
-#pragma unroll
-                for (int n = 0; n < S; ++n) h[0][n] = 0.f;
-            if (i > 0) {                          // own state, and what is left of the entering one
-                const int64_t at = (first + i) * p.C + ch.c;
-                float own[S];
-                load_entries<S>(own, p.border + at * S);
-                const float sum = p.bdt[at];
-#pragma unroll
-                for (int n = 0; n < S; ++n) h[0][n] = enter ? __builtin_fmaf(fast_exp2(sum * A2[n]), h[0][n], own[n]) : own[n];
-            }
-            UniformRow<T, S> nb, nc;
-            nb.load(B + t0 * p.b_stride);
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-                if (k >= count) break;
-                const UniformRow<T, S> b = nb;
-                nb.load(B + (t0 + (k + 1 < count ? k + 1 : k)) * p.b_stride);   // the last stays for the way back
                 d[k] = step_size(to_f32(td[k]), bias, p.softplus);
+                if (!whole.value) d[k] = k < count ? d[k] : 0.f;
+            }
+            UniformRows<T, S> B((const T*)p.B + t0 * p.b_stride + (int64_t)ch.group * S, p.b_stride);
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                __builtin_amdgcn_sched_barrier(0);
+                const UniformRow<T, S> b = B.next(whole.value ? k + 1 < K : k + 1 < count);
                 const float w = ch.valid ? d[k] * to_f32(tx[k]) : 0.f;
 #pragma unroll
                 for (int n = 0; n < S; ++n) h[k + 1][n] = __builtin_fmaf(fast_exp2(d[k] * A2[n]), h[k][n], w * b[n]);
             }
-            nc.load(C + (t0 + count - 1) * p.c_stride);
+            B.step = -p.b_stride;                 // it stands at the block's last token
+            asm("" : "+s"(B.p));                  // rows are loaded again, not kept from above
+            int64_t t = t0 + count - 1;
+            const ParamsAgain r = params_again();
+            UniformRows<T, S> C((const T*)r->Cm + t * r->c_stride + (int64_t)ch.group * S, -r->c_stride);
 #pragma unroll
             for (int k = K - 1; k >= 0; --k) {
-                if (k >= count) continue;
-                const int64_t t = t0 + k;
-                const UniformRow<T, S> b = nb, c = nc;
-                const int64_t ahead = k > 0 ? t - 1 : t;
-                nb.load(B + ahead * p.b_stride);
-                nc.load(C + ahead * p.c_stride);
-                const float xv = to_f32(tx[k]), w = ch.valid ? d[k] * xv : 0.f;
-                float dyv = ch.valid ? to_f32(tg[k]) : 0.f;
-                if (p.z) {
+                const bool real = whole.value || k < count;
+                __builtin_amdgcn_sched_barrier(0);    // or rows of many tokens are loaded at once and spill
+                const UniformRow<T, S> b = B.next(real && k > 0), c = C.next(real && k > 0);
+                float dk = d[k];
+                asm("" : "+v"(dk));               // the decays are formed again: kept from above they would take S registers a token
+                const float xv = to_f32(tx[k]), w = ch.valid ? dk * xv : 0.f;
+                float dyv = ch.valid && real ? to_f32(tg[k]) : 0.f, dz = 0.f;
+                if constexpr (GATED) {
                     const float zv = to_f32(tz[k]), sig = sigmoid_fast(zv);
                     float y[4] = {skip * xv, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int n = 0; n < S; ++n) y[n & 3] = __builtin_fmaf(h[k + 1][n], c[n], y[n & 3]);
-                    const float o = (y[0] + y[1]) + (y[2] + y[3]);
-                    if (ch.valid) store_out(p.dz, t * p.C + ch.c, dyv * o * sig * __builtin_fmaf(zv, 1.f - sig, 1.f), p.out_bf16);
+                    dz = dyv * ((y[0] + y[1]) + (y[2] + y[3])) * sig * __builtin_fmaf(zv, 1.f - sig, 1.f);
                     dyv *= zv * sig;
                 }
                 float v[S], du[4] = {0.f, 0.f, 0.f, 0.f}, dd[4] = {0.f, 0.f, 0.f, 0.f};
@@ -136,28 +168,53 @@ __global__ __launch_bounds__(kLayerThreads, S == 32 ? 1 : 2) void selective_grad
                     const float e = __builtin_fmaf(dyv, c[n], g[n]);
                     v[n] = w * e;
                     du[n & 3] = __builtin_fmaf(e, b[n], du[n & 3]);
-                    g[n] = fast_exp2(d[k] * A2[n]) * e;
+                    g[n] = fast_exp2(dk * A2[n]) * e;
                     const float m = g[n] * h[k][n];
                     dd[n & 3] = __builtin_fmaf(m, A2[n], dd[n & 3]);
-                    dA[n] = __builtin_fmaf(m, d[k], dA[n]);
+                    dA[n] = __builtin_fmaf(m, dk, dA[n]);
                 }
                 const float dB = lane_sums<S>(v);
-                constexpr int R = 64 / S;         // lanes with the same sum
-                if ((lane & (R - 1)) < 2) {
-                    float* part = p.bc_part + (t * p.waves + wave) * (2 * S);
-                    part[(lane & 1) * S + lane / R] = lane & 1 ? dC : dB;
-                }
                 const float dus = (du[0] + du[1]) + (du[2] + du[3]);
                 float ddt = __builtin_fmaf(dus, xv, ((dd[0] + dd[1]) + (dd[2] + dd[3])) * kLn2);
-                if (p.softplus) ddt *= sigmoid_fast(to_f32(td[k]) + bias);
+                if (r->softplus) ddt *= sigmoid_fast(to_f32(td[k]) + bias);
+                const float dx = __builtin_fmaf(skip, dyv, dus * dk);
                 dD = __builtin_fmaf(dyv, xv, dD);
+                if (k == 1) ahead(kept ? t0 - K : t0, kept ? K : count);
+                if (!real) continue;
                 dbias += ddt;
+                float* part = r->bc_part + (t * r->waves + wave) * (2 * S);
+                constexpr int R = 64 / S;         // lanes with the same sum
+                if ((lane & (R - 1)) < 2) part[(lane & 1) * S + lane / R] = lane & 1 ? dC : dB;
                 if (ch.valid) {
-                    store_out(p.ddt, t * p.C + ch.c, ddt, p.out_bf16);
-                    store_out(p.dx, t * p.C + ch.c, __builtin_fmaf(skip, dyv, dus * d[k]), p.out_bf16);
+                    const int64_t out = t * r->C;
+                    if (r->out_bf16) {
+                        ((bf16*)r->dx + out)[ch.c] = (bf16)dx;
+                        ((bf16*)r->ddt + out)[ch.c] = (bf16)ddt;
+                        if (GATED) ((bf16*)r->dz + out)[ch.c] = (bf16)dz;
+                    } else {
+                        ((float*)r->dx + out)[ch.c] = dx;
+                        ((float*)r->ddt + out)[ch.c] = ddt;
+                        if (GATED) ((float*)r->dz + out)[ch.c] = dz;
+                    }
                 }
+                --t;
             }
+        };
+        {
+            float e[S];
+            if (s.j > 0) load_kept<S>(e, p.seg, blockIdx.x, p.C, ch.c);
+            else if (p.s0) load_entries<S>(e, p.s0 + state);
+            else
+#pragma unroll
+                for (int n = 0; n < S; ++n) e[n] = 0.f;
+#pragma unroll
+            for (int n = 0; n < S; n += 4) enter[n / 4 * 64] = f32x4{e[n], e[n + 1], e[n + 2], e[n + 3]};   // a wave's own
         }
+        int64_t t0 = s.begin + (s.end - s.begin) / K * K;
+        if (t0 < s.end) ahead(t0, (int)(s.end - t0));
+        else if (s.begin < s.end) ahead(t0 - K, K);
+        if (t0 < s.end) block(std::false_type(), t0, (int)(s.end - t0));
+        for (t0 -= K; t0 >= s.begin; t0 -= K) block(std::true_type(), t0, K);
         if (s.j == 0 && p.ds0 && ch.valid) store_entries<S>(p.ds0 + state, g);
     }
     if (!ch.valid) return;
@@ -185,7 +242,9 @@ __global__ __launch_bounds__(kLayerThreads) void selective_bc_kernel(SelectivePa
 
 // ---------------------------------------------------------------- launches
 template <typename T, int S> static void grads_launch(const SelectiveParams& p, hipStream_t stream) {
-    hipLaunchKernelGGL((selective_grads_kernel<T, S>), dim3((unsigned)p.slots, (unsigned)((p.waves + 3) / 4)), dim3(kLayerThreads), 0, stream, p);
+    const dim3 grid((unsigned)p.slots, (unsigned)((p.waves + 3) / 4));
+    if (p.z) hipLaunchKernelGGL((selective_grads_kernel<T, S, true>), grid, dim3(kLayerThreads), 0, stream, p);
+    else hipLaunchKernelGGL((selective_grads_kernel<T, S, false>), grid, dim3(kLayerThreads), 0, stream, p);
 }
 template <typename T> static void grads_size(const SelectiveParams& p, int S, hipStream_t stream) {
     if (S == 8) grads_launch<T, 8>(p, stream);

@@ -10,7 +10,7 @@ namespace kda {
 
 template <typename T, int S>
 __global__ __launch_bounds__(kLayerThreads) void selective_out_kernel(SelectiveParams p) {
-    constexpr int U = 4;
+    constexpr int U = 4;                          // tokens a block: their loads are one block ahead
     const Segment s = find_segment(p.cu, p.N, p.seqlen, p.T, p.len, blockIdx.x);
     const int wave = __builtin_amdgcn_readfirstlane((int)(blockIdx.y * 4 + (threadIdx.x >> 6)));
     if ((s.begin >= s.end && !s.last) || wave >= p.waves) return;
@@ -18,60 +18,65 @@ __global__ __launch_bounds__(kLayerThreads) void selective_out_kernel(SelectiveP
     float A2[S], h[S];
     load_A<S>(A2, p.A + (int64_t)ch.c * S);
     const int64_t state = ((int64_t)s.n * p.C + ch.c) * S;
-    if (s.j > 0) load_entries<S>(h, p.seg + ((int64_t)blockIdx.x * p.C + ch.c) * S);
+    if (s.j > 0) load_kept<S>(h, p.seg, blockIdx.x, p.C, ch.c);
     else if (p.s0) load_entries<S>(h, p.s0 + state);
     else
 #pragma unroll
         for (int n = 0; n < S; ++n) h[n] = 0.f;
     if (s.begin < s.end) {
         const float bias = p.bias ? p.bias[ch.c] : 0.f, skip = p.D ? p.D[ch.c] : 0.f;
-        const T* x = (const T*)p.x + ch.c;
-        const T* dt = (const T*)p.dt + ch.c;
-        const T* z = p.z ? (const T*)p.z + ch.c : x;
+        const T* x = (const T*)p.x + s.begin * p.x_stride;
+        const T* dt = (const T*)p.dt + s.begin * p.dt_stride;
         const int64_t z_stride = p.z ? p.z_stride : p.x_stride;
-        const T* B = (const T*)p.B + (int64_t)ch.group * S;
-        const T* C = (const T*)p.Cm + (int64_t)ch.group * S;
+        const T* z = p.z ? (const T*)p.z + s.begin * z_stride : x;
+        UniformRows<T, S> B((const T*)p.B + s.begin * p.b_stride + (int64_t)ch.group * S, p.b_stride);
+        UniformRows<T, S> C((const T*)p.Cm + s.begin * p.c_stride + (int64_t)ch.group * S, p.c_stride);
+        int64_t out = s.begin * p.C;
         T nx[U], nd[U], nz[U];
-        auto load = [&](int64_t t) {
+        int left = (int)(s.end - s.begin);        // tokens from the block on
+        auto load = [&](int count) {              // the block at x, dt, z; rows behind the segment are its last
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int64_t at = t + u < s.end ? t + u : s.end - 1;
-                nx[u] = x[at * p.x_stride];
-                nd[u] = dt[at * p.dt_stride];
-                nz[u] = z[at * z_stride];
+                nx[u] = row_at(x, ch.c);
+                nd[u] = row_at(dt, ch.c);
+                nz[u] = row_at(z, ch.c);
+                if (u + 1 < count) { x += p.x_stride; dt += p.dt_stride; z += z_stride; }
             }
         };
-        load(s.begin);
-        UniformRow<T, S> nb, nc;
-        nb.load(B + s.begin * p.b_stride);
-        nc.load(C + s.begin * p.c_stride);
-        for (int64_t t = s.begin; t < s.end; t += U) {
-            T cx[U], cd[U], cz[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) { cx[u] = nx[u]; cd[u] = nd[u]; cz[u] = nz[u]; }
-            if (t + U < s.end) load(t + U);
+        load(left);
+        auto block = [&](auto whole, int count) {
+            float d[U], w[U], o[U];
+            T cx[U], cz[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                if (t + u >= s.end) break;
-                const UniformRow<T, S> b = nb, c = nc;
-                const int64_t at = t + u + 1 < s.end ? t + u + 1 : s.end - 1;
-                nb.load(B + at * p.b_stride);
-                nc.load(C + at * p.c_stride);
-                const float d = step_size(to_f32(cd[u]), bias, p.softplus), xv = to_f32(cx[u]), w = d * xv;
-                float y[4] = {skip * xv, 0.f, 0.f, 0.f};      // four sums, so that they need not wait for one another
+                d[u] = step_size(to_f32(nd[u]), bias, p.softplus);
+                w[u] = d[u] * to_f32(nx[u]);
+                cx[u] = nx[u];
+                cz[u] = nz[u];
+            }
+            if (whole.value ? left > U : false) load(left - U);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (!whole.value && u >= count) break;
+                const UniformRow<T, S> b = B.next(u + 1 < left), c = C.next(u + 1 < left);
+                float y[4] = {skip * to_f32(cx[u]), 0.f, 0.f, 0.f};   // four sums, so that they need not wait for one another
 #pragma unroll
                 for (int n = 0; n < S; ++n) {
-                    h[n] = __builtin_fmaf(fast_exp2(d * A2[n]), h[n], w * b[n]);
+                    h[n] = __builtin_fmaf(fast_exp2(d[u] * A2[n]), h[n], w[u] * b[n]);
                     y[n & 3] = __builtin_fmaf(h[n], c[n], y[n & 3]);
                 }
-                float o = (y[0] + y[1]) + (y[2] + y[3]);
-                if (p.z) {
-                    const float zv = to_f32(cz[u]);
-                    o *= zv * sigmoid_fast(zv);
-                }
-                if (ch.valid) store_out(p.y, (t + u) * p.C + ch.c, o, p.out_bf16);
+                o[u] = (y[0] + y[1]) + (y[2] + y[3]);
             }
-        }
+            if (p.z)
+#pragma unroll
+                for (int u = 0; u < U; ++u) o[u] *= to_f32(cz[u]) * sigmoid_fast(to_f32(cz[u]));
+            if (ch.valid)
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (whole.value || u < count) row_put(p.y, out + (int64_t)u * p.C, ch.c, o[u], p.out_bf16);
+        };
+        for (; left >= U; left -= U, out += (int64_t)U * p.C) block(std::true_type(), U);
+        if (left > 0) block(std::false_type(), left);
     }
     if (s.last && p.sfinal && ch.valid) store_entries<S>(p.sfinal + state, h);
 }
