@@ -87,16 +87,27 @@ int64_t row_stride(int64_t stride, int64_t width) { return stride ? stride : wid
 // From the first element to the last, in bytes.
 size_t extent(int64_t rows, int64_t stride, int64_t width, size_t es) { return rows > 0 ? ((size_t)(rows - 1) * stride + width) * es : 0; }
 
-// Tokens a strip.
-int32_t conv_len(const kda_conv_config* c, int64_t T) {
-    const int64_t per = c->C % 8 == 0 && row_stride(c->x_stride, c->C) % 8 == 0 ? c->C / 8 : c->C;
-    const int64_t share = T * per >> 18;
-    int32_t len = 8;
-    while (len < 64 && len < share) len *= 2;
-    return len;
+// Channels a thread: eight move whole 16-byte pieces, one gives small calls eight times the threads, each with an eighth
+// to do.  us of a forward and a backward, eight and one, width 4: bf16 1000 x 512 5.0, 16.0 and 4.0, 10.6;  1000 x 2048
+// 5.4, 18.6 and 5.7, 13.3;  16000 x 333 7.8, 29.2 and 8.6, 27.1;  1000 x 8192 7.3, 27.1 and 9.5, 32.3;  fp32 4000 x 2048
+// 16.9, 36.5 and 15.5, 32.9;  16000 x 2048 54.1, 93.5 and 45.6, 106.8.
+bool conv_eight(const kda_conv_config* c, int64_t T) {
+    return c->C >= 8 && T * c->C >= (c->in_dtype == KDA_BF16 ? (int64_t)1 << 22 : (int64_t)1 << 24);
 }
-kda_status conv_plan(const kda_conv_config* c, int64_t T, int32_t N, int32_t* len, int64_t* slots) {
-    *len = conv_len(c, T);
+// Tokens a strip.  A strip begins with W - 1 rows and the taps, and in the backward ends with its sums; many strips
+// even out.  us for 8, 16, 32, 64, 96, 128, 192 tokens: forward of 16411 x 12288 168, 157, 167, 179, 191, 199, 203;
+// backward of 32768 x 4096 362, 263, 225, 182, 232, 166, 218, where 64 and 128 are two and one wave a SIMD's two
+// registers' worth, so strips there make whole rounds of 2048 waves.
+int32_t conv_len(const kda_conv_config* c, int64_t T, bool backward) {
+    const int64_t per = conv_eight(c, T) ? (c->C + 7) / 8 : c->C;
+    const int64_t share = T * per / (64 * 2048);      // tokens a wave in one round
+    if (share < 16) return share < 8 ? 8 : 16;
+    if (!backward) return 16;
+    const int64_t rounds = (share + 127) / 128;
+    return (int32_t)((share + rounds - 1) / rounds);
+}
+kda_status conv_plan(const kda_conv_config* c, int64_t T, int32_t N, bool backward, int32_t* len, int64_t* slots) {
+    *len = conv_len(c, T, backward);
     *slots = layer_slots(T, N, *len);
     return grid_fits(*slots, kLayerThreads) ? KDA_OK : fail(KDA_ERR_UNSUPPORTED, "num_seqs or total_tokens too large for one launch%s");
 }
@@ -311,16 +322,16 @@ kda_status kda_conv_fwd(const kda_conv_config* cfg, int64_t T, int32_t N, const 
     KDA_TRY(apart(sfinal, state, "final_state", s0, state));
     KDA_TRY(apart(y, ny, "y", x, extent(T, p.x_stride, p.C, es)));
     int64_t slots;
-    KDA_TRY(conv_plan(cfg, T, N, &p.len, &slots));
+    KDA_TRY(conv_plan(cfg, T, N, false, &p.len, &slots));
     p.x = x; p.weight = weight; p.bias = bias; p.cu = cu; p.s0 = s0; p.y = y; p.sfinal = sfinal;
-    p.T = T; p.N = N; p.seqlen = cu ? 0 : (int32_t)(T / N); p.slots = (int32_t)slots;
+    p.T = T; p.N = N; p.seqlen = cu ? 0 : (int32_t)(T / N); p.slots = (int32_t)slots; p.eight = conv_eight(cfg, T);
     return launched(launch_conv_fwd(p, cfg->width, cfg->in_dtype == KDA_BF16, (hipStream_t)stream));
 }
 
 size_t kda_conv_bwd_workspace_size(const kda_conv_config* cfg, int64_t T, int32_t N) {
     int32_t len;
     int64_t slots;
-    if (check_conv(cfg) != KDA_OK || check_sizes(T, N) != KDA_OK || conv_plan(cfg, T, N, &len, &slots) != KDA_OK) return 0;
+    if (check_conv(cfg) != KDA_OK || check_sizes(T, N) != KDA_OK || conv_plan(cfg, T, N, true, &len, &slots) != KDA_OK) return 0;
     return (size_t)slots * (cfg->width + 1) * cfg->C * sizeof(float);
 }
 
@@ -348,13 +359,13 @@ kda_status kda_conv_bwd(const kda_conv_config* cfg, int64_t T, int32_t N, const 
     KDA_TRY(apart(dx, nx, "dx", x, extent(T, p.x_stride, p.C, es)));
     KDA_TRY(apart(dx, nx, "dx", dy, (size_t)T * cfg->C * es));
     int64_t slots;
-    KDA_TRY(conv_plan(cfg, T, N, &p.len, &slots));
+    KDA_TRY(conv_plan(cfg, T, N, true, &p.len, &slots));
     const size_t need = kda_conv_bwd_workspace_size(cfg, T, N);
     if (workspace_bytes < need) return fail(KDA_ERR_WORKSPACE, "workspace too small%s");
     KDA_TRY(ptr(workspace, "workspace", true));
     p.x = x; p.weight = weight; p.bias = bias; p.cu = cu; p.s0 = s0; p.dy = dy; p.dsf = dsf; p.dx = dx; p.ds0 = ds0;
     p.part = (float*)workspace;
-    p.T = T; p.N = N; p.seqlen = cu ? 0 : (int32_t)(T / N); p.slots = (int32_t)slots;
+    p.T = T; p.N = N; p.seqlen = cu ? 0 : (int32_t)(T / N); p.slots = (int32_t)slots; p.eight = conv_eight(cfg, T);
     return launched(launch_conv_bwd(p, cfg->width, cfg->in_dtype == KDA_BF16, dw, db, (hipStream_t)stream));
 }
 

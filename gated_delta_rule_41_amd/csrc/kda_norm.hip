@@ -7,65 +7,44 @@
 
 namespace kda {
 
-// Columns of a thread: i-th group of eight side by side (VEC), or all of them TPR apart.
-template <int TPR, bool VEC> __device__ __forceinline__ int norm_col(int tid, int i, int j) {
-    return VEC ? (tid + TPR * i) * 8 + j : tid + TPR * (8 * i + j);
-}
-template <typename T, int TPR, int NC, bool VEC>
-__device__ __forceinline__ void norm_load(float (&v)[NC][8], const T* row, int tid, int C) {
-#pragma unroll
-    for (int i = 0; i < NC; ++i) {
-        if constexpr (VEC) {
-            const int c = norm_col<TPR, VEC>(tid, i, 0);
-            if (c < C) load8(v[i], row + c);
-            else
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int c = norm_col<TPR, VEC>(tid, i, j);
-                v[i][j] = c < C ? to_f32(row[c]) : 0.f;
-            }
-        }
-    }
-}
-template <int TPR, bool VEC>
-__device__ __forceinline__ void norm_store(void* base, int64_t at, int tid, int i, int C, const float (&v)[8], bool as_bf16) {
-    if constexpr (VEC) {
-        const int c = norm_col<TPR, VEC>(tid, i, 0);
-        if (c < C) store8_out(base, at + c, v, as_bf16);
+// A thread's i-th eight channels begin at (tid + TPR i) 8; a row's last eight may be fewer.
+template <int TPR> __device__ __forceinline__ int norm_col(int tid, int i) { return (tid + TPR * i) * 8; }
+template <typename T> __device__ __forceinline__ void norm_load8(float (&v)[8], const T* row, int c, int C) {
+    if (c + 8 <= C) {
+        load8(v, row + c);
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int c = norm_col<TPR, VEC>(tid, i, j);
-            if (c < C) store_out(base, at + c, v[j], as_bf16);
-        }
+        for (int j = 0; j < 8; ++j) v[j] = c + j < C ? to_f32(row[c + j]) : 0.f;
     }
 }
-template <int TPR, bool VEC>
-__device__ __forceinline__ void norm_weight(float (&w)[8], const NormParams& p, int tid, int i) {
+template <typename T, int TPR, int NC> __device__ __forceinline__ void norm_load(float (&v)[NC][8], const T* row, int tid, int C) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = 1.f;
-    if (!p.weight) return;
-    if constexpr (VEC) {
-        const int c = norm_col<TPR, VEC>(tid, i, 0);
-        if (c >= p.C) return;
-        if (p.weight_bf16) load8(w, (const bf16*)p.weight + c);
-        else load8(w, (const float*)p.weight + c);
+    for (int i = 0; i < NC; ++i) norm_load8(v[i], row, norm_col<TPR>(tid, i), C);
+}
+__device__ __forceinline__ void norm_store8(void* base, int64_t at, int c, int C, const float (&v)[8], bool as_bf16) {
+    if (c + 8 <= C) {
+        store8_out<true>(base, at + c, v, as_bf16);
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int c = norm_col<TPR, VEC>(tid, i, j);
-            if (c < p.C) w[j] = p.weight_bf16 ? to_f32(((const bf16*)p.weight)[c]) : ((const float*)p.weight)[c];
-        }
+        for (int j = 0; j < 8; ++j)
+            if (c + j < C) store_out(base, at + c + j, v[j], as_bf16);
+    }
+}
+__device__ __forceinline__ void norm_weight(float (&w)[8], const NormParams& p, int c) {
+    if (!p.weight) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = 1.f;
+    } else if (p.weight_bf16) {
+        norm_load8(w, (const bf16*)p.weight, c, p.C);
+    } else {
+        norm_load8(w, (const float*)p.weight, c, p.C);
     }
 }
 
 // Over the TPR threads of a row, the same value in each; `red` holds one value a wave.
 template <int TPR, typename V, typename F> __device__ __forceinline__ V row_reduce(V x, V* red, F f) {
 #pragma unroll
-    for (int m = 32; m; m >>= 1) x = f(x, __shfl_xor(x, m, 64));
+    for (int m = (TPR < 64 ? TPR : 64) / 2; m; m >>= 1) x = f(x, __shfl_xor(x, m, 64));
     if constexpr (TPR > 64) {
         constexpr int W = TPR / 64;
         __syncthreads();
@@ -93,7 +72,10 @@ __device__ __forceinline__ float odd_quotient(float p, float Q, float m, float i
     return __uint_as_float(b);
 }
 
-// mean(s^2) may leave fp32's range where s does not: such rows are summed again scaled by a power of two.
+// mean(s^2) may leave fp32's range where s does not: such rows are summed again scaled by a power of two, beside
+// which eps is nothing.
+constexpr float kNormShrink = 0x1p-80f;
+__device__ __forceinline__ bool norm_overflows(float sum) { return __builtin_expect(!(sum < __builtin_huge_valf()), 0); }
 template <int TPR, int NC> __device__ __forceinline__ float norm_rstd(const float (&v)[NC][8], const NormParams& p, float* red) {
     float sum = 0.f;
 #pragma unroll
@@ -101,49 +83,48 @@ template <int TPR, int NC> __device__ __forceinline__ float norm_rstd(const floa
 #pragma unroll
         for (int j = 0; j < 8; ++j) sum = __builtin_fmaf(v[i][j], v[i][j], sum);
     sum = row_reduce<TPR>(sum, red, Add());
-    if (__builtin_expect(!(sum < __builtin_huge_valf()), 0)) {
-        constexpr float k = 0x1p-80f;
+    if (norm_overflows(sum)) {
         sum = 0.f;
 #pragma unroll
         for (int i = 0; i < NC; ++i)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum = __builtin_fmaf(v[i][j] * k, v[i][j] * k, sum);
+            for (int j = 0; j < 8; ++j) sum = __builtin_fmaf(v[i][j] * kNormShrink, v[i][j] * kNormShrink, sum);
         sum = row_reduce<TPR>(sum, red, Add());
-        return k / sqrtf(sum / (float)p.C);      // eps is far below such a mean
+        return kNormShrink / sqrtf(sum / (float)p.C);
     }
     return 1.f / sqrtf(sum / (float)p.C + p.eps);
 }
 
-template <typename TI, typename TR, int TPR, int NC, bool VEC>
+template <typename TI, typename TR, int TPR, int NC>
 __global__ __launch_bounds__(TPR < kLayerThreads ? kLayerThreads : TPR) void norm_fwd_kernel(NormParams p) {
     constexpr int RPB = TPR < kLayerThreads ? kLayerThreads / TPR : 1;
-    __shared__ float red[TPR / 64];
+    __shared__ float red[TPR > 64 ? TPR / 64 : 1];
     const int tid = threadIdx.x % TPR;
     const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
-    if (row >= p.rows) return;                   // whole waves: a row of several waves is a workgroup of its own
+    if (row >= p.rows) return;                   // a row of several waves is a workgroup of its own
     const int64_t at = row * p.C;
     float v[NC][8];
-    norm_load<TI, TPR, NC, VEC>(v, (const TI*)p.x + at, tid, p.C);
+    norm_load<TI, TPR, NC>(v, (const TI*)p.x + at, tid, p.C);
     if (p.residual) {
         float r[NC][8];
-        norm_load<TR, TPR, NC, VEC>(r, (const TR*)p.residual + at, tid, p.C);
+        norm_load<TR, TPR, NC>(r, (const TR*)p.residual + at, tid, p.C);
 #pragma unroll
         for (int i = 0; i < NC; ++i)
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[i][j] = to_f32(from_f32<TR>(v[i][j] + r[i][j]));
         if (p.s)
 #pragma unroll
-            for (int i = 0; i < NC; ++i) norm_store<TPR, VEC>(p.s, at, tid, i, p.C, v[i], sizeof(TR) == 2);
+            for (int i = 0; i < NC; ++i) norm_store8(p.s, at, norm_col<TPR>(tid, i), p.C, v[i], sizeof(TR) == 2);
     }
     const float rstd = norm_rstd<TPR>(v, p, red);
     if (p.out < 2) {
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             float w[8];
-            norm_weight<TPR, VEC>(w, p, tid, i);
+            norm_weight(w, p, norm_col<TPR>(tid, i));
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[i][j] *= rstd * w[j];
-            norm_store<TPR, VEC>(p.y, at, tid, i, p.C, v[i], p.out == 1);
+            norm_store8(p.y, at, norm_col<TPR>(tid, i), p.C, v[i], p.out == 1);
         }
         return;
     }
@@ -151,7 +132,7 @@ __global__ __launch_bounds__(TPR < kLayerThreads ? kLayerThreads : TPR) void nor
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
         float w[8];
-        norm_weight<TPR, VEC>(w, p, tid, i);
+        norm_weight(w, p, norm_col<TPR>(tid, i));
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             v[i][j] *= w[j];
@@ -179,70 +160,152 @@ __global__ __launch_bounds__(TPR < kLayerThreads ? kLayerThreads : TPR) void nor
             word[j >> 2] |= pair << (8 * (j & 2));
         }
         if (!codes) word[0] = word[1] = 0;
-        if constexpr (VEC) {
-            const int c = norm_col<TPR, VEC>(tid, i, 0);
-            const u32x2 both = {word[0], word[1]};
-            if (c < p.C) *reinterpret_cast<u32x2*>(y + c) = both;
+        const int c = norm_col<TPR>(tid, i);
+        if (c + 8 <= p.C) {
+            typedef u32x2 __attribute__((aligned(1))) codes8;
+            __builtin_nontemporal_store(u32x2{word[0], word[1]}, reinterpret_cast<codes8*>(y + c));
         } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int c = norm_col<TPR, VEC>(tid, i, j);
-                if (c < p.C) y[c] = (uint8_t)(word[j >> 2] >> (8 * (j & 3)));
-            }
+            for (int j = 0; j < 8; ++j)
+                if (c + j < p.C) y[c + j] = (uint8_t)(word[j >> 2] >> (8 * (j & 3)));
         }
     }
 }
 
-// A workgroup goes over rows gridDim apart and keeps its sums for dw in registers.
-template <typename TI, typename TR, int TPR, int NC, bool VEC>
+// A row's groups as they lie in memory, to be asked for early.
+template <typename T, int TPR, int NC> struct NormRow {
+    Raw8<T> r[NC];
+    __device__ __forceinline__ void load(const T* row, int tid, int C) {
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const int c = norm_col<TPR>(tid, i);
+            if (c + 8 <= C) {
+                r[i].load(row + c);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) r[i].set(j, c + j < C ? row[c + j] : T(0.f));
+            }
+        }
+    }
+};
+
+struct Sums { float square, dot; };
+struct AddSums { __device__ Sums operator()(Sums a, Sums b) const { return {a.square + b.square, a.dot + b.dot}; } };
+template <int TPR> __device__ __forceinline__ Sums row_sums(Sums x, Sums* red) {
+#pragma unroll
+    for (int m = (TPR < 64 ? TPR : 64) / 2; m; m >>= 1) x = AddSums()(x, {__shfl_xor(x.square, m, 64), __shfl_xor(x.dot, m, 64)});
+    if constexpr (TPR > 64) {
+        constexpr int W = TPR / 64;
+        __syncthreads();
+        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;
+        __syncthreads();
+        x = red[0];
+#pragma unroll
+        for (int w = 1; w < W; ++w) x = AddSums()(x, red[w]);
+    }
+    return x;
+}
+
+// dx = rstd (w dy - s rstd^2 mean(w dy s)) + ds: both sums of a row come from one pass over it.  A workgroup goes over
+// rows gridDim apart and keeps its sums for dw in registers.  Up to two groups of eight channels a thread stay there as
+// well, the weights too, with the next row's s and dy and this one's ds on their way; rows of more channels are read
+// again from the caches.
+template <typename TI, typename TR, int TPR, int NC>
 __global__ __launch_bounds__(TPR < kLayerThreads ? kLayerThreads : TPR) void norm_bwd_kernel(NormParams p) {
     constexpr int RPB = TPR < kLayerThreads ? kLayerThreads / TPR : 1;
-    __shared__ float red[TPR / 64];
+    constexpr bool kHeld = TPR < 1024;
+    static_assert(!kHeld || NC <= 2, "a held row has up to two groups a thread");
+    constexpr int H = kHeld ? NC : 1;
+    __shared__ Sums red[TPR > 64 ? TPR / 64 : 1];
     const int tid = threadIdx.x % TPR;
     const int64_t first = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR, step = (int64_t)gridDim.x * RPB;
-    float acc[NC][8];
+    float acc[NC][8], w[H][8], v[H][8], g[H][8];
 #pragma unroll
     for (int i = 0; i < NC; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
+    NormRow<TR, TPR, H> ns, nds;
+    NormRow<TI, TPR, H> ng;
+    if constexpr (kHeld) {
+#pragma unroll
+        for (int i = 0; i < NC; ++i) norm_weight(w[i], p, norm_col<TPR>(tid, i));
+        if (first < p.rows) {
+            ns.load((const TR*)p.x + first * p.C, tid, p.C);
+            ng.load((const TI*)p.dy + first * p.C, tid, p.C);
+        }
+    }
     for (int64_t row = first; row < p.rows; row += step) {
         const int64_t at = row * p.C;
-        float v[NC][8], g[NC][8];
-        norm_load<TR, TPR, NC, VEC>(v, (const TR*)p.x + at, tid, p.C);
-        norm_load<TI, TPR, NC, VEC>(g, (const TI*)p.dy + at, tid, p.C);
-        const float rstd = norm_rstd<TPR>(v, p, red);
-        float dot = 0.f;
+        const TR* s = (const TR*)p.x + at;
+        const TI* dy = (const TI*)p.dy + at;
+        if constexpr (kHeld) {
 #pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            float w[8];
-            norm_weight<TPR, VEC>(w, p, tid, i);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                v[i][j] *= rstd;
-                acc[i][j] = __builtin_fmaf(g[i][j], v[i][j], acc[i][j]);
-                g[i][j] *= w[j];
-                dot = __builtin_fmaf(g[i][j], v[i][j], dot);
+            for (int i = 0; i < NC; ++i) {
+                ns.r[i].get(v[i]);
+                ng.r[i].get(g[i]);
+            }
+            if (p.ds) nds.load((const TR*)p.ds + at, tid, p.C);
+            if (row + step < p.rows) {
+                ns.load(s + step * p.C, tid, p.C);
+                ng.load(dy + step * p.C, tid, p.C);
             }
         }
-        const float mean = row_reduce<TPR>(dot, red, Add()) / (float)p.C;
+        auto group = [&](int i) {                 // s, dy and the weights of the i-th group, in v, g, w[h]
+            if constexpr (!kHeld) {
+                const int c = norm_col<TPR>(tid, i);
+                norm_load8(v[0], s, c, p.C);
+                norm_load8(g[0], dy, c, p.C);
+                norm_weight(w[0], p, c);
+            }
+            return kHeld ? i : 0;
+        };
+        auto sums = [&](float shrink) {
+            Sums x = {0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                const int h = group(i);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float u = v[h][j] * shrink;
+                    x.square = __builtin_fmaf(u, u, x.square);
+                    x.dot = __builtin_fmaf(w[h][j] * g[h][j], u, x.dot);
+                }
+            }
+            return row_sums<TPR>(x, red);
+        };
+        float shrink = 1.f, rstd;
+        Sums x = sums(1.f);
+        if (norm_overflows(x.square)) {
+            shrink = kNormShrink;
+            x = sums(shrink);
+            rstd = 1.f / sqrtf(x.square / (float)p.C);
+        } else {
+            rstd = 1.f / sqrtf(x.square / (float)p.C + p.eps);
+        }
+        const float mean = x.dot * rstd / (float)p.C;       // of w dy and the normed row
+        rstd *= shrink;
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
+            const int h = group(i), c = norm_col<TPR>(tid, i);
+            float dx[8], e[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = rstd * (g[i][j] - v[i][j] * mean);
+            for (int j = 0; j < 8; ++j) {
+                const float xh = v[h][j] * rstd;
+                acc[i][j] = __builtin_fmaf(g[h][j], xh, acc[i][j]);
+                dx[j] = rstd * (w[h][j] * g[h][j] - xh * mean);
+            }
+            if (p.ds) {
+                if constexpr (kHeld) nds.r[i].get(e);
+                else norm_load8(e, (const TR*)p.ds + at, c, p.C);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) dx[j] += e[j];
+            }
+            norm_store8(p.dx, at, c, p.C, dx, p.out == 1);
         }
-        if (p.ds) {
-            norm_load<TR, TPR, NC, VEC>(g, (const TR*)p.ds + at, tid, p.C);
-#pragma unroll
-            for (int i = 0; i < NC; ++i)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[i][j] += g[i][j];
-        }
-#pragma unroll
-        for (int i = 0; i < NC; ++i) norm_store<TPR, VEC>(p.dx, at, tid, i, p.C, v[i], p.out == 1);
     }
     if (p.dw_part)
 #pragma unroll
-        for (int i = 0; i < NC; ++i) norm_store<TPR, VEC>(p.dw_part, first * p.C, tid, i, p.C, acc[i], false);
+        for (int i = 0; i < NC; ++i) norm_store8(p.dw_part, first * p.C, norm_col<TPR>(tid, i), p.C, acc[i], false);
 }
 
 // One workgroup for 64 columns: 16 waves take every 16th row, then their sums in order.
@@ -270,47 +333,62 @@ hipError_t launch_part_sums(const PartSums& s, hipStream_t stream) {
 }
 
 // ---------------------------------------------------------------- launches
-template <typename TI, typename TR, int TPR, int NC, bool VEC>
-static void norm_launch(const NormParams& p, bool backward, int blocks, hipStream_t stream) {
+// A row's threads and groups of eight channels a thread.  The backward keeps five values a channel and rows on their
+// way; 32768 x 4096 bf16 takes 191 us with 256 threads and two groups, 201 with 512 and one.
+template <typename TI, typename TR, int TPR, int NC> static void norm_fwd_launch(const NormParams& p, hipStream_t stream) {
     constexpr int threads = TPR < kLayerThreads ? kLayerThreads : TPR, RPB = threads / TPR;
-    if (backward) hipLaunchKernelGGL((norm_bwd_kernel<TI, TR, TPR, NC, VEC>), dim3((unsigned)blocks), dim3(threads), 0, stream, p);
-    else hipLaunchKernelGGL((norm_fwd_kernel<TI, TR, TPR, NC, VEC>), dim3((unsigned)((p.rows + RPB - 1) / RPB)), dim3(threads), 0, stream, p);
+    hipLaunchKernelGGL((norm_fwd_kernel<TI, TR, TPR, NC>), dim3((unsigned)((p.rows + RPB - 1) / RPB)), dim3(threads), 0, stream, p);
 }
-template <typename TI, typename TR, bool VEC>
-static void norm_size(const NormParams& p, bool backward, int blocks, hipStream_t stream) {
+template <typename TI, typename TR, int TPR, int NC> static void norm_bwd_launch(const NormParams& p, hipStream_t stream) {
+    constexpr int threads = TPR < kLayerThreads ? kLayerThreads : TPR;
+    hipLaunchKernelGGL((norm_bwd_kernel<TI, TR, TPR, NC>), dim3((unsigned)norm_bwd_blocks(p.C, p.rows)), dim3(threads), 0, stream, p);
+}
+template <typename TI, typename TR> static void norm_types(const NormParams& p, bool backward, hipStream_t stream) {
     const int C = p.C;
-    if (C <= 512) norm_launch<TI, TR, 64, 1, VEC>(p, backward, blocks, stream);
-    else if (C <= 1024) norm_launch<TI, TR, 64, 2, VEC>(p, backward, blocks, stream);
-    else if (C <= 2048) norm_launch<TI, TR, 256, 1, VEC>(p, backward, blocks, stream);
-    else if (C <= 4096) norm_launch<TI, TR, 256, 2, VEC>(p, backward, blocks, stream);
-    else if (C <= 8192) norm_launch<TI, TR, 256, 4, VEC>(p, backward, blocks, stream);
-    else if (C <= 16384) norm_launch<TI, TR, 512, 4, VEC>(p, backward, blocks, stream);
-    else norm_launch<TI, TR, 512, 8, VEC>(p, backward, blocks, stream);
+    if (backward) {
+        if (C <= 128) norm_bwd_launch<TI, TR, 16, 1>(p, stream);
+        else if (C <= 256) norm_bwd_launch<TI, TR, 32, 1>(p, stream);
+        else if (C <= 512) norm_bwd_launch<TI, TR, 64, 1>(p, stream);
+        else if (C <= 1024) norm_bwd_launch<TI, TR, 64, 2>(p, stream);
+        else if (C <= 2048) norm_bwd_launch<TI, TR, 256, 1>(p, stream);
+        else if (C <= 4096) norm_bwd_launch<TI, TR, 256, 2>(p, stream);
+        else if (C <= 8192) norm_bwd_launch<TI, TR, 512, 2>(p, stream);
+        else norm_bwd_launch<TI, TR, 1024, 2>(p, stream);
+    } else {
+        if (C <= 128) norm_fwd_launch<TI, TR, 16, 1>(p, stream);
+        else if (C <= 256) norm_fwd_launch<TI, TR, 32, 1>(p, stream);
+        else if (C <= 512) norm_fwd_launch<TI, TR, 64, 1>(p, stream);
+        else if (C <= 1024) norm_fwd_launch<TI, TR, 64, 2>(p, stream);
+        else if (C <= 2048) norm_fwd_launch<TI, TR, 256, 1>(p, stream);
+        else if (C <= 4096) norm_fwd_launch<TI, TR, 256, 2>(p, stream);
+        else if (C <= 8192) norm_fwd_launch<TI, TR, 256, 4>(p, stream);
+        else norm_fwd_launch<TI, TR, 512, 4>(p, stream);
+    }
 }
-template <typename TI, typename TR> static void norm_vec(const NormParams& p, bool backward, int blocks, hipStream_t stream) {
-    if (p.C % 8 == 0) norm_size<TI, TR, true>(p, backward, blocks, stream);
-    else norm_size<TI, TR, false>(p, backward, blocks, stream);
-}
-static hipError_t norm_any(const NormParams& p, int in_bf16, int res_bf16, bool backward, int blocks, hipStream_t stream) {
-    if (in_bf16 && res_bf16) norm_vec<bf16, bf16>(p, backward, blocks, stream);
-    else if (in_bf16) norm_vec<bf16, float>(p, backward, blocks, stream);
-    else norm_vec<float, float>(p, backward, blocks, stream);
+static hipError_t norm_any(const NormParams& p, int in_bf16, int res_bf16, bool backward, hipStream_t stream) {
+    if (in_bf16 && res_bf16) norm_types<bf16, bf16>(p, backward, stream);
+    else if (in_bf16) norm_types<bf16, float>(p, backward, stream);
+    else norm_types<float, float>(p, backward, stream);
     return hipGetLastError();
 }
 hipError_t launch_norm_fwd(const NormParams& p, int in_bf16, int res_bf16, hipStream_t stream) {
-    return norm_any(p, in_bf16, res_bf16, false, 0, stream);
+    return norm_any(p, in_bf16, res_bf16, false, stream);
 }
 
-// Rows of partial sums of dw: one a row's worth of threads of every workgroup.
-static int norm_rows_at_once(int32_t C) { return C <= 1024 ? 4 : 1; }
+// Rows of partial sums of dw: one for each row that a workgroup has at a time.  As many workgroups as the compute units
+// hold at once, so that all go over as many rows: bf16, 2^27 values, us for 256, 512, 768, 1024, 1280 workgroups:
+// 512 channels 545, 331, 256, 230, 219;  1024: 275, 200, 211, 242, 233;  768: 549, 327, 251, 339, 299;  2048: 525, 329,
+// 251, 218, 201;  4096: 264, 191, 199, 233, 213;  8192: 201, 206, 210, 213, 217.
+static int norm_rows_at_once(int32_t C) { return C <= 128 ? 16 : C <= 256 ? 8 : C <= 1024 ? 4 : 1; }
 int norm_bwd_blocks(int32_t C, int64_t rows) {
     const int64_t groups = (rows + norm_rows_at_once(C) - 1) / norm_rows_at_once(C);
-    return (int)(groups < 1024 ? groups : 1024);
+    const int64_t most = 256 * (C <= 512 ? 4 : C <= 1024 ? 3 : C <= 2048 ? 4 : C <= 4096 ? 2 : 1);
+    return (int)(groups < most ? groups : most);
 }
 int64_t norm_bwd_parts(int32_t C, int64_t rows) { return (int64_t)norm_bwd_blocks(C, rows) * norm_rows_at_once(C); }
 hipError_t launch_norm_bwd(const NormParams& p, int in_bf16, int res_bf16, float* dw, hipStream_t stream) {
     if (p.rows) {
-        const hipError_t e = norm_any(p, in_bf16, res_bf16, true, norm_bwd_blocks(p.C, p.rows), stream);
+        const hipError_t e = norm_any(p, in_bf16, res_bf16, true, stream);
         if (e != hipSuccess) return e;
     }
     if (!dw) return hipSuccess;

@@ -435,7 +435,7 @@ kda_status kda_tree_commit(const kda_tree_config* cfg, int32_t num_seqs, const v
 #define KDA_I8 2   /* signed 8-bit integers in [-127, 127]                     */
 #define KDA_E4M3 3 /* 8-bit floats, 4 exponent and 3 mantissa bits, largest 448 */
 
-#define KDA_NORM_MAX_CHANNELS 32768
+#define KDA_NORM_MAX_CHANNELS 16384
 
 typedef struct kda_norm_config {
     int32_t C;            /* channels, 1 .. KDA_NORM_MAX_CHANNELS              */
@@ -501,8 +501,7 @@ void kda_conv_config_init(kda_conv_config* cfg, int32_t C, int32_t width);
  * before it, oldest first; the final state is the last width - 1 rows of both.
  *   x, y, dy, dx : [total_tokens, C]    weight : [C, width]    bias : [C] or NULL
  *   states : [num_seqs, width - 1, C] in in_dtype (NULL: zero / not kept)
- * initial_state and final_state must not overlap, nor y and x.  Any C; rows of
- * 8 channels at 16-byte addresses (C and x_stride multiples of 8) are faster. */
+ * initial_state and final_state must not overlap, nor y and x. */
 kda_status kda_conv_fwd(const kda_conv_config* cfg, int64_t total_tokens, int32_t num_seqs, const void* x,
                         const void* weight, const void* bias, const int32_t* cu_seqlens, const void* initial_state,
                         void* y, void* final_state, void* stream);

@@ -56,11 +56,13 @@ def test_forward_and_backward(lens, W, C, dtype, wt, act):
         check(g[n], *want[n], t)
 
 
-def test_long_strips():
-    """Strips of 32 tokens, several blocks of channels, another output type."""
+@pytest.mark.parametrize("C,dtype", [(4099, BF16), (4104, BF16), (14003, F32)])
+@pytest.mark.parametrize("W", [2, 3, 4])
+def test_eight_channels_a_thread(C, dtype, W):
+    """Larger calls: eight channels a thread, the last of a row's threads moved back, strips of 16 to 64 tokens."""
     need_gpu()
-    lens = [700, 1, 0, 130, 64, 1153]
-    d = make(lens, 4099, 4, BF16)
+    lens = [700, 1, 0, 130, 64, 2, 303]
+    d = make(lens, C, W, dtype)
     h = {n: host(x) for n, x in d.items()}
     y, end = kda.kda_conv_fwd(d["x"], d["w"], d["b"], d["cu"], d["state"], out_dtype=F32)
     want, last, bound = ref.conv_fwd(h["x"], h["w"], h["b"], h["state"], lens)
@@ -68,7 +70,7 @@ def test_long_strips():
     assert (host(end) == last).all()
     g = kda.kda_conv_bwd(d["x"], d["w"], d["b"], d["dy"], d["cu"], d["state"], d["dend"], out_dtype=F32)
     want = ref.conv_bwd(h["x"], h["w"], h["b"], h["state"], lens, h["dy"], h["dend"])
-    for n, t in (("dx", F32), ("dw", F32), ("db", F32), ("dstate", BF16)):
+    for n, t in (("dx", F32), ("dw", F32), ("db", F32), ("dstate", dtype)):
         check(g[n], *want[n], t)
 
 

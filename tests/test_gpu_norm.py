@@ -24,7 +24,7 @@ def rand(rows, C, dtype, seed, scale=1.0):
 
 # every width of a row's threads, rows of eight channels and odd ones, one channel, one row
 SIZES = [(1, 1), (3, 7), (5, 64), (2, 333), (9, 512), (7, 1000), (4, 1024), (6, 1032), (3, 2048), (257, 2056), (5, 4096), (3, 4099), (2, 8192),
-         (2, 8200), (2, 16384), (2, 20001), (1, 32768)]
+         (2, 8200), (9, 100), (20, 128), (11, 200), (8, 256), (2, 12001), (1, 16384)]
 
 
 @pytest.mark.parametrize("rows,C", SIZES)
@@ -49,7 +49,7 @@ def test_forward(rows, C, types):
     assert (np.abs(host(y) - want) <= np.abs(want) * (ref.RSTD + 3) * ref.U * 1.01).all()
 
 
-@pytest.mark.parametrize("rows,C", [(1, 1), (3, 7), (9, 512), (2, 333), (40, 1032), (33, 4096), (3, 4099), (2, 8200), (2, 20001), (1, 32768)])
+@pytest.mark.parametrize("rows,C", [(1, 1), (3, 7), (9, 512), (2, 333), (40, 1032), (33, 4096), (3, 4099), (2, 8200), (2, 12001), (1, 16384)])
 @pytest.mark.parametrize("types", [(BF16, BF16), (BF16, F32), (F32, F32)])
 @pytest.mark.parametrize("out", [torch.int8, torch.float8_e4m3fn])
 def test_codes(rows, C, types, out):
@@ -134,7 +134,7 @@ def test_in_place_and_no_rows():
 
 
 @pytest.mark.parametrize("rows,C", [(1, 1), (3, 7), (70, 64), (2, 333), (9, 512), (7, 1000), (1100, 1032), (5, 4096), (3, 4099), (2, 8192), (2, 8200),
-                                    (2, 20001), (1, 32768)])
+                                    (40, 100), (70, 128), (33, 200), (2, 12001), (1, 16384)])
 @pytest.mark.parametrize("types", [(BF16, BF16, BF16), (BF16, F32, F32), (F32, F32, F32)])
 def test_backward(rows, C, types):
     need_gpu()
@@ -200,5 +200,5 @@ def test_refusals():
     with pytest.raises(ValueError, match="shape"):
         kda.kda_norm_fwd(x, weight=x[0, :32])
     with pytest.raises(kda.KdaError, match="too large"):
-        kda.kda_norm_fwd(torch.zeros(1, 32769, device="cuda"))
+        kda.kda_norm_fwd(torch.zeros(1, 16385, device="cuda"))
 

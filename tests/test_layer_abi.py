@@ -180,7 +180,7 @@ def test_selective_configs():
     need = _lib.kda_selective_fwd_workspace_size(cfg, 4096, 2)
     assert need > 0 and sel_fwd(T=4096, wsb=need - 1) == KDA_ERR_WORKSPACE
     # a stream of one segment needs none
-    assert _lib.kda_selective_fwd_workspace_size(cfg, 64, 1) == 0
+    assert _lib.kda_selective_fwd_workspace_size(cfg, 12, 1) == 0
     for T, N in ((-1, 1), (1 << 31, 1), (128, 0)):
         assert _lib.kda_selective_fwd_workspace_size(cfg, T, N) == 0 and _lib.kda_selective_bwd_workspace_size(cfg, T, N) == 0
 
