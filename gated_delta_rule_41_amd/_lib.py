@@ -42,7 +42,7 @@ KDA_GATE_GRAD_F32 = 0x100
 KDA_RULE_DELTA, KDA_RULE_LINEAR = 0, 1
 KDA_TREE_MAX_NODES = 64
 KDA_I8, KDA_E4M3 = 2, 3   # outputs of kda_norm_fwd
-KDA_NORM_MAX_CHANNELS = 16384
+KDA_NORM_MAX_CHANNELS, KDA_CONV_MAX_CHANNELS, KDA_SELECTIVE_MAX_CHANNELS = 16384, 1 << 20, 1 << 16
 KDA_ACT_NONE, KDA_ACT_SILU = 0, 1
 KDA_SELECTIVE_SOFTPLUS = 1
 

@@ -128,12 +128,12 @@ __device__ __forceinline__ Segment find_segment(const int32_t* cu, int N, int se
 // x / (1 + e^-x): the exponential of a very negative x is infinite and the quotient 0.
 __device__ __forceinline__ float sigmoid_fast(float x) { return __builtin_amdgcn_rcpf(1.f + fast_exp2(-1.44269504f * x)); }
 
-// log(1 + e^v).  With w = 1 + e rounded, log(1 + e) = log(w) + (e - (w - 1)) / w to first
-// order, which keeps every bit of a small e.
+// log(1 + e^v).  With w = 1 + e rounded, log(1 + e) = log(w) + (e - (w - 1)) / w to first order, which keeps every bit of a
+// small e.  The quotient may go: w is near 1 where the term counts, and elsewhere it is below half a step of the result.
 __device__ __forceinline__ float softplus(float v) {
     const float e = fast_exp2(-1.44269504f * __builtin_fabsf(v)), w = 1.f + e;
-    const float l = __builtin_amdgcn_logf(w) * 0.693147181f + (e - (w - 1.f)) * __builtin_amdgcn_rcpf(w);
-    return (v > 0.f ? v : 0.f) + l;
+    const float l = __builtin_fmaf(__builtin_amdgcn_logf(w), 0.693147181f, e - (w - 1.f));
+    return __builtin_fmaxf(v, 0.f) + l;
 }
 
 // Eight channels side by side as they lie in memory, at any address: global memory takes 16-byte accesses at the

@@ -55,7 +55,6 @@ kda_status check_stream(int64_t T, int32_t N, const int32_t* cu) {
     if (!cu && T % N) return fail(KDA_ERR_INVALID_ARG, "cu_seqlens is NULL but total_tokens is not a multiple of num_seqs%s");
     return ptr(cu, "cu_seqlens", false);
 }
-constexpr int32_t kMostChannels = 1 << 20;
 
 // ---------------------------------------------------------------- norm
 kda_status check_norm(const kda_norm_config* c, int64_t rows, bool backward) {
@@ -76,7 +75,7 @@ kda_status check_norm(const kda_norm_config* c, int64_t rows, bool backward) {
 kda_status check_conv(const kda_conv_config* c) {
     if (!c) return fail(KDA_ERR_INVALID_ARG, "config is NULL%s");
     if (c->C < 1) return fail(KDA_ERR_INVALID_ARG, "C must be >= 1%s");
-    if (c->C >= kMostChannels) return fail(KDA_ERR_UNSUPPORTED, "C too large%s");
+    if (c->C > KDA_CONV_MAX_CHANNELS) return fail(KDA_ERR_UNSUPPORTED, "C too large%s");
     if (c->width < 2 || c->width > 4) return fail(KDA_ERR_UNSUPPORTED, "width must be 2, 3 or 4%s");
     if (!is_dtype(c->in_dtype) || !is_dtype(c->out_dtype) || !is_dtype(c->weight_dtype)) return fail(KDA_ERR_INVALID_ARG, "unknown dtype%s");
     if (c->activation != KDA_ACT_NONE && c->activation != KDA_ACT_SILU) return fail(KDA_ERR_INVALID_ARG, "unknown activation%s");
@@ -126,7 +125,7 @@ ConvParams conv_params(const kda_conv_config* c) {
 kda_status check_selective(const kda_selective_config* c) {
     if (!c) return fail(KDA_ERR_INVALID_ARG, "config is NULL%s");
     if (c->C < 1 || c->G < 1 || c->C % c->G) return fail(KDA_ERR_INVALID_ARG, "C and G must be >= 1 and G must divide C%s");
-    if (c->C >= kMostChannels) return fail(KDA_ERR_UNSUPPORTED, "C too large%s");
+    if (c->C > KDA_SELECTIVE_MAX_CHANNELS) return fail(KDA_ERR_UNSUPPORTED, "C too large%s");
     if (c->S != 8 && c->S != 16 && c->S != 32) return fail(KDA_ERR_UNSUPPORTED, "S must be 8, 16 or 32%s");
     if (!is_dtype(c->in_dtype) || !is_dtype(c->out_dtype)) return fail(KDA_ERR_INVALID_ARG, "unknown dtype%s");
     if (c->flags & ~KDA_SELECTIVE_SOFTPLUS) return fail(KDA_ERR_INVALID_ARG, "unknown flags%s");

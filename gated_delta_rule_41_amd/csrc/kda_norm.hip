@@ -143,7 +143,7 @@ __global__ __launch_bounds__(TPR < kLayerThreads ? kLayerThreads : TPR) void nor
     top = row_reduce<TPR>(top, reinterpret_cast<unsigned*>(red), MaxBits());
     const float amax = __uint_as_float(top), Q = p.out == 2 ? 127.f : 448.f;
     const bool codes = top != 0 && top < 0x7f800000u;
-    if (tid == 0) p.scale[row] = top < 0x7f800000u ? amax * rstd / Q : __builtin_nanf("");
+    if (tid == 0) p.scale[row] = codes ? amax * rstd / Q : top == 0 ? 0.f : __builtin_nanf("");
     const int e = codes ? __builtin_amdgcn_frexp_expf(amax) : 0;
     const float m = codes ? __builtin_amdgcn_ldexpf(amax, -e) : 1.f, inv = __builtin_amdgcn_rcpf(m);
     uint8_t* y = (uint8_t*)p.y + at;

@@ -42,14 +42,16 @@ __global__ __launch_bounds__(kLayerThreads) void selective_states_kernel(Selecti
             w[u] = d[u] * to_f32(nx[u]);
         }
         if (whole.value ? left > U : false) load(left - U);
+        float part = 0.f;                         // block by block, so that long segments' sums round less
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (!whole.value && u >= count) break;
             const UniformRow<T, S> b = B.next(u + 1 < left);
-            sum += d[u];
+            part += d[u];
 #pragma unroll
             for (int n = 0; n < S; ++n) h[n] = __builtin_fmaf(fast_exp2(d[u] * A2[n]), h[n], w[u] * b[n]);
         }
+        sum += part;
     };
     int64_t kept = KEEP ? s.lo / U + s.n + (s.begin - s.lo) / U : 0;
     auto keep = [&]() {                           // before every block but the first

@@ -480,6 +480,8 @@ kda_status kda_norm_bwd(const kda_norm_config* cfg, int64_t rows, const void* s,
                         const void* ds, void* dx, float* dweight, void* workspace, size_t workspace_bytes,
                         void* stream);
 
+#define KDA_CONV_MAX_CHANNELS 1048576
+
 typedef enum kda_activation { KDA_ACT_NONE = 0, KDA_ACT_SILU = 1 } kda_activation;
 
 typedef struct kda_conv_config {
@@ -501,7 +503,8 @@ void kda_conv_config_init(kda_conv_config* cfg, int32_t C, int32_t width);
  * before it, oldest first; the final state is the last width - 1 rows of both.
  *   x, y, dy, dx : [total_tokens, C]    weight : [C, width]    bias : [C] or NULL
  *   states : [num_seqs, width - 1, C] in in_dtype (NULL: zero / not kept)
- * initial_state and final_state must not overlap, nor y and x. */
+ * initial_state and final_state must not overlap, nor y and x.  total_tokens / 8 +
+ * num_seqs below 2^24 (kda_conv_decode: num_seqs * C below 2^32). */
 kda_status kda_conv_fwd(const kda_conv_config* cfg, int64_t total_tokens, int32_t num_seqs, const void* x,
                         const void* weight, const void* bias, const int32_t* cu_seqlens, const void* initial_state,
                         void* y, void* final_state, void* stream);
@@ -520,6 +523,8 @@ kda_status kda_conv_bwd(const kda_conv_config* cfg, int64_t total_tokens, int32_
  * it.  num_seqs = 0 enqueues nothing. */
 kda_status kda_conv_decode(const kda_conv_config* cfg, int32_t num_seqs, const void* x, const void* weight,
                            const void* bias, const void* state_in, void* state_out, void* y, void* stream);
+
+#define KDA_SELECTIVE_MAX_CHANNELS 65536
 
 /* kda_selective_config.flags */
 #define KDA_SELECTIVE_SOFTPLUS 1u /* dt = softplus(dt + dt_bias), else dt + dt_bias */
@@ -554,9 +559,13 @@ void kda_selective_config_init(kda_selective_config* cfg, int32_t C, int32_t S, 
  * what depends on them by the recurrence and nothing else (dA, dD and dt_bias's
  * gradient are sums over all tokens); which of the two a result is, is open.
  * Documents are cut into segments where that fills the GPU (a rule on the config
- * and the sizes): own sums first, then a carry, then the walks; the workspace
- * holds the segments' states (0 bytes where nothing is cut, or for an invalid
- * config or sizes).  initial_state and final_state must not overlap. */
+ * and the sizes): own sums first, then a carry, then the walks; the forward's
+ * workspace holds the segments' states (0 bytes where nothing is cut, or for an
+ * invalid config or sizes), the backward's also the states before every few
+ * tokens (about 11 bytes a token and channel at S = 16) and, for every 64 channels,
+ * a share of dB and dC.  initial_state and final_state must not overlap.
+ * total_tokens * G * S below 2^31, and num_seqs below 2^23 (kda_selective_decode:
+ * num_seqs * C * S below 2^34). */
 size_t kda_selective_fwd_workspace_size(const kda_selective_config* cfg, int64_t total_tokens, int32_t num_seqs);
 size_t kda_selective_bwd_workspace_size(const kda_selective_config* cfg, int64_t total_tokens, int32_t num_seqs);
 kda_status kda_selective_fwd(const kda_selective_config* cfg, int64_t total_tokens, int32_t num_seqs, const void* x,

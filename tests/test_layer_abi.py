@@ -135,7 +135,7 @@ def test_norm_overlaps():
 
 def test_conv_configs():
     for call in (conv_fwd, conv_bwd, conv_decode):
-        for change, status in ((dict(C=0), KDA_ERR_INVALID_ARG), (dict(C=1 << 20), KDA_ERR_UNSUPPORTED), (dict(width=1), KDA_ERR_UNSUPPORTED),
+        for change, status in ((dict(C=0), KDA_ERR_INVALID_ARG), (dict(C=_lib.KDA_CONV_MAX_CHANNELS + 1), KDA_ERR_UNSUPPORTED), (dict(width=1), KDA_ERR_UNSUPPORTED),
                                (dict(width=5), KDA_ERR_UNSUPPORTED), (dict(in_dtype=2), KDA_ERR_INVALID_ARG),
                                (dict(out_dtype=3), KDA_ERR_INVALID_ARG), (dict(weight_dtype=-1), KDA_ERR_INVALID_ARG),
                                (dict(activation=2), KDA_ERR_INVALID_ARG), (dict(x_stride=63), KDA_ERR_INVALID_ARG),
@@ -163,7 +163,7 @@ def test_conv_overlaps():
 def test_selective_configs():
     for call in (sel_fwd, sel_bwd, sel_decode):
         for change, status in ((dict(C=0), KDA_ERR_INVALID_ARG), (dict(G=0), KDA_ERR_INVALID_ARG), (dict(G=3), KDA_ERR_INVALID_ARG),
-                               (dict(C=1 << 20), KDA_ERR_UNSUPPORTED), (dict(S=64), KDA_ERR_UNSUPPORTED), (dict(S=12), KDA_ERR_UNSUPPORTED),
+                               (dict(C=_lib.KDA_SELECTIVE_MAX_CHANNELS + 2), KDA_ERR_UNSUPPORTED), (dict(S=64), KDA_ERR_UNSUPPORTED), (dict(S=12), KDA_ERR_UNSUPPORTED),
                                (dict(in_dtype=2), KDA_ERR_INVALID_ARG), (dict(out_dtype=2), KDA_ERR_INVALID_ARG),
                                (dict(flags=2), KDA_ERR_INVALID_ARG), (dict(x_stride=63), KDA_ERR_INVALID_ARG),
                                (dict(dt_stride=1), KDA_ERR_INVALID_ARG), (dict(z_stride=-1), KDA_ERR_INVALID_ARG),
