@@ -8,9 +8,11 @@ namespace kda {
 
 constexpr int kLayerThreads = 256;   // 4 wave64
 // Tokens between the states that the selective backward keeps, whose own states a lane then holds: S x (6 + 1) registers
-// at S = 16; 7 and 8 spill, 4 with the decays kept beside the states moves half as much again (1182 us a call for
-// 4 x 4096 tokens x 4096 channels, where 6 take 1109).
-constexpr int selective_kept(int S) { return S == 32 ? 4 : 6; }
+// at S = 16.  Fewer move more, more spill.  A backward of 4 x 4096 tokens x 4096 channels (bf16, gated), in us:
+//     S = 8     4: 866   5: 856   6: 820   7: 846   8: 884   10: 885
+//     S = 16    4: 1501  5: 1439  6: 1369  7: 1785
+//     S = 32    2: 4558  3: 4137  4: 3872  5: 3765  6: 3852  7: 4312  8: 4967
+constexpr int selective_kept(int S) { return S == 32 ? 5 : 6; }
 
 // ---------------------------------------------------------------- norm
 struct NormParams {

@@ -3,9 +3,10 @@
 // A lane holds one channel with all its S state entries in registers, a wave 64 channels of
 // one group, so B_t and C_t are the same for the whole wave: they come through the scalar
 // cache and enter the products as scalar operands, and the sums over the state's entries stay
-// in a lane.  An entry and token costs a multiply and an exponential for the decay (the
-// exponential a quarter of the rate), a multiply and a multiply-add for the state and a
-// multiply-add for the output: 8 issue slots, which bound these kernels.
+// in a lane.  An entry and token costs a multiply and an exponential for the decay, a
+// multiply and a multiply-add for the state and a multiply-add for the output.  The exponential
+// takes two issue slots (measured, as logarithms and quotients do), so these are 6, which bound
+// the kernels: 217 us for 67.1M tokens and channels of 16 entries, where HBM would ask 105.
 #pragma once
 #include "kda_layer.h"
 
@@ -59,16 +60,32 @@ template <typename T, int S> struct UniformRows {
 // A wave's channels: `c` of a lane is clamped to its group, `valid` says whether it is its own.
 struct Channels {
     int group;
-    unsigned c;
+    unsigned c, two, four;    // the channel, and its offset in bytes in rows of 2- and 4-byte elements
     bool valid;
     __device__ __forceinline__ Channels(const SelectiveParams& p, int wave) {
         const int per = p.C / p.G, in = (wave % p.group_waves) * 64 + (int)(threadIdx.x & 63);
         group = wave / p.group_waves;
         valid = in < per;
         c = group * per + (valid ? in : per - 1);
-        __builtin_assume(c < (1u << 20));     // the host's limit: offsets of a lane fit 32 bits
+        two = c * 2;
+        four = c * 4;
     }
 };
+// A lane's place in a row at a uniform address: one scalar base and a 32-bit offset.  Both pass through registers by
+// force at each use; the compiler else widens the offset once before the loop and adds it to every row in vectors.
+template <typename T> __device__ __forceinline__ T* lane_bytes(T* row, unsigned bytes) {
+    __attribute__((address_space(1))) T* global = (__attribute__((address_space(1))) T*)row;
+    asm("" : "+s"(global), "+v"(bytes));
+    return atb((T*)global, bytes);
+}
+template <typename T> __device__ __forceinline__ T* lane_of(T* row, const Channels& ch) {
+    return lane_bytes(row, sizeof(T) == 2 ? ch.two : ch.four);
+}
+template <typename T> __device__ __forceinline__ T row_at(const T* row, const Channels& ch) { return *lane_of(row, ch); }
+__device__ __forceinline__ void row_put(void* base, int64_t row_start, const Channels& ch, float x, bool as_bf16) {
+    if (as_bf16) *lane_of((bf16*)base + row_start, ch) = (bf16)x;
+    else *lane_of((float*)base + row_start, ch) = x;
+}
 
 template <int S> __device__ __forceinline__ void load_entries(float (&v)[S], const float* p) {
 #pragma unroll
@@ -89,7 +106,7 @@ template <int S> __device__ __forceinline__ void store_entries(float* p, const f
 template <int S> __device__ __forceinline__ void load_kept(float (&v)[S], const float* p, int64_t slot, int C, unsigned c) {
 #pragma unroll
     for (int n = 0; n < S; n += 4) {
-        const f32x4 x = reinterpret_cast<const f32x4*>(p + (slot * (S / 4) + n / 4) * C * 4)[c];
+        const f32x4 x = *lane_bytes(reinterpret_cast<const f32x4*>(p + (slot * (S / 4) + n / 4) * C * 4), c * 16);
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[n + j] = x[j];
     }
@@ -98,7 +115,7 @@ template <int S> __device__ __forceinline__ void store_kept(float* p, int64_t sl
 #pragma unroll
     for (int n = 0; n < S; n += 4) {
         const f32x4 x = {v[n], v[n + 1], v[n + 2], v[n + 3]};
-        reinterpret_cast<f32x4*>(p + (slot * (S / 4) + n / 4) * C * 4)[c] = x;
+        *lane_bytes(reinterpret_cast<f32x4*>(p + (slot * (S / 4) + n / 4) * C * 4), c * 16) = x;
     }
 }
 // A in units of log 2, so that a decay is one multiply and one exponential.
@@ -106,13 +123,6 @@ template <int S> __device__ __forceinline__ void load_A(float (&A2)[S], const fl
     load_entries<S>(A2, A);
 #pragma unroll
     for (int n = 0; n < S; ++n) A2[n] *= kLog2e;
-}
-
-// Element c of a row at a uniform address: one scalar base, a 32-bit offset a lane.
-template <typename T> __device__ __forceinline__ T row_at(const T* row, unsigned c) { return row[c]; }
-__device__ __forceinline__ void row_put(void* base, int64_t row_start, unsigned c, float x, bool as_bf16) {
-    if (as_bf16) ((bf16*)base + row_start)[c] = (bf16)x;
-    else ((float*)base + row_start)[c] = x;
 }
 
 __device__ __forceinline__ float step_size(float raw, float bias, bool soft) {

@@ -3,11 +3,11 @@
 //     dx_t = dt_t (e_t . B_t) + D dy'_t,              dB_t = sum_c dt_t x_t e_t,  dC_t = sum_c dy'_t h_t
 //     d(dt_t) = x_t (e_t . B_t) + A . m_t,            m_t = e^{dt_t A} e_t h_{t-1},  dA = sum_t dt_t m_t
 // A wave walks a segment backwards in blocks of K tokens: from the kept state before the block
-// it forms the block's states in registers, then goes back over them with e.  In a block that the
-// document ends in, the tokens behind it are its last with dt = dy = 0, which move neither h nor e,
-// and whose outputs are dropped; there is no branch around a token.  A channel is a
+// it forms the block's states in registers, then goes back over them with e.  A channel is a
 // lane (kda_selective.h), so sums over the state's entries stay in a lane, and dB and dC are sums
-// over the lanes of a wave; the waves' shares are added by a last launch.
+// over the lanes of a wave; the waves' shares are added by a last launch.  An entry and token
+// costs 15 multiplies and multiply-adds, two exponentials and its share of 70 exchanges and
+// additions: vector instructions bound the kernel.
 #include "kda_selective.h"
 
 namespace kda {
@@ -72,6 +72,9 @@ __global__ __launch_bounds__(kLayerThreads, S == 32 ? 1 : 2) void selective_grad
     if (wave >= p.waves) return;
     const Channels ch(p, wave);
     const int lane = threadIdx.x & 63;
+    constexpr int R = 64 / S;                     // lanes with the same sum over lanes: the first stores dB's, the second dC's
+    unsigned part_at = ((lane & 1) * S + lane / R) * 4;
+    asm("" : "+v"(part_at));
     float A2[S], g[S], dA[S], dD = 0.f, dbias = 0.f;
     load_A<S>(A2, p.A + (int64_t)ch.c * S);
     const int64_t state = ((int64_t)s.n * p.C + ch.c) * S;
@@ -91,13 +94,13 @@ __global__ __launch_bounds__(kLayerThreads, S == 32 ? 1 : 2) void selective_grad
             const T* dt = (const T*)q->dt + t0 * q->dt_stride;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                nx[k] = row_at(x, ch.c);
-                nd[k] = row_at(dt, ch.c);
+                nx[k] = row_at(x, ch);
+                nd[k] = row_at(dt, ch);
                 if (k + 1 < count) { x += q->x_stride; dt += q->dt_stride; }
             }
             const int64_t at = s.lo / K + s.n + (t0 - s.lo) / K;
             load_kept<S>(own, q->border, at, q->C, ch.c);
-            own_dt = (q->bdt + at * q->C)[ch.c];
+            own_dt = row_at(q->bdt + at * q->C, ch);
         };
         f32x4* const enter = enters + (threadIdx.x >> 6) * (S / 4) * 64 + lane;
         // the block of `count` tokens from t0 on
@@ -112,8 +115,8 @@ __global__ __launch_bounds__(kLayerThreads, S == 32 ? 1 : 2) void selective_grad
                 for (int k = 0; k < K; ++k) {
                     tx[k] = nx[k];
                     td[k] = nd[k];
-                    tg[k] = row_at(dy, ch.c);
-                    if (GATED) tz[k] = row_at(z, ch.c);
+                    tg[k] = row_at(dy, ch);
+                    if (GATED) tz[k] = row_at(z, ch);
                     if (whole.value || k + 1 < count) { dy += q->C; z += GATED ? q->z_stride : 0; }
                 }
             }
@@ -126,12 +129,12 @@ __global__ __launch_bounds__(kLayerThreads, S == 32 ? 1 : 2) void selective_grad
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 d[k] = step_size(to_f32(td[k]), bias, p.softplus);
-                if (!whole.value) d[k] = k < count ? d[k] : 0.f;
             }
             UniformRows<T, S> B((const T*)p.B + t0 * p.b_stride + (int64_t)ch.group * S, p.b_stride);
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 __builtin_amdgcn_sched_barrier(0);
+                if (!whole.value && k >= count) continue;
                 const UniformRow<T, S> b = B.next(whole.value ? k + 1 < K : k + 1 < count);
                 const float w = ch.valid ? d[k] * to_f32(tx[k]) : 0.f;
 #pragma unroll
@@ -144,13 +147,16 @@ __global__ __launch_bounds__(kLayerThreads, S == 32 ? 1 : 2) void selective_grad
             UniformRows<T, S> C((const T*)r->Cm + t * r->c_stride + (int64_t)ch.group * S, -r->c_stride);
 #pragma unroll
             for (int k = K - 1; k >= 0; --k) {
-                const bool real = whole.value || k < count;
                 __builtin_amdgcn_sched_barrier(0);    // or rows of many tokens are loaded at once and spill
-                const UniformRow<T, S> b = B.next(real && k > 0), c = C.next(real && k > 0);
+                if (!whole.value && k >= count) {
+                    if (k == 1) ahead(kept ? t0 - K : t0, kept ? K : count);
+                    continue;
+                }
+                const UniformRow<T, S> b = B.next(k > 0), c = C.next(k > 0);
                 float dk = d[k];
                 asm("" : "+v"(dk));               // the decays are formed again: kept from above they would take S registers a token
                 const float xv = to_f32(tx[k]), w = ch.valid ? dk * xv : 0.f;
-                float dyv = ch.valid && real ? to_f32(tg[k]) : 0.f, dz = 0.f;
+                float dyv = ch.valid ? to_f32(tg[k]) : 0.f, dz = 0.f;
                 if constexpr (GATED) {
                     const float zv = to_f32(tz[k]), sig = sigmoid_fast(zv);
                     float y[4] = {skip * xv, 0.f, 0.f, 0.f};
@@ -180,21 +186,19 @@ __global__ __launch_bounds__(kLayerThreads, S == 32 ? 1 : 2) void selective_grad
                 const float dx = __builtin_fmaf(skip, dyv, dus * dk);
                 dD = __builtin_fmaf(dyv, xv, dD);
                 if (k == 1) ahead(kept ? t0 - K : t0, kept ? K : count);
-                if (!real) continue;
                 dbias += ddt;
                 float* part = r->bc_part + (t * r->waves + wave) * (2 * S);
-                constexpr int R = 64 / S;         // lanes with the same sum
-                if ((lane & (R - 1)) < 2) part[(lane & 1) * S + lane / R] = lane & 1 ? dC : dB;
+                if ((lane & (R - 1)) < 2) *lane_bytes(part, part_at) = lane & 1 ? dC : dB;
                 if (ch.valid) {
                     const int64_t out = t * r->C;
                     if (r->out_bf16) {
-                        ((bf16*)r->dx + out)[ch.c] = (bf16)dx;
-                        ((bf16*)r->ddt + out)[ch.c] = (bf16)ddt;
-                        if (GATED) ((bf16*)r->dz + out)[ch.c] = (bf16)dz;
+                        *lane_of((bf16*)r->dx + out, ch) = (bf16)dx;
+                        *lane_of((bf16*)r->ddt + out, ch) = (bf16)ddt;
+                        if (GATED) *lane_of((bf16*)r->dz + out, ch) = (bf16)dz;
                     } else {
-                        ((float*)r->dx + out)[ch.c] = dx;
-                        ((float*)r->ddt + out)[ch.c] = ddt;
-                        if (GATED) ((float*)r->dz + out)[ch.c] = dz;
+                        *lane_of((float*)r->dx + out, ch) = dx;
+                        *lane_of((float*)r->ddt + out, ch) = ddt;
+                        if (GATED) *lane_of((float*)r->dz + out, ch) = dz;
                     }
                 }
                 --t;

@@ -37,9 +37,9 @@ __global__ __launch_bounds__(kLayerThreads) void selective_out_kernel(SelectiveP
         auto load = [&](int count) {              // the block at x, dt, z; rows behind the segment are its last
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                nx[u] = row_at(x, ch.c);
-                nd[u] = row_at(dt, ch.c);
-                nz[u] = row_at(z, ch.c);
+                nx[u] = row_at(x, ch);
+                nd[u] = row_at(dt, ch);
+                nz[u] = row_at(z, ch);
                 if (u + 1 < count) { x += p.x_stride; dt += p.dt_stride; z += z_stride; }
             }
         };
@@ -73,7 +73,7 @@ __global__ __launch_bounds__(kLayerThreads) void selective_out_kernel(SelectiveP
             if (ch.valid)
 #pragma unroll
                 for (int u = 0; u < U; ++u)
-                    if (whole.value || u < count) row_put(p.y, out + (int64_t)u * p.C, ch.c, o[u], p.out_bf16);
+                    if (whole.value || u < count) row_put(p.y, out + (int64_t)u * p.C, ch, o[u], p.out_bf16);
         };
         for (; left >= U; left -= U, out += (int64_t)U * p.C) block(std::true_type(), U);
         if (left > 0) block(std::false_type(), left);

@@ -118,6 +118,19 @@ def test_extreme_rows(C):
         assert (np.abs(back - want)[fine] <= (step * 1.001 + tol)[fine]).all()
 
 
+@pytest.mark.parametrize("C", [64, 333, 4096])
+def test_zero_rows_without_eps(C):
+    """0 / 0 in the formula: values are NaN, as the formula has them; the row's codes and its scale are zeros."""
+    need_gpu()
+    x = rand(3, C, BF16, 1)
+    x[1] = 0
+    y, _ = kda.kda_norm_fwd(x, eps=0.0)
+    assert torch.isnan(y[1]).all() and torch.isfinite(y[0]).all() and torch.isfinite(y[2]).all()
+    for out in (torch.int8, torch.float8_e4m3fn):
+        codes, _, scale = kda.kda_norm_fwd(x, eps=0.0, out_dtype=out)
+        assert scale[1] == 0 and (codes[1].float() == 0).all() and (scale[[0, 2]] > 0).all()
+
+
 def test_in_place_and_no_rows():
     need_gpu()
     for C in (64, 333, 4096):

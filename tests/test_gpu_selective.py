@@ -287,6 +287,31 @@ def test_nonfinite_values_stay_where_they_belong():
     assert torch.equal(y2[:100], y[:100]) and torch.equal(y2[180:270], y[180:270])
 
 
+@pytest.mark.parametrize("S", [8, 16, 32])
+@pytest.mark.parametrize("gated", [True, False])
+def test_infinity_at_a_documents_last_token(S, gated):
+    """x_T is in no other token's gradient and not in dA, which has h_T only through later tokens: there are none."""
+    need_gpu()
+    lens = [100, 7, 9, 1, 6]
+    d = make(lens, 70, S, 1, F32, S, gated)
+    y, final = fwd(d)
+    g = bwd(d)
+    last = (np.cumsum(lens) - 1).tolist()
+    e = dict(d, x=d["x"].clone())
+    e["x"][last, 5] = float("inf")
+    y2, final2 = fwd(e)
+    g2 = bwd(e)
+    rest = [t for t in range(sum(lens)) if t not in last]
+    assert torch.equal(y2[rest], y[rest]) and not torch.isfinite(y2[last, 5]).any() and not torch.isfinite(final2[:, 5]).any()
+    for n in ("dx", "ddt", "dz", "dB", "dC"):
+        if g[n] is not None:
+            assert torch.equal(g2[n][rest], g[n][rest]), n
+    for n in ("dA", "dS0", "dx"):
+        assert torch.equal(g2[n], g[n]), n
+    assert torch.equal(g2["dD"][:5], g["dD"][:5]) and torch.equal(g2["dD"][6:], g["dD"][6:]) and not torch.isfinite(g2["dD"][5])
+    assert not torch.isfinite(g2["ddt"][last, 5]).any()
+
+
 def test_rows_behind_the_documents_are_left():
     need_gpu()
     lens, T = [40, 37], 90
