@@ -148,7 +148,7 @@ int32_t group_waves(const kda_selective_config* c) { return (c->C / c->G + 63) /
 // channels takes 64 us at 12, 82 at 24 and 129 at 48; the root is where a token's walk (0.8 us alone) and its
 // share of the carry (0.05 us a segment) are equal.
 constexpr int64_t kSelectiveWaves = 10922;
-constexpr int64_t kSelectiveUnit = 12;      // tokens; a multiple of the kept blocks
+constexpr int64_t kSelectiveUnit = 12;      // tokens; whole kept blocks at 8 and 16 entries
 struct SelectivePlan {
     int64_t len, slots, borders;
     bool cut;

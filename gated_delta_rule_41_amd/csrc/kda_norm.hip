@@ -72,27 +72,33 @@ __device__ __forceinline__ float odd_quotient(float p, float Q, float m, float i
     return __uint_as_float(b);
 }
 
-// mean(s^2) may leave fp32's range where s does not: such rows are summed again scaled by a power of two, beside
-// which eps is nothing.
-constexpr float kNormShrink = 0x1p-80f;
-__device__ __forceinline__ bool norm_overflows(float sum) { return __builtin_expect(!(sum < __builtin_huge_valf()), 0); }
-template <int TPR, int NC> __device__ __forceinline__ float norm_rstd(const float (&v)[NC][8], const NormParams& p, float* red) {
-    float sum = 0.f;
+// mean(s^2) may leave fp32's range, or the part of it where squares keep their bits, though s does not: such rows are
+// summed again, scaled by a power of two.  The normed row is then s by rstd.
+struct NormScale { float rstd, by; };
+__device__ __forceinline__ float norm_scale_by(float mean_eps) {
+    if (__builtin_expect(mean_eps >= 0x1p-96f && mean_eps < __builtin_huge_valf(), 1)) return 1.f;
+    return mean_eps < 1.f ? 0x1p100f : 0x1p-80f;
+}
+__device__ __forceinline__ float norm_mean_eps(float sum, const NormParams& p, float by) { return sum / (float)p.C + p.eps * by * by; }
+template <int NC> __device__ __forceinline__ void norm_scale(float (&v)[NC][8], float by) {
 #pragma unroll
     for (int i = 0; i < NC; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum = __builtin_fmaf(v[i][j], v[i][j], sum);
-    sum = row_reduce<TPR>(sum, red, Add());
-    if (norm_overflows(sum)) {
-        sum = 0.f;
+        for (int j = 0; j < 8; ++j) v[i][j] *= by;
+}
+template <int TPR, int NC> __device__ __forceinline__ NormScale norm_rstd(const float (&v)[NC][8], const NormParams& p, float* red) {
+    auto mean = [&](float by) {
+        float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < NC; ++i)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum = __builtin_fmaf(v[i][j] * kNormShrink, v[i][j] * kNormShrink, sum);
-        sum = row_reduce<TPR>(sum, red, Add());
-        return kNormShrink / sqrtf(sum / (float)p.C);
-    }
-    return 1.f / sqrtf(sum / (float)p.C + p.eps);
+            for (int j = 0; j < 8; ++j) sum = __builtin_fmaf(v[i][j] * by, v[i][j] * by, sum);
+        return norm_mean_eps(row_reduce<TPR>(sum, red, Add()), p, by);
+    };
+    float m = mean(1.f);
+    const float by = norm_scale_by(m);
+    if (by != 1.f) m = mean(by);
+    return {1.f / sqrtf(m), by};
 }
 
 template <typename TI, typename TR, int TPR, int NC>
@@ -116,14 +122,15 @@ __global__ __launch_bounds__(TPR < kLayerThreads ? kLayerThreads : TPR) void nor
 #pragma unroll
             for (int i = 0; i < NC; ++i) norm_store8(p.s, at, norm_col<TPR>(tid, i), p.C, v[i], sizeof(TR) == 2);
     }
-    const float rstd = norm_rstd<TPR>(v, p, red);
+    const NormScale n = norm_rstd<TPR>(v, p, red);
     if (p.out < 2) {
+        if (n.by != 1.f) norm_scale(v, n.by);
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             float w[8];
             norm_weight(w, p, norm_col<TPR>(tid, i));
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] *= rstd * w[j];
+            for (int j = 0; j < 8; ++j) v[i][j] *= n.rstd * w[j];
             norm_store8(p.y, at, norm_col<TPR>(tid, i), p.C, v[i], p.out == 1);
         }
         return;
@@ -143,7 +150,7 @@ __global__ __launch_bounds__(TPR < kLayerThreads ? kLayerThreads : TPR) void nor
     top = row_reduce<TPR>(top, reinterpret_cast<unsigned*>(red), MaxBits());
     const float amax = __uint_as_float(top), Q = p.out == 2 ? 127.f : 448.f;
     const bool codes = top != 0 && top < 0x7f800000u;
-    if (tid == 0) p.scale[row] = codes ? amax * rstd / Q : top == 0 ? 0.f : __builtin_nanf("");
+    if (tid == 0) p.scale[row] = codes ? amax * n.by * n.rstd / Q : top == 0 ? 0.f : __builtin_nanf("");
     const int e = codes ? __builtin_amdgcn_frexp_expf(amax) : 0;
     const float m = codes ? __builtin_amdgcn_ldexpf(amax, -e) : 1.f, inv = __builtin_amdgcn_rcpf(m);
     uint8_t* y = (uint8_t*)p.y + at;
@@ -250,40 +257,39 @@ __global__ __launch_bounds__(TPR < kLayerThreads ? kLayerThreads : TPR) void nor
                 ng.load(dy + step * p.C, tid, p.C);
             }
         }
+        float by = 1.f;
         auto group = [&](int i) {                 // s, dy and the weights of the i-th group, in v, g, w[h]
             if constexpr (!kHeld) {
                 const int c = norm_col<TPR>(tid, i);
                 norm_load8(v[0], s, c, p.C);
+                if (by != 1.f) norm_scale(v, by);
                 norm_load8(g[0], dy, c, p.C);
                 norm_weight(w[0], p, c);
             }
             return kHeld ? i : 0;
         };
-        auto sums = [&](float shrink) {
+        auto sums = [&]() {
             Sums x = {0.f, 0.f};
 #pragma unroll
             for (int i = 0; i < NC; ++i) {
                 const int h = group(i);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float u = v[h][j] * shrink;
-                    x.square = __builtin_fmaf(u, u, x.square);
-                    x.dot = __builtin_fmaf(w[h][j] * g[h][j], u, x.dot);
+                    x.square = __builtin_fmaf(v[h][j], v[h][j], x.square);
+                    x.dot = __builtin_fmaf(w[h][j] * g[h][j], v[h][j], x.dot);
                 }
             }
             return row_sums<TPR>(x, red);
         };
-        float shrink = 1.f, rstd;
-        Sums x = sums(1.f);
-        if (norm_overflows(x.square)) {
-            shrink = kNormShrink;
-            x = sums(shrink);
-            rstd = 1.f / sqrtf(x.square / (float)p.C);
-        } else {
-            rstd = 1.f / sqrtf(x.square / (float)p.C + p.eps);
+        Sums x = sums();
+        by = norm_scale_by(norm_mean_eps(x.square, p, 1.f));
+        if (by != 1.f) {
+            if constexpr (kHeld) norm_scale(v, by);
+            x = sums();
         }
+        const float rstd = 1.f / sqrtf(norm_mean_eps(x.square, p, by));
         const float mean = x.dot * rstd / (float)p.C;       // of w dy and the normed row
-        rstd *= shrink;
+        const float slope = rstd * by;
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int h = group(i), c = norm_col<TPR>(tid, i);
@@ -292,7 +298,7 @@ __global__ __launch_bounds__(TPR < kLayerThreads ? kLayerThreads : TPR) void nor
             for (int j = 0; j < 8; ++j) {
                 const float xh = v[h][j] * rstd;
                 acc[i][j] = __builtin_fmaf(g[h][j], xh, acc[i][j]);
-                dx[j] = rstd * (w[h][j] * g[h][j] - xh * mean);
+                dx[j] = slope * (w[h][j] * g[h][j] - xh * mean);
             }
             if (p.ds) {
                 if constexpr (kHeld) nds.r[i].get(e);

@@ -452,7 +452,8 @@ void kda_norm_config_init(kda_norm_config* cfg, int32_t C);
 /* Root-mean-square norm of rows, with the residual's addition:
  *     s = x + residual,   y = s weight / sqrt(mean(s^2) + eps)
  * s is rounded to res_dtype once and the norm is of the rounded row, so that a
- * backward from the stored s is that of this forward.
+ * backward from the stored s is that of this forward.  Rows whose squares leave
+ * fp32's range are summed scaled, so that every finite row has its norm.
  *   x, y : [rows, C]    residual, s : [rows, C]    weight : [C] or NULL (ones)
  * residual NULL: s = x (res_dtype must be in_dtype then) and `s` is not written.
  * s NULL: the sum is not kept.  s may be residual or x themselves, y may be x,

@@ -131,6 +131,44 @@ def test_zero_rows_without_eps(C):
         assert scale[1] == 0 and (codes[1].float() == 0).all() and (scale[[0, 2]] > 0).all()
 
 
+@pytest.mark.parametrize("C", [64, 1000, 4096, 8200, 12001])
+@pytest.mark.parametrize("eps", [0.0, 1e-30])
+def test_rows_whose_squares_leave_the_range(C, eps):
+    """Rows of 2^-110 to 2^126: their squares are zeros, of few bits, or infinite in fp32."""
+    need_gpu()
+    powers = [-110, -90, -70, -64, -60, -50, -40, 0, 60, 64, 100, 124]
+    x = rand(len(powers), C, F32, 3).clamp(-3.9, 3.9) * torch.tensor([2.0 ** p for p in powers], device="cuda")[:, None]
+    w = 1 + 0.2 * rand(1, C, F32, 4)[0]
+    y, _ = kda.kda_norm_fwd(x, w, eps=eps)
+    eps = float(np.float32(eps))
+    want, rstd = ref.norm_fwd(host(x), host(w), eps)
+    # a product may fall below the normal range, where it is held in steps of 2^-149
+    assert (np.abs(host(y) - want) <= (np.abs(want) * (ref.RSTD + 3) * ref.U + 2.0 ** -149) * 1.01).all()
+    for out, limit in ((torch.int8, 127), (torch.float8_e4m3fn, 448)):
+        _, _, scale = kda.kda_norm_fwd(x, w, eps=eps, out_dtype=out)
+        top = ref.codes(x.cpu().numpy(), w.cpu().numpy(), limit)[1]
+        want = (top * rstd / limit)[:, 0]
+        assert (np.abs(host(scale) - want) <= want * (ref.RSTD + 3) * ref.U * 1.01).all()
+    dy, ds = rand(len(powers), C, F32, 5), rand(len(powers), C, F32, 6)
+    d = kda.kda_norm_bwd(x, w, dy, ds, eps=eps)
+    args = host(x), host(w), host(dy), host(ds), eps
+    (dx, dw), (dxm, dwm) = ref.norm_bwd(*args), ref.norm_bwd_bound(*args)
+    assert (np.abs(host(d["dx"]) - dx) <= (dxm + np.abs(dx) * ref.U + 2.0 ** -149) * 1.01).all()
+    assert (np.abs(host(d["dw"]) - dw) <= (dwm + 2.0 ** -149 * len(powers)) * 1.01).all()
+
+
+@pytest.mark.parametrize("types", [(F32, F32), (BF16, BF16)])
+def test_gradients_of_both_terms_do_not_share_memory(types):
+    need_gpu()
+    x, r = rand(3, 64, types[0], 1).requires_grad_(), rand(3, 64, types[1], 2).requires_grad_()
+    y, s = kda.kda_norm(x, None, r, eps=EPS)
+    (y.sum() + s.sum()).backward()
+    assert torch.equal(x.grad, r.grad) and x.grad.data_ptr() != r.grad.data_ptr()
+    kept = r.grad.clone()
+    x.grad.zero_()
+    assert torch.equal(r.grad, kept)
+
+
 def test_in_place_and_no_rows():
     need_gpu()
     for C in (64, 333, 4096):
