@@ -217,7 +217,6 @@ __device__ __forceinline__ void store_out(void* p, int64_t i, float x, bool as_b
 
 hipError_t launch_norm_fwd(const NormParams& p, int in_bf16, int res_bf16, hipStream_t stream);
 hipError_t launch_norm_bwd(const NormParams& p, int in_bf16, int res_bf16, float* dw, hipStream_t stream);
-int64_t norm_bwd_parts(int32_t C, int64_t rows);
 int norm_bwd_blocks(int32_t C, int64_t rows);
 hipError_t launch_conv_fwd(const ConvParams& p, int W, int in_bf16, hipStream_t stream);
 hipError_t launch_conv_bwd(const ConvParams& p, int W, int in_bf16, float* dw, float* db, hipStream_t stream);

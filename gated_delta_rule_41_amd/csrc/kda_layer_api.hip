@@ -260,7 +260,7 @@ kda_status kda_norm_fwd(const kda_norm_config* cfg, int64_t rows, const void* x,
 
 size_t kda_norm_bwd_workspace_size(const kda_norm_config* cfg, int64_t rows) {
     if (check_norm(cfg, rows, true) != KDA_OK) return 0;
-    return (size_t)norm_bwd_parts(cfg->C, rows) * cfg->C * sizeof(float);
+    return (size_t)norm_bwd_blocks(cfg->C, rows) * cfg->C * sizeof(float);
 }
 
 kda_status kda_norm_bwd(const kda_norm_config* cfg, int64_t rows, const void* s, const void* weight, const void* dy,

@@ -309,23 +309,48 @@ __global__ __launch_bounds__(TPR < kLayerThreads ? kLayerThreads : TPR) void nor
             norm_store8(p.dx, at, c, p.C, dx, p.out == 1);
         }
     }
-    if (p.dw_part)
+    if (!p.dw_part) return;
+    if constexpr (RPB > 1) {                      // the workgroup's rows together: over a wave's lanes, then its waves in order
+        __shared__ float waves[kLayerThreads / 64][TPR * NC * 8];
+        const int wave = threadIdx.x >> 6;
 #pragma unroll
-        for (int i = 0; i < NC; ++i) norm_store8(p.dw_part, first * p.C, norm_col<TPR>(tid, i), p.C, acc[i], false);
+        for (int i = 0; i < NC; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+#pragma unroll
+                for (int m = TPR; m < 64; m <<= 1) acc[i][j] += __shfl_xor(acc[i][j], m, 64);
+                if ((threadIdx.x & 63) < TPR) waves[wave][(i * 8 + j) * TPR + tid] = acc[i][j];
+            }
+        __syncthreads();
+        if (threadIdx.x >= TPR) return;
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+#pragma unroll
+                for (int w = 1; w < kLayerThreads / 64; ++w) acc[i][j] += waves[w][(i * 8 + j) * TPR + tid];
+            }
+    }
+#pragma unroll
+    for (int i = 0; i < NC; ++i) norm_store8(p.dw_part, (int64_t)blockIdx.x * p.C, norm_col<TPR>(tid, i), p.C, acc[i], false);
 }
 
-// One workgroup for 64 columns: 16 waves take every 16th row, then their sums in order.
-__global__ __launch_bounds__(1024) void part_sums_kernel(PartSums s) {
-    __shared__ float sum[16][64];
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    const int64_t cols = (int64_t)s.K * s.C, col = (int64_t)blockIdx.x * 64 + lane;
+// One workgroup for COLS columns: its 1024 / COLS rows of threads take every so many rows, then their sums: over a wave's
+// lanes, and its waves in order.
+template <int COLS> __global__ __launch_bounds__(1024) void part_sums_kernel(PartSums s) {
+    constexpr int ROWS = 1024 / COLS;
+    __shared__ float sum[16][COLS];
+    const int lane = threadIdx.x % COLS, w = threadIdx.x >> 6;
+    const int64_t cols = (int64_t)s.K * s.C, col = (int64_t)blockIdx.x * COLS + lane;
     float x = 0.f;
     if (col < cols)
 #pragma unroll 8
-        for (int64_t r = w; r < s.parts; r += 16) x += s.part[r * cols + col];
-    sum[w][lane] = x;
+        for (int64_t r = threadIdx.x / COLS; r < s.parts; r += ROWS) x += s.part[r * cols + col];
+#pragma unroll
+    for (int m = COLS; m < 64; m <<= 1) x += __shfl_xor(x, m, 64);
+    if ((threadIdx.x & 63) < COLS) sum[w][lane] = x;
     __syncthreads();
-    if (w || col >= cols) return;
+    if (threadIdx.x >= COLS || col >= cols) return;
 #pragma unroll
     for (int i = 1; i < 16; ++i) x += sum[i][lane];
     const int k = (int)(col / s.C), c = (int)(col % s.C);
@@ -334,7 +359,10 @@ __global__ __launch_bounds__(1024) void part_sums_kernel(PartSums s) {
 }
 hipError_t launch_part_sums(const PartSums& s, hipStream_t stream) {
     const int64_t cols = (int64_t)s.K * s.C;
-    hipLaunchKernelGGL(part_sums_kernel, dim3((unsigned)((cols + 63) / 64)), dim3(1024), 0, stream, s);
+    // Few columns take more workgroups of narrower pieces.  us for 16 and 64 columns a workgroup: 128 columns of 1024
+    // parts 4.6 and 6.9, 4096 of 512 5.0 and 5.2, 9216 of 256 4.5 and 3.8, 73728 of 171 25.1 and 13.7.
+    if (cols > 4096) hipLaunchKernelGGL((part_sums_kernel<64>), dim3((unsigned)((cols + 63) / 64)), dim3(1024), 0, stream, s);
+    else hipLaunchKernelGGL((part_sums_kernel<16>), dim3((unsigned)((cols + 15) / 16)), dim3(1024), 0, stream, s);
     return hipGetLastError();
 }
 
@@ -381,7 +409,7 @@ hipError_t launch_norm_fwd(const NormParams& p, int in_bf16, int res_bf16, hipSt
     return norm_any(p, in_bf16, res_bf16, false, stream);
 }
 
-// Rows of partial sums of dw: one for each row that a workgroup has at a time.  As many workgroups as the compute units
+// Rows of partial sums of dw: one a workgroup.  As many workgroups as the compute units
 // hold at once, so that all go over as many rows: bf16, 2^27 values, us for 256, 512, 768, 1024, 1280 workgroups:
 // 512 channels 545, 331, 256, 230, 219;  1024: 275, 200, 211, 242, 233;  768: 549, 327, 251, 339, 299;  2048: 525, 329,
 // 251, 218, 201;  4096: 264, 191, 199, 233, 213;  8192: 201, 206, 210, 213, 217.
@@ -391,14 +419,13 @@ int norm_bwd_blocks(int32_t C, int64_t rows) {
     const int64_t most = 256 * (C <= 512 ? 4 : C <= 1024 ? 3 : C <= 2048 ? 4 : C <= 4096 ? 2 : 1);
     return (int)(groups < most ? groups : most);
 }
-int64_t norm_bwd_parts(int32_t C, int64_t rows) { return (int64_t)norm_bwd_blocks(C, rows) * norm_rows_at_once(C); }
 hipError_t launch_norm_bwd(const NormParams& p, int in_bf16, int res_bf16, float* dw, hipStream_t stream) {
     if (p.rows) {
         const hipError_t e = norm_any(p, in_bf16, res_bf16, true, stream);
         if (e != hipSuccess) return e;
     }
     if (!dw) return hipSuccess;
-    const PartSums s = {p.dw_part, norm_bwd_parts(p.C, p.rows), 1, p.C, 1, dw, {nullptr, nullptr}};
+    const PartSums s = {p.dw_part, norm_bwd_blocks(p.C, p.rows), 1, p.C, 1, dw, {nullptr, nullptr}};
     return launch_part_sums(s, stream);
 }
 
