@@ -3,30 +3,63 @@
 //     s = x + residual,  y = s w rstd,  rstd = 1 / sqrt(mean(s^2) + eps)
 //     dx = rstd (w dy - s rstd^2 mean(w dy s)) + ds,  dw = sum over rows of dy s rstd
 // A row is read once into registers, summed across its lanes, and written: the bytes bound it.
+// bf16, with a residual, 16411 x 4096 take 76 us (7.1 TB/s, the last cache's share in it), the
+// backward of 32768 x 4096 193 (5.6 TB/s).
 #include "kda_layer.h"
 
 namespace kda {
 
-// A thread's i-th eight channels begin at (tid + TPR i) 8; a row's last eight may be fewer.
+// A thread's i-th eight channels begin at (tid + TPR i) 8; a row's last eight may be fewer.  Every thread loads eight
+// channels, the row's last ones where its own are not all there, and puts them right when they have come.  LOOP: threads
+// behind the row load too, for rows asked for early: zeros written in a branch beside a load wait for that load (backward
+// of 26214 x 2560 187 us so, 119 without; 209715 x 320 176 and 104).  Where nothing is early they load nothing (forward of
+// 52428 x 1280 90, and 94 if they do).
 template <int TPR> __device__ __forceinline__ int norm_col(int tid, int i) { return (tid + TPR * i) * 8; }
-template <typename T> __device__ __forceinline__ void norm_load8(float (&v)[8], const T* row, int c, int C) {
-    if (c + 8 <= C) {
-        load8(v, row + c);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = c + j < C ? to_f32(row[c + j]) : 0.f;
+template <typename T, bool LOOP> struct NormEight : Raw8<T> {
+    __device__ __forceinline__ void ask(const T* row, int c, int C) {
+        if (LOOP || (c < C && C >= 8)) this->load(row + (c + 8 <= C ? c : C - 8));
     }
-}
-template <typename T, int TPR, int NC> __device__ __forceinline__ void norm_load(float (&v)[NC][8], const T* row, int tid, int C) {
+    __device__ __forceinline__ void take(float (&v)[8], const T* row, int c, int C) const {
+        this->get(v);
+        if (c + 8 <= C) return;
+        if (!LOOP && C < 8) {                     // too short for pieces of eight: read here; such rows are not asked for early
 #pragma unroll
-    for (int i = 0; i < NC; ++i) norm_load8(v[i], row, norm_col<TPR>(tid, i), C);
+            for (int j = 0; j < 8; ++j) v[j] = to_f32(row[j < C ? j : 0]);
+        } else {
+            const int by = 8 - (C & 7);           // the same for the whole row's end; 8: a row of whole pieces
+#pragma unroll
+            for (int m = 4; m; m >>= 1)
+                if (by & m)
+#pragma unroll
+                    for (int j = 0; j + m < 8; ++j) v[j] = v[j + m];
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = c + j < C ? v[j] : 0.f;
+    }
+};
+template <typename T> __device__ __forceinline__ void norm_load8(float (&v)[8], const T* row, int c, int C) {
+    NormEight<T, false> r;
+    r.ask(row, c, C);
+    r.take(v, row, c, C);
 }
+// A row's groups as they lie in memory, to be asked for early.
+template <typename T, int TPR, int NC, bool LOOP> struct NormRow {
+    NormEight<T, LOOP> r[NC];
+    __device__ __forceinline__ void load(const T* row, int tid, int C) {
+#pragma unroll
+        for (int i = 0; i < NC; ++i) r[i].ask(row, norm_col<TPR>(tid, i), C);
+    }
+    __device__ __forceinline__ void get(float (&v)[NC][8], const T* row, int tid, int C) const {
+#pragma unroll
+        for (int i = 0; i < NC; ++i) r[i].take(v[i], row, norm_col<TPR>(tid, i), C);
+    }
+};
 __device__ __forceinline__ void norm_store8(void* base, int64_t at, int c, int C, const float (&v)[8], bool as_bf16) {
     if (c + 8 <= C) {
         store8_out<true>(base, at + c, v, as_bf16);
-    } else {
+    } else if (c < C) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < 7; ++j)
             if (c + j < C) store_out(base, at + c + j, v[j], as_bf16);
     }
 }
@@ -110,10 +143,14 @@ __global__ __launch_bounds__(TPR < kLayerThreads ? kLayerThreads : TPR) void nor
     if (row >= p.rows) return;                   // a row of several waves is a workgroup of its own
     const int64_t at = row * p.C;
     float v[NC][8];
-    norm_load<TI, TPR, NC>(v, (const TI*)p.x + at, tid, p.C);
+    NormRow<TI, TPR, NC, false> x;
+    NormRow<TR, TPR, NC, false> res;
+    x.load((const TI*)p.x + at, tid, p.C);
+    if (p.residual) res.load((const TR*)p.residual + at, tid, p.C);
+    x.get(v, (const TI*)p.x + at, tid, p.C);
     if (p.residual) {
         float r[NC][8];
-        norm_load<TR, TPR, NC>(r, (const TR*)p.residual + at, tid, p.C);
+        res.get(r, (const TR*)p.residual + at, tid, p.C);
 #pragma unroll
         for (int i = 0; i < NC; ++i)
 #pragma unroll
@@ -171,30 +208,13 @@ __global__ __launch_bounds__(TPR < kLayerThreads ? kLayerThreads : TPR) void nor
         if (c + 8 <= p.C) {
             typedef u32x2 __attribute__((aligned(1))) codes8;
             __builtin_nontemporal_store(u32x2{word[0], word[1]}, reinterpret_cast<codes8*>(y + c));
-        } else {
+        } else if (c < p.C) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
+            for (int j = 0; j < 7; ++j)
                 if (c + j < p.C) y[c + j] = (uint8_t)(word[j >> 2] >> (8 * (j & 3)));
         }
     }
 }
-
-// A row's groups as they lie in memory, to be asked for early.
-template <typename T, int TPR, int NC> struct NormRow {
-    Raw8<T> r[NC];
-    __device__ __forceinline__ void load(const T* row, int tid, int C) {
-#pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            const int c = norm_col<TPR>(tid, i);
-            if (c + 8 <= C) {
-                r[i].load(row + c);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) r[i].set(j, c + j < C ? row[c + j] : T(0.f));
-            }
-        }
-    }
-};
 
 struct Sums { float square, dot; };
 struct AddSums { __device__ Sums operator()(Sums a, Sums b) const { return {a.square + b.square, a.dot + b.dot}; } };
@@ -214,14 +234,15 @@ template <int TPR> __device__ __forceinline__ Sums row_sums(Sums x, Sums* red) {
 }
 
 // dx = rstd (w dy - s rstd^2 mean(w dy s)) + ds: both sums of a row come from one pass over it.  A workgroup goes over
-// rows gridDim apart and keeps its sums for dw in registers.  Up to two groups of eight channels a thread stay there as
-// well, the weights too, with the next row's s and dy and this one's ds on their way; rows of more channels are read
-// again from the caches.
+// rows gridDim apart and keeps its sums for dw in registers.  Up to three groups of eight channels a thread stay there as
+// well, the weights too, with the next row's s and dy on their way, which have to be there before this row's dx is
+// stored: a later wait for them would be one for the stores as well (209715 x 320 bf16 162 -> 143 us).  Rows above 12288
+// channels are read again from the caches.
 template <typename TI, typename TR, int TPR, int NC>
 __global__ __launch_bounds__(TPR < kLayerThreads ? kLayerThreads : TPR) void norm_bwd_kernel(NormParams p) {
     constexpr int RPB = TPR < kLayerThreads ? kLayerThreads / TPR : 1;
-    constexpr bool kHeld = TPR < 1024;
-    static_assert(!kHeld || NC <= 2, "a held row has up to two groups a thread");
+    constexpr bool kHeld = TPR <= 512;
+    static_assert(!kHeld || NC <= 3, "a held row has up to three groups a thread");
     constexpr int H = kHeld ? NC : 1;
     __shared__ Sums red[TPR > 64 ? TPR / 64 : 1];
     const int tid = threadIdx.x % TPR;
@@ -231,8 +252,8 @@ __global__ __launch_bounds__(TPR < kLayerThreads ? kLayerThreads : TPR) void nor
     for (int i = 0; i < NC; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
-    NormRow<TR, TPR, H> ns, nds;
-    NormRow<TI, TPR, H> ng;
+    NormRow<TR, TPR, H, true> ns, nds;
+    NormRow<TI, TPR, H, true> ng;
     if constexpr (kHeld) {
 #pragma unroll
         for (int i = 0; i < NC; ++i) norm_weight(w[i], p, norm_col<TPR>(tid, i));
@@ -246,11 +267,8 @@ __global__ __launch_bounds__(TPR < kLayerThreads ? kLayerThreads : TPR) void nor
         const TR* s = (const TR*)p.x + at;
         const TI* dy = (const TI*)p.dy + at;
         if constexpr (kHeld) {
-#pragma unroll
-            for (int i = 0; i < NC; ++i) {
-                ns.r[i].get(v[i]);
-                ng.r[i].get(g[i]);
-            }
+            ns.get(v, s, tid, p.C);
+            ng.get(g, dy, tid, p.C);
             if (p.ds) nds.load((const TR*)p.ds + at, tid, p.C);
             if (row + step < p.rows) {
                 ns.load(s + step * p.C, tid, p.C);
@@ -293,7 +311,7 @@ __global__ __launch_bounds__(TPR < kLayerThreads ? kLayerThreads : TPR) void nor
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int h = group(i), c = norm_col<TPR>(tid, i);
-            float dx[8], e[8];
+            float (&dx)[8] = kHeld ? v[h] : v[0], e[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float xh = v[h][j] * rstd;
@@ -301,12 +319,18 @@ __global__ __launch_bounds__(TPR < kLayerThreads ? kLayerThreads : TPR) void nor
                 dx[j] = slope * (w[h][j] * g[h][j] - xh * mean);
             }
             if (p.ds) {
-                if constexpr (kHeld) nds.r[i].get(e);
+                if constexpr (kHeld) nds.r[i].take(e, (const TR*)p.ds + at, c, p.C);
                 else norm_load8(e, (const TR*)p.ds + at, c, p.C);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) dx[j] += e[j];
             }
-            norm_store8(p.dx, at, c, p.C, dx, p.out == 1);
+            if constexpr (!kHeld) norm_store8(p.dx, at, c, p.C, dx, p.out == 1);
+        }
+        if constexpr (kHeld) {
+#pragma unroll
+            for (int i = 0; i < NC; ++i) { ns.r[i].arrived(); ng.r[i].arrived(); }
+#pragma unroll
+            for (int i = 0; i < NC; ++i) norm_store8(p.dx, at, norm_col<TPR>(tid, i), p.C, v[i], p.out == 1);
         }
     }
     if (!p.dw_part) return;
@@ -367,8 +391,10 @@ hipError_t launch_part_sums(const PartSums& s, hipStream_t stream) {
 }
 
 // ---------------------------------------------------------------- launches
-// A row's threads and groups of eight channels a thread.  The backward keeps five values a channel and rows on their
-// way; 32768 x 4096 bf16 takes 191 us with 256 threads and two groups, 201 with 512 and one.
+// A row's threads and groups of eight channels a thread: few threads without channels, and in the backward, which keeps
+// five values a channel and rows on their way, up to 24 channels each.  bf16, 2^26 values: 1280 channels 104 us with 64
+// threads and three groups, 139 with 192 and one; 5120: 102 with 256 and three, 112 with 320 and two; 12288: 183 with 1024
+// and two, read again.
 template <typename TI, typename TR, int TPR, int NC> static void norm_fwd_launch(const NormParams& p, hipStream_t stream) {
     constexpr int threads = TPR < kLayerThreads ? kLayerThreads : TPR, RPB = threads / TPR;
     hipLaunchKernelGGL((norm_fwd_kernel<TI, TR, TPR, NC>), dim3((unsigned)((p.rows + RPB - 1) / RPB)), dim3(threads), 0, stream, p);
@@ -380,13 +406,19 @@ template <typename TI, typename TR, int TPR, int NC> static void norm_bwd_launch
 template <typename TI, typename TR> static void norm_types(const NormParams& p, bool backward, hipStream_t stream) {
     const int C = p.C;
     if (backward) {
-        if (C <= 128) norm_bwd_launch<TI, TR, 16, 1>(p, stream);
+        if (C < 8) norm_bwd_launch<TI, TR, 1024, 2>(p, stream);    // read where they are used, element by element
+        else if (C <= 128) norm_bwd_launch<TI, TR, 16, 1>(p, stream);
         else if (C <= 256) norm_bwd_launch<TI, TR, 32, 1>(p, stream);
+        else if (C <= 384) norm_bwd_launch<TI, TR, 16, 3>(p, stream);
         else if (C <= 512) norm_bwd_launch<TI, TR, 64, 1>(p, stream);
+        else if (C <= 768) norm_bwd_launch<TI, TR, 32, 3>(p, stream);
         else if (C <= 1024) norm_bwd_launch<TI, TR, 64, 2>(p, stream);
+        else if (C <= 1536) norm_bwd_launch<TI, TR, 64, 3>(p, stream);
         else if (C <= 2048) norm_bwd_launch<TI, TR, 256, 1>(p, stream);
         else if (C <= 4096) norm_bwd_launch<TI, TR, 256, 2>(p, stream);
+        else if (C <= 6144) norm_bwd_launch<TI, TR, 256, 3>(p, stream);
         else if (C <= 8192) norm_bwd_launch<TI, TR, 512, 2>(p, stream);
+        else if (C <= 12288) norm_bwd_launch<TI, TR, 512, 3>(p, stream);
         else norm_bwd_launch<TI, TR, 1024, 2>(p, stream);
     } else {
         if (C <= 128) norm_fwd_launch<TI, TR, 16, 1>(p, stream);
@@ -409,14 +441,15 @@ hipError_t launch_norm_fwd(const NormParams& p, int in_bf16, int res_bf16, hipSt
     return norm_any(p, in_bf16, res_bf16, false, stream);
 }
 
-// Rows of partial sums of dw: one a workgroup.  As many workgroups as the compute units
-// hold at once, so that all go over as many rows: bf16, 2^27 values, us for 256, 512, 768, 1024, 1280 workgroups:
-// 512 channels 545, 331, 256, 230, 219;  1024: 275, 200, 211, 242, 233;  768: 549, 327, 251, 339, 299;  2048: 525, 329,
-// 251, 218, 201;  4096: 264, 191, 199, 233, 213;  8192: 201, 206, 210, 213, 217.
-static int norm_rows_at_once(int32_t C) { return C <= 128 ? 16 : C <= 256 ? 8 : C <= 1024 ? 4 : 1; }
+// Workgroups, each with one row of partial sums of dw: as many as the compute units hold at once, so that all go over as
+// many rows.  bf16, 2^26 values, us for 1, 2, 3, 4 on a compute unit:  128 channels 300, 176, 136, 121 (100 channels);
+// 200: 213, 127, 110, 145;  384: 115, 103, 116, 107;  512: 171, 112, 100, 121;  768: 115, 104, 115, 107;  1000: 145, 101,
+// 119, 107;  1280: 139, 104, 121, 107;  2048: 148, 112, 101, 122;  4096: 111, 101, 115, 107;  5120: 122, 102, 119, 108;
+// 8192: 98, 102, 106, 113.  Moving the bytes takes 104 at a large copy's rate.
+static int norm_rows_at_once(int32_t C) { return C < 8 ? 1 : C <= 128 ? 16 : C <= 256 ? 8 : C <= 384 ? 16 : C <= 512 ? 4 : C <= 768 ? 8 : C <= 1536 ? 4 : 1; }
 int norm_bwd_blocks(int32_t C, int64_t rows) {
     const int64_t groups = (rows + norm_rows_at_once(C) - 1) / norm_rows_at_once(C);
-    const int64_t most = 256 * (C <= 512 ? 4 : C <= 1024 ? 3 : C <= 2048 ? 4 : C <= 4096 ? 2 : 1);
+    const int64_t most = 256 * (C < 8 ? 1 : C <= 128 ? 4 : C <= 256 ? 3 : C <= 384 ? 2 : C <= 512 ? 3 : C <= 1536 ? 2 : C <= 2048 ? 3 : C <= 6144 ? 2 : 1);
     return (int)(groups < most ? groups : most);
 }
 hipError_t launch_norm_bwd(const NormParams& p, int in_bf16, int res_bf16, float* dw, hipStream_t stream) {

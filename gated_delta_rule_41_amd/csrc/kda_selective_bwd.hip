@@ -7,7 +7,8 @@
 // lane (kda_selective.h), so sums over the state's entries stay in a lane, and dB and dC are sums
 // over the lanes of a wave; the waves' shares are added by a last launch.  An entry and token
 // costs 15 multiplies and multiply-adds, two exponentials and its share of 70 exchanges and
-// additions: vector instructions bound the kernel.
+// additions: vector instructions bound the kernel, which takes 924 us for 4 x 4096 tokens x 4096
+// channels of 16 entries (bf16, gated) where their issue alone would take 714.
 #include "kda_selective.h"
 
 namespace kda {

@@ -206,6 +206,14 @@ def test_backward(rows, C, types):
     assert d["dw"] is None and (np.abs(host(d["dx"]) - dx) <= (dxm + np.abs(dx) * ref.U) * 1.01).all()
 
 
+@pytest.mark.parametrize("rows,C", [(5, 2), (5, 8), (9000, 9), (17, 15), (40, 130), (9000, 320), (33, 377), (9, 384), (2500, 640), (2100, 761), (2100, 1280),
+                                    (9, 1529), (1100, 2560), (600, 5120), (7, 6137), (300, 10240), (3, 12281)])
+@pytest.mark.parametrize("types", [(BF16, BF16, BF16), (BF16, F32, F32), (F32, F32, F32)])
+def test_backward_of_every_split(rows, C, types):
+    """Each number of threads and groups a row, with rows for more than one turn, with ends of less than eight channels."""
+    test_backward(rows, C, types)
+
+
 def test_autograd():
     need_gpu()
     x, r, w = rand(6, 96, F32, 1).requires_grad_(), rand(6, 96, F32, 2).requires_grad_(), rand(1, 96, F32, 3)[0].requires_grad_()
