@@ -139,13 +139,13 @@ __device__ __forceinline__ float softplus(float v) {
 }
 
 // Eight channels side by side as they lie in memory, at any address: global memory takes 16-byte accesses at the
-// alignment of an element.  (fp32 ones are two vectors of four: of eight in one, this compiler lost the upper half
-// where several branches load it.)
+// alignment of an element.
 template <typename T> struct Raw8;
 template <> struct Raw8<bf16> {
     typedef bf16x8 __attribute__((aligned(2))) Any;
     bf16x8 r;
     __device__ __forceinline__ void load(const bf16* p) { r = *reinterpret_cast<const Any*>(p); }
+    __device__ __forceinline__ void set(int j, bf16 x) { r[j] = x; }
     __device__ __forceinline__ void arrived() { asm volatile("" : "+v"(r)); }   // waits for the load here
     __device__ __forceinline__ void get(float (&v)[8]) const {
         const f32x4 a = unpack4(__builtin_shufflevector(r, r, 0, 1, 2, 3)), b = unpack4(__builtin_shufflevector(r, r, 4, 5, 6, 7));
@@ -159,6 +159,10 @@ template <> struct Raw8<float> {
     __device__ __forceinline__ void load(const float* p) {
         a = *reinterpret_cast<const Any*>(p);
         b = *reinterpret_cast<const Any*>(p + 4);
+    }
+    __device__ __forceinline__ void set(int j, float x) {
+        if (j < 4) a[j] = x;
+        else b[j - 4] = x;
     }
     __device__ __forceinline__ void arrived() { asm volatile("" : "+v"(a), "+v"(b)); }
     __device__ __forceinline__ void get(float (&v)[8]) const {

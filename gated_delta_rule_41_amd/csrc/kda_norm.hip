@@ -10,22 +10,29 @@
 namespace kda {
 
 // A thread's i-th eight channels begin at (tid + TPR i) 8; a row's last eight may be fewer.  Every thread loads eight
-// channels, the row's last ones where its own are not all there, and puts them right when they have come.  LOOP: threads
-// behind the row load too, for rows asked for early: zeros written in a branch beside a load wait for that load (backward
-// of 26214 x 2560 187 us so, 119 without; 209715 x 320 176 and 104).  Where nothing is early they load nothing (forward of
-// 52428 x 1280 90, and 94 if they do).
+// channels, the row's last ones where its own are not all there, and puts them right when they have come.  kEarly, for rows
+// asked for early: threads behind the row load too, as zeros written in a branch beside a load wait for that load (backward
+// of 26214 x 2560 187 us so, 119 without; 209715 x 320 176 and 104).  kHere: where nothing is early they load nothing
+// (forward of 52428 x 1280 90, and 94 if they do).  kShort: early rows of fewer than eight channels, which have no eight to
+// load, element by element.
+enum NormWay { kHere, kEarly, kShort };
 template <int TPR> __device__ __forceinline__ int norm_col(int tid, int i) { return (tid + TPR * i) * 8; }
-template <typename T, bool LOOP> struct NormEight : Raw8<T> {
+template <typename T, int WAY> struct NormEight : Raw8<T> {
     __device__ __forceinline__ void ask(const T* row, int c, int C) {
-        if (LOOP || (c < C && C >= 8)) this->load(row + (c + 8 <= C ? c : C - 8));
+        if constexpr (WAY == kShort) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) this->set(j, row[c + j < C ? c + j : 0]);
+        } else if (WAY == kEarly || (c < C && C >= 8)) {
+            this->load(row + (c + 8 <= C ? c : C - 8));
+        }
     }
     __device__ __forceinline__ void take(float (&v)[8], const T* row, int c, int C) const {
         this->get(v);
-        if (c + 8 <= C) return;
-        if (!LOOP && C < 8) {                     // too short for pieces of eight: read here; such rows are not asked for early
+        if (WAY != kShort && c + 8 <= C) return;
+        if (WAY == kHere && C < 8) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] = to_f32(row[j < C ? j : 0]);
-        } else {
+        } else if (WAY != kShort) {
             const int by = 8 - (C & 7);           // the same for the whole row's end; 8: a row of whole pieces
 #pragma unroll
             for (int m = 4; m; m >>= 1)
@@ -38,13 +45,13 @@ template <typename T, bool LOOP> struct NormEight : Raw8<T> {
     }
 };
 template <typename T> __device__ __forceinline__ void norm_load8(float (&v)[8], const T* row, int c, int C) {
-    NormEight<T, false> r;
+    NormEight<T, kHere> r;
     r.ask(row, c, C);
     r.take(v, row, c, C);
 }
 // A row's groups as they lie in memory, to be asked for early.
-template <typename T, int TPR, int NC, bool LOOP> struct NormRow {
-    NormEight<T, LOOP> r[NC];
+template <typename T, int TPR, int NC, int WAY> struct NormRow {
+    NormEight<T, WAY> r[NC];
     __device__ __forceinline__ void load(const T* row, int tid, int C) {
 #pragma unroll
         for (int i = 0; i < NC; ++i) r[i].ask(row, norm_col<TPR>(tid, i), C);
@@ -63,14 +70,30 @@ __device__ __forceinline__ void norm_store8(void* base, int64_t at, int c, int C
             if (c + j < C) store_out(base, at + c + j, v[j], as_bf16);
     }
 }
+// Fewer than eight weights in fp32 by constant indexes, each behind its own test: at j < C ? j : 0, the same for all lanes,
+// this compiler made scalar loads with half of the byte offset in the base, where bf16 has all of it, and half in the
+// index, and a scalar load drops the two lowest bits of each, so that elements 1, 3 and 5 were their neighbours.  (bf16
+// has no scalar loads; by tests the forward of 1048576 x 7 takes 103 us, 91 without.)
+template <typename T> __device__ __forceinline__ void norm_weight(float (&w)[8], const NormParams& p, int c) {
+    const T* weight = (const T*)p.weight;
+    if (sizeof(T) == 2 || p.C >= 8) {
+        norm_load8(w, weight, c, p.C);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            w[j] = 0.f;
+            if (c + j < p.C) w[j] = to_f32(weight[j]);   // c is 0
+        }
+    }
+}
 __device__ __forceinline__ void norm_weight(float (&w)[8], const NormParams& p, int c) {
     if (!p.weight) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) w[j] = 1.f;
     } else if (p.weight_bf16) {
-        norm_load8(w, (const bf16*)p.weight, c, p.C);
+        norm_weight<bf16>(w, p, c);
     } else {
-        norm_load8(w, (const float*)p.weight, c, p.C);
+        norm_weight<float>(w, p, c);
     }
 }
 
@@ -143,8 +166,8 @@ __global__ __launch_bounds__(TPR < kLayerThreads ? kLayerThreads : TPR) void nor
     if (row >= p.rows) return;                   // a row of several waves is a workgroup of its own
     const int64_t at = row * p.C;
     float v[NC][8];
-    NormRow<TI, TPR, NC, false> x;
-    NormRow<TR, TPR, NC, false> res;
+    NormRow<TI, TPR, NC, kHere> x;
+    NormRow<TR, TPR, NC, kHere> res;
     x.load((const TI*)p.x + at, tid, p.C);
     if (p.residual) res.load((const TR*)p.residual + at, tid, p.C);
     x.get(v, (const TI*)p.x + at, tid, p.C);
@@ -238,7 +261,7 @@ template <int TPR> __device__ __forceinline__ Sums row_sums(Sums x, Sums* red) {
 // well, the weights too, with the next row's s and dy on their way, which have to be there before this row's dx is
 // stored: a later wait for them would be one for the stores as well (209715 x 320 bf16 162 -> 143 us).  Rows above 12288
 // channels are read again from the caches.
-template <typename TI, typename TR, int TPR, int NC>
+template <typename TI, typename TR, int TPR, int NC, int WAY>
 __global__ __launch_bounds__(TPR < kLayerThreads ? kLayerThreads : TPR) void norm_bwd_kernel(NormParams p) {
     constexpr int RPB = TPR < kLayerThreads ? kLayerThreads / TPR : 1;
     constexpr bool kHeld = TPR <= 512;
@@ -252,8 +275,8 @@ __global__ __launch_bounds__(TPR < kLayerThreads ? kLayerThreads : TPR) void nor
     for (int i = 0; i < NC; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
-    NormRow<TR, TPR, H, true> ns, nds;
-    NormRow<TI, TPR, H, true> ng;
+    NormRow<TR, TPR, H, WAY> ns, nds;
+    NormRow<TI, TPR, H, WAY> ng;
     if constexpr (kHeld) {
 #pragma unroll
         for (int i = 0; i < NC; ++i) norm_weight(w[i], p, norm_col<TPR>(tid, i));
@@ -399,14 +422,14 @@ template <typename TI, typename TR, int TPR, int NC> static void norm_fwd_launch
     constexpr int threads = TPR < kLayerThreads ? kLayerThreads : TPR, RPB = threads / TPR;
     hipLaunchKernelGGL((norm_fwd_kernel<TI, TR, TPR, NC>), dim3((unsigned)((p.rows + RPB - 1) / RPB)), dim3(threads), 0, stream, p);
 }
-template <typename TI, typename TR, int TPR, int NC> static void norm_bwd_launch(const NormParams& p, hipStream_t stream) {
+template <typename TI, typename TR, int TPR, int NC, int WAY = kEarly> static void norm_bwd_launch(const NormParams& p, hipStream_t stream) {
     constexpr int threads = TPR < kLayerThreads ? kLayerThreads : TPR;
-    hipLaunchKernelGGL((norm_bwd_kernel<TI, TR, TPR, NC>), dim3((unsigned)norm_bwd_blocks(p.C, p.rows)), dim3(threads), 0, stream, p);
+    hipLaunchKernelGGL((norm_bwd_kernel<TI, TR, TPR, NC, WAY>), dim3((unsigned)norm_bwd_blocks(p.C, p.rows)), dim3(threads), 0, stream, p);
 }
 template <typename TI, typename TR> static void norm_types(const NormParams& p, bool backward, hipStream_t stream) {
     const int C = p.C;
     if (backward) {
-        if (C < 8) norm_bwd_launch<TI, TR, 1024, 2>(p, stream);    // read where they are used, element by element
+        if (C < 8) norm_bwd_launch<TI, TR, 16, 1, kShort>(p, stream);
         else if (C <= 128) norm_bwd_launch<TI, TR, 16, 1>(p, stream);
         else if (C <= 256) norm_bwd_launch<TI, TR, 32, 1>(p, stream);
         else if (C <= 384) norm_bwd_launch<TI, TR, 16, 3>(p, stream);
@@ -446,10 +469,10 @@ hipError_t launch_norm_fwd(const NormParams& p, int in_bf16, int res_bf16, hipSt
 // 200: 213, 127, 110, 145;  384: 115, 103, 116, 107;  512: 171, 112, 100, 121;  768: 115, 104, 115, 107;  1000: 145, 101,
 // 119, 107;  1280: 139, 104, 121, 107;  2048: 148, 112, 101, 122;  4096: 111, 101, 115, 107;  5120: 122, 102, 119, 108;
 // 8192: 98, 102, 106, 113.  Moving the bytes takes 104 at a large copy's rate.
-static int norm_rows_at_once(int32_t C) { return C < 8 ? 1 : C <= 128 ? 16 : C <= 256 ? 8 : C <= 384 ? 16 : C <= 512 ? 4 : C <= 768 ? 8 : C <= 1536 ? 4 : 1; }
+static int norm_rows_at_once(int32_t C) { return C <= 128 ? 16 : C <= 256 ? 8 : C <= 384 ? 16 : C <= 512 ? 4 : C <= 768 ? 8 : C <= 1536 ? 4 : 1; }
 int norm_bwd_blocks(int32_t C, int64_t rows) {
     const int64_t groups = (rows + norm_rows_at_once(C) - 1) / norm_rows_at_once(C);
-    const int64_t most = 256 * (C < 8 ? 1 : C <= 128 ? 4 : C <= 256 ? 3 : C <= 384 ? 2 : C <= 512 ? 3 : C <= 1536 ? 2 : C <= 2048 ? 3 : C <= 6144 ? 2 : 1);
+    const int64_t most = 256 * (C <= 128 ? 4 : C <= 256 ? 3 : C <= 384 ? 2 : C <= 512 ? 3 : C <= 1536 ? 2 : C <= 2048 ? 3 : C <= 6144 ? 2 : 1);
     return (int)(groups < most ? groups : most);
 }
 hipError_t launch_norm_bwd(const NormParams& p, int in_bf16, int res_bf16, float* dw, hipStream_t stream) {
