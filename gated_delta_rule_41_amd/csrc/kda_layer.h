@@ -216,6 +216,9 @@ __device__ __forceinline__ void store_out(void* p, int64_t i, float x, bool as_b
     else ((float*)p)[i] = x;
 }
 
+// The forward's rows a workgroup and its threads.
+inline int norm_fwd_rows(int32_t C) { return C <= 128 ? 16 : C <= 256 ? 8 : C <= 1024 ? 4 : 1; }
+inline int norm_fwd_threads(int32_t C) { return C <= 8192 ? kLayerThreads : 512; }
 hipError_t launch_norm_fwd(const NormParams& p, int in_bf16, int res_bf16, hipStream_t stream);
 hipError_t launch_norm_bwd(const NormParams& p, int in_bf16, int res_bf16, float* dw, hipStream_t stream);
 int norm_bwd_blocks(int32_t C, int64_t rows);

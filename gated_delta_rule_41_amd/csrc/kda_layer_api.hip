@@ -67,7 +67,10 @@ kda_status check_norm(const kda_norm_config* c, int64_t rows, bool backward) {
     if (c->in_dtype == KDA_F32 && c->res_dtype == KDA_BF16) return fail(KDA_ERR_UNSUPPORTED, "fp32 inputs take an fp32 residual%s");
     if (!(c->eps >= 0.f) || !isfinite(c->eps)) return fail(KDA_ERR_INVALID_ARG, "eps must be finite and >= 0%s");
     if (rows < 0) return fail(KDA_ERR_INVALID_ARG, "rows must be >= 0%s");
-    if (!grid_fits(rows, 512)) return fail(KDA_ERR_UNSUPPORTED, "rows too large for one launch%s");
+    // the forward's launch; the backward's workgroups take as many rows as there are
+    const int at_once = norm_fwd_rows(c->C);
+    if (!grid_fits(rows / at_once + (rows % at_once != 0), norm_fwd_threads(c->C)))
+        return fail(KDA_ERR_UNSUPPORTED, "rows too large for one launch%s");
     return KDA_OK;
 }
 

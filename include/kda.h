@@ -465,7 +465,9 @@ void kda_norm_config_init(kda_norm_config* cfg, int32_t C);
  * scale[row] = m / (Q sqrt(mean(s^2) + eps)), fp32 [rows]: y = code * scale.  A
  * row of zeros has zero codes and scale 0; one with an infinity or NaN has
  * scale NaN and unspecified codes.  scale is NULL for the other types.
- * rows = 0 enqueues nothing. */
+ * rows = 0 enqueues nothing.  One launch takes up to 2^24 - 1 workgroups of 16
+ * rows (C <= 128), 8 (C <= 256), 4 (C <= 1024) or one (C <= 8192), and 2^23 - 1
+ * of one row above; the backward takes as many rows. */
 kda_status kda_norm_fwd(const kda_norm_config* cfg, int64_t rows, const void* x, const void* residual,
                         const void* weight, void* y, void* s, float* scale, void* stream);
 

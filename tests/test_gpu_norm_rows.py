@@ -61,3 +61,21 @@ def test_backward_with_ends_of_every_length(whole):
     for C in range(whole + 1, whole + 8):
         s, dy, ds = (rand(rows, C, F32, C + i) for i in range(3))
         check_backward(s, 1 + rand(1, C, F32, C + 3)[0], dy, ds)
+
+
+def test_more_rows_than_2_to_the_23():
+    """262144 tokens of 32 heads and some more: their last rows as those rows alone."""
+    need_gpu()
+    rows, last, C = 262144 * 32 + 21, 40, 128
+    x, w = rand(last, C, BF16, 1), 1 + rand(1, C, F32, 2)[0]
+    big = torch.zeros(rows, C, dtype=BF16, device="cuda")
+    big[-last:] = x
+    y, _ = kda.kda_norm_fwd(big, w, eps=EPS)
+    want, _ = kda.kda_norm_fwd(x, w, eps=EPS)
+    assert torch.equal(y[-last:], want) and not y[:-last].any()
+    del y
+    d = kda.kda_norm_bwd(big, w, big, eps=EPS)
+    small = kda.kda_norm_bwd(x, w, x, eps=EPS)
+    assert torch.equal(d["dx"][-last:], small["dx"]) and not d["dx"][:-last].any()
+    _, dwm = ref.norm_bwd_bound(host(x), host(w), host(x), np.zeros(x.shape), EPS)
+    assert (np.abs(host(d["dw"]) - host(small["dw"])) <= 2 * dwm).all()
