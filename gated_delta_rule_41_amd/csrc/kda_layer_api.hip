@@ -6,6 +6,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <initializer_list>
 
 #include "../../include/kda.h"
 #include "kda_internal.h"
@@ -42,6 +43,22 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
 }
 kda_status apart(const void* a, size_t na, const char* name, const void* b, size_t nb) {
     return overlap(a, na, b, nb) ? fail(KDA_ERR_INVALID_ARG, "%s overlaps another argument", name) : KDA_OK;
+}
+// An argument's memory.  An output may lie in memory of its own only, or be an input of its `kind` itself, of the same bytes.
+struct Span {
+    const void* p;
+    size_t bytes;
+    const char* name;
+    int kind;                                     // 0: shared with nothing
+};
+constexpr int kRowsOf = 1, kStates = 2;
+kda_status outputs_apart(std::initializer_list<Span> outputs, std::initializer_list<Span> inputs) {
+    for (const Span* o = outputs.begin(); o != outputs.end(); ++o) {
+        for (const Span& i : inputs)
+            if (!(o->kind && o->kind == i.kind && o->p == i.p && o->bytes == i.bytes)) KDA_TRY(apart(o->p, o->bytes, o->name, i.p, i.bytes));
+        for (const Span* other = outputs.begin(); other != o; ++other) KDA_TRY(apart(o->p, o->bytes, o->name, other->p, other->bytes));
+    }
+    return KDA_OK;
 }
 // The largest number of workgroups along x: one launch covers at most 2^32 - 1 work-items.
 bool grid_fits(int64_t workgroups, int threads) { return workgroups >= 0 && workgroups <= (int64_t)UINT32_MAX / threads; }
@@ -86,6 +103,7 @@ kda_status check_conv(const kda_conv_config* c) {
     return KDA_OK;
 }
 int64_t row_stride(int64_t stride, int64_t width) { return stride ? stride : width; }
+size_t cu_bytes(int32_t N) { return ((size_t)N + 1) * sizeof(int32_t); }
 // From the first element to the last, in bytes.
 size_t extent(int64_t rows, int64_t stride, int64_t width, size_t es) { return rows > 0 ? ((size_t)(rows - 1) * stride + width) * es : 0; }
 
@@ -113,6 +131,9 @@ kda_status conv_plan(const kda_conv_config* c, int64_t T, int32_t N, bool backwa
     *slots = layer_slots(T, N, *len);
     return grid_fits(*slots, kLayerThreads) ? KDA_OK : fail(KDA_ERR_UNSUPPORTED, "num_seqs or total_tokens too large for one launch%s");
 }
+size_t conv_state(const kda_conv_config* c, int32_t N) { return (size_t)N * (c->width - 1) * c->C * elem(c->in_dtype); }
+size_t conv_weights(const kda_conv_config* c) { return (size_t)c->C * c->width * elem(c->weight_dtype); }
+size_t conv_bias(const kda_conv_config* c) { return c->C * elem(c->weight_dtype); }
 ConvParams conv_params(const kda_conv_config* c) {
     ConvParams p;
     memset(&p, 0, sizeof p);
@@ -196,6 +217,27 @@ kda_status check_selective_sizes(const kda_selective_config* c, int64_t T, int32
         return fail(KDA_ERR_UNSUPPORTED, "num_seqs or total_tokens too large for one launch%s");
     return KDA_OK;
 }
+// Bytes of the arguments, T rows of each.
+struct SelectiveSizes {
+    size_t x, dt, z, dy, out, B, C, dB, A, D, state;
+    int in_place;                                 // outputs of rows may be inputs of rows
+    SelectiveSizes(const kda_selective_config* c, int64_t T, int32_t N) {
+        const size_t es = elem(c->in_dtype), os = elem(c->out_dtype);
+        const int64_t gs = (int64_t)c->G * c->S;
+        x = extent(T, row_stride(c->x_stride, c->C), c->C, es);
+        dt = extent(T, row_stride(c->dt_stride, c->C), c->C, es);
+        z = extent(T, row_stride(c->z_stride, c->C), c->C, es);
+        dy = extent(T, c->C, c->C, es);
+        out = extent(T, c->C, c->C, os);
+        B = extent(T, row_stride(c->b_stride, gs), gs, es);
+        C = extent(T, row_stride(c->c_stride, gs), gs, es);
+        dB = extent(T, gs, gs, os);
+        A = (size_t)c->C * c->S * sizeof(float);
+        D = c->C * sizeof(float);
+        state = N * A;
+        in_place = es == os ? kRowsOf : 0;
+    }
+};
 SelectiveParams selective_params(const kda_selective_config* c) {
     SelectiveParams p;
     memset(&p, 0, sizeof p);
@@ -320,9 +362,10 @@ kda_status kda_conv_fwd(const kda_conv_config* cfg, int64_t T, int32_t N, const 
     KDA_TRY(ptr(sfinal, "final_state", false));
     ConvParams p = conv_params(cfg);
     // strips of a document run at the same time and read the rows before their own
-    const size_t es = elem(cfg->in_dtype), state = (size_t)N * (cfg->width - 1) * cfg->C * es, ny = (size_t)T * cfg->C * elem(cfg->out_dtype);
-    KDA_TRY(apart(sfinal, state, "final_state", s0, state));
-    KDA_TRY(apart(y, ny, "y", x, extent(T, p.x_stride, p.C, es)));
+    const size_t state = conv_state(cfg, N);
+    KDA_TRY(outputs_apart({{y, (size_t)T * cfg->C * elem(cfg->out_dtype), "y", 0}, {sfinal, state, "final_state", 0}},
+                          {{x, extent(T, p.x_stride, p.C, elem(cfg->in_dtype)), "x", 0}, {weight, conv_weights(cfg), "weight", 0},
+                           {bias, conv_bias(cfg), "bias", 0}, {cu, cu_bytes(N), "cu_seqlens", 0}, {s0, state, "initial_state", 0}}));
     int64_t slots;
     KDA_TRY(conv_plan(cfg, T, N, false, &p.len, &slots));
     p.x = x; p.weight = weight; p.bias = bias; p.cu = cu; p.s0 = s0; p.y = y; p.sfinal = sfinal;
@@ -355,11 +398,12 @@ kda_status kda_conv_bwd(const kda_conv_config* cfg, int64_t T, int32_t N, const 
     KDA_TRY(ptr(db, "dbias", false));
     KDA_TRY(ptr(ds0, "d_initial_state", false));
     ConvParams p = conv_params(cfg);
-    const size_t es = elem(cfg->in_dtype), state = (size_t)N * (cfg->width - 1) * cfg->C * es, nx = (size_t)T * cfg->C * elem(cfg->out_dtype);
-    KDA_TRY(apart(ds0, state, "d_initial_state", s0, state));
-    KDA_TRY(apart(ds0, state, "d_initial_state", dsf, state));
-    KDA_TRY(apart(dx, nx, "dx", x, extent(T, p.x_stride, p.C, es)));
-    KDA_TRY(apart(dx, nx, "dx", dy, (size_t)T * cfg->C * es));
+    const size_t es = elem(cfg->in_dtype), state = conv_state(cfg, N), rows = (size_t)T * cfg->C;
+    KDA_TRY(outputs_apart({{dx, rows * elem(cfg->out_dtype), "dx", 0}, {dw, (size_t)cfg->C * cfg->width * sizeof(float), "dweight", 0},
+                           {db, cfg->C * sizeof(float), "dbias", 0}, {ds0, state, "d_initial_state", 0}},
+                          {{x, extent(T, p.x_stride, p.C, es), "x", 0}, {weight, conv_weights(cfg), "weight", 0},
+                           {bias, conv_bias(cfg), "bias", 0}, {cu, cu_bytes(N), "cu_seqlens", 0}, {s0, state, "initial_state", 0},
+                           {dy, rows * es, "dy", 0}, {dsf, state, "d_final_state", 0}}));
     int64_t slots;
     KDA_TRY(conv_plan(cfg, T, N, true, &p.len, &slots));
     const size_t need = kda_conv_bwd_workspace_size(cfg, T, N);
@@ -385,9 +429,14 @@ kda_status kda_conv_decode(const kda_conv_config* cfg, int32_t N, const void* x,
     KDA_TRY(ptr(state_out, "state_out", N > 0));
     KDA_TRY(ptr(y, "y", N > 0));
     ConvParams p = conv_params(cfg);
-    const size_t state = (size_t)N * (cfg->width - 1) * cfg->C * elem(cfg->in_dtype);
+    const size_t state = conv_state(cfg, N);
     if (state_in != state_out && overlap(state_in, state, state_out, state))
         return fail(KDA_ERR_INVALID_ARG, "state_in and state_out overlap without being equal%s");
+    // a thread reads its channels before it writes them
+    KDA_TRY(outputs_apart({{y, (size_t)N * cfg->C * elem(cfg->out_dtype), "y", cfg->out_dtype == cfg->in_dtype ? kRowsOf : 0},
+                           {state_out, state, "state_out", kStates}},
+                          {{x, extent(N, p.x_stride, p.C, elem(cfg->in_dtype)), "x", kRowsOf}, {weight, conv_weights(cfg), "weight", 0},
+                           {bias, conv_bias(cfg), "bias", 0}, {state_in, state, "state_in", kStates}}));
     if (N == 0) return KDA_OK;
     p.x = x; p.weight = weight; p.bias = bias; p.s0 = state_in; p.sfinal = state_out; p.y = y; p.N = N;
     return launched(launch_conv_decode(p, cfg->width, cfg->in_dtype == KDA_BF16, (hipStream_t)stream));
@@ -433,8 +482,12 @@ kda_status kda_selective_fwd(const kda_selective_config* cfg, int64_t T, int32_t
     KDA_TRY(check_selective_call(cfg, T, N, x, dt, A, B, C, D, z, bias, cu, s0));
     KDA_TRY(ptr(y, "y", T > 0));
     KDA_TRY(ptr(sfinal, "final_state", false));
-    const size_t state = (size_t)N * cfg->C * cfg->S * sizeof(float);
-    KDA_TRY(apart(sfinal, state, "final_state", s0, state));
+    const SelectiveSizes n(cfg, T, N);
+    // a lane has its own channel's rows of a block of tokens before it writes any of them
+    KDA_TRY(outputs_apart({{y, n.out, "y", n.in_place}, {sfinal, n.state, "final_state", 0}},
+                          {{x, n.x, "x", kRowsOf}, {dt, n.dt, "dt", kRowsOf}, {z, n.z, "z", kRowsOf}, {A, n.A, "A", 0}, {B, n.B, "B", 0},
+                           {C, n.C, "C", 0}, {D, n.D, "D", 0}, {bias, n.D, "dt_bias", 0}, {cu, cu_bytes(N), "cu_seqlens", 0},
+                           {s0, n.state, "initial_state", 0}}));
     const SelectivePlan f = selective_plan(cfg, T, N, false);
     if (workspace_bytes < f.total) return fail(KDA_ERR_WORKSPACE, "workspace too small%s");
     KDA_TRY(ptr(workspace, "workspace", f.total > 0));
@@ -468,9 +521,14 @@ kda_status kda_selective_bwd(const kda_selective_config* cfg, int64_t T, int32_t
     KDA_TRY(ptr(dz, "dz", T > 0 && z));
     KDA_TRY(ptr(dbias, "ddt_bias", false));
     KDA_TRY(ptr(ds0, "d_initial_state", false));
-    const size_t state = (size_t)N * cfg->C * cfg->S * sizeof(float);
-    KDA_TRY(apart(ds0, state, "d_initial_state", s0, state));
-    KDA_TRY(apart(ds0, state, "d_initial_state", dsf, state));
+    const SelectiveSizes n(cfg, T, N);
+    // as in the forward; the walks that read the others' rows have ended before
+    KDA_TRY(outputs_apart({{dx, n.out, "dx", n.in_place}, {ddt, n.out, "ddt", n.in_place}, {z ? dz : nullptr, n.out, "dz", n.in_place},
+                           {dA, n.A, "dA", 0}, {dB, n.dB, "dB", 0}, {dC, n.dB, "dC", 0}, {dD, n.D, "dD", 0}, {dbias, n.D, "ddt_bias", 0},
+                           {ds0, n.state, "d_initial_state", 0}},
+                          {{x, n.x, "x", kRowsOf}, {dt, n.dt, "dt", kRowsOf}, {z, n.z, "z", kRowsOf}, {dy, n.dy, "dy", kRowsOf},
+                           {A, n.A, "A", 0}, {B, n.B, "B", 0}, {C, n.C, "C", 0}, {D, n.D, "D", 0}, {bias, n.D, "dt_bias", 0},
+                           {cu, cu_bytes(N), "cu_seqlens", 0}, {s0, n.state, "initial_state", 0}, {dsf, n.state, "dS_final", 0}}));
     const SelectivePlan f = selective_plan(cfg, T, N, true);
     if (workspace_bytes < f.total) return fail(KDA_ERR_WORKSPACE, "workspace too small%s");
     KDA_TRY(ptr(workspace, "workspace", true));
@@ -506,9 +564,13 @@ kda_status kda_selective_decode(const kda_selective_config* cfg, int32_t N, cons
     KDA_TRY(ptr(state_in, "state_in", false));
     KDA_TRY(ptr(state_out, "state_out", N > 0));
     KDA_TRY(ptr(y, "y", N > 0));
-    const size_t state = (size_t)N * cfg->C * cfg->S * sizeof(float);
-    if (state_in != state_out && overlap(state_in, state, state_out, state))
+    const SelectiveSizes n(cfg, N, N);
+    if (state_in != state_out && overlap(state_in, n.state, state_out, n.state))
         return fail(KDA_ERR_INVALID_ARG, "state_in and state_out overlap without being equal%s");
+    // the lanes that share a channel are in one wave and read its values before the first of them writes
+    KDA_TRY(outputs_apart({{y, n.out, "y", n.in_place}, {state_out, n.state, "state_out", kStates}},
+                          {{x, n.x, "x", kRowsOf}, {dt, n.dt, "dt", kRowsOf}, {z, n.z, "z", kRowsOf}, {A, n.A, "A", 0}, {B, n.B, "B", 0},
+                           {C, n.C, "C", 0}, {D, n.D, "D", 0}, {bias, n.D, "dt_bias", 0}, {state_in, n.state, "state_in", kStates}}));
     if (N == 0) return KDA_OK;
     SelectiveParams p = selective_params(cfg);
     p.x = x; p.dt = dt; p.A = A; p.B = B; p.Cm = C; p.D = D; p.z = z; p.bias = bias; p.s0 = state_in; p.sfinal = state_out; p.y = y;

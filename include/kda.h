@@ -506,8 +506,9 @@ void kda_conv_config_init(kda_conv_config* cfg, int32_t C, int32_t width);
  * before it, oldest first; the final state is the last width - 1 rows of both.
  *   x, y, dy, dx : [total_tokens, C]    weight : [C, width]    bias : [C] or NULL
  *   states : [num_seqs, width - 1, C] in in_dtype (NULL: zero / not kept)
- * initial_state and final_state must not overlap, nor y and x.  total_tokens / 8 +
- * num_seqs below 2^24 (kda_conv_decode: num_seqs * C below 2^32). */
+ * Outputs must not overlap inputs or each other (KDA_ERR_INVALID_ARG; for
+ * kda_conv_decode see there).  total_tokens / 8 + num_seqs below 2^24
+ * (kda_conv_decode: num_seqs * C below 2^32). */
 kda_status kda_conv_fwd(const kda_conv_config* cfg, int64_t total_tokens, int32_t num_seqs, const void* x,
                         const void* weight, const void* bias, const int32_t* cu_seqlens, const void* initial_state,
                         void* y, void* final_state, void* stream);
@@ -522,8 +523,9 @@ kda_status kda_conv_bwd(const kda_conv_config* cfg, int64_t total_tokens, int32_
                         void* d_initial_state, void* workspace, size_t workspace_bytes, void* stream);
 
 /* One token per sequence: x, y [num_seqs, C]; state_out is the state after the
- * token and may be state_in itself (NULL: zero), but must not otherwise overlap
- * it.  num_seqs = 0 enqueues nothing. */
+ * token and may be state_in itself (NULL: zero), and y may be x where their types
+ * are equal and x's rows have no gaps; outputs must not otherwise overlap inputs or
+ * each other.  num_seqs = 0 enqueues nothing. */
 kda_status kda_conv_decode(const kda_conv_config* cfg, int32_t num_seqs, const void* x, const void* weight,
                            const void* bias, const void* state_in, void* state_out, void* y, void* stream);
 
@@ -566,8 +568,9 @@ void kda_selective_config_init(kda_selective_config* cfg, int32_t C, int32_t S, 
  * workspace holds the segments' states (0 bytes where nothing is cut, or for an
  * invalid config or sizes), the backward's also the states before every few
  * tokens (about 11 bytes a token and channel at S = 16) and, for every 64 channels,
- * a share of dB and dC.  initial_state and final_state must not overlap.
- * total_tokens * G * S below 2^31, and num_seqs below 2^23 (kda_selective_decode:
+ * a share of dB and dC.  y may be x, dt or z itself where their types are equal
+ * and its rows have no gaps; outputs must not otherwise overlap inputs or each
+ * other (KDA_ERR_INVALID_ARG).  total_tokens * G * S below 2^31, and num_seqs below 2^23 (kda_selective_decode:
  * num_seqs * C * S below 2^34). */
 size_t kda_selective_fwd_workspace_size(const kda_selective_config* cfg, int64_t total_tokens, int32_t num_seqs);
 size_t kda_selective_bwd_workspace_size(const kda_selective_config* cfg, int64_t total_tokens, int32_t num_seqs);
@@ -581,8 +584,9 @@ kda_status kda_selective_fwd(const kda_selective_config* cfg, int64_t total_toke
  * from the forward's inputs.  dy : [total_tokens, C], in_dtype.  Outputs: dx,
  * ddt (of dt as given), dz [total_tokens, C] and dB, dC [total_tokens, G, S] in
  * out_dtype; dA [C, S], dD [C], ddt_bias [C] in fp32 (dD, ddt_bias may be NULL; dz
- * is not used without z); d_initial_state fp32 or NULL, which must not overlap
- * initial_state or dS_final. */
+ * is not used without z); d_initial_state fp32 or NULL.  dx, ddt and dz may be x,
+ * dt, z or dy themselves as y may be in the forward; outputs must not otherwise
+ * overlap inputs or each other. */
 kda_status kda_selective_bwd(const kda_selective_config* cfg, int64_t total_tokens, int32_t num_seqs, const void* x,
                              const void* dt, const float* A, const void* B, const void* C, const float* D,
                              const void* z, const float* dt_bias, const int32_t* cu_seqlens,
@@ -592,8 +596,8 @@ kda_status kda_selective_bwd(const kda_selective_config* cfg, int64_t total_toke
 
 /* One token per sequence on a resident state, as kda_decode: x, dt, z, y
  * [num_seqs, C], B, C [num_seqs, G, S]; state_in (NULL: zero), state_out (may be
- * state_in itself, must not otherwise overlap it).  num_seqs = 0 enqueues
- * nothing. */
+ * state_in itself).  y as in the forward; outputs must not otherwise overlap
+ * inputs or each other.  num_seqs = 0 enqueues nothing. */
 kda_status kda_selective_decode(const kda_selective_config* cfg, int32_t num_seqs, const void* x, const void* dt,
                                 const float* A, const void* B, const void* C, const float* D, const void* z,
                                 const float* dt_bias, const float* state_in, float* state_out, void* y,
