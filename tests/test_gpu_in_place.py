@@ -98,3 +98,54 @@ def test_scan_step_over_an_input(c, S, G, dtype, over):
     assert _lib.kda_selective_decode_raw(cfg, N, *(p(d[n]) for n in ("x", "dt", "A", "B", "C", "D", "z", "bias")), p(d["h0"]), p(d["h0"]), p(y),
                                          stream()) == 0
     assert torch.equal(y, want) and torch.equal(d["h0"], end)
+
+
+# row ends in a thread's second group, in a wave of their own, rows read again, fewer than eight channels
+WIDTHS = [5, 100, 333, 1000, 1025, 2049, 2561, 4096, 4099, 6137, 8200, 12281, 12289, 16377, 16384]
+
+
+@pytest.mark.parametrize("C", WIDTHS)
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_norm_over_its_inputs(C, dtype):
+    """y over x, and s over the residual or over x with y elsewhere."""
+    need_gpu()
+    rows = 300
+    x, r, w = rand(rows, C, dtype=dtype, seed=1), rand(rows, C, dtype=dtype, seed=2), rand(1, C, dtype=dtype, seed=3)[0]
+    want, total = kda.kda_norm_fwd(x, w, r)
+    alone, _ = kda.kda_norm_fwd(x, w)
+    cfg = _lib.make_norm_config(C, *[CODE[dtype]] * 4)
+
+    def call(x, r, y, s):
+        assert _lib.kda_norm_fwd_raw(cfg, rows, p(x), p(r), p(w), p(y), p(s), 0, stream()) == 0
+        return y, s
+
+    a, b = x.clone(), r.clone()
+    y, s = call(a, b, a, b)
+    assert torch.equal(y, want) and torch.equal(s, total)
+    a = x.clone()
+    y, s = call(a, r, torch.empty_like(x), a)
+    assert torch.equal(y, want) and torch.equal(s, total)
+    a = x.clone()
+    assert torch.equal(call(a, None, a, None)[0], alone)
+    codes, _, scale = kda.kda_norm_fwd(x, w, r, out_dtype=torch.int8)
+    cfg.out_dtype = _lib.KDA_I8
+    a, got, got_scale = x.clone(), torch.empty_like(codes), torch.empty_like(scale)
+    assert _lib.kda_norm_fwd_raw(cfg, rows, p(a), p(r), p(w), p(got), p(a), p(got_scale), stream()) == 0
+    assert torch.equal(got, codes) and torch.equal(a, total) and torch.equal(got_scale, scale)
+
+
+@pytest.mark.parametrize("C", WIDTHS)
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("over", ["dy", "ds"])
+def test_norm_backward_over_a_gradient(C, dtype, over):
+    """More rows than one turn of the workgroups takes: rows asked for early lie beside rows that are written."""
+    need_gpu()
+    rows = 20011 if C < 400 else 1700
+    s, dy, ds = (rand(rows, C, dtype=dtype, seed=i) for i in range(3))
+    w = rand(1, C, dtype=dtype, seed=3)[0]
+    want = kda.kda_norm_bwd(s, w, dy, ds)
+    cfg = _lib.make_norm_config(C, *[CODE[dtype]] * 4, eps=1e-6)
+    ws = torch.empty(_lib.kda_norm_bwd_workspace_size(cfg, rows), dtype=torch.uint8, device="cuda")
+    dx, dw = {"dy": dy, "ds": ds}[over], torch.empty_like(want["dw"])
+    assert _lib.kda_norm_bwd_raw(cfg, rows, p(s), p(w), p(dy), p(ds), p(dx), p(dw), p(ws), ws.numel(), stream()) == 0
+    assert torch.equal(dx, want["dx"]) and torch.equal(dw, want["dw"])
