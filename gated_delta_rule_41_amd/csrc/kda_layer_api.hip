@@ -108,9 +108,10 @@ size_t cu_bytes(int32_t N) { return ((size_t)N + 1) * sizeof(int32_t); }
 size_t extent(int64_t rows, int64_t stride, int64_t width, size_t es) { return rows > 0 ? ((size_t)(rows - 1) * stride + width) * es : 0; }
 
 // Channels a thread: eight move whole 16-byte pieces, one gives small calls eight times the threads, each with an eighth
-// to do.  us of a forward and a backward, eight and one, width 4: bf16 1000 x 512 5.0, 16.0 and 4.0, 10.6;  1000 x 2048
-// 5.4, 18.6 and 5.7, 13.3;  16000 x 333 7.8, 29.2 and 8.6, 27.1;  1000 x 8192 7.3, 27.1 and 9.5, 32.3;  fp32 4000 x 2048
-// 16.9, 36.5 and 15.5, 32.9;  16000 x 2048 54.1, 93.5 and 45.6, 106.8.
+// to do.  One rule for both directions, by the sum of the two.  us of a forward and a backward, eight and one, width 4:
+// bf16 1000 x 512 5.0, 16.0 and 4.0, 10.6;  1000 x 2048 5.4, 18.6 and 5.7, 13.3;  16000 x 333 7.8, 29.2 and 8.6, 27.1;
+// 1000 x 8192 7.3, 27.1 and 9.5, 32.3;  fp32 4000 x 2048 16.9, 36.5 and 15.5, 32.9;  16000 x 2048 54.1, 93.5 and 45.6,
+// 106.8: there a forward by itself would gain from one.
 bool conv_eight(const kda_conv_config* c, int64_t T) {
     return c->C >= 8 && T * c->C >= (c->in_dtype == KDA_BF16 ? (int64_t)1 << 22 : (int64_t)1 << 24);
 }

@@ -4,9 +4,11 @@
 // one group, so B_t and C_t are the same for the whole wave: they come through the scalar
 // cache and enter the products as scalar operands, and the sums over the state's entries stay
 // in a lane.  An entry and token costs a multiply and an exponential for the decay, a
-// multiply and a multiply-add for the state and a multiply-add for the output.  The exponential
-// takes two issue slots (measured, as logarithms and quotients do), so these are 6, which bound
-// the kernels: 217 us for 67.1M tokens and channels of 16 entries, where HBM would ask 105.
+// multiply and a multiply-add for the state and a multiply-add for the output.  With 34 more a
+// token for the step size, the gate, conversions and accesses these are 114 instructions at 16
+// entries (counted), and they bound the kernels: 195 us at an instruction every four cycles and
+// 229 with a second slot for the 20 exponentials, logarithms and quotients among them, which
+// part of the time is another wave's, for 67.1M tokens and channels, where HBM would ask 105.
 #pragma once
 #include "kda_layer.h"
 

@@ -1,8 +1,9 @@
 // kda_selective_states.hip -- states across the segments of a document, forward and in reverse:
 // every segment's own sum from a zero state, its share of the gradient of the state that enters
 // it, and the carries along the segments.  The own sums walk as the forward does
-// (kda_selective.h), without the output's multiply-add: 5 issue slots an entry and token, 162 us
-// for 67.1M tokens and channels of 16 entries.
+// (kda_selective.h), without the output's multiply-add and the gate: four instructions an entry
+// and token and 19 beside them, 142 us for 67.1M tokens and channels of 16 entries at an
+// instruction every four cycles, 173 with second slots.
 #include "kda_selective.h"
 
 namespace kda {

@@ -3,8 +3,9 @@ addition, the short causal convolution, and the selective scan.  Marshalling onl
 as in the package's ``__init__``: see include/kda.h for the layouts.
 
 Inputs called x, dt, B, C and z may be parts of wider rows (a split projection):
-their last dimensions have to be contiguous, rows may be further apart.  All other
-tensors are contiguous.
+their last dimensions have to be contiguous, rows may be further apart.  They begin
+at a multiple of 16 bytes, and so does every row of B and C.  All other tensors are
+contiguous.
 """
 from __future__ import annotations
 

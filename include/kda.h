@@ -567,8 +567,8 @@ void kda_selective_config_init(kda_selective_config* cfg, int32_t C, int32_t S, 
  * and the sizes): own sums first, then a carry, then the walks; the forward's
  * workspace holds the segments' states (0 bytes where nothing is cut, or for an
  * invalid config or sizes), the backward's also the states before every few
- * tokens (about 11 bytes a token and channel at S = 16) and, for every 64 channels,
- * a share of dB and dC.  y may be x, dt or z itself where their types are equal
+ * tokens (about 11 bytes a token and channel at S = 16) and, for every started 64
+ * channels of each group, a share of dB and dC (8 S bytes a token).  y may be x, dt or z itself where their types are equal
  * and its rows have no gaps; outputs must not otherwise overlap inputs or each
  * other (KDA_ERR_INVALID_ARG).  total_tokens * G * S below 2^31, and num_seqs below 2^23 (kda_selective_decode:
  * num_seqs * C * S below 2^34). */
