@@ -560,7 +560,8 @@ void kda_selective_config_init(kda_selective_config* cfg, int32_t C, int32_t S, 
  *   A      : fp32 [C, S]      D, dt_bias : fp32 [C] or NULL (0)
  *   states : fp32 [num_seqs, C, S]
  * A is finite, and dt A <= 0 is meant (decays); larger ones work as long as the
- * decays over a document stay in range.  Everything inside is fp32.  Infinities and NaN reach
+ * decays over a document stay in range.  Everything inside is fp32, decays and gates
+ * below 2^-126 are zero.  Infinities and NaN reach
  * what depends on them by the recurrence and nothing else (dA, dD and dt_bias's
  * gradient are sums over all tokens); which of the two a result is, is open.
  * Documents are cut into segments where that fills the GPU (a rule on the config
